@@ -19,6 +19,9 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnrc.so")
 SOURCES = ["api.cpp", "context_norms.hip", "norms_ex.hip", "draft_boundary.hip", "kv_project.hip", "kv_store.hip", "selftest.hip"]
+# the chain's kernels: what the stored counter measurements were taken of
+CHAIN_SOURCES = ["context_norms.hip", "device_common.h", "draft_boundary.hip", "kernels.h", "kv_project.hip", "kv_store.hip",
+                 "norms_ex.hip", "selftest.hip"]
 
 ARCH = "gfx950"
 COMMON = [
@@ -84,13 +87,14 @@ def _code_only(text):
 
 
 def source_hash():
-    """Hash of every library source and header with comments and layout
+    """Hash of the chain's kernel sources and headers with comments and layout
     removed (identifies the kernels that a stored counter measurement belongs
-    to; a change to comments alone keeps it)."""
+    to; a change to comments, to host-side checks or to other operators keeps
+    it)."""
     import hashlib
 
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
+    for name in CHAIN_SOURCES:
         with open(os.path.join(CSRC, name), encoding="utf-8") as f:
             h.update(name.encode() + b"\0" + _code_only(f.read()).encode())
     return h.hexdigest()[:16]

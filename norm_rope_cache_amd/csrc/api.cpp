@@ -18,10 +18,11 @@
 
 #include "../../include/nrc.h"
 #include "kernels.h"
+#include "status.h"
 
-namespace {
+namespace nrc {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -30,8 +31,6 @@ int fail(int code, const char* fmt, ...) {
     va_end(ap);
     return code;
 }
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // CUs of the current device, looked up once per device (relaxed atomics:
 // concurrent first calls store the same value).
@@ -55,11 +54,16 @@ int launch_status(int rc, const char* what) {
     return NRC_OK;
 }
 
-}  // namespace
+}  // namespace nrc
+
+using nrc::aligned;
+using nrc::fail;
+using nrc::launch_status;
+using nrc::num_cus;
 
 extern "C" {
 
-const char* nrc_last_error(void) { return g_err; }
+const char* nrc_last_error(void) { return nrc::g_err; }
 
 int32_t nrc_abi_version(void) { return 1; }
 
