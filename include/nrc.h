@@ -2,7 +2,8 @@
  * nrc.h - C ABI of libnrc, the MI355X (gfx950) context K/V chain of the
  * DSpark draft: hidden RMSNorm -> per-layer input RMSNorm, stacked -> batched
  * K/V projection -> weightless 64-wide K-norm -> GPT-J RoPE -> paged-cache
- * insert.
+ * insert; and of the operators that use the cache: rotary positions,
+ * attention of drafted tokens over it, the weight its cells receive, eviction.
  *
  * Sources: the vLLM API pages of the Muse Spark specialized decode,
  *   "...cutedsl.draft.context"       (ContextNorms, ContextKvStore and their kernels),
@@ -420,6 +421,222 @@ int32_t nrc_context_kv_project_store(const uint16_t* normed, const uint16_t* w, 
                                      int64_t rows, const uint16_t* cos_sin, int64_t max_position,
                                      uint16_t* const* caches, int64_t num_blocks, int64_t block_size, float eps,
                                      void* stream);
+
+/* Element types. */
+#define NRC_DTYPE_BF16 0
+#define NRC_DTYPE_F16 1
+#define NRC_DTYPE_F32 2
+
+/* Scalings of nrc_rope_table. */
+#define NRC_ROPE_SCALE_NONE 0
+#define NRC_ROPE_SCALE_LINEAR 1
+#define NRC_ROPE_SCALE_BASE 2
+#define NRC_ROPE_SCALE_BANDS 3
+#define NRC_ROPE_SCALE_RAMP 4
+
+/* Pair layouts of nrc_rope_rotate. */
+#define NRC_ROPE_INTERLEAVED 0 /* pairs (2j, 2j + 1) */
+#define NRC_ROPE_HALF 1        /* pairs (j, j + rotary_dim / 2) */
+
+/* Positions lie below this (their angles keep 24 bits after the point in double). */
+#define NRC_ROPE_MAX_POSITION (1LL << 28)
+
+/*
+ * nrc_rope_table - the cos/sin table that nrc_context_kv_store and
+ * nrc_rope_rotate read (page "...cutedsl.draft.context", _rope: a row holds
+ * the cosines, then the sines), for plain and for stretched contexts.
+ *
+ *   start, count  the positions start .. start + count - 1, one row each.
+ *   rotary_dim    R, even, 2 .. 256: R / 2 pairs turn.
+ *   width         the row's length, even, R .. 512: cos of width / 2 pairs, then
+ *                 their sin. The pairs after the R / 2 do not turn (cos 1,
+ *                 sin 0): width 64 with R < 64 makes nrc_context_kv_store
+ *                 rotate a part of the head.
+ *   base, scaling, factor, original_max, low, high
+ *                 pair j's angle per position f_j, from v_j = base^(-2 j / R)
+ *                 and its turns over the original length, t_j =
+ *                 original_max v_j / (2 pi):
+ *                 NONE    v_j
+ *                 LINEAR  v_j / factor
+ *                 BASE    v_j of the base base factor^(R / (R - 2))
+ *                 BANDS   v_j (m + (1 - m) / factor), m = (t_j - low) / (high -
+ *                         low) held to [0, 1]: above `high` turns kept, below
+ *                         `low` divided
+ *                 RAMP    v_j (1 - m + m / factor), m = (j - a) / (b - a) held
+ *                         to [0, 1], a and b the pair indexes where the turns
+ *                         are `high` (rounded down, at least 0) and `low`
+ *                         (rounded up, at most R / 2 - 1)
+ *   magnitude     factor of the turning pairs' cos and sin.
+ *   out           [count, width] of dtype NRC_DTYPE_BF16 or NRC_DTYPE_F32.
+ * Angles, cos and sin are in double; each element is rounded once.
+ * count == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or misaligned out,
+ * positions outside [0, NRC_ROPE_MAX_POSITION), a width or scaling argument
+ * out of range), NRC_ENOTSUP (another type, rotary_dim out of range).
+ */
+int32_t nrc_rope_table(int64_t start, int64_t count, int32_t rotary_dim, int32_t width, double base, int32_t scaling,
+                       double factor, double original_max, double low, double high, double magnitude, void* out,
+                       int32_t dtype, void* stream);
+
+/*
+ * nrc_rope_rotate - rotary positions applied to heads: the queries that meet
+ * the keys nrc_context_kv_store rotated (page "...cutedsl.draft.context",
+ * _rope), or, with inverse, their gradients.
+ *
+ *   x          [T, H, head_dim] of dtype (NRC_DTYPE_*), unit stride in the head,
+ *              row and head strides in elements. H head_dim <= 65536,
+ *              T <= 2^23. 16-byte aligned heads take 16-byte accesses, others
+ *              single elements.
+ *   positions  [T] int64; a row whose position is outside [0, max_position)
+ *              is left as it is.
+ *   cos_sin    [max_position, rotary_dim] of table_dtype (bf16 or FP32),
+ *              contiguous: cos of the rotary_dim / 2 pairs, then sin.
+ *   layout     NRC_ROPE_INTERLEAVED or NRC_ROPE_HALF; elements from
+ *              rotary_dim on are copied.
+ *   inverse    1: turns by the negative angles (the transposed, for gradients).
+ *   out        the same shape and type, its own strides; x itself (same
+ *              pointer and strides), or memory apart from x's.
+ * (a, b) -> (a c - b s, b c + a s), each an FP32 product and one FMA, rounded to
+ * the type once. T == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or
+ * misaligned operands, shapes, strides, an out that overlaps x or itself),
+ * NRC_ENOTSUP (types, too many rows or elements for one call).
+ */
+int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int32_t head_dim, int64_t x_row_stride,
+                        int64_t x_head_stride, const int64_t* positions, const void* cos_sin, int32_t table_dtype,
+                        int64_t max_position, int32_t rotary_dim, int32_t layout, int32_t inverse, void* out,
+                        int64_t out_row_stride, int64_t out_head_stride, void* stream);
+
+/*
+ * nrc_context_tree_attention - drafted tokens attending to their sequence's
+ * cached keys: one token (decoding), a chain, or a tree (an ancestor mask),
+ * over the cache that nrc_context_kv_store fills (page
+ * "...runtime.draft", DraftDecode._attention: the draft's queries over its
+ * context cache).
+ *
+ *   q          [T, Hq, 64] bf16, unit last stride, row and head strides in
+ *              elements, multiples of 8, 16-byte aligned. Query head i belongs to
+ *              KV head i / (Hq / H).
+ *   cache      one layer's cache view as nrc_context_kv_store_ex's
+ *              (block, page and head strides, multiples of 8), K in [0, 64), V in
+ *              [64, 128) of each run; 16-byte aligned.
+ *   tables     [B, table_width] int32, row stride table_stride: the sequences'
+ *              blocks; key i of sequence b is page i % block_size of
+ *              tables[b][i / block_size].
+ *   ctx_lens   [B] int32: keys 0 .. ctx_lens[b] - 1 are the context.
+ *   q_starts   [B + 1] int32, rising: sequence b's nodes are rows q_starts[b]
+ *              .. q_starts[b + 1] - 1; node i's own K and V are key
+ *              ctx_lens[b] + i, stored before the call. Rows outside them are
+ *              left as they are.
+ *   max_nodes  at least every sequence's nodes (later rows of a longer one
+ *              are left as they are); 1 .. 65535.
+ *   max_ctx    at least every ctx_lens[b] (a longer one is cut to it).
+ *   tree_mask  [T, mask_words] int64, 64 mask_words >= max_nodes: bit j of row
+ *              q_starts[b] + i set: node i sees node j of its sequence. NULL
+ *              (mask_words 0): a chain, node i sees nodes 0 .. i. Every
+ *              node sees the whole context.
+ *   scale      factor of the scores, > 0. softcap: 0, or scores become
+ *              softcap tanh(score / softcap).
+ *   out        [T, Hq, 64] bf16, contiguous, 16-byte aligned.
+ *   lse        [T, Hq] float: the log of the row's sum of e^score.
+ *   workspace  nrc_context_tree_attention_workspace_bytes(...) bytes,
+ *              16-byte aligned, caller-owned; unused (may be NULL) when that is
+ *              0. Its contents on return are unspecified; calls that share one
+ *              must not overlap.
+ * A row that sees no key gets out 0 and lse -inf. K and V of keys that a row does
+ * not see do not reach it, NaN and infinities included. Scores, maxima and
+ * sums are FP32; the weights are rounded to bf16 for the product with V, the
+ * output once.
+ * Keys whose block is outside [0, num_blocks) or past the table are seen by
+ * no row and not read. T == 0 or B == 0 returns NRC_OK.
+ * Errors: NRC_EINVAL (NULL or misaligned operands, shapes, strides, scale,
+ * softcap, a small workspace), NRC_ENOTSUP (Hq not a multiple of H, more than
+ * 2^31 slots, shapes too large for one call).
+ */
+int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
+                                   int32_t Hq, const uint16_t* cache, int64_t num_blocks, int64_t block_size,
+                                   int64_t block_stride, int64_t page_stride, int64_t head_stride, int32_t H,
+                                   const int32_t* tables, int64_t table_stride, int64_t table_width, int32_t B,
+                                   const int32_t* ctx_lens, const int32_t* q_starts, int32_t max_nodes,
+                                   int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale,
+                                   float softcap, uint16_t* out, float* lse, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/*
+ * nrc_context_tree_attention_workspace_bytes - the workspace of
+ * nrc_context_tree_attention for these sizes on the current device: 0 when
+ * the keys are not split, else FP32 partial sums of every row and split.
+ * Negative status for sizes that nrc_context_tree_attention rejects.
+ */
+int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t Hq, int32_t H, int32_t max_nodes,
+                                                   int64_t max_ctx);
+
+/*
+ * nrc_context_attention_mass - the attention weight that each cached cell
+ * receives, by which nrc_context_kv_evict keeps cells:
+ *   out[b, h, j] = decay weights[b, h, j] + sum over the rows of KV head h of
+ *   sequence b that see key j of e^(score - lse)
+ * for j < ctx_lens[b] + its nodes, and 0 for the other j < width (so that a later
+ * token's cell starts from 0). Scores as nrc_context_tree_attention's.
+ *
+ *   q .. softcap  as nrc_context_tree_attention.
+ *   lse        [T, Hq] float from nrc_context_tree_attention. Rows with -inf
+ *              add nothing.
+ *   weights    [B, H, width] float, batch and head strides in elements, or
+ *              NULL (0); may be out itself.
+ *   decay      factor of the earlier weights.
+ *   out        [B, H, width] float, batch and head strides in elements.
+ * FP32 sums in one fixed order. B == 0 or width == 0 returns NRC_OK.
+ * Errors as nrc_context_tree_attention.
+ */
+int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
+                                   int32_t Hq, const uint16_t* cache, int64_t num_blocks, int64_t block_size,
+                                   int64_t block_stride, int64_t page_stride, int64_t head_stride, int32_t H,
+                                   const int32_t* tables, int64_t table_stride, int64_t table_width, int32_t B,
+                                   const int32_t* ctx_lens, const int32_t* q_starts, int32_t max_nodes,
+                                   int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale,
+                                   float softcap, const float* lse, const float* weights, int64_t w_batch_stride,
+                                   int64_t w_head_stride, float decay, float* out, int64_t out_batch_stride,
+                                   int64_t out_head_stride, int64_t width, void* stream);
+
+/*
+ * nrc_context_kv_evict - keeps the `budget` cells of every (sequence, KV
+ * head) that come first in the order: protected cells, then the larger
+ * weight (a NaN as -inf), among equals the lower index. Protected are
+ * positions below `sinks` and positions from ends[b] - recent on. Kept cells
+ * at index new_len and above move into the evicted cells' places below it, the
+ * first into the first; the others stay where they are. Keys keep their
+ * rotation, so attention over the kept cells needs no order.
+ *
+ *   cache      one layer's cache view as nrc_context_kv_store_ex's; cells
+ *              move in place. A sequence's blocks must belong to it alone.
+ *   tables, lens  as nrc_context_tree_attention: cells 0 .. lens[b] - 1.
+ *   weights    [B, H, width] float and positions [B, H, width] int32, batch
+ *              and head strides in elements; width >= every lens[b] (a longer
+ *              one is cut to it).
+ *   ends       [B] int32: one past the newest token's position.
+ *   sinks, recent, budget  >= 0, >= 0, >= 1.
+ *   new_weights, new_positions  [B, H, budget] contiguous: of the kept cells in
+ *              their new places; 0 and -1 from new_lens[b] on. Apart from
+ *              weights and positions, which are not written.
+ *   new_lens   [B] int32: min(lens[b], budget).
+ *   workspace  nrc_context_kv_evict_workspace_bytes(B, H, width, budget) bytes,
+ *              16-byte aligned; unused (may be NULL) when that is 0. Contents on
+ *              return unspecified; calls that share one must not overlap.
+ * Cells whose block is outside [0, num_blocks) are neither read nor written.
+ * B == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or misaligned operands,
+ * shapes, strides, a small workspace), NRC_ENOTSUP (more than 2^31 slots,
+ * shapes too large for one call).
+ */
+int32_t nrc_context_kv_evict(uint16_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,
+                             int64_t page_stride, int64_t head_stride, int32_t H, const int32_t* tables,
+                             int64_t table_stride, int64_t table_width, int32_t B, const int32_t* lens,
+                             const float* weights, int64_t w_batch_stride, int64_t w_head_stride,
+                             const int32_t* positions, int64_t p_batch_stride, int64_t p_head_stride, int64_t width,
+                             const int32_t* ends, int32_t sinks, int32_t recent, int32_t budget, float* new_weights,
+                             int32_t* new_positions, int32_t* new_lens, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/* Bytes of nrc_context_kv_evict's workspace: 0 when no cell can move; negative status for bad sizes. */
+int64_t nrc_context_kv_evict_workspace_bytes(int32_t B, int32_t H, int64_t width, int32_t budget);
 
 /*
  * nrc_check_scalars - diagnostic: the device primitives every kernel uses,

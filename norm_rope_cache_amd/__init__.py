@@ -15,6 +15,14 @@ libnrc.so is missing, every call raises.
     context_kv_project_fused(h, r, pre_w, w_kv)    projection with the layer norms fused in
     context_kv_chain(...)                          the whole chain (unfused by default)
     draft_boundary(branch, stream_in, alpha, beta, ...)   the residual boundary
+
+and the operators that use the cache the chain fills:
+
+    rope_table(count, rotary_dim, ...)             the cos/sin table, also for stretched contexts
+    rope_rotate(x, positions, cos_sin, ...)        query heads, or their gradients, rotated by it
+    context_tree_attention(q, cache, tables, ...)  drafted tokens attending to the cache -> (out, lse)
+    context_attention_mass(q, cache, tables, ..., lse, ...)   the weight each cached cell receives
+    context_kv_evict(cache, tables, lens, weights, ...)       the cells of most weight kept (in place)
 """
 
 import ctypes
@@ -32,6 +40,11 @@ __all__ = [
     "context_hidden_norm",
     "context_kv_project_fused",
     "context_kv_project_noalloc",
+    "rope_table",
+    "rope_rotate",
+    "context_tree_attention",
+    "context_attention_mass",
+    "context_kv_evict",
     "kv_views",
     "check_scalars",
     "check_bf16_pair",
@@ -120,6 +133,25 @@ def _load():
     L.nrc_traffic_twin.argtypes = [_vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp]
     L.nrc_check_bf16_pair.restype = _i32
     L.nrc_check_bf16_pair.argtypes = [_vp, _vp, _i64, _vp]
+    f64 = ctypes.c_double
+    L.nrc_rope_table.restype = _i32
+    L.nrc_rope_table.argtypes = [_i64, _i64, _i32, _i32, f64, _i32, f64, f64, f64, f64, f64, _vp, _i32, _vp]
+    L.nrc_rope_rotate.restype = _i32
+    L.nrc_rope_rotate.argtypes = [_vp, _i32, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
+                                  _i64, _i64, _vp]
+    paged = [_vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _i64, _i32]
+    queries = [_vp, _i64, _i64, _i64, _i32] + paged + [_vp, _vp, _i32, _i64, _vp, _i32, _f32, _f32]
+    L.nrc_context_tree_attention.restype = _i32
+    L.nrc_context_tree_attention.argtypes = queries + [_vp, _vp, _vp, _i64, _vp]
+    L.nrc_context_tree_attention_workspace_bytes.restype = _i64
+    L.nrc_context_tree_attention_workspace_bytes.argtypes = [_i32, _i64, _i32, _i32, _i32, _i64]
+    L.nrc_context_attention_mass.restype = _i32
+    L.nrc_context_attention_mass.argtypes = queries + [_vp, _vp, _i64, _i64, _f32, _vp, _i64, _i64, _i64, _vp]
+    L.nrc_context_kv_evict.restype = _i32
+    L.nrc_context_kv_evict.argtypes = paged + [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _i32, _vp,
+                                               _vp, _vp, _vp, _i64, _vp]
+    L.nrc_context_kv_evict_workspace_bytes.restype = _i64
+    L.nrc_context_kv_evict_workspace_bytes.argtypes = [_i32, _i32, _i64, _i32]
     _lib = L
     return L
 
@@ -784,6 +816,332 @@ def traffic_twin(x, L, mode, out=None, per_cu=1, stream=None):
     _call(x, _load().nrc_traffic_twin, _ptr(x), T, L, mode, per_cu, _ptr(out), _ptr(sink),
           0 if sink is None else sink.numel(), _stream(stream, x))
     return out
+
+
+def _empty(shape, dtype, device, stream):
+    """An uninitialized tensor of the call's stream: as under
+    torch.cuda.stream(stream) when one is given, so that its memory is not one that
+    another stream still uses."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _fits32(**values):
+    """Raise unless every value is an integer of 32 bits (ctypes would cut it)."""
+    for name, v in values.items():
+        if not isinstance(v, int) or not -(1 << 31) <= v < 1 << 31:
+            raise ValueError(f"{name} must be an integer of 32 bits, not {v!r}")
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+
+
+def _dtype_code(dtype, name, table=False):
+    import torch
+
+    codes = {torch.bfloat16: 0, torch.float32: 2} if table else {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    if dtype not in codes:
+        raise TypeError(f"{name} must be bfloat16 or float32{'' if table else ' or float16'}, not {dtype}")
+    return codes[dtype]
+
+
+def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, original_max=0, low=1.0, high=32.0,
+               magnitude=1.0, width=None, start=0, dtype=None, device=None, out=None, stream=None):
+    """The cos/sin table [count, width] of positions start .. start + count - 1
+    (bf16 unless dtype is float32): cos of width / 2 pairs, then sin.
+
+    rotary_dim  the elements that turn; width (default rotary_dim) adds pairs
+                that do not (64 with a smaller rotary_dim lets context_kv_store
+                rotate a part of the head)
+    scaling     "none"; "linear" (angles divided by factor); "base" (base
+                times factor^(R / (R - 2))); "bands" and "ramp" (slow pairs
+                divided, fast ones kept, those between `low` and `high` turns over
+                original_max in between: by their turns, or by their index)
+    magnitude   factor of cos and sin
+    """
+    import torch
+
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {', '.join(ROPE_SCALINGS)}")
+    width = rotary_dim if width is None else width
+    _fits32(rotary_dim=rotary_dim, width=width)
+    if out is None:
+        if count < 0 or width < 0:
+            raise ValueError("count and width must not be negative")
+        device = torch.device("cuda") if device is None else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"the table is made on a GPU, not on {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        out = _empty((count, width), torch.bfloat16 if dtype is None else dtype, device, stream)
+    elif not out.is_cuda or not out.is_contiguous() or tuple(out.shape) != (count, width):
+        raise ValueError("out must be a contiguous device tensor [count, width]")
+    elif dtype is not None and out.dtype != dtype or device is not None and torch.device(device) not in (
+            out.device, torch.device(out.device.type)):
+        raise ValueError("out is of another dtype or device than asked for")
+    code = _dtype_code(out.dtype, "the table", table=True)
+    _call(out, _load().nrc_rope_table, start, count, rotary_dim, width, base, ROPE_SCALINGS[scaling], factor,
+          original_max, low, high, magnitude, _ptr(out), code, _stream(stream, out))
+    return out
+
+
+def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=None, stream=None):
+    """x [T, H, d] (bf16, float16 or float32; any row and head strides) with the
+    first R = cos_sin.shape[1] elements of each head turned by its row's
+    position; the rest is copied.
+
+    positions  [T] int64; a row outside the table is left as it is
+    cos_sin    [max_position, R] bf16 or float32 (rope_table)
+    layout     "interleaved" (pairs 2j, 2j + 1, as context_kv_store turns its
+               keys) or "half" (pairs j, j + R / 2)
+    inverse    turn back: the gradient of the rotation
+    out        x itself, or a tensor apart from it (default: a new one)
+    """
+    import torch
+
+    code = _dtype_code(x.dtype, "x")
+    if not x.is_cuda:
+        raise TypeError("x must be a GPU tensor")
+    if x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1:
+        raise ValueError("x must be [T, H, d] with unit last stride")
+    T, H, d = x.shape
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout is 'interleaved' or 'half'")
+    tcode = _dtype_code(cos_sin.dtype, "cos_sin", table=True)
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_position, R]")
+    if positions.dtype != torch.int64 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 [T] tensor")
+    if out is None:
+        out = _empty((T, H, d), x.dtype, x.device, stream)
+    elif out.dtype != x.dtype or tuple(out.shape) != (T, H, d) or out.stride(2) != 1:
+        raise ValueError("out must be shaped like x, of its dtype, with unit last stride")
+    _all_on(x, positions=positions, cos_sin=cos_sin, out=out)
+    _call(x, _load().nrc_rope_rotate, _ptr(x), code, T, H, d, x.stride(0), x.stride(1), _ptr(positions), _ptr(cos_sin),
+          tcode, cos_sin.shape[0], cos_sin.shape[1], ROPE_LAYOUTS[layout], 1 if inverse else 0, _ptr(out),
+          out.stride(0), out.stride(1), _stream(stream, x))
+    return out
+
+
+def _int32(t, name, ref, shape=None):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _same_device(t, ref, name)
+
+
+def _paged_operands(cache, tables):
+    """Checks of one layer's cache view and its block tables; the C ABI's
+    arguments from `cache` to `B`."""
+    import torch
+
+    _bf16(cache, "cache", contiguous=False)
+    if cache.dim() != 4 or cache.shape[3] != 2 * HEAD_DIM or cache.stride(3) != 1:
+        raise ValueError("cache must be a [num_blocks, H, block_size, 128] view with unit last stride")
+    if not isinstance(tables, torch.Tensor) or tables.dtype != torch.int32 or tables.dim() != 2 or (
+            tables.shape[1] > 1 and tables.stride(1) != 1):
+        raise ValueError("tables must be an int32 [B, blocks] tensor with unit last stride")
+    _same_device(tables, cache, "tables")
+    nb, H, bs, _ = cache.shape
+    st = [n if size > 1 else 0 for n, size in zip(cache.stride(), cache.shape)]  # (one of a kind has no stride)
+    return (_ptr(cache), nb, bs, st[0], st[2], st[1], H, _ptr(tables), tables.stride(0), tables.shape[1],
+            tables.shape[0])
+
+
+def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap):
+    """Checks shared by the attention and its received weights; the C ABI's
+    arguments from `q` to `softcap`, and max_ctx."""
+    import torch
+
+    paged = _paged_operands(cache, tables)
+    _fits32(max_nodes=max_nodes)
+    _bf16(q, "q", contiguous=False)
+    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+        raise ValueError("q must be [T, Hq, 64] with unit last stride")
+    T, Hq, _ = q.shape
+    B = tables.shape[0]
+    _same_device(q, cache, "q")
+    _int32(ctx_lens, "ctx_lens", cache, (B,))
+    _int32(q_starts, "q_starts", cache, (B + 1,))
+    words = 0
+    if tree_mask is not None:
+        if (not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64 or tree_mask.dim() != 2
+                or tree_mask.shape[0] != T or not tree_mask.is_contiguous()):
+            raise ValueError("tree_mask must be a contiguous int64 [T, words] tensor")
+        _same_device(tree_mask, cache, "tree_mask")
+        words = tree_mask.shape[1]
+        if words == 0:
+            raise ValueError("tree_mask must have a word a row at least")
+    if max_ctx is None:
+        max_ctx = tables.shape[1] * cache.shape[2]
+    scale = HEAD_DIM ** -0.5 if scale is None else scale
+    # (a [0, words] mask has no address, and no row to read)
+    mask = _ptr(tree_mask) if words and T else None
+    st = [n if size > 1 else 0 for n, size in zip(q.stride(), q.shape)]
+    return (_ptr(q), st[0], st[1], T, Hq, *paged, _ptr(ctx_lens), _ptr(q_starts), max_nodes, max_ctx, mask,
+            words if T else 0, scale, softcap), max_ctx
+
+
+def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx=None, tree_mask=None, scale=None,
+                           softcap=0.0, out=None, lse=None, stream=None):
+    """Drafted tokens attending to the cache of one layer -> (out [T, Hq, 64]
+    bf16, lse [T, Hq] float32).
+
+    q         [T, Hq, 64] bf16, every sequence's nodes one after the other;
+              query head i reads KV head i // (Hq // H)
+    cache     [num_blocks, H, block_size, 128] bf16 (context_kv_store), any
+              strides that are multiples of 8
+    tables    [B, blocks] int32: the sequences' blocks
+    ctx_lens  [B] int32: keys before the nodes; node i's K and V are key
+              ctx_lens + i, stored before the call
+    q_starts  [B + 1] int32: sequence b's rows of q
+    max_nodes most nodes of a sequence; max_ctx most of ctx_lens (default: what
+              the tables hold)
+    tree_mask [T, words] int64: bit j set, the row sees node j of its
+              sequence; None: a chain (each node sees those up to itself)
+    scale     factor of the scores (1/8); softcap: scores become
+              softcap tanh(score / softcap) when it is not 0
+    A row that sees no key gets 0 and -inf. The keys of long contexts are split
+    over workgroups, with a workspace from torch's allocator."""
+    import torch
+
+    args, max_ctx = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale,
+                                    softcap)
+    T, Hq, _ = q.shape
+    B, H = tables.shape[0], cache.shape[1]
+    if out is None:
+        out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
+    else:
+        _bf16(out, "out")
+        if tuple(out.shape) != (T, Hq, HEAD_DIM):
+            raise ValueError("out must be [T, Hq, 64]")
+        _same_device(out, q, "out")
+    if lse is None:
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
+    else:
+        _float_lse(lse, q)
+    lib = _load()
+    # the split follows the device's size: asked with q's GPU as the current device
+    with torch.cuda.device(q.device):
+        need = lib.nrc_context_tree_attention_workspace_bytes(B, T, Hq, H, max_nodes, max_ctx)
+    if need < 0:
+        _check(need)
+    ws = _empty(need, torch.uint8, q.device, stream) if need > 0 else None
+    _call(q, lib.nrc_context_tree_attention, *args, _ptr(out), _ptr(lse), _ptr(ws), need, _stream(stream, q))
+    return out, lse
+
+
+def _float_lse(lse, q):
+    import torch
+
+    if lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
+    return _same_device(lse, q, "lse")
+
+
+def _cells(t, name, ref, dtype, shape):
+    """A [B, H, width] tensor of per-cell values with unit last stride."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be a {dtype} [B, H, width] tensor with unit last stride")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _same_device(t, ref, name)
+
+
+def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes, max_ctx=None, tree_mask=None,
+                           scale=None, softcap=0.0, weights=None, decay=1.0, width=None, out=None, stream=None):
+    """decay * weights + the attention weight each cached cell receives from
+    the rows of q, [B, H, width] float32; 0 past each sequence's keys.
+
+    lse      [T, Hq] float32 from context_tree_attention on the same operands
+    weights  [B, H, width] float32 (any batch and head strides) or None (0)
+    width    cells a head (default: weights' or out's, else what the tables hold)
+    out      may be weights itself (default: a new tensor)
+    Other arguments as context_tree_attention."""
+    import torch
+
+    args, _ = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap)
+    B, H = tables.shape[0], cache.shape[1]
+    _float_lse(lse, q)
+    if width is None:
+        given = weights if weights is not None else out
+        width = tables.shape[1] * cache.shape[2] if given is None or given.dim() != 3 else given.shape[2]
+    if weights is not None:
+        _cells(weights, "weights", q, torch.float32, (B, H, width))
+    if out is None:
+        out = _empty((B, H, width), torch.float32, q.device, stream)
+    else:
+        _cells(out, "out", q, torch.float32, (B, H, width))
+    ws = (0, 0) if weights is None else (weights.stride(0), weights.stride(1))
+    _call(q, _load().nrc_context_attention_mass, *args, _ptr(lse), _ptr(weights), ws[0], ws[1], decay, _ptr(out),
+          out.stride(0), out.stride(1), width, _stream(stream, q))
+    return out
+
+
+def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sinks=0, recent=0, new_weights=None,
+                     new_positions=None, new_lens=None, stream=None):
+    """Keep, in place, the `budget` cells of every (sequence, KV head) with the
+    most weight -> (new_weights [B, H, budget] float32, new_positions
+    [B, H, budget] int32, new_lens [B] int32).
+
+    cache, tables  as context_tree_attention; no block in two tables
+    lens       [B] int32: cells of each sequence
+    weights    [B, H, width] float32, positions [B, H, width] int32 (any batch
+               and head strides), width >= every length
+    ends       [B] int32: one past the newest token's position
+    sinks, recent  positions below sinks, and from ends - recent on, come first
+    Equal weights: the lower index stays. Kept cells past the new length move
+    into the holes before it; weights and positions follow them."""
+    import torch
+
+    paged = _paged_operands(cache, tables)
+    _fits32(budget=budget, sinks=sinks, recent=recent)
+    B, H = tables.shape[0], cache.shape[1]
+    _int32(lens, "lens", cache, (B,))
+    _int32(ends, "ends", cache, (B,))
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise ValueError("weights must be a float32 [B, H, width] tensor")
+    width = weights.shape[2]
+    _cells(weights, "weights", cache, torch.float32, (B, H, width))
+    _cells(positions, "positions", cache, torch.int32, (B, H, width))
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    lib = _load()
+    need = lib.nrc_context_kv_evict_workspace_bytes(B, H, width, budget)
+    if need < 0:
+        _check(need)
+    dev = cache.device
+    if new_weights is None:
+        new_weights = _empty((B, H, budget), torch.float32, dev, stream)
+    else:
+        _cells(new_weights, "new_weights", cache, torch.float32, (B, H, budget))
+    if new_positions is None:
+        new_positions = _empty((B, H, budget), torch.int32, dev, stream)
+    else:
+        _cells(new_positions, "new_positions", cache, torch.int32, (B, H, budget))
+    if not new_weights.is_contiguous() or not new_positions.is_contiguous():
+        raise ValueError("new_weights and new_positions must be contiguous")
+    if new_lens is None:
+        new_lens = _empty((B,), torch.int32, dev, stream)
+    else:
+        _int32(new_lens, "new_lens", cache, (B,))
+    ws = _empty(need, torch.uint8, dev, stream) if need > 0 else None
+    _call(cache, lib.nrc_context_kv_evict, *paged, _ptr(lens), _ptr(weights), weights.stride(0), weights.stride(1),
+          _ptr(positions), positions.stride(0), positions.stride(1), width, _ptr(ends), sinks, recent, budget,
+          _ptr(new_weights), _ptr(new_positions), _ptr(new_lens), _ptr(ws), need, _stream(stream, cache))
+    return new_weights, new_positions, new_lens
 
 
 def context_kv_chain(x, hidden_w, pre_w, w_kv, positions, slots, cos_sin, caches, H, hidden_eps=1e-6,

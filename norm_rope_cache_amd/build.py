@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnrc.so")
-SOURCES = ["api.cpp", "context_norms.hip", "norms_ex.hip", "draft_boundary.hip", "kv_project.hip", "kv_store.hip", "selftest.hip"]
+SOURCES = ["api.cpp", "context_norms.hip", "norms_ex.hip", "draft_boundary.hip", "kv_project.hip", "kv_store.hip", "selftest.hip",
+           "cache_api.cpp", "rope.hip", "tree_attention.hip", "attention_mass.hip", "kv_evict.hip"]
 # the chain's kernels: what the stored counter measurements were taken of
 CHAIN_SOURCES = ["context_norms.hip", "device_common.h", "draft_boundary.hip", "kernels.h", "kv_project.hip", "kv_store.hip",
                  "norms_ex.hip", "selftest.hip"]

@@ -1,0 +1,66 @@
+// Device helpers of the kernels that read the paged cache.
+#pragma once
+
+#include "cache_ops.h"
+#include "device_common.h"
+
+namespace nrc {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x4 mfma16(U32x4 a, U32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+__device__ __forceinline__ uint32_t block_of(uint32_t key, const PagedCache& c) {
+    return c.bs_shift >= 0 ? key >> c.bs_shift : key / c.block_size;
+}
+
+// Element offset of the key's 128-element run within head 0, or -1 where
+// there is no such key.
+__device__ __forceinline__ int64_t key_offset(const PagedCache& c, const int32_t* table, uint32_t key) {
+    const uint32_t blk = block_of(key, c);
+    if (blk >= c.table_width) return -1;
+    const uint32_t page = (uint32_t)table[blk];
+    if (page >= c.num_blocks) return -1;
+    return (int64_t)page * c.block_stride + (int64_t)(key - blk * c.block_size) * c.page_stride;
+}
+
+// A sequence's rows of q: the first, and how many (both within [0, T]).
+struct Nodes {
+    int32_t first, count;
+};
+__device__ __forceinline__ Nodes nodes_of(const TreeQueries& t, int32_t b) {
+    const int32_t lo = t.q_starts[b], hi = t.q_starts[b + 1];
+    Nodes n{lo, hi - lo};
+    if (lo < 0 || hi > t.T || n.count < 0) n.count = 0;
+    if (n.count > t.max_nodes) n.count = t.max_nodes;
+    return n;
+}
+__device__ __forceinline__ int32_t context_of(const TreeQueries& t, int32_t b) {
+    const int32_t c = t.ctx_lens[b];
+    return c < 0 ? 0 : c > t.max_ctx ? t.max_ctx : c;
+}
+
+// Which of the nodes 32 w .. 32 w + 31 of a sequence of n node i (row `row`
+// of q) sees, as bits.
+__device__ __forceinline__ uint32_t seen_word(const TreeQueries& t, int32_t row, int32_t i, int32_t n, int32_t w) {
+    const int32_t first = 32 * w;
+    const int32_t last = t.mask ? n - 1 : i;  // the last node that can be seen
+    if (last < first) return 0u;
+    const uint32_t there = last - first >= 31 ? 0xFFFFFFFFu : (2u << (last - first)) - 1u;
+    if (!t.mask) return there;
+    return w < t.mask_words ? t.mask[(int64_t)row * t.mask_words + w] & there : 0u;
+}
+
+// e^x and log in base 2, the hardware's (relative error about 2^-23).
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }
+__device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
+
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+}  // namespace nrc
