@@ -224,10 +224,6 @@ int32_t queries(const char* what, const uint16_t* q, int64_t q_rs, int64_t q_hs,
     return NRC_OK;
 }
 
-int64_t attention_workspace(const nrc::AttentionPlan& p, int64_t T, int32_t Hq) {
-    return p.splits > 1 ? (int64_t)p.splits * T * Hq * (NRC_HEAD_DIM + 2) * 4 : 0;
-}
-
 // A [B, H, width] view of 4-byte elements.
 int32_t per_cell(const char* what, const char* name, const void* p, int64_t bs, int64_t hs, bool need) {
     if (need && !p) return fail(NRC_EINVAL, "%s: NULL %s", what, name);
@@ -250,7 +246,7 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
                                                    int64_t max_ctx) {
     if (int32_t rc = query_sizes("context_tree_attention", B, T, Hq, H, max_nodes, max_ctx)) return rc;
     if (B == 0 || T == 0) return 0;
-    return attention_workspace(nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, num_cus()), T, Hq);
+    return nrc::tree_attention_workspace(nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, num_cus()), T, Hq, B);
 }
 
 int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
@@ -274,12 +270,14 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
     if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
     a.plan = nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, num_cus());
-    const int64_t bytes = attention_workspace(a.plan, T, Hq);
+    const int64_t bytes = nrc::tree_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
     a.out = out;
     a.lse = lse;
     a.part = static_cast<float*>(workspace);
+    if (bytes > 0 && a.plan.many)  // the last [B, 2] of it
+        a.shares = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + bytes) - 2 * (int64_t)B;
     return launch_status(nrc::launch_tree_attention(a, (hipStream_t)stream), what);
 }
 

@@ -75,23 +75,27 @@ struct TreeQueries {
     float scale, softcap;  // softcap 0: none
 };
 
-// How a shape is split: a workgroup's query rows and waves, and the 32-key
-// tiles of one split.
+// How a shape is worked on: the kernel (many rows: keys shared through LDS),
+// the 16-row query tiles a wave holds, a workgroup's waves, the workgroups along the
+// rows. Few rows: the number of splits and the tiles of one. Many rows: splits 1
+// (none) or 2 (by the lengths: into at most `groups` workgroups per row block, of
+// at least split_tiles tiles each).
 struct AttentionPlan {
-    int32_t q_tiles;     // 16-row query tiles a wave holds: 1, 2 or 4
-    int32_t waves;       // of a workgroup, sharing its split's keys
-    int32_t row_blocks;  // workgroups along the query rows
-    int32_t splits, split_tiles;
+    bool many;
+    int32_t q_tiles, waves, row_blocks, splits, split_tiles, groups;
 };
 
 AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t num_cus);
+// Bytes of TreeAttentionArgs::part and, behind it, shares.
+int64_t tree_attention_workspace(const AttentionPlan& p, int64_t T, int64_t heads, int32_t B);
 
 struct TreeAttentionArgs {
     PagedCache kv;
     TreeQueries tq;
     uint16_t* out;  // [T, H G, 64]
     float* lse;     // [T, H G]
-    float* part;    // splits > 1: [splits, T, H G, 64] then [splits, T, H G, 2]
+    float* part;      // splits > 1: the partial sums' rows, [., 64] then [., 2]
+    int32_t* shares;  // many rows: [B, 2], each sequence's first group and its splits
     AttentionPlan plan;
 };
 

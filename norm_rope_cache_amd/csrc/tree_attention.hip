@@ -72,8 +72,8 @@ template <int R>
 struct Rows {
     U32x4 q[R][2];   // S's B operand: row l % 16, halves of d
     f32x4 o[R][4];   // O^T: row l % 16, d = 4 (4 (l / 16) + r) + c at [c][r]
-    float m[R];      // the running maximum, raw scores (-inf: none yet)
-    float base[R];   // subtracted from the scores in base 2: m's, or 0 without one
+    float limit[R];  // the running maximum and the slack, raw scores (-inf: no key yet)
+    float base[R];   // what is subtracted from the scores in base 2: the maximum's, or 0 without one
     float l[R];      // this lane's share of the sum
 };
 
@@ -83,12 +83,91 @@ __device__ __forceinline__ float in_base2(float raw, float c, float capped) {
     return raw * c;
 }
 
-// One tile. c: raw scores to base 2 (scale log2 e), or with CAP to the
+// Moves row rq's maximum up to the lanes' largest score `top`, and l and O with it.
+// (slack: 8 in base 2 as raw scores; the cap only brings scores nearer to each other.)
+template <int R, bool CAP>
+__device__ __forceinline__ void raise(Rows<R>& w, int rq, float top, float c, float capped, float slack) {
+    const float limit = __builtin_fmaxf(w.limit[rq], group_max(top) + slack);
+    const float base = limit == -__builtin_inff() ? 0.0f : in_base2<CAP>(limit - slack, c, capped);
+    // -inf before: no key yet, l and O are 0
+    const float shrink = w.limit[rq] == -__builtin_inff() ? 1.0f : exp2_hw(w.base[rq] - base);
+    w.l[rq] *= shrink;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w.o[rq][i][r] *= shrink;
+    w.limit[rq] = limit;
+    w.base[rq] = base;
+}
+
+__device__ __forceinline__ float max8(const f32x4 (&s)[2]) {
+    const float a = __builtin_fmaxf(__builtin_fmaxf(s[0][0], s[0][1]), s[0][2]);
+    const float b = __builtin_fmaxf(__builtin_fmaxf(s[0][3], s[1][0]), s[1][1]);
+    return __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(a, b), s[1][2]), s[1][3]);
+}
+
+// The weights of one query tile as the second product's operand; their sum.
+template <bool CAP>
+__device__ __forceinline__ float open_weights(const f32x4 (&s)[2], float base, float c, float capped, U32x4& pb) {
+    const float from = CAP ? capped - base : -base;
+    float p[8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            p[4 * t + r] = exp2_hw(CAP ? __builtin_fmaf(rcp_hw(exp2_hw(s[t][r] * c) + 1.0f), -2.0f * capped, from)
+                                       : __builtin_fmaf(s[t][r], c, from));
+    pb = U32x4{pack_bf16_pair_hw(p[0], p[1]), pack_bf16_pair_hw(p[2], p[3]), pack_bf16_pair_hw(p[4], p[5]),
+               pack_bf16_pair_hw(p[6], p[7])};
+    return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+}
+
+// A tile whose keys every row sees, two query tiles side by side: the products'
+// latencies and the exponentials of one hide behind the other's, and their
+// scores leave room in the registers.
+template <int R, bool CAP>
+__device__ __forceinline__ void open_tile(Rows<R>& w, const Keys& kv, float c, float capped, float slack) {
+    constexpr int P = R < 2 ? 1 : 2;
+#pragma unroll
+    for (int r0 = 0; r0 < R; r0 += P) {
+        f32x4 s[P][2];
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[j][t] = mfma16(kv.k[t][0], w.q[r0 + j][0], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[j][t] = mfma16(kv.k[t][1], w.q[r0 + j][1], s[j][t]);
+        float top[P];
+        bool up = false;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            top[j] = max8(s[j]);
+            up = up || top[j] > w.limit[r0 + j];
+        }
+        if (__any(up)) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) raise<R, CAP>(w, r0 + j, top[j], c, capped, slack);
+        }
+        U32x4 pb[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) w.l[r0 + j] += open_weights<CAP>(s[j], w.base[r0 + j], c, capped, pb[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const U32x4 va = v_operand(kv, i);
+#pragma unroll
+            for (int j = 0; j < P; ++j) w.o[r0 + j][i] = mfma16(va, pb[j], w.o[r0 + j][i]);
+        }
+    }
+}
+
+// One tile of which some rows may not see some keys. c: raw scores to base 2 (scale log2 e), or with CAP to the
 // exponent of tanh (2 scale log2 e / cap), capped then being cap log2 e.
-// MASKED: seen[rq] has this lane's rows' bits of the tile's keys.
-template <int R, bool CAP, bool MASKED>
-__device__ __forceinline__ void tile(Rows<R>& w, const Keys& kv, float c, float capped, float slack,
-                                     const uint32_t (&seen)[R], uint32_t lane) {
+// seen[rq]: this lane's rows' bits of the tile's keys.
+template <int R, bool CAP>
+__device__ __forceinline__ void masked_tile(Rows<R>& w, const Keys& kv, float c, float capped, float slack,
+                                            const uint32_t (&seen)[R], uint32_t lane) {
     const uint32_t g = lane >> 4;
     U32x4 va[4];
 #pragma unroll
@@ -101,29 +180,13 @@ __device__ __forceinline__ void tile(Rows<R>& w, const Keys& kv, float c, float 
             s[t] = mfma16(kv.k[t][0], w.q[rq][0], f32x4{0.f, 0.f, 0.f, 0.f});
             s[t] = mfma16(kv.k[t][1], w.q[rq][1], s[t]);
         }
-        if constexpr (MASKED) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) s[t][r] = -__builtin_inff();
-        }
-        float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(s[0][0], s[0][1]), __builtin_fmaxf(s[0][2], s[0][3])),
-                                    __builtin_fmaxf(__builtin_fmaxf(s[1][0], s[1][1]), __builtin_fmaxf(s[1][2], s[1][3])));
-        // (slack: 8 in raw scores; the cap only brings scores nearer to each other)
-        if (__any(top > w.m[rq] + slack)) {
-            const float m = __builtin_fmaxf(w.m[rq], group_max(top));
-            const float base = m == -__builtin_inff() ? 0.0f : in_base2<CAP>(m, c, capped);
-            // -inf before: no key yet, l and O are 0
-            const float shrink = w.m[rq] == -__builtin_inff() ? 1.0f : exp2_hw(w.base[rq] - base);
-            w.l[rq] *= shrink;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) w.o[rq][i][r] *= shrink;
-            w.m[rq] = m;
-            w.base[rq] = base;
-        }
+            for (int r = 0; r < 4; ++r)
+                if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) s[t][r] = -__builtin_inff();
+        const float top = max8(s);
+        if (__any(top > w.limit[rq])) raise<R, CAP>(w, rq, top, c, capped, slack);
         float p[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -132,7 +195,7 @@ __device__ __forceinline__ void tile(Rows<R>& w, const Keys& kv, float c, float 
                 float e;
                 if constexpr (CAP) {
                     e = __builtin_fmaf(rcp_hw(exp2_hw(s[t][r] * c) + 1.0f), -2.0f * capped, capped - w.base[rq]);
-                    if (MASKED && !(seen[rq] >> (16 * t + 4 * g + r) & 1u)) e = -__builtin_inff();
+                    if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) e = -__builtin_inff();
                 } else {
                     e = __builtin_fmaf(s[t][r], c, -w.base[rq]);
                 }
@@ -173,76 +236,524 @@ __device__ __forceinline__ void load_keys(Keys& kv, const uint16_t* head, int64_
     }
 }
 
-// A tile of which some rows do not see some keys. Infinities and NaN in V
-// reach only the rows that see their key: they leave V for the products
-// (0 times them would be NaN in every row), and a product of "sees the key" with
-// "is +inf / -inf / NaN there" tells each row which of them it meets.
-template <int R, bool CAP>
-__device__ __forceinline__ void masked_tile(Rows<R>& w, Keys& kv, float c, float capped, float slack,
-                                            const uint32_t (&seen)[R], uint32_t lane) {
+// Infinities and NaN in the V of nodes, which not every row sees: they leave V
+// for the products (0 times them would be NaN in every row), and afterwards a
+// product of "sees the key" with "is +inf (or -inf, or NaN) there" tells each row
+// which of them it meets.
+__device__ __forceinline__ bool any_odd(const Keys& kv) {
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) odd = odd || inf_or_nan_pair(kv.v[i].x) || inf_or_nan_pair(kv.v[i].y);
-    if (!__any(odd)) {
-        tile<R, CAP, true>(w, kv, c, capped, slack, seen, lane);
-        return;
+    return __any(odd);
+}
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v) {
+    if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+    return (v & 0x7F800000u) == 0x7F800000u ? v & 0xFFFFu : v;
+}
+__device__ __forceinline__ void drop_odd(Keys& kv) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) kv.v[i] = uint2{finite_pair(kv.v[i].x), finite_pair(kv.v[i].y)};
+}
+// The elements of one kind as 1.0: which is 0x7F80 (+inf), 0xFF80 (-inf) or 0 (NaN).
+__device__ __forceinline__ uint32_t ones_of_kind(uint32_t v, uint32_t which) {
+    uint32_t w = 0u;
+#pragma unroll
+    for (int s = 0; s < 32; s += 16) {
+        const uint32_t e = v >> s & 0xFFFFu;
+        const bool is = which ? e == which : (e & 0x7F80u) == 0x7F80u && (e & 0x7Fu) != 0u;
+        w |= is ? 0x3F80u << s : 0u;
     }
-    Keys kinds[3];  // 1.0 where V is +inf, -inf, NaN
-    auto sort_out = [&](uint32_t& v, uint32_t& p, uint32_t& n, uint32_t& q) {
-        p = n = q = 0u;
+    return w;
+}
+template <int R>
+__device__ __forceinline__ void add_odd(Rows<R>& w, const Keys& kv, const uint32_t (&seen)[R], uint32_t lane) {
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+        const uint32_t which = k == 0 ? 0x7F80u : k == 1 ? 0xFF80u : 0u;
+        const float adds = k == 0 ? __builtin_inff() : k == 1 ? -__builtin_inff() : __builtin_nanf("");
+        Keys ones;
 #pragma unroll
-        for (int s = 0; s < 32; s += 16) {
-            const uint32_t e = v >> s & 0xFFFFu;
-            if ((e & 0x7F80u) != 0x7F80u) continue;
-            if (e == 0x7F80u) p |= 0x3F80u << s;
-            else if (e == 0xFF80u) n |= 0x3F80u << s;
-            else q |= 0x3F80u << s;
-            v &= ~(0xFFFFu << s);
-        }
-    };
+        for (int i = 0; i < 8; ++i) ones.v[i] = uint2{ones_of_kind(kv.v[i].x, which), ones_of_kind(kv.v[i].y, which)};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        sort_out(kv.v[i].x, kinds[0].v[i].x, kinds[1].v[i].x, kinds[2].v[i].x);
-        sort_out(kv.v[i].y, kinds[0].v[i].y, kinds[1].v[i].y, kinds[2].v[i].y);
-    }
-    tile<R, CAP, true>(w, kv, c, capped, slack, seen, lane);
+        for (int rq = 0; rq < R; ++rq) {
+            uint32_t sees[4];
 #pragma unroll
-    for (int rq = 0; rq < R; ++rq) {
-        uint32_t sees[4];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bit = 16 * (i / 2) + 4 * (lane >> 4) + 2 * (i % 2);
+                sees[i] = (seen[rq] >> bit & 1u ? 0x3F80u : 0u) | (seen[rq] >> (bit + 1) & 1u ? 0x3F800000u : 0u);
+            }
+            const U32x4 sb{sees[0], sees[1], sees[2], sees[3]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t bit = 16 * (i / 2) + 4 * (lane >> 4) + 2 * (i % 2);
-            sees[i] = (seen[rq] >> bit & 1u ? 0x3F80u : 0u) | (seen[rq] >> (bit + 1) & 1u ? 0x3F800000u : 0u);
-        }
-        const U32x4 sb{sees[0], sees[1], sees[2], sees[3]};
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 met = mfma16(v_operand(ones, i), sb, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f32x4 met[3];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) met[k] = mfma16(v_operand(kinds[k], i), sb, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (met[0][r] > 0.0f) w.o[rq][i][r] += __builtin_inff();
-                if (met[1][r] > 0.0f) w.o[rq][i][r] -= __builtin_inff();
-                if (met[2][r] > 0.0f) w.o[rq][i][r] = __builtin_nanf("");
+                for (int r = 0; r < 4; ++r)
+                    if (met[r] > 0.0f) w.o[rq][i][r] += adds;
             }
         }
     }
 }
 
-// Grid: one workgroup per (sequence, KV head, split, block of 16 R query
-// rows); its WAVES waves hold the same rows and take the split's tiles in turn,
-// and join their sums in LDS. The row blocks of one split, which read the same
-// keys, run on one XCD next to each other (workgroup i runs on XCD i % 8), so
-// its L2 holds those keys for all of them.
-template <int R, int WAVES, bool CAP>
-__global__ __launch_bounds__(64 * WAVES) void tree_attention_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
-                                                                    uint16_t* __restrict__ out,
-                                                                    float* __restrict__ lse, float* __restrict__ part,
-                                                                    uint32_t groups) {
+// What a workgroup works on.
+struct Span {
+    Nodes nodes;
+    int32_t ctx, rows;             // of the sequence; rows = nodes x heads per KV head
+    int32_t ctx_tiles, all_tiles;  // of TILE keys: the context's, and with the nodes' after them
+};
+template <int TILE>
+__device__ __forceinline__ Span span_of(const TreeQueries& tq, int32_t b) {
+    Span s;
+    s.nodes = nodes_of(tq, b);
+    s.ctx = context_of(tq, b);
+    s.rows = s.nodes.count * tq.G;
+    s.ctx_tiles = (s.ctx + TILE - 1) / TILE;
+    s.all_tiles = s.ctx_tiles + (s.nodes.count + TILE - 1) / TILE;
+    return s;
+}
+// A tile's first key, and how many keys it has at most.
+template <int TILE>
+__device__ __forceinline__ void tile_keys(const Span& s, int32_t t, uint32_t& key0, uint32_t& there) {
+    const int32_t in_tree = t - s.ctx_tiles;
+    key0 = in_tree < 0 ? (uint32_t)t * TILE : (uint32_t)(s.ctx + in_tree * TILE);
+    there = in_tree < 0 ? (uint32_t)(s.ctx - t * TILE) : (uint32_t)(s.nodes.count - in_tree * TILE);
+}
+// One past the last tile that rows up to `last_row` look at (a chain's nodes end with their own).
+template <int TILE>
+__device__ __forceinline__ int32_t last_tile(const TreeQueries& tq, const Span& s, int32_t last_row) {
+    if (tq.mask) return s.all_tiles;
+    if (last_row >= s.rows) last_row = s.rows - 1;
+    return s.ctx_tiles + last_row / tq.G / TILE + 1;
+}
+
+// The lane's rows row0 + 16 rq + l % 16: their queries, and their nodes (-1 past the last row).
+template <int R>
+__device__ __forceinline__ void load_rows(Rows<R>& w, int32_t (&node)[R], const TreeQueries& tq, const Span& s, int32_t h,
+                                          int32_t row0, uint32_t lane) {
+#pragma unroll
+    for (int rq = 0; rq < R; ++rq) {
+        const int32_t r = row0 + 16 * rq + (int32_t)(lane & 15u);
+        node[rq] = -1;
+        w.q[rq][0] = w.q[rq][1] = U32x4{0u, 0u, 0u, 0u};
+        if (r < s.rows) {
+            node[rq] = r / tq.G;
+            const uint16_t* q = tq.q + (int64_t)(s.nodes.first + node[rq]) * tq.q_rs +
+                                (int64_t)(h * tq.G + r - node[rq] * tq.G) * tq.q_hs + 8 * (lane >> 4);
+            w.q[rq][0] = load16(q);
+            w.q[rq][1] = load16(q + 32);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.o[rq][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        w.limit[rq] = -__builtin_inff();
+        w.base[rq] = 0.0f;
+        w.l[rq] = 0.0f;
+    }
+}
+
+// Which keys of a tile each of the lane's rows sees. word: the tile's place among the nodes' 32-key
+// words, negative for the context.
+template <int R>
+__device__ __forceinline__ void seen_rows(uint32_t (&seen)[R], const int32_t (&node)[R], uint32_t exists,
+                                          const TreeQueries& tq, const Span& s, int32_t word) {
+#pragma unroll
+    for (int rq = 0; rq < R; ++rq) {
+        seen[rq] = exists;
+        if (word >= 0)
+            seen[rq] &= node[rq] < 0 ? 0u : seen_word(tq, s.nodes.first + node[rq], node[rq], s.nodes.count, word);
+    }
+}
+
+struct Factors {
+    float c, capped, slack;
+};
+template <bool CAP>
+__device__ __forceinline__ Factors factors(const TreeQueries& tq) {
+    return Factors{CAP ? 2.0f * kLog2E * tq.scale / tq.softcap : kLog2E * tq.scale, CAP ? tq.softcap * kLog2E : 0.0f,
+                   8.0f / (kLog2E * tq.scale)};
+}
+
+// Where a row's results go: out and lse of row `at`, or, of one of several splits, its partial sums at
+// row `at` of `o` [., 64] and `ml` [., 2].
+struct Results {
+    uint16_t* out;
+    float* lse;
+    float* o;
+    float* ml;
+    bool whole;
+};
+__device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d, float top, float l, f32x4 o) {
+    const float base = top == -__builtin_inff() ? 0.0f : top;
+    if (!t.whole) {
+        *reinterpret_cast<f32x4*>(t.o + at * kHeadDim + d) = o;
+        if (d == 0) {
+            t.ml[at * 2] = top;
+            t.ml[at * 2 + 1] = l;
+        }
+    } else {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint2 w;
+        w.x = pack_bf16(o[0] * inv, o[1] * inv);
+        w.y = pack_bf16(o[2] * inv, o[3] * inv);
+        *reinterpret_cast<uint2*>(t.out + at * kHeadDim + d) = w;
+        if (d == 0) t.lse[at] = l == 0.0f ? -__builtin_inff() : (base + log2_hw(l)) * kLn2;
+    }
+}
+
+// Few rows (up to 16 R, R <= 4): one workgroup per (sequence, KV head,
+// split); its WAVES waves hold the same rows and take the split's tiles in turn, and
+// join their sums in LDS. Bound by the cache's bytes: a wave keeps the next
+// tile's K and V on the way while it works on one, the tile after that's block
+// numbers too.
+// PAGE16 (block_size a multiple of 16, page rows near each other): the 16
+// keys of half a tile lie in one page, so a tile's two bases are scalars.
+template <int R, int WAVES, bool CAP, bool PAGE16>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
+                                                              uint16_t* __restrict__ out, float* __restrict__ lse,
+                                                              float* __restrict__ part) {
     extern __shared__ float smem[];
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
+    const int32_t split = blockIdx.x % plan.splits;
+    const uint32_t bh = blockIdx.x / plan.splits;
+    const int32_t h = bh % tq.H, b = bh / tq.H;
+    const Span s = span_of<kTile>(tq, b);
+    const int32_t first = split * plan.split_tiles;
+    if (s.rows == 0 || first >= s.all_tiles) return;  // (nor does the join look at such a split)
+    int32_t end = first + plan.split_tiles;
+    const int32_t last = last_tile<kTile>(tq, s, 16 * R - 1);
+    if (end > last) end = last;
+    const int32_t ctx_full = s.ctx / kTile;
+
+    const uint16_t* head = kv.cache + (int64_t)h * kv.head_stride;
+    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
+    const Factors f = factors<CAP>(tq);
+    auto offsets = [&](int32_t t) -> int64_t {
+        uint32_t key0, there;
+        if (t >= end) return -1;
+        tile_keys<kTile>(s, t, key0, there);
+        return lane < kTile && lane < there ? key_offset(kv, table, key0 + lane) : -1;
+    };
+    // a whole tile of context, every key there
+    auto whole = [&](int32_t t, int64_t off) { return t < end && t < ctx_full && (uint32_t)__ballot(off >= 0) == 0xFFFFFFFFu; };
+    const uint32_t k_at = n16 * (uint32_t)kv.page_stride + 8 * g, v_at = 4 * g * (uint32_t)kv.page_stride + kHeadDim + 4 * n16;
+    auto fetch = [&](Keys& k, int64_t off) {
+        if constexpr (PAGE16) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)off, 16 * t);
+                const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)((uint64_t)off >> 32), 16 * t);
+                const uint16_t* page = head + (int64_t)((uint64_t)hi << 32 | lo);
+                k.k[t][0] = load16(page + k_at);
+                k.k[t][1] = load16(page + k_at + 32);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    k.v[4 * t + r] = *reinterpret_cast<const uint2*>(page + v_at + r * (uint32_t)kv.page_stride);
+            }
+        } else {
+            load_keys(k, head, off, lane);
+        }
+    };
+
+    Rows<R> w;
+    int32_t node[R];
+    uint32_t seen[R];
+    int32_t t = first + (int32_t)wave;
+    const int32_t full_end = end < ctx_full ? end : ctx_full;
+    bool left_out = false;  // a tile of the context with a key that is not there
+    {
+        // the tiles whose every key is there and seen by all
+        Keys keys[2];
+        int64_t off = offsets(t), off1 = offsets(t + WAVES);
+        bool cur_whole = whole(t, off);
+        if (cur_whole) fetch(keys[0], off);
+        load_rows<R>(w, node, tq, s, h, 0, lane);
+        auto step = [&](Keys& cur, Keys& next) {
+            const bool next_whole = whole(t + WAVES, off1);
+            if (next_whole) fetch(next, off1);
+            off1 = offsets(t + 2 * WAVES);
+            if (cur_whole)
+                open_tile<R, CAP>(w, cur, f.c, f.capped, f.slack);
+            else
+                left_out = true;
+            cur_whole = next_whole;
+            t += WAVES;
+        };
+        while (t < full_end) {
+            step(keys[0], keys[1]);
+            if (t >= full_end) break;
+            step(keys[1], keys[0]);
+        }
+    }
+    // the others: the context's last, the nodes', those left out
+    for (t = left_out ? first + (int32_t)wave : t; t < end; t += WAVES) {
+        const int64_t off = offsets(t);
+        if (whole(t, off)) continue;
+        Keys keys;
+        load_keys(keys, head, off, lane);
+        seen_rows<R>(seen, node, (uint32_t)__ballot(off >= 0), tq, s, t - s.ctx_tiles);
+        const bool odd = t >= s.ctx_tiles && any_odd(keys);
+        if (odd) drop_odd(keys);
+        masked_tile<R, CAP>(w, keys, f.c, f.capped, f.slack, seen, lane);
+        if (odd) {
+            load_keys(keys, head, off, lane);
+            add_odd<R>(w, keys, seen, lane);
+        }
+    }
+
+    // Join the waves: each leaves m's base, l and O of its rows in LDS.
+    float* so = smem;                          // [WAVES][16 R][kPad]
+    float* sm = smem + WAVES * 16 * R * kPad;  // [WAVES][16 R]
+    float* sl = sm + WAVES * 16 * R;           // [WAVES][16 R]
+#pragma unroll
+    for (int rq = 0; rq < R; ++rq) {
+        const float l = group_sum(w.l[rq]);
+        const uint32_t row = wave * 16 * R + 16 * rq + n16;
+        if (g == 0) {
+            sm[row] = w.limit[rq] == -__builtin_inff() ? -__builtin_inff() : w.base[rq];
+            sl[row] = l;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<f32x4*>(so + row * kPad + 16 * g + 4 * r) =
+                f32x4{w.o[rq][0][r], w.o[rq][1][r], w.o[rq][2][r], w.o[rq][3][r]};
+    }
+    __syncthreads();
+    const int32_t heads = tq.H * tq.G;
+    const int64_t rows_all = (int64_t)tq.T * heads;
+    const Results to{out, lse, part + split * rows_all * kHeadDim,
+                     part + (plan.splits * kHeadDim + 2 * split) * rows_all, plan.splits == 1};
+    for (int32_t e = threadIdx.x; e < 16 * R * 16; e += 64 * WAVES) {
+        const int32_t r = e >> 4, d = (e & 15) * 4;
+        if (r >= s.rows) continue;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) top = __builtin_fmaxf(top, sm[k * 16 * R + r]);
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+        float l = 0.0f;
+        f32x4 o{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+            const float x = exp2_hw(sm[k * 16 * R + r] - base);
+            l = __builtin_fmaf(sl[k * 16 * R + r], x, l);
+            const f32x4 p = *reinterpret_cast<const f32x4*>(so + (k * 16 * R + r) * kPad + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[i], x, o[i]);
+        }
+        const int32_t node_r = r / tq.G;
+        put_row4(to, (int64_t)(s.nodes.first + node_r) * heads + h * tq.G + (r - node_r * tq.G), d, top, l, o);
+    }
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f32x16 mfma32(U32x4 a, U32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// What a wave of the many-rows kernel carries for R query tiles of 32 rows.
+// Scores come as S^T = K Q^T by v_mfma_f32_32x32x16_bf16: lane l holds, for
+// row l % 32, the keys 8 (i / 4) + 4 (l / 32) + i % 4 of 32 at i = 0 .. 15; slot 8
+// (l / 32) + j of step ks of the second product stands for the key at i = 8 ks + j.
+template <int R>
+struct Rows32 {
+    U32x4 q[R][4];   // row l % 32, d = 16 i + 8 (l / 32) ...
+    f32x16 o[R][2];  // O^T: row l % 32, d = 32 c + 8 (i / 4) + 4 (l / 32) + i % 4 at [c][i]
+    float base[R];   // subtracted from the scores in base 2
+    float most[R];   // weights that sum to more than this move base; -1 while the row has met no key
+    float l[R];
+};
+struct Keys32 {
+    U32x4 k[4];     // key l % 32, d as q's
+    U32x4 v[2][2];  // [c][ks]: d = 32 c + l % 32, the keys of slots 8 (l / 32) .. + 7 of step ks
+};
+constexpr float kMost = 256.0f;
+
+template <int R, bool CAP>
+__device__ __forceinline__ void raise32(Rows32<R>& w, int rt, const f32x16& s, float c, float capped) {
+    float top = s[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, s[i]);
+    top = __builtin_fmaxf(top, lane_xor<32>(top));
+    if (top == -__builtin_inff()) return;  // (for these lanes)
+    const bool none = w.most[rt] < 0.0f;
+    const float at = in_base2<CAP>(top, c, capped);
+    const float base = none ? at : __builtin_fmaxf(w.base[rt], at);
+    const float shrink = none ? 1.0f : exp2_hw(w.base[rt] - base);
+    w.l[rt] *= shrink;
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w.o[rt][d][i] *= shrink;
+    w.base[rt] = base;
+    w.most[rt] = kMost;
+}
+
+// The weights of 16 scores, as the second product's operands, and their sum.
+// seen: bit i of a masked tile's scores.
+template <bool CAP, bool MASKED>
+__device__ __forceinline__ float weights32(const f32x16& s, float base, float c, float capped, uint32_t seen,
+                                           U32x4 (&pb)[2]) {
+    const float from = CAP ? capped - base : -base;
+    float p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        p[i] = exp2_hw(CAP ? __builtin_fmaf(rcp_hw(exp2_hw(s[i] * c) + 1.0f), -2.0f * capped, from)
+                           : __builtin_fmaf(s[i], c, from));
+        if (MASKED && !(seen >> i & 1u)) p[i] = 0.0f;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+        pb[ks] = U32x4{pack_bf16_pair_hw(p[8 * ks], p[8 * ks + 1]), pack_bf16_pair_hw(p[8 * ks + 2], p[8 * ks + 3]),
+                       pack_bf16_pair_hw(p[8 * ks + 4], p[8 * ks + 5]), pack_bf16_pair_hw(p[8 * ks + 6], p[8 * ks + 7])};
+    float sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = (p[4 * i] + p[4 * i + 1]) + (p[4 * i + 2] + p[4 * i + 3]);
+    return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+template <int R>
+__device__ __forceinline__ void scores32(f32x16& s, const Rows32<R>& w, int rt, const Keys32& kv) {
+    s = f32x16{0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = mfma32(kv.k[i], w.q[rt][i], s);
+}
+// Weights of row tile rt's scores, its sum, and V by them. Weights are taken against base as it stands;
+// where their sum passes `most` (rare), base moves up and they are taken again.
+template <int R, bool CAP, bool MASKED>
+__device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Keys32& kv, const Factors& f,
+                                      uint32_t seen) {
+    U32x4 pb[2];
+    float sum = weights32<CAP, MASKED>(s, w.base[rt], f.c, f.capped, seen, pb);
+    if (__any(!(sum <= w.most[rt]))) {
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (!(seen >> i & 1u)) s[i] = -__builtin_inff();
+        }
+        raise32<R, CAP>(w, rt, s, f.c, f.capped);
+        sum = weights32<CAP, MASKED>(s, w.base[rt], f.c, f.capped, seen, pb);
+    }
+    w.l[rt] += sum;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) w.o[rt][c] = mfma32(kv.v[c][ks], pb[ks], w.o[rt][c]);
+}
+
+// 16 bytes a lane from global memory to LDS at lds + 16 lane, without a register. As inline assembly, so
+// that the kernel alone accounts for it (the barrier of a tile waits for all of them) instead of a wait before
+// every LDS read. An LDS DMA right after a write of M0 needs a wait state in between.
+__device__ __forceinline__ void to_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
+}
+
+// Many rows: the WAVES waves of a workgroup hold 32 R rows each and share the
+// keys, staged in LDS kStage at a time in two buffers: while the waves work on
+// one tile the next one comes in (global_load_lds, no registers), and one barrier
+// a tile. Bound by what the vector unit issues: a matrix instruction takes it 8
+// cycles and keeps the matrix core 32, an exponential takes 8, other operations
+// 4; of 32 keys and 32 rows that is 8, 16 and about 50.
+// LDS: K rows of 128 bytes whose 16-byte chunk c lies at c ^ (key & 7), so
+// that 8 lanes reading one chunk of 8 keys meet all banks; V rows with c at
+// c ^ 4 in every second pair of keys, so that the 4 keys and 64 bytes that half a wave
+// reads meet all banks. V's operands come by ds_read_b64_tr_b16: 16 lanes read 4
+// keys of 16 elements and each gets the 4 keys of its element.
+// The row blocks of one split, which read the same keys, run on one XCD next
+// to each other (workgroup i runs on XCD i % 8): its L2 holds them for all.
+constexpr int kStage = 128;
+
+// How a batch whose workgroups fit the chip at once is split: into shares of
+// at most `tiles` tiles, the least for which all of them are at most
+// plan.groups, so that ragged sequences end together. Worked out by every wave
+// from the lengths (B <= 512).
+struct Shares {
+    int32_t tiles, groups;          // of a share; of all sequences and heads
+    int32_t b, h, split, splits;    // of group g (b < 0: there is none)
+    int32_t first;                  // of the sequence: its first group
+};
+__device__ __forceinline__ int32_t wave_sum_of(int32_t v) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d, 64);
+    return v;
+}
+__device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const AttentionPlan& plan, int32_t g, uint32_t lane) {
+    constexpr int kMost = 8;
+    int32_t tiles[kMost];
+    int32_t sum = 0, longest = 0;
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        tiles[j] = 0;
+        const int32_t b = 64 * j + (int32_t)lane;
+        if (64 * j < tq.B && b < tq.B) {
+            const Span s = span_of<kStage>(tq, b);
+            tiles[j] = s.rows > 0 ? s.all_tiles : 0;
+        }
+        sum += tiles[j];
+        longest = longest > tiles[j] ? longest : tiles[j];
+    }
+    sum = wave_sum_of(sum);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) {
+        const int32_t o = __shfl_xor(longest, d, 64);
+        longest = longest > o ? longest : o;
+    }
+    auto count = [&](int32_t c) {
+        int32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < kMost; ++j)
+            if (64 * j < tq.B) n += (tiles[j] + c - 1) / c;
+        return wave_sum_of(n) * tq.H;
+    };
+    int32_t lo = (int32_t)(((int64_t)sum * tq.H + plan.groups - 1) / plan.groups), hi = longest;
+    if (lo < plan.split_tiles) lo = plan.split_tiles;  // (no share is smaller)
+    while (lo < hi) {
+        const int32_t mid = (lo + hi) / 2;
+        if (count(mid) <= plan.groups)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    Shares r{lo, 0, -1, 0, 0, 1, 0};
+    int32_t before = 0;  // groups of the sequences before
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+        if (64 * j >= tq.B) break;
+        const int32_t n = (tiles[j] + lo - 1) / lo * tq.H;
+        int32_t upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int32_t o = __shfl_up(upto, d, 64);
+            if ((int32_t)lane >= d) upto += o;
+        }
+        upto += before;
+        const uint64_t past = __ballot(upto > g);
+        if (r.b < 0 && past != 0) {
+            const int32_t l = __builtin_ctzll(past);
+            r.b = 64 * j + l;
+            const int32_t mine = __builtin_amdgcn_readlane(n, l);
+            r.first = __builtin_amdgcn_readlane(upto, l) - mine;
+            r.splits = mine / tq.H;
+            r.h = (g - r.first) / r.splits;
+            r.split = (g - r.first) - r.h * r.splits;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
+    r.groups = before;
+    return r;
+}
+constexpr int kManyLds = 2 * (kStage * 256 + kStage * 4);
+template <int R, int WAVES, bool CAP>
+__global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
+                                                                  uint16_t* __restrict__ out, float* __restrict__ lse,
+                                                                  float* __restrict__ part, int32_t* __restrict__ shares,
+                                                                  uint32_t groups) {
+    constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    uint32_t* present = reinterpret_cast<uint32_t*>(lds + 2 * kStage * 256);  // [2][kStage]
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t hl = lane >> 5, n32 = lane & 31u;
     uint32_t id = blockIdx.x, rb = 0;
     if (plan.row_blocks > 1) {
         const uint32_t slot = id >> 3;
@@ -250,180 +761,413 @@ __global__ __launch_bounds__(64 * WAVES) void tree_attention_kernel(PagedCache k
         id = slot / plan.row_blocks * 8 + (id & 7u);
         if (id >= groups) return;
     }
-    const int32_t split = id % plan.splits;
-    const uint32_t bh = id / plan.splits;
-    const int32_t h = bh % tq.H, b = bh / tq.H;
-    const Nodes nodes = nodes_of(tq, b);
-    const int32_t ctx = context_of(tq, b);
-    const int32_t rows = nodes.count * tq.G, row0 = rb * 16 * R;
-    if (row0 >= rows) return;
-    const int32_t heads = tq.H * tq.G;
-
-    // The tiles: the context's, then the nodes' (a chain: up to the last of this block's).
-    const int32_t ctx_tiles = (ctx + kTile - 1) / kTile, ctx_full = ctx / kTile;
-    const int32_t all_tiles = ctx_tiles + (nodes.count + kTile - 1) / kTile;
-    const int32_t first = split * plan.split_tiles;
-    if (first >= all_tiles) return;  // nor does the join look at this split
-    int32_t end = first + plan.split_tiles < all_tiles ? first + plan.split_tiles : all_tiles;
-    int32_t last_row = row0 + 16 * R - 1;
-    if (last_row >= rows) last_row = rows - 1;
-    if (!tq.mask) {
-        const int32_t need = ctx_tiles + last_row / tq.G / kTile + 1;
-        if (end > need) end = need;
-    }
-
-    Rows<R> w;
-    int32_t node[R];  // the lane's rows' nodes, -1 past the last row
-#pragma unroll
-    for (int rq = 0; rq < R; ++rq) {
-        const int32_t r = row0 + 16 * rq + n16;
-        node[rq] = -1;
-        w.q[rq][0] = w.q[rq][1] = U32x4{0u, 0u, 0u, 0u};
-        if (r < rows) {
-            node[rq] = r / tq.G;
-            const uint16_t* q = tq.q + (int64_t)(nodes.first + node[rq]) * tq.q_rs +
-                                (int64_t)(h * tq.G + r - node[rq] * tq.G) * tq.q_hs + 8 * g;
-            w.q[rq][0] = load16(q);
-            w.q[rq][1] = load16(q + 32);
+    int32_t b, h, split, splits, share;
+    if (plan.splits > 1) {
+        const Shares r = shares_of(tq, plan, (int32_t)id, lane);
+        if (r.b < 0) return;
+        b = r.b, h = r.h, split = r.split, splits = r.splits, share = r.tiles;
+        // for the join: each sequence's first group and its splits
+        if (rb == 0 && h == 0 && split == 0 && tid == 0) {
+            shares[2 * b] = r.first;
+            shares[2 * b + 1] = splits;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w.o[rq][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        w.m[rq] = -__builtin_inff();
-        w.base[rq] = 0.0f;
-        w.l[rq] = 0.0f;
+    } else {
+        b = id / tq.H, h = id % tq.H, split = 0, splits = 1, share = 1 << 30;
     }
-    const float c = CAP ? 2.0f * kLog2E * tq.scale / tq.softcap : kLog2E * tq.scale;
-    const float capped = CAP ? tq.softcap * kLog2E : 0.0f;
-    const float slack = 8.0f / (kLog2E * tq.scale);
+    b = __builtin_amdgcn_readfirstlane(b);
+    h = __builtin_amdgcn_readfirstlane(h);
+    split = __builtin_amdgcn_readfirstlane(split);
+    splits = __builtin_amdgcn_readfirstlane(splits);
+    share = __builtin_amdgcn_readfirstlane(share);
+    const Span s = span_of<kStage>(tq, b);
+    const int32_t block0 = rb * WAVES * 32 * R;
+    const int32_t first = split * share;
+    if (block0 >= s.rows || first >= s.all_tiles) return;
+    int32_t end = s.all_tiles - first < share ? s.all_tiles : first + share;
+    const int32_t last = last_tile<kStage>(tq, s, block0 + WAVES * 32 * R - 1);
+    if (end > last) end = last;
+    const int32_t ctx_full = s.ctx / kStage;
+    const int32_t row0 = block0 + (int32_t)wave * 32 * R;
+    const bool active = row0 < s.rows;
+
     const uint16_t* head = kv.cache + (int64_t)h * kv.head_stride;
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
-
-    for (int32_t t = first + wave; t < end; t += WAVES) {
-        const int32_t in_tree = t - ctx_tiles;  // >= 0: a tile of nodes
-        const uint32_t key0 = in_tree < 0 ? (uint32_t)t * kTile : (uint32_t)(ctx + in_tree * kTile);
-        const uint32_t there = in_tree < 0 ? (uint32_t)(ctx - t * kTile) : (uint32_t)(nodes.count - in_tree * kTile);
-        int64_t off = -1;
-        if (lane < kTile && lane < there) off = key_offset(kv, table, key0 + lane);
-        const uint32_t exists = (uint32_t)__ballot(off >= 0);
-        Keys keys;
-        load_keys(keys, head, off, lane);
-        uint32_t seen[R];
-        if (exists == 0xFFFFFFFFu && t < ctx_full) {
-            tile<R, CAP, false>(w, keys, c, capped, slack, seen, lane);
-        } else {
+    const Factors f = factors<CAP>(tq);
+    // Run i of the wave: 8 keys, a lane key lane / 8, the chunks that belong in place lane % 8 of its rows.
+    int64_t off[kRuns];
+    const uint32_t row8 = lane >> 3, c8 = lane & 7u;
+    auto find = [&](int32_t t, int32_t stop) {
+        if (t >= stop) return;
+        uint32_t key0, there;
+        tile_keys<kStage>(s, t, key0, there);
 #pragma unroll
-            for (int rq = 0; rq < R; ++rq) {
-                seen[rq] = exists;
-                if (in_tree >= 0)
-                    seen[rq] &= node[rq] < 0 ? 0u
-                                             : seen_word(tq, nodes.first + node[rq], node[rq], nodes.count, in_tree);
-            }
-            masked_tile<R, CAP>(w, keys, c, capped, slack, seen, lane);
+        for (int i = 0; i < kRuns; ++i) {
+            const uint32_t k = 8 * (kRuns * wave + i) + row8;
+            off[i] = k < there ? key_offset(kv, table, key0 + k) : -1;
         }
+    };
+    // (a key that is not there is read from the cache's first cell, and masked)
+    auto bring = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const uint32_t at = lds0 + buf * (kStage * 256) + (kRuns * wave + i) * 1024;
+            const uint16_t* row = head + (off[i] >= 0 ? off[i] : 0);
+            to_lds(row + 8 * (c8 ^ row8), at);
+            to_lds(row + kHeadDim + 8 * (c8 ^ (row8 >> 1 & 1u) << 2), at + kStage * 128);
+            if (c8 == 0) present[buf * kStage + 8 * (kRuns * wave + i) + row8] = off[i] >= 0;
+        }
+    };
+    // this wave's loads of the next tile have landed, and everybody's with the barrier
+    auto landed = [&]() {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+        __syncthreads();
+    };
+    auto ballots = [&](int buf, uint64_t (&exists)[kStage / 64]) {
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < kStage / 64; ++i) {
+            exists[i] = __ballot(present[buf * kStage + 64 * i + lane] != 0u);
+            all &= exists[i] == ~0ull;
+        }
+        return all;
+    };
+    // this lane's places in a stage
+    const uint32_t k_at = n32 * 128, k_c = n32 & 7u, t16 = lane & 15u;
+    const uint32_t v_at = kStage * 128 + (4 * hl + (t16 >> 2)) * 128 +
+                          ((2 * (lane >> 4 & 1u) + (t16 >> 1 & 1u)) ^ (t16 >> 3) << 2) * 16 + (t16 & 1u) * 8;
+    auto read_k = [&](Keys32& k, int buf, int sub) {
+        const uint8_t* at = lds + buf * (kStage * 256) + sub * 4096 + k_at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k.k[i] = load16(at + (((2 * i + hl) ^ k_c) << 4));
+    };
+    auto read_v = [&](Keys32& k, int buf, int sub) {
+        const uint32_t at = buf * (kStage * 256) + sub * 4096;
+        auto four = [&](uint32_t o) {
+            typedef __attribute__((address_space(3))) i16x4 LdsFour;
+            return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour*)(uintptr_t)(lds0 + o)));
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const uint2 a = four(at + (v_at ^ c * 64) + ks * 2048), z = four(at + (v_at ^ c * 64) + ks * 2048 + 1024);
+                k.v[c][ks] = U32x4{a.x, a.y, z.x, z.y};
+            }
+    };
+
+    Rows32<R> w;
+    int32_t node[R];  // of row l % 32 of each tile, -1 past the last row
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        const int32_t r = row0 + 32 * rt + (int32_t)n32;
+        node[rt] = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.q[rt][i] = U32x4{0u, 0u, 0u, 0u};
+        if (r < s.rows) {
+            node[rt] = r / tq.G;
+            const uint16_t* q = tq.q + (int64_t)(s.nodes.first + node[rt]) * tq.q_rs +
+                                (int64_t)(h * tq.G + r - node[rt] * tq.G) * tq.q_hs + 8 * hl;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.q[rt][i] = load16(q + 16 * i);
+        }
+        w.o[rt][0] = w.o[rt][1] = f32x16{0.f};
+        w.base[rt] = w.l[rt] = 0.0f;
+        w.most[rt] = -1.0f;
     }
 
-    // Join the waves: each leaves m's base, l and O of its rows in LDS.
-    float* so = smem;                               // [WAVES][16 R][kPad]
-    float* sm = smem + WAVES * 16 * R * kPad;       // [WAVES][16 R]
-    float* sl = sm + WAVES * 16 * R;                // [WAVES][16 R]
+    // The tiles that every row sees whole. One row tile's scores are on the way in the matrix cores while the
+    // vector unit takes the other's exponentials (of one row tile: the next 32 keys' scores).
+    constexpr int kSubs = kStage / 32;
+    bool left_out = false;  // a tile of the context with a key that is not there
+    const int32_t full_end = end < ctx_full ? end : ctx_full;
+    if (first < full_end) {
+        Keys32 k;
+        f32x16 s0, s1;  // scores: of row tile 0 and 1 (of one row tile: of even and odd 32 keys)
+        uint64_t exists[kStage / 64];
+        find(first, full_end);
+        bring(0);
+        find(first + 1, full_end);
+        landed();
+        if (first + 1 < full_end) bring(1);
+        find(first + 2, full_end);
+        bool whole = ballots(0, exists), primed = false;
+        for (int32_t t = first; t < full_end; ++t) {
+            const int buf = (t - first) & 1;
+            const bool work = whole && active;
+            if (work) {
+                if (!primed) {
+                    read_k(k, buf, 0);
+                    scores32<R>(s0, w, 0, k);
+                }
 #pragma unroll
-    for (int rq = 0; rq < R; ++rq) {
-        const float l = group_sum(w.l[rq]);
-        const uint32_t row = wave * 16 * R + 16 * rq + n16;
-        if (g == 0) {
-            sm[row] = w.m[rq] == -__builtin_inff() ? -__builtin_inff() : w.base[rq];
-            sl[row] = l;
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) so[row * kPad + 16 * g + 4 * r + i] = w.o[rq][i][r];
-    }
-    __syncthreads();
-    constexpr int kThreads = 64 * WAVES;
-    for (int32_t e = threadIdx.x; e < 16 * R * 16; e += kThreads) {
-        const int32_t lr = e >> 4, d = (e & 15) * 4;
-        const int32_t r = row0 + lr;
-        if (r >= rows) continue;
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k) top = __builtin_fmaxf(top, sm[k * 16 * R + lr]);
-        const float base = top == -__builtin_inff() ? 0.0f : top;
-        float l = 0.0f, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k) {
-            const float f = exp2_hw(sm[k * 16 * R + lr] - base);
-            l = __builtin_fmaf(sl[k * 16 * R + lr], f, l);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(so[(k * 16 * R + lr) * kPad + d + i], f, o[i]);
-        }
-        const int32_t node_r = r / tq.G;
-        const int64_t at = (int64_t)(nodes.first + node_r) * heads + h * tq.G + (r - node_r * tq.G);
-        if (plan.splits > 1) {
-            const int64_t rows_all = (int64_t)tq.T * heads;
-            float* po = part + ((int64_t)split * rows_all + at) * kHeadDim + d;
-            *reinterpret_cast<f32x4*>(po) = f32x4{o[0], o[1], o[2], o[3]};
-            if (d == 0) {
-                float* pm = part + (int64_t)plan.splits * rows_all * kHeadDim + ((int64_t)split * rows_all + at) * 2;
-                pm[0] = top;
-                pm[1] = l;
+                for (int sub = 0; sub < kSubs; ++sub) {
+                    read_v(k, buf, sub);
+                    if constexpr (R == 2) {
+                        scores32<R>(s1, w, 1, k);
+                        add32<R, CAP, false>(w, 0, s0, k, f, 0u);
+                        if (sub + 1 < kSubs) {
+                            read_k(k, buf, sub + 1);
+                            scores32<R>(s0, w, 0, k);
+                            add32<R, CAP, false>(w, 1, s1, k, f, 0u);
+                        }
+                    } else if (sub + 1 < kSubs) {
+                        read_k(k, buf, sub + 1);
+                        scores32<R>(sub % 2 ? s0 : s1, w, 0, k);
+                        add32<R, CAP, false>(w, 0, sub % 2 ? s1 : s0, k, f, 0u);
+                    }
+                }
             }
-        } else {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint32_t* po = reinterpret_cast<uint32_t*>(out + at * kHeadDim + d);
-            po[0] = pack_bf16(o[0] * inv, o[1] * inv);
-            po[1] = pack_bf16(o[2] * inv, o[3] * inv);
-            if (d == 0) lse[at] = l == 0.0f ? -__builtin_inff() : (base + log2_hw(l)) * kLn2;
+            // the wave has what it needs of this buffer
+            landed();
+            if (t + 2 < full_end) bring(buf);
+            find(t + 3, full_end);
+            const bool next_whole = t + 1 < full_end && ballots(buf ^ 1, exists);
+            primed = work && next_whole;
+            if (primed) {
+                read_k(k, buf ^ 1, 0);
+                scores32<R>(s0, w, 0, k);
+            }
+            if (work) add32<R, CAP, false>(w, R - 1, s1, k, f, 0u);
+            if (!whole) left_out = true;
+            whole = next_whole;
         }
+        __syncthreads();  // (nobody reads the buffers any more)
+    }
+    // the others: the context's last, the nodes', those left out
+    const int32_t rest = left_out || first > full_end ? first : full_end;
+    if (rest < end) {
+        find(rest, end);
+        bring(0);
+        find(rest + 1, end);
+        for (int32_t t = rest; t < end; ++t) {
+            const int buf = (t - rest) & 1;
+            const int32_t in_tree = t - s.ctx_tiles;
+            uint32_t words[kSubs][R];  // what the lane's rows see of the tile's nodes
+            if (in_tree >= 0) {
+#pragma unroll
+                for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+                    for (int rt = 0; rt < R; ++rt)
+                        words[sub][rt] = node[rt] < 0 ? 0u
+                                                      : seen_word(tq, s.nodes.first + node[rt], node[rt], s.nodes.count,
+                                                                  kSubs * in_tree + sub);
+            }
+            landed();
+            if (t + 1 < end) bring(buf ^ 1);
+            find(t + 2, end);
+            uint64_t exists[kStage / 64];
+            const bool whole = ballots(buf, exists);
+            if (!active || (whole && t < ctx_full)) continue;
+#pragma unroll 1
+            for (int sub = 0; sub < kSubs; ++sub) {
+                const uint32_t there = (uint32_t)(exists[sub / 2] >> (32 * (sub & 1)));
+                uint32_t word[R];
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) {
+                    word[rt] = words[0][rt];
+#pragma unroll
+                    for (int i = 1; i < kSubs; ++i) words[i - 1][rt] = words[i][rt];
+                }
+                if (there == 0u) continue;
+                Keys32 k;
+                // the lane's keys' bits of a word in the order of its scores
+                auto own = [&](uint32_t word) {
+                    word >>= 4 * hl;
+                    return (word & 0xFu) | (word >> 4 & 0xF0u) | (word >> 8 & 0xF00u) | (word >> 12 & 0xF000u);
+                };
+                const uint32_t mine = own(there);
+                auto v_there = [&]() {
+                    read_v(k, buf, sub);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks) {
+                            uint32_t* v = &k.v[c][ks].x;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t two = mine >> (8 * ks + 2 * j);
+                                v[j] &= (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u);
+                            }
+                        }
+                };
+                read_k(k, buf, sub);
+                v_there();
+                bool odd = false;  // infinities and NaN in nodes' V: see add_odd
+                if (in_tree >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) odd = odd || inf_or_nan_pair((&k.v[i / 8][i / 4 % 2].x)[i % 4]);
+                    odd = __any(odd);
+                    if (odd) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            uint32_t& v = (&k.v[i / 8][i / 4 % 2].x)[i % 4];
+                            v = finite_pair(v);
+                        }
+                    }
+                }
+                uint32_t seen[R];
+#pragma unroll
+                for (int rt = 0; rt < R; ++rt) {
+                    seen[rt] = own(in_tree >= 0 ? there & word[rt] : there);
+                    f32x16 sc;
+                    scores32<R>(sc, w, rt, k);
+                    add32<R, CAP, true>(w, rt, sc, k, f, seen[rt]);
+                }
+                if (!odd) continue;
+                v_there();
+#pragma unroll 1
+                for (int kind = 0; kind < 3; ++kind) {
+                    const float adds = kind == 0 ? __builtin_inff() : kind == 1 ? -__builtin_inff() : __builtin_nanf("");
+                    const uint32_t which = kind == 0 ? 0x7F80u : kind == 1 ? 0xFF80u : 0u;
+#pragma unroll
+                    for (int rt = 0; rt < R; ++rt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            f32x16 met{0.f};
+#pragma unroll
+                            for (int ks = 0; ks < 2; ++ks) {
+                                U32x4 ones, sees;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    (&ones.x)[j] = ones_of_kind((&k.v[c][ks].x)[j], which);
+                                    const uint32_t two = seen[rt] >> (8 * ks + 2 * j);
+                                    (&sees.x)[j] = (two & 1u ? 0x3F80u : 0u) | (two & 2u ? 0x3F800000u : 0u);
+                                }
+                                met = mfma32(ones, sees, met);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (met[i] > 0.0f) w.o[rt][c][i] += adds;
+                        }
+                }
+            }
+        }
+    }
+    if (!active) return;
+    const int32_t heads = tq.H * tq.G;
+    constexpr int kRows = WAVES * 32 * R;
+    const int64_t part0 = ((int64_t)id * plan.row_blocks + rb) * kRows - block0;
+    const Results to{out, lse, part, part + (int64_t)plan.groups * plan.row_blocks * kRows * kHeadDim, splits == 1};
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt) {
+        const float l = w.l[rt] + lane_xor<32>(w.l[rt]);
+        const float top = w.most[rt] < 0.0f ? -__builtin_inff() : w.base[rt];
+        if (node[rt] < 0) continue;
+        const int32_t r = row0 + 32 * rt + (int32_t)n32;
+        const int64_t at = splits > 1 ? part0 + r
+                                      : (int64_t)(s.nodes.first + node[rt]) * heads + h * tq.G + r - node[rt] * tq.G;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                put_row4(to, at, 32 * c + 8 * i + 4 * (int32_t)hl, top, l,
+                         f32x4{w.o[rt][c][4 * i], w.o[rt][c][4 * i + 1], w.o[rt][c][4 * i + 2], w.o[rt][c][4 * i + 3]});
     }
 }
 
-// The splits of a row joined, one wave per row, one element of d per lane.
+// The splits of a row joined: 16 lanes a row, 4 elements of d a lane, eight splits' loads on the way at a
+// time.
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq, AttentionPlan plan,
                                                                   const float* __restrict__ part,
+                                                                  const int32_t* __restrict__ shares,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse) {
-    const uint32_t lane = threadIdx.x & 63u;
     const int32_t heads = tq.H * tq.G;
-    const int32_t hq = blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int32_t i = blockIdx.y, b = blockIdx.z;
+    const int32_t row = blockIdx.x * 16 + (int32_t)(threadIdx.x >> 4), d = 4 * (int32_t)(threadIdx.x & 15u);
+    const int32_t b = blockIdx.y;
     const Nodes nodes = nodes_of(tq, b);
-    if (i >= nodes.count || hq >= heads) return;
-    const int32_t ctx = context_of(tq, b);
-    const int32_t tiles = (ctx + kTile - 1) / kTile + (nodes.count + kTile - 1) / kTile;
-    int32_t splits = (tiles + plan.split_tiles - 1) / plan.split_tiles;
-    if (splits > plan.splits) splits = plan.splits;
-    const int64_t rows_all = (int64_t)tq.T * heads;
-    const int64_t at = (int64_t)(nodes.first + i) * heads + hq;
-    const float* pm = part + (int64_t)plan.splits * rows_all * kHeadDim + at * 2;
-    float top = -__builtin_inff();
-    for (int32_t s = 0; s < splits; ++s) top = __builtin_fmaxf(top, pm[(int64_t)s * rows_all * 2]);
-    const float base = top == -__builtin_inff() ? 0.0f : top;
-    float l = 0.0f, o = 0.0f;
-    for (int32_t s = 0; s < splits; ++s) {
-        const float f = exp2_hw(pm[(int64_t)s * rows_all * 2] - base);
-        l = __builtin_fmaf(pm[(int64_t)s * rows_all * 2 + 1], f, l);
-        o = __builtin_fmaf(part[((int64_t)s * rows_all + at) * kHeadDim + lane], f, o);
+    if (row >= nodes.count * heads) return;
+    const int64_t at = (int64_t)nodes.first * heads + row;
+    int64_t from, step;  // the first split's row of the partial sums, and the next one's distance
+    const float* ml;
+    int32_t splits;
+    if (plan.many) {
+        const int32_t rows = 16 * plan.q_tiles * plan.waves;
+        const int32_t node = row / heads, hq = row - node * heads, h = hq / tq.G, r = node * tq.G + hq - h * tq.G;
+        splits = shares[2 * b + 1];
+        if (splits <= 1) return;  // written whole
+        step = (int64_t)plan.row_blocks * rows;
+        from = ((int64_t)(shares[2 * b] + h * splits) * plan.row_blocks + r / rows) * rows + r % rows;
+        ml = part + (int64_t)plan.groups * step * kHeadDim;
+    } else {
+        const int32_t ctx = context_of(tq, b);
+        const int32_t tiles = (ctx + kTile - 1) / kTile + (nodes.count + kTile - 1) / kTile;
+        splits = (tiles + plan.split_tiles - 1) / plan.split_tiles;
+        if (splits > plan.splits) splits = plan.splits;
+        step = (int64_t)tq.T * heads;
+        from = at;
+        ml = part + plan.splits * step * kHeadDim;
     }
-    out[at * kHeadDim + lane] = (uint16_t)to_bf16(l == 0.0f ? 0.0f : o / l);
-    if (lane == 0) lse[at] = l == 0.0f ? -__builtin_inff() : (base + log2_hw(l)) * kLn2;
+    const float* pm = ml + from * 2;
+    const float* po = part + from * kHeadDim + d;
+    float base = -__builtin_inff(), l = 0.0f;  // the largest base so far
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    constexpr int kAtOnce = 8;
+    for (int32_t s0 = 0; s0 < splits; s0 += kAtOnce) {
+        f32x4 p[kAtOnce];
+        float2 ml[kAtOnce];
+        float top = base;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t s = s0 + j < splits ? s0 + j : s0;
+            p[j] = *reinterpret_cast<const f32x4*>(po + s * step * kHeadDim);
+            ml[j] = *reinterpret_cast<const float2*>(pm + s * step * 2);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) top = __builtin_fmaxf(top, ml[j].x);  // (a repeated one changes nothing)
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        const float keep = exp2_hw(base - ref);
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= keep;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (s0 + j >= splits) break;
+            const float f = exp2_hw(ml[j].x - ref);
+            l = __builtin_fmaf(ml[j].y, f, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[j][i], f, o[i]);
+        }
+        base = top;
+    }
+    if (base == -__builtin_inff()) base = 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint2 w;
+    w.x = pack_bf16(o[0] * inv, o[1] * inv);
+    w.y = pack_bf16(o[2] * inv, o[3] * inv);
+    *reinterpret_cast<uint2*>(out + at * kHeadDim + d) = w;
+    if (d == 0) lse[at] = l == 0.0f ? -__builtin_inff() : (base + log2_hw(l)) * kLn2;
 }
 
-template <int R, int WAVES, bool CAP>
-int launch(const TreeAttentionArgs& a, hipStream_t stream) {
+template <int R, int WAVES, bool CAP, bool PAGE16>
+int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
     static std::atomic<int> done[64] = {};
-    auto kernel = tree_attention_kernel<R, WAVES, CAP>;
+    auto kernel = few_rows_kernel<R, WAVES, CAP, PAGE16>;
     if (kLds > 65536 && raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, done) != 0) return -1;
-    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
-    const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), kLds, stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
-                       groups);
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)a.tq.B * a.tq.H * a.plan.splits), dim3(64 * WAVES), kLds, stream, a.kv,
+                       a.tq, a.plan, a.out, a.lse, a.part);
     return 0;
 }
 
 template <int R, int WAVES>
-int launch_cap(const TreeAttentionArgs& a, hipStream_t stream) {
-    return a.tq.softcap > 0.0f ? launch<R, WAVES, true>(a, stream) : launch<R, WAVES, false>(a, stream);
+int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
+    // (32-bit offsets of a page's rows)
+    const bool page16 = a.kv.block_size % 16 == 0 && a.kv.page_stride < (1 << 24);
+    if (a.tq.softcap > 0.0f)
+        return page16 ? launch_few<R, WAVES, true, true>(a, stream) : launch_few<R, WAVES, true, false>(a, stream);
+    return page16 ? launch_few<R, WAVES, false, true>(a, stream) : launch_few<R, WAVES, false, false>(a, stream);
+}
+
+template <int R, int WAVES>
+int launch_many(const TreeAttentionArgs& a, hipStream_t stream) {
+    const uint32_t groups = a.plan.splits > 1 ? (uint32_t)a.plan.groups : (uint32_t)a.tq.B * a.tq.H;
+    const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
+    auto kernel = a.tq.softcap > 0.0f ? many_rows_kernel<R, WAVES, true> : many_rows_kernel<R, WAVES, false>;
+    static std::atomic<int> done[2][64] = {};
+    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), kManyLds, done[a.tq.softcap > 0.0f]) != 0) return -1;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), kManyLds, stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
+                       a.shares, groups);
+    return 0;
 }
 
 }  // namespace
@@ -432,12 +1176,34 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
                                   int32_t num_cus) {
     AttentionPlan p{};
     const int64_t rows = (int64_t)max_nodes * G;
+    p.many = rows > 64;
+    p.splits = 1;
+    if (p.many) {
+        // 128, 256 or 512 rows a workgroup; two, two or one of them a CU
+        p.waves = rows > 256 ? 8 : 4;
+        p.q_tiles = rows > 128 ? 4 : 2;
+        const int64_t block_rows = 16 * p.q_tiles * p.waves;
+        p.row_blocks = (int32_t)((rows + block_rows - 1) / block_rows);
+        const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2);
+        const int64_t tiles = (max_ctx + kStage - 1) / kStage + (max_nodes + kStage - 1) / kStage;
+        p.split_tiles = 2;
+        p.groups = (int32_t)(at_once / p.row_blocks);
+        // split when the chip has room for twice the workgroups, by what the lengths turn out to be
+        if (2 * (int64_t)B * H <= p.groups && tiles > p.split_tiles) p.splits = 2;
+        return p;
+    }
     p.q_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.waves = 4;
-    p.row_blocks = (int32_t)((rows + 16 * p.q_tiles - 1) / (16 * p.q_tiles));
+    p.row_blocks = 1;
     const int64_t tiles = (max_ctx + kTile - 1) / kTile + (max_nodes + kTile - 1) / kTile;
+    const int64_t base = (int64_t)B * H;
+    if (p.q_tiles == 1 && tiles <= 64 && base <= num_cus) {
+        // short and few: 16 waves, 4 tiles each at most, and no second launch
+        p.waves = 16;
+        p.split_tiles = (int32_t)tiles;
+        return p;
+    }
     // Splits until there are two workgroups per CU, each of at least 4 tiles a wave.
-    const int64_t base = (int64_t)B * H * p.row_blocks;
     int64_t splits = (2 * num_cus + base - 1) / base;
     const int64_t most = tiles / (4 * p.waves);
     if (splits > most) splits = most;
@@ -447,18 +1213,29 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
     return p;
 }
 
+int64_t tree_attention_workspace(const AttentionPlan& p, int64_t T, int64_t heads, int32_t B) {
+    if (p.splits == 1) return 0;
+    const int64_t rows = p.many ? (int64_t)p.groups * p.row_blocks * 16 * p.q_tiles * p.waves : p.splits * T * heads;
+    return rows * (kHeadDim + 2) * 4 + (p.many ? (int64_t)B * 2 * 4 : 0);
+}
+
 int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
     int rc;
-    if (a.plan.q_tiles == 1)
-        rc = launch_cap<1, 4>(a, stream);
-    else if (a.plan.q_tiles == 2)
-        rc = launch_cap<2, 4>(a, stream);
+    if (a.plan.many)
+        rc = a.plan.waves == 8     ? launch_many<2, 8>(a, stream)
+             : a.plan.q_tiles == 4 ? launch_many<2, 4>(a, stream)
+                                   : launch_many<1, 4>(a, stream);
+    else if (a.plan.waves == 16)
+        rc = launch_few<1, 16>(a, stream);
     else
-        rc = launch_cap<4, 4>(a, stream);
+        rc = a.plan.q_tiles == 1   ? launch_few<1, 4>(a, stream)
+             : a.plan.q_tiles == 2 ? launch_few<2, 4>(a, stream)
+                                   : launch_few<4, 4>(a, stream);
     if (rc) return rc;
     if (a.plan.splits > 1) {
-        const dim3 grid((uint32_t)(a.tq.H * a.tq.G + 3) / 4, (uint32_t)a.tq.max_nodes, (uint32_t)a.tq.B);
-        hipLaunchKernelGGL(tree_attention_join_kernel, grid, dim3(256), 0, stream, a.tq, a.plan, a.part, a.out, a.lse);
+        const dim3 grid((uint32_t)(((int64_t)a.tq.max_nodes * a.tq.H * a.tq.G + 15) / 16), (uint32_t)a.tq.B);
+        hipLaunchKernelGGL(tree_attention_join_kernel, grid, dim3(256), 0, stream, a.tq, a.plan, a.part, a.shares, a.out,
+                           a.lse);
     }
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }

@@ -103,6 +103,39 @@ def test_long_contexts_are_split(nrc):
     check(nrc, bt, cap=20.0, max_ctx=5000)
 
 
+@pytest.mark.parametrize("ctx,nodes,H,G", [([3000, 0, 900, 130], [30, 20, 0, 33], 1, 4), ([1500, 700], [40, 33], 2, 8),
+                                           ([2100, 64, 128], [100, 3, 70], 1, 6), ([1000] * 70, [9] * 70, 1, 8)])
+def test_large_trees_over_split_contexts(nrc, ctx, nodes, H, G):
+    """Many rows: shares by the lengths, empty sequences, several row blocks, more sequences than a wave's lanes."""
+    bt = ref.Batch(ctx, nodes, H=H, G=G, seed=sum(ctx))
+    need = nrc._load().nrc_context_tree_attention_workspace_bytes(bt.B, bt.T, H * G, H, bt.max_nodes, max(ctx))
+    assert need > 0
+    check(nrc, bt, max_ctx=max(ctx))
+    check(nrc, ref.Batch(ctx, nodes, H=H, G=G, seed=1, tree=False), cap=25.0, max_ctx=max(ctx), mass=False)
+
+
+def test_large_trees_with_absent_blocks_and_odd_values(nrc):
+    """Tiles with keys that are not there among whole ones; NaN and infinities in a node of a large tree."""
+    bt = ref.Batch([1000, 600], [40, 40], H=1, G=4, seed=30)
+    bt.tables[0, 20] = -1
+    bt.tables[0, 21] = bt.nb
+    bt.tables[1, 3] = 2 ** 31 - 1
+    check(nrc, bt)
+    for bad in (math.nan, math.inf, -math.inf):
+        b2 = ref.Batch([1000, 600], [40, 40], H=1, G=4, seed=31)
+        o, l, to, tl = ref.attention(b2)
+        c = b2.cell(1, 600 + 5)
+        b2.cache[c[0], :, c[1], 64 + 9] = bad
+        out, lse, args, d = run(nrc, b2)
+        sees = torch.from_numpy(np.array([i >= 40 and ref.bits(b2.mask[i], 40)[5] for i in range(80)]))
+        assert_within(out[~sees.cuda()], o[~sees], to[~sees], "out")
+        hit = out[sees.cuda()].float().cpu()
+        assert bool((torch.isnan(hit[..., 9]) if math.isnan(bad) else hit[..., 9] == bad).all())
+        rest = [i for i in range(64) if i != 9]
+        assert_within(out[sees.cuda()][..., rest], o[sees][..., rest], to[sees][..., rest], "out beside it")
+        assert_within(lse, l, tl, "lse")
+
+
 def test_large_scores_and_equal_scores(nrc):
     """Scores that rise along the context (the running maximum moves), and scores all equal."""
     bt = ref.Batch([300], [2], H=1, G=2, seed=7, q_scale=1.0)
