@@ -176,10 +176,10 @@ def _stream(stream, ref):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream(ref.device)
-    elif stream.device != ref.device:
+        return torch._C._cuda_getCurrentRawStream(ref.get_device())  # the handle alone, without a stream object
+    if stream.device != ref.device:
         raise ValueError(f"stream is on {stream.device}, the operands on {ref.device}")
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _call(ref, fn, *args):
@@ -188,12 +188,14 @@ def _call(ref, fn, *args):
     NrcError on a non-zero status."""
     import torch
 
-    dev = ref.device.index
-    if dev is not None and dev != torch.cuda.current_device():
+    dev = ref.get_device()
+    if dev >= 0 and dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            _check(fn(*args))
+            code = fn(*args)
     else:
-        _check(fn(*args))
+        code = fn(*args)
+    if code != 0:
+        _check(code)
 
 
 def _all_on(ref, **tensors):
@@ -846,10 +848,13 @@ ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 def _dtype_code(dtype, name, table=False):
     import torch
 
-    codes = {torch.bfloat16: 0, torch.float32: 2} if table else {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-    if dtype not in codes:
-        raise TypeError(f"{name} must be bfloat16 or float32{'' if table else ' or float16'}, not {dtype}")
-    return codes[dtype]
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float32:
+        return 2
+    if dtype == torch.float16 and not table:
+        return 1
+    raise TypeError(f"{name} must be bfloat16 or float32{'' if table else ' or float16'}, not {dtype}")
 
 
 def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, original_max=0, low=1.0, high=32.0,
@@ -907,89 +912,112 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
     import torch
 
     code = _dtype_code(x.dtype, "x")
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise TypeError("x must be a GPU tensor")
-    if x.dim() != 3 or x.stride(2) != 1 and x.shape[2] != 1:
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or st[2] != 1 and shape[2] != 1:
         raise ValueError("x must be [T, H, d] with unit last stride")
-    T, H, d = x.shape
+    T, H, d = shape
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout is 'interleaved' or 'half'")
     tcode = _dtype_code(cos_sin.dtype, "cos_sin", table=True)
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    table = cos_sin.shape
+    if len(table) != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous [max_position, R]")
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (T,) or not positions.is_contiguous():
+    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int64 [T] tensor")
+    _at(positions, dev, "positions")
+    _at(cos_sin, dev, "cos_sin")
     if out is None:
-        out = _empty((T, H, d), x.dtype, x.device, stream)
-    elif out.dtype != x.dtype or tuple(out.shape) != (T, H, d) or out.stride(2) != 1:
-        raise ValueError("out must be shaped like x, of its dtype, with unit last stride")
-    _all_on(x, positions=positions, cos_sin=cos_sin, out=out)
-    _call(x, _load().nrc_rope_rotate, _ptr(x), code, T, H, d, x.stride(0), x.stride(1), _ptr(positions), _ptr(cos_sin),
-          tcode, cos_sin.shape[0], cos_sin.shape[1], ROPE_LAYOUTS[layout], 1 if inverse else 0, _ptr(out),
-          out.stride(0), out.stride(1), _stream(stream, x))
+        out = _empty(shape, x.dtype, x.device, stream)
+        ost = (H * d, d)
+    else:
+        ost = out.stride()
+        if out.dtype != x.dtype or out.shape != shape or ost[2] != 1:
+            raise ValueError("out must be shaped like x, of its dtype, with unit last stride")
+        _at(out, dev, "out")
+    _call(x, _load().nrc_rope_rotate, x.data_ptr(), code, T, H, d, st[0], st[1], positions.data_ptr(),
+          cos_sin.data_ptr(), tcode, table[0], table[1], ROPE_LAYOUTS[layout], 1 if inverse else 0, out.data_ptr(), ost[0],
+          ost[1], _stream(stream, x))
     return out
 
 
-def _int32(t, name, ref, shape=None):
+def _at(t, dev, name):
+    """Raise unless t is a tensor on GPU `dev`."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
-    return _same_device(t, ref, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        where = "not a tensor" if not isinstance(t, torch.Tensor) else str(t.device)
+        raise ValueError(f"{name} must be a tensor on cuda:{dev} ({where})")
+
+
+def _int32(t, name, dev, shape):
+    import torch
+
+    _at(t, dev, name)
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
 def _paged_operands(cache, tables):
-    """Checks of one layer's cache view and its block tables; the C ABI's
-    arguments from `cache` to `B`."""
+    """Checks of one layer's cache view and its block tables; the GPU, and the
+    C ABI's arguments from `cache` to `B`."""
     import torch
 
-    _bf16(cache, "cache", contiguous=False)
-    if cache.dim() != 4 or cache.shape[3] != 2 * HEAD_DIM or cache.stride(3) != 1:
+    dev = cache.get_device()
+    if cache.dtype != torch.bfloat16 or dev < 0:
+        raise TypeError(f"cache must be a bfloat16 GPU tensor, not {cache.dtype} on {cache.device}")
+    shape, st = cache.shape, cache.stride()
+    if len(shape) != 4 or shape[3] != 2 * HEAD_DIM or st[3] != 1:
         raise ValueError("cache must be a [num_blocks, H, block_size, 128] view with unit last stride")
-    if not isinstance(tables, torch.Tensor) or tables.dtype != torch.int32 or tables.dim() != 2 or (
-            tables.shape[1] > 1 and tables.stride(1) != 1):
-        raise ValueError("tables must be an int32 [B, blocks] tensor with unit last stride")
-    _same_device(tables, cache, "tables")
-    nb, H, bs, _ = cache.shape
-    st = [n if size > 1 else 0 for n, size in zip(cache.stride(), cache.shape)]  # (one of a kind has no stride)
-    return (_ptr(cache), nb, bs, st[0], st[2], st[1], H, _ptr(tables), tables.stride(0), tables.shape[1],
-            tables.shape[0])
+    _at(tables, dev, "tables")
+    if tables.dtype != torch.int32 or tables.dim() != 2:
+        raise ValueError("tables must be an int32 [B, blocks] tensor")
+    B, width = tables.shape
+    tst = tables.stride()
+    if width > 1 and tst[1] != 1:
+        raise ValueError("tables must have unit last stride")
+    nb, H, bs, _ = shape
+    # (one of a kind has no stride)
+    return dev, (cache.data_ptr(), nb, bs, st[0] if nb > 1 else 0, st[2] if bs > 1 else 0, st[1] if H > 1 else 0, H,
+                 tables.data_ptr(), tst[0], width, B)
 
 
 def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap):
-    """Checks shared by the attention and its received weights; the C ABI's
-    arguments from `q` to `softcap`, and max_ctx."""
+    """Checks shared by the attention and its received weights; the GPU, T, Hq, H,
+    B, max_ctx and the C ABI's arguments from `q` to `softcap`."""
     import torch
 
-    paged = _paged_operands(cache, tables)
+    dev, paged = _paged_operands(cache, tables)
+    bs, H, width, B = paged[2], paged[6], paged[9], paged[10]
     _fits32(max_nodes=max_nodes)
-    _bf16(q, "q", contiguous=False)
-    if q.dim() != 3 or q.shape[2] != HEAD_DIM or q.stride(2) != 1:
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, not {q.dtype}")
+    _at(q, dev, "q")
+    shape, st = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != HEAD_DIM or st[2] != 1:
         raise ValueError("q must be [T, Hq, 64] with unit last stride")
-    T, Hq, _ = q.shape
-    B = tables.shape[0]
-    _same_device(q, cache, "q")
-    _int32(ctx_lens, "ctx_lens", cache, (B,))
-    _int32(q_starts, "q_starts", cache, (B + 1,))
-    words = 0
+    T, Hq, _ = shape
+    _int32(ctx_lens, "ctx_lens", dev, (B,))
+    _int32(q_starts, "q_starts", dev, (B + 1,))
+    mask, words = None, 0
     if tree_mask is not None:
-        if (not isinstance(tree_mask, torch.Tensor) or tree_mask.dtype != torch.int64 or tree_mask.dim() != 2
-                or tree_mask.shape[0] != T or not tree_mask.is_contiguous()):
+        _at(tree_mask, dev, "tree_mask")
+        if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or not tree_mask.is_contiguous():
             raise ValueError("tree_mask must be a contiguous int64 [T, words] tensor")
-        _same_device(tree_mask, cache, "tree_mask")
-        words = tree_mask.shape[1]
-        if words == 0:
-            raise ValueError("tree_mask must have a word a row at least")
+        rows, words = tree_mask.shape
+        if rows != T or words == 0:
+            raise ValueError("tree_mask must have T rows of a word at least")
+        if T:
+            mask = tree_mask.data_ptr()
+        else:
+            words = 0  # (no row to read)
     if max_ctx is None:
-        max_ctx = tables.shape[1] * cache.shape[2]
-    scale = HEAD_DIM ** -0.5 if scale is None else scale
-    # (a [0, words] mask has no address, and no row to read)
-    mask = _ptr(tree_mask) if words and T else None
-    st = [n if size > 1 else 0 for n, size in zip(q.stride(), q.shape)]
-    return (_ptr(q), st[0], st[1], T, Hq, *paged, _ptr(ctx_lens), _ptr(q_starts), max_nodes, max_ctx, mask,
-            words if T else 0, scale, softcap), max_ctx
+        max_ctx = width * bs
+    return dev, T, Hq, H, B, max_ctx, (
+        q.data_ptr(), st[0] if T > 1 else 0, st[1] if Hq > 1 else 0, T, Hq, *paged, ctx_lens.data_ptr(),
+        q_starts.data_ptr(), max_nodes, max_ctx, mask, words, HEAD_DIM ** -0.5 if scale is None else scale, softcap)
 
 
 def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx=None, tree_mask=None, scale=None,
@@ -1015,49 +1043,50 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
     over workgroups, with a workspace from torch's allocator."""
     import torch
 
-    args, max_ctx = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale,
-                                    softcap)
-    T, Hq, _ = q.shape
-    B, H = tables.shape[0], cache.shape[1]
+    dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
+                                                      tree_mask, scale, softcap)
     if out is None:
         out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
     else:
-        _bf16(out, "out")
-        if tuple(out.shape) != (T, Hq, HEAD_DIM):
-            raise ValueError("out must be [T, Hq, 64]")
-        _same_device(out, q, "out")
+        _at(out, dev, "out")
+        if out.dtype != torch.bfloat16 or out.shape != (T, Hq, HEAD_DIM) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bfloat16 [T, Hq, 64]")
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, stream)
     else:
-        _float_lse(lse, q)
+        _float_lse(lse, dev, (T, Hq))
     lib = _load()
     # the split follows the device's size: asked with q's GPU as the current device
-    with torch.cuda.device(q.device):
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            need = lib.nrc_context_tree_attention_workspace_bytes(B, T, Hq, H, max_nodes, max_ctx)
+    else:
         need = lib.nrc_context_tree_attention_workspace_bytes(B, T, Hq, H, max_nodes, max_ctx)
     if need < 0:
         _check(need)
-    ws = _empty(need, torch.uint8, q.device, stream) if need > 0 else None
-    _call(q, lib.nrc_context_tree_attention, *args, _ptr(out), _ptr(lse), _ptr(ws), need, _stream(stream, q))
+    ws = _empty((need,), torch.uint8, q.device, stream) if need > 0 else None
+    _call(q, lib.nrc_context_tree_attention, *args, out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(),
+          need, _stream(stream, q))
     return out, lse
 
 
-def _float_lse(lse, q):
+def _float_lse(lse, dev, shape):
     import torch
 
-    if lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous():
+    _at(lse, dev, "lse")
+    if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
-    return _same_device(lse, q, "lse")
 
 
-def _cells(t, name, ref, dtype, shape):
-    """A [B, H, width] tensor of per-cell values with unit last stride."""
-    import torch
-
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be a {dtype} [B, H, width] tensor with unit last stride")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}")
-    return _same_device(t, ref, name)
+def _cells(t, name, dev, dtype, shape):
+    """A [B, H, width] tensor of per-cell values with unit last stride; its strides."""
+    _at(t, dev, name)
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor")
+    st = t.stride()
+    if shape[2] > 1 and st[2] != 1:
+        raise ValueError(f"{name} must have unit last stride")
+    return st
 
 
 def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes, max_ctx=None, tree_mask=None,
@@ -1072,21 +1101,26 @@ def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes,
     Other arguments as context_tree_attention."""
     import torch
 
-    args, _ = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap)
-    B, H = tables.shape[0], cache.shape[1]
-    _float_lse(lse, q)
+    dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
+                                                      tree_mask, scale, softcap)
+    _float_lse(lse, dev, (T, Hq))
     if width is None:
         given = weights if weights is not None else out
         width = tables.shape[1] * cache.shape[2] if given is None or given.dim() != 3 else given.shape[2]
+    if width < 0:
+        raise ValueError("width must not be negative")
+    shape = (B, H, width)
+    w, wst = None, (0, 0)
     if weights is not None:
-        _cells(weights, "weights", q, torch.float32, (B, H, width))
+        wst = _cells(weights, "weights", dev, torch.float32, shape)
+        w = weights.data_ptr()
     if out is None:
-        out = _empty((B, H, width), torch.float32, q.device, stream)
+        out = _empty(shape, torch.float32, q.device, stream)
+        ost = (H * width, width)
     else:
-        _cells(out, "out", q, torch.float32, (B, H, width))
-    ws = (0, 0) if weights is None else (weights.stride(0), weights.stride(1))
-    _call(q, _load().nrc_context_attention_mass, *args, _ptr(lse), _ptr(weights), ws[0], ws[1], decay, _ptr(out),
-          out.stride(0), out.stride(1), width, _stream(stream, q))
+        ost = _cells(out, "out", dev, torch.float32, shape)
+    _call(q, _load().nrc_context_attention_mass, *args, lse.data_ptr(), w, wst[0], wst[1], decay, out.data_ptr(), ost[0],
+          ost[1], width, _stream(stream, q))
     return out
 
 
@@ -1106,41 +1140,42 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
     into the holes before it; weights and positions follow them."""
     import torch
 
-    paged = _paged_operands(cache, tables)
+    dev, paged = _paged_operands(cache, tables)
+    H, B = paged[6], paged[10]
     _fits32(budget=budget, sinks=sinks, recent=recent)
-    B, H = tables.shape[0], cache.shape[1]
-    _int32(lens, "lens", cache, (B,))
-    _int32(ends, "ends", cache, (B,))
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    _int32(lens, "lens", dev, (B,))
+    _int32(ends, "ends", dev, (B,))
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise ValueError("weights must be a float32 [B, H, width] tensor")
     width = weights.shape[2]
-    _cells(weights, "weights", cache, torch.float32, (B, H, width))
-    _cells(positions, "positions", cache, torch.int32, (B, H, width))
-    if budget < 1:
-        raise ValueError("budget must be at least 1")
+    wst = _cells(weights, "weights", dev, torch.float32, (B, H, width))
+    pst = _cells(positions, "positions", dev, torch.int32, (B, H, width))
     lib = _load()
     need = lib.nrc_context_kv_evict_workspace_bytes(B, H, width, budget)
     if need < 0:
         _check(need)
-    dev = cache.device
+    device, shape = cache.device, (B, H, budget)
     if new_weights is None:
-        new_weights = _empty((B, H, budget), torch.float32, dev, stream)
+        new_weights = _empty(shape, torch.float32, device, stream)
     else:
-        _cells(new_weights, "new_weights", cache, torch.float32, (B, H, budget))
+        _cells(new_weights, "new_weights", dev, torch.float32, shape)
     if new_positions is None:
-        new_positions = _empty((B, H, budget), torch.int32, dev, stream)
+        new_positions = _empty(shape, torch.int32, device, stream)
     else:
-        _cells(new_positions, "new_positions", cache, torch.int32, (B, H, budget))
+        _cells(new_positions, "new_positions", dev, torch.int32, shape)
     if not new_weights.is_contiguous() or not new_positions.is_contiguous():
         raise ValueError("new_weights and new_positions must be contiguous")
     if new_lens is None:
-        new_lens = _empty((B,), torch.int32, dev, stream)
+        new_lens = _empty((B,), torch.int32, device, stream)
     else:
-        _int32(new_lens, "new_lens", cache, (B,))
-    ws = _empty(need, torch.uint8, dev, stream) if need > 0 else None
-    _call(cache, lib.nrc_context_kv_evict, *paged, _ptr(lens), _ptr(weights), weights.stride(0), weights.stride(1),
-          _ptr(positions), positions.stride(0), positions.stride(1), width, _ptr(ends), sinks, recent, budget,
-          _ptr(new_weights), _ptr(new_positions), _ptr(new_lens), _ptr(ws), need, _stream(stream, cache))
+        _int32(new_lens, "new_lens", dev, (B,))
+    ws = _empty((need,), torch.uint8, device, stream) if need > 0 else None
+    _call(cache, lib.nrc_context_kv_evict, *paged, lens.data_ptr(), weights.data_ptr(), wst[0], wst[1],
+          positions.data_ptr(), pst[0], pst[1], width, ends.data_ptr(), sinks, recent, budget, new_weights.data_ptr(),
+          new_positions.data_ptr(), new_lens.data_ptr(), None if ws is None else ws.data_ptr(), need,
+          _stream(stream, cache))
     return new_weights, new_positions, new_lens
 
 
