@@ -55,6 +55,37 @@ __device__ __forceinline__ uint32_t seen_word(const TreeQueries& t, int32_t row,
     return w < t.mask_words ? t.mask[(int64_t)row * t.mask_words + w] & there : 0u;
 }
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mfma32(U32x4 a, U32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+// S^T = K Q^T by v_mfma_f32_32x32x16_bf16: lane l holds, for row l % 32, the keys 8 (i / 4) + 4 (l / 32) + i % 4 of
+// 32 at i = 0 .. 15. The bits of a word of 32 keys in that order:
+__device__ __forceinline__ uint32_t bits_of_scores(uint32_t word, uint32_t half) {
+    word >>= 4 * half;
+    return (word & 0xFu) | (word >> 4 & 0xF0u) | (word >> 8 & 0xF00u) | (word >> 12 & 0xF000u);
+}
+
+// 16 bytes a lane from global memory to LDS at lds + 16 lane, without a register. As inline assembly, so
+// that the kernel alone accounts for it (a wait for all of them before the barrier) instead of a wait before
+// every LDS read. An LDS DMA right after a write of M0 needs a wait state in between.
+__device__ __forceinline__ void to_lds(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
+}
+// The same with 4 bytes a lane, at lds + 4 lane.
+__device__ __forceinline__ void to_lds4(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory");
+}
+// This wave's loads to LDS have landed, and everybody's after the barrier.
+__device__ __forceinline__ void landed() {
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    __syncthreads();
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
 // e^x and log in base 2, the hardware's (relative error about 2^-23).
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_hw(float x) { return __builtin_amdgcn_logf(x); }

@@ -543,13 +543,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
     }
 }
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ f32x16 mfma32(U32x4 a, U32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
 
 // What a wave of the many-rows kernel carries for R query tiles of 32 rows.
 // Scores come as S^T = K Q^T by v_mfma_f32_32x32x16_bf16: lane l holds, for
@@ -639,13 +633,6 @@ __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Key
     for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) w.o[rt][c] = mfma32(kv.v[c][ks], pb[ks], w.o[rt][c]);
-}
-
-// 16 bytes a lane from global memory to LDS at lds + 16 lane, without a register. As inline assembly, so
-// that the kernel alone accounts for it (the barrier of a tile waits for all of them) instead of a wait before
-// every LDS read. An LDS DMA right after a write of M0 needs a wait state in between.
-__device__ __forceinline__ void to_lds(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
 }
 
 // Many rows: the WAVES waves of a workgroup hold 32 R rows each and share the
@@ -751,7 +738,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
     constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint32_t* present = reinterpret_cast<uint32_t*>(lds + 2 * kStage * 256);  // [2][kStage]
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+    const uint32_t lds0 = lds_address(lds);
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t hl = lane >> 5, n32 = lane & 31u;
     uint32_t id = blockIdx.x, rb = 0;
@@ -816,11 +803,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
             to_lds(row + kHeadDim + 8 * (c8 ^ (row8 >> 1 & 1u) << 2), at + kStage * 128);
             if (c8 == 0) present[buf * kStage + 8 * (kRuns * wave + i) + row8] = off[i] >= 0;
         }
-    };
-    // this wave's loads of the next tile have landed, and everybody's with the barrier
-    auto landed = [&]() {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
-        __syncthreads();
     };
     auto ballots = [&](int buf, uint64_t (&exists)[kStage / 64]) {
         bool all = true;
@@ -970,12 +952,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                 }
                 if (there == 0u) continue;
                 Keys32 k;
-                // the lane's keys' bits of a word in the order of its scores
-                auto own = [&](uint32_t word) {
-                    word >>= 4 * hl;
-                    return (word & 0xFu) | (word >> 4 & 0xF0u) | (word >> 8 & 0xF00u) | (word >> 12 & 0xF000u);
-                };
-                const uint32_t mine = own(there);
+                const uint32_t mine = bits_of_scores(there, hl);
                 auto v_there = [&]() {
                     read_v(k, buf, sub);
 #pragma unroll
@@ -1008,7 +985,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                 uint32_t seen[R];
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
-                    seen[rt] = own(in_tree >= 0 ? there & word[rt] : there);
+                    seen[rt] = bits_of_scores(in_tree >= 0 ? there & word[rt] : there, hl);
                     f32x16 sc;
                     scores32<R>(sc, w, rt, k);
                     add32<R, CAP, true>(w, rt, sc, k, f, seen[rt]);
