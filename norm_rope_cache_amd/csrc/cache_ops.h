@@ -130,9 +130,14 @@ struct KvEvictArgs {
     float* new_weights;      // [B, H, budget]
     int32_t* new_positions;  // [B, H, budget]
     int32_t* new_lens;       // [B]
-    int32_t* moves;          // workspace: [B H] counts, padded to 4; [B H, max_moves] holes; the same sources
+    int32_t* moves;          // the workspace
     int32_t max_moves;       // min(budget, width - budget), 0 when nothing can move
+    int32_t blocks;          // kv_evict_blocks(budget)
 };
+
+// Bytes of KvEvictArgs::moves; workgroups along a list's places.
+int64_t kv_evict_workspace(int64_t lists, int64_t max_moves, int64_t blocks);
+int32_t kv_evict_blocks(int64_t budget);
 
 int launch_kv_evict(const KvEvictArgs& a, hipStream_t stream);
 

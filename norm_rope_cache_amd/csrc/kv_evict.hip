@@ -7,9 +7,11 @@
 // Kernel 1, one workgroup per (sequence, head): the keys (weights mapped to
 // unsigned integers of the same order, protected cells above them all, absent
 // ones below) in registers, the budget-th largest found by three passes over
-// their digits (11, 11 and 10 bits) with a histogram in LDS, ties and moves
-// numbered by ballots in index order. Kernel 2 moves the 256-byte cells, 16
-// bytes a lane. Kernel 1 is bound by its passes' latency, kernel 2 by memory.
+// their digits (11, 11 and 10 bits) with a histogram in LDS; then the list of
+// holes and the list of the cells that fill them, numbered by ballots in index
+// order. Kernel 2, one workgroup per 256 places of a list: the new weights and
+// positions, and the 256-byte cells that move, 16 bytes a lane. Kernel 1 is bound
+// by its passes' latency on one CU, kernel 2 by memory.
 #include "cache_ops.h"
 #include "paged.h"
 
@@ -26,69 +28,111 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v, uint32_t lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint32_t o = (uint32_t)__builtin_amdgcn_ds_bpermute((int)((lane - d) << 2), (int)v);
-        if (lane >= (uint32_t)d) v += o;
-    }
+// Sums over the lanes up to each one: within rows of 16 by shifts, then the
+// rows' totals handed on (DPP: no LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_0(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
+    v += dpp_or_0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += dpp_or_0<0x112, 0xF>(v);
+    v += dpp_or_0<0x114, 0xF>(v);
+    v += dpp_or_0<0x118, 0xF>(v);
+    v += dpp_or_0<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    v += dpp_or_0<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
     return v;
+}
+__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)wave_inclusive(v), 63);
 }
 
 __device__ __forceinline__ uint32_t bits_below(uint64_t m, uint32_t lane) {
     return (uint32_t)__popcll(m & (((uint64_t)1 << lane) - 1));
 }
 
-// SLOTS > 0: a thread holds its cells' keys, at most SLOTS 64-cell slots a
-// wave; 0: they are worked out again in every pass.
+// The workspace: [B H] counts of moves, padded to 4; [B H, blocks + 1] how many
+// holes lie before each block of 256 places; [B H, max_moves] holes; the same
+// many sources.
+constexpr int kPlaces = 256;
+struct Moves {
+    int32_t* count;
+    int32_t* starts;
+    int32_t* holes;
+    int32_t* sources;
+};
+__device__ __forceinline__ Moves moves_of(const KvEvictArgs& a, int32_t bh) {
+    const int64_t lists = (int64_t)a.B * a.H, per = a.blocks + 1;
+    int32_t* starts = a.moves + (lists + 3) / 4 * 4;
+    int32_t* holes = starts + lists * per;
+    return Moves{a.moves + bh, starts + bh * per, holes + (int64_t)bh * a.max_moves,
+                 holes + (lists + bh) * a.max_moves};
+}
+__device__ __forceinline__ int32_t cells_of(const KvEvictArgs& a, int32_t b) {
+    int64_t n = a.lens[b];
+    const int64_t cap = (int64_t)a.kv.table_width * a.kv.block_size;
+    n = n > a.width ? a.width : n;
+    n = n > cap ? cap : n;
+    return n < 0 ? 0 : (int32_t)n;
+}
+
+// SLOTS > 0: a thread holds its cells' keys, at most SLOTS (<= 64) of them, 64
+// cells to a wave and slot; 0: they are worked out again in every pass.
 template <int SLOTS>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t wave_sum[kWaves], wave_sum2[kWaves];
-    __shared__ uint32_t picked[2];  // the digit, and how many are wanted among its cells
+    __shared__ uint32_t picked[3];  // the digit, how many are wanted among its cells, how many those are
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int32_t bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
-    int64_t n64 = a.lens[b];
-    if (n64 < 0) n64 = 0;
-    if (n64 > a.width) n64 = a.width;
-    const int64_t cap = (int64_t)a.kv.table_width * a.kv.block_size;
-    if (n64 > cap) n64 = cap;
-    const int32_t n = (int32_t)n64;
-    const int32_t kept = n < a.budget ? n : a.budget;
-    const float* weights = a.weights + (int64_t)b * a.w_bs + (int64_t)h * a.w_hs;
-    const int32_t* positions = a.positions + (int64_t)b * a.p_bs + (int64_t)h * a.p_hs;
-    float* new_w = a.new_weights + (int64_t)bh * a.budget;
-    int32_t* new_p = a.new_positions + (int64_t)bh * a.budget;
-    if (h == 0 && tid == 0) a.new_lens[b] = kept;
-    for (int32_t i = kept + (int32_t)tid; i < a.budget; i += kThreads) {
-        new_w[i] = 0.0f;
-        new_p[i] = -1;
-    }
-    const int32_t lists = (gridDim.x + 3) / 4 * 4;
+    const int32_t n = cells_of(a, b);
+    const Moves mv = moves_of(a, bh);
     if (n <= a.budget) {
-        for (int32_t i = (int32_t)tid; i < n; i += kThreads) {
-            new_w[i] = weights[i];
-            new_p[i] = positions[i];
-        }
-        if (tid == 0 && a.max_moves > 0) a.moves[bh] = 0;
+        if (tid == 0) *mv.count = 0;
         return;
     }
+    const int32_t kept = a.budget;
+    const float* __restrict__ weights = a.weights + (int64_t)b * a.w_bs + (int64_t)h * a.w_hs;
+    const int32_t* __restrict__ positions = a.positions + (int64_t)b * a.p_bs + (int64_t)h * a.p_hs;
 
     // The wave's cells: slots of 64 from wave * per_wave * 64 on.
     const int32_t per_wave = (n + kThreads - 1) / kThreads;
     const int32_t base = (int32_t)wave * per_wave * 64 + (int32_t)lane;
     const int64_t horizon = (int64_t)a.ends[b] - a.recent;
+    auto key_of = [&](int32_t at, int32_t p, float w) -> uint32_t {
+        return at >= n ? 0u : p < a.sinks || p >= horizon ? 0xFFFFFFFFu : ordered(w);
+    };
     auto work_out = [&](int32_t i) -> uint32_t {
-        const int32_t at = base + i * 64;
-        if (at >= n) return 0u;
-        const int32_t p = positions[at];
-        return p < a.sinks || p >= horizon ? 0xFFFFFFFFu : ordered(weights[at]);
+        const int32_t at = base + i * 64, in = at < n ? at : n - 1;
+        return key_of(at, positions[in], weights[in]);
     };
     uint32_t held[SLOTS ? SLOTS : 1];
     if constexpr (SLOTS > 0) {
+        // eight slots' loads on the way together (a position decides only what its weight counts for)
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) held[i] = i < per_wave ? work_out(i) : 0u;
+        for (int i0 = 0; i0 < SLOTS; i0 += 8) {
+            int32_t p[8];
+            float w[8];
+            if (i0 < per_wave) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t at = base + (i0 + i) * 64, in = at < n ? at : n - 1;
+                    p[i] = positions[in];
+                    w[i] = weights[in];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                held[i0 + i] = i0 + i < per_wave ? key_of(base + (i0 + i) * 64, p[i], w[i]) : 0u;
+        }
     }
+    // what the waves before this one add up to, of a sum each wave has left in LDS
+    auto before_this = [&](const uint32_t* sums, uint32_t* all) {
+        const uint32_t v = sums[lane & 15u];
+        const uint32_t first16 = lane < 16 ? v : 0u;
+        if (all) *all = wave_total(first16);
+        return wave_total(lane < wave ? first16 : 0u);
+    };
     auto each = [&](auto f) {
         if constexpr (SLOTS > 0) {
 #pragma unroll
@@ -100,6 +144,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
     };
 
     uint32_t border = 0, want = (uint32_t)kept;  // the digits found so far; how many of the cells with them
+    bool all_ties = false;
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
         hist[tid] = 0u;
@@ -120,136 +165,166 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
         __syncthreads();
         // from the largest digit down: thread t the digits 2047 - 2t and 2046 - 2t
         const uint32_t hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
-        const uint32_t incl = wave_inclusive(hi + lo, lane);
+        const uint32_t incl = wave_inclusive(hi + lo);
         if (lane == 63) wave_sum[wave] = incl;
         __syncthreads();
-        uint32_t before = incl - hi - lo;
-        for (uint32_t w = 0; w < wave; ++w) before += wave_sum[w];
+        const uint32_t before = incl - hi - lo + before_this(wave_sum, nullptr);
         if (before < want && want <= before + hi + lo) {
             const bool first = want <= before + hi;
             picked[0] = kBins - 1 - 2 * tid - (first ? 0u : 1u);
             picked[1] = want - before - (first ? 0u : hi);
+            picked[2] = first ? hi : lo;
         }
         __syncthreads();
         border = border << bits | picked[0];
         want = picked[1];
+        all_ties = picked[2] == want;
+        if (all_ties) {  // every cell with these digits is kept: the others do not matter
+            border <<= shift;
+            break;
+        }
+    }
+    // Kept: keys above `border`, and the first `want` cells that equal it (a cell past n has key 0, which no
+    // border reaches); with all_ties the keys from `border` on.
+    __syncthreads();
+    uint32_t tie0 = 0;  // equal cells of the waves before
+    if (!all_ties) {
+        uint32_t ties = 0;
+        each([&](int, uint32_t key) { ties += (uint32_t)__popcll(__ballot(key == border)); });
+        if (lane == 0) wave_sum[wave] = ties;
+        __syncthreads();
+        tie0 = before_this(wave_sum, nullptr);
         __syncthreads();
     }
-    // Kept: keys above `border`, and the first `want` cells that equal it.
-
-    uint32_t ties = 0;
-    each([&](int, uint32_t key) { ties += (uint32_t)__popcll(__ballot(key == border)); });
-    if (lane == 0) wave_sum[wave] = ties;
-    __syncthreads();
-    uint32_t tie0 = 0;
-    for (uint32_t w = 0; w < wave; ++w) tie0 += wave_sum[w];
-    __syncthreads();
-
-    // (the ballots take every lane of the wave: cells past n have key 0, which
-    // no border reaches)
+    // f(slot, is a hole, is a source): of each of the lane's cells, the wave together
     auto walk = [&](auto f) {
         uint32_t seen = tie0;
         each([&](int i, uint32_t key) {
             const int32_t at = base + i * 64;
-            const uint64_t tied = __ballot(key == border);
-            const bool keep = key > border || (key == border && seen + bits_below(tied, lane) < want);
-            seen += (uint32_t)__popcll(tied);
-            f(at, keep && at < n, !keep && at < kept, keep && at >= kept && at < n);
+            bool keep = key >= border;
+            if (!all_ties) {
+                const uint64_t tied = __ballot(key == border);
+                keep = key > border || (key == border && seen + bits_below(tied, lane) < want);
+                seen += (uint32_t)__popcll(tied);
+            }
+            f(i, !keep && at < kept, keep && at >= kept);
         });
     };
     uint32_t holes = 0, sources = 0;
-    walk([&](int32_t, bool, bool hole, bool source) {
-        holes += (uint32_t)__popcll(__ballot(hole));
-        sources += (uint32_t)__popcll(__ballot(source));
+    walk([&](int, bool hole, bool source) {
+        holes += hole;
+        sources += source;
     });
+    holes = wave_total(holes);
+    sources = wave_total(sources);
     if (lane == 0) {
         wave_sum[wave] = holes;
         wave_sum2[wave] = sources;
     }
     __syncthreads();
-    uint32_t hole0 = 0, source0 = 0, count = 0;
-    for (uint32_t w = 0; w < (uint32_t)kWaves; ++w) {
-        if (w < wave) {
-            hole0 += wave_sum[w];
-            source0 += wave_sum2[w];
-        }
-        count += wave_sum[w];
+    uint32_t count = 0;
+    uint32_t hole0 = before_this(wave_sum, &count), source0 = before_this(wave_sum2, nullptr);
+    if (tid == 0) {
+        *mv.count = (int32_t)count;
+        mv.starts[a.blocks] = (int32_t)count;
     }
-    int32_t* hole_list = a.moves + lists + (int64_t)bh * a.max_moves;
-    int32_t* source_list = hole_list + (int64_t)gridDim.x * a.max_moves;
-    if (tid == 0) a.moves[bh] = (int32_t)count;
-    // the holes' list first: the sources look their targets up in it
-    {
-        uint32_t next = hole0;
-        walk([&](int32_t at, bool keep, bool hole, bool source) {
-            const uint64_t m = __ballot(hole);
-            if (hole) hole_list[next + bits_below(m, lane)] = at;
-            next += (uint32_t)__popcll(m);
-            if (keep && !source) {
-                new_w[at] = weights[at];
-                new_p[at] = positions[at];
-            }
-        });
-    }
-    __syncthreads();
-    uint32_t next = source0;
-    walk([&](int32_t at, bool, bool, bool source) {
-        const uint64_t m = __ballot(source);
-        if (source) {
-            const uint32_t rank = next + bits_below(m, lane);
-            const int32_t to = hole_list[rank];
-            source_list[rank] = at;
-            new_w[to] = weights[at];
-            new_p[to] = positions[at];
-        }
-        next += (uint32_t)__popcll(m);
+    walk([&](int i, bool hole, bool source) {
+        const int32_t at = base + i * 64, group = (int32_t)wave * per_wave + i;
+        // 64 cells a slot: every fourth begins a block of places
+        if ((group & 3) == 0 && group * 64 < kept && lane == 0) mv.starts[group >> 2] = (int32_t)hole0;
+        const uint64_t hm = __ballot(hole), sm = __ballot(source);
+        if (hole) mv.holes[hole0 + bits_below(hm, lane)] = at;
+        if (source) mv.sources[source0 + bits_below(sm, lane)] = at;
+        hole0 += (uint32_t)__popcll(hm);
+        source0 += (uint32_t)__popcll(sm);
     });
 }
 
-// 16 cells a workgroup and pass, 16 lanes to a cell.
-constexpr int kMovesPerBlock = 64;
-__global__ __launch_bounds__(256) void evict_move_kernel(PagedCache kv, int32_t H, const int32_t* __restrict__ moves,
-                                                         int32_t max_moves) {
-    const int32_t bh = blockIdx.y, b = bh / H, h = bh - b * H;
-    const int32_t count = moves[bh] < max_moves ? moves[bh] : max_moves;
-    const int32_t lists = (gridDim.y + 3) / 4 * 4;
-    const int32_t* holes = moves + lists + (int64_t)bh * max_moves;
-    const int32_t* sources = holes + (int64_t)gridDim.y * max_moves;
-    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
-    uint16_t* head = kv.cache + (int64_t)h * kv.head_stride + 8 * (threadIdx.x & 15u);
-    int64_t from[kMovesPerBlock / 16], to[kMovesPerBlock / 16];
-    U32x4 cell[kMovesPerBlock / 16];
-#pragma unroll
-    for (int i = 0; i < kMovesPerBlock / 16; ++i) {
-        const int32_t m = (int32_t)blockIdx.x * kMovesPerBlock + 16 * i + (int32_t)(threadIdx.x >> 4);
-        from[i] = to[i] = -1;
-        if (m < count) {
-            from[i] = key_offset(kv, table, (uint32_t)sources[m]);
-            to[i] = key_offset(kv, table, (uint32_t)holes[m]);
-        }
+// One workgroup: 256 places of a list.
+__global__ __launch_bounds__(kPlaces) void evict_apply_kernel(KvEvictArgs a) {
+    __shared__ int32_t origin[kPlaces], hole[kPlaces];
+    const int32_t tid = (int32_t)threadIdx.x, j0 = (int32_t)blockIdx.x * kPlaces, j = j0 + tid;
+    const int32_t bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
+    const int32_t n = cells_of(a, b), kept = n < a.budget ? n : a.budget;
+    const float* weights = a.weights + (int64_t)b * a.w_bs + (int64_t)h * a.w_hs;
+    const int32_t* positions = a.positions + (int64_t)b * a.p_bs + (int64_t)h * a.p_hs;
+    float weight = 0.0f;
+    int32_t position = -1;
+    if (j < kept) {  // on the way before it is known which places are holes
+        weight = weights[j];
+        position = positions[j];
     }
+    int32_t first = 0, moved = 0;  // of the holes among these places
+    origin[tid] = j;
+    if (n > a.budget) {
+        const Moves mv = moves_of(a, bh);
+        first = mv.starts[blockIdx.x];
+        moved = mv.starts[blockIdx.x + 1] - first;
+        __syncthreads();
+        if (tid < moved) {
+            const int32_t to = mv.holes[first + tid];
+            hole[tid] = to;
+            origin[to - j0] = mv.sources[first + tid];
+        }
+        __syncthreads();
+    }
+    if (j < a.budget) {
+        const int64_t at = (int64_t)bh * a.budget + j;
+        const int32_t from = origin[tid];
+        if (from != j) {
+            weight = weights[from];
+            position = positions[from];
+        }
+        a.new_weights[at] = weight;
+        a.new_positions[at] = position;
+    }
+    if (bh - b * a.H == 0 && j == 0) a.new_lens[b] = kept;
+    // 16 lanes to a cell, 16 cells at a time, four times on the way
+    const int32_t* table = a.kv.tables + (int64_t)b * a.kv.table_stride;
+    uint16_t* head = a.kv.cache + (int64_t)h * a.kv.head_stride + 8 * (tid & 15);
+    constexpr int kAtOnce = 4;
+    for (int32_t m0 = 0; m0 < moved; m0 += 16 * kAtOnce) {
+        int64_t from[kAtOnce], to[kAtOnce];
+        U32x4 cell[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < kMovesPerBlock / 16; ++i)
-        if ((from[i] | to[i]) >= 0) cell[i] = load16(head + from[i]);
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int32_t m = m0 + 16 * i + (tid >> 4);
+            from[i] = to[i] = -1;
+            if (m < moved) {
+                const int32_t t = hole[m];
+                to[i] = key_offset(a.kv, table, (uint32_t)t);
+                from[i] = key_offset(a.kv, table, (uint32_t)origin[t - j0]);
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < kMovesPerBlock / 16; ++i)
-        if ((from[i] | to[i]) >= 0) store16(head + to[i], cell[i]);
+        for (int i = 0; i < kAtOnce; ++i)
+            if ((from[i] | to[i]) >= 0) cell[i] = load16(head + from[i]);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if ((from[i] | to[i]) >= 0) store16(head + to[i], cell[i]);
+    }
 }
 
 }  // namespace
 
+int64_t kv_evict_workspace(int64_t lists, int64_t max_moves, int64_t blocks) {
+    return max_moves == 0 ? 0 : ((lists + 3) / 4 * 4 + lists * (blocks + 1) + 2 * lists * max_moves) * 4;
+}
+
+int32_t kv_evict_blocks(int64_t budget) { return (int32_t)((budget + kPlaces - 1) / kPlaces); }
+
 int launch_kv_evict(const KvEvictArgs& a, hipStream_t stream) {
     const uint32_t lists = (uint32_t)a.B * a.H;
-    // what a thread can hold, by the longest sequence there may be
-    auto kernel = a.width <= 4 * kThreads    ? evict_select_kernel<4>
-                  : a.width <= 16 * kThreads ? evict_select_kernel<16>
-                  : a.width <= 64 * kThreads ? evict_select_kernel<64>
-                                             : evict_select_kernel<0>;
-    hipLaunchKernelGGL(kernel, dim3(lists), dim3(kThreads), 0, stream, a);
     if (a.max_moves > 0) {
-        const dim3 grid((uint32_t)(a.max_moves + kMovesPerBlock - 1) / kMovesPerBlock, lists);
-        hipLaunchKernelGGL(evict_move_kernel, grid, dim3(256), 0, stream, a.kv, a.H, a.moves, a.max_moves);
+        // what a thread can hold, by the longest sequence there may be
+        auto kernel = a.width <= 8 * kThreads    ? evict_select_kernel<8>
+                      : a.width <= 16 * kThreads ? evict_select_kernel<16>
+                      : a.width <= 32 * kThreads ? evict_select_kernel<32>
+                      : a.width <= 64 * kThreads ? evict_select_kernel<64>
+                                                 : evict_select_kernel<0>;
+        hipLaunchKernelGGL(kernel, dim3(lists), dim3(kThreads), 0, stream, a);
     }
+    hipLaunchKernelGGL(evict_apply_kernel, dim3((uint32_t)a.blocks, lists), dim3(kPlaces), 0, stream, a);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

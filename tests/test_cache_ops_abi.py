@@ -136,7 +136,7 @@ def test_kv_evict(lib):
                               dict(lens=MISALIGNED), dict(ends=MISALIGNED)]:
         assert call(**kw, **({"ws": FAKE, "ws_bytes": 1 << 40} if "ws" not in kw else {})) == EINVAL, kw
     need = lib.nrc_context_kv_evict_workspace_bytes(3, 2, 64, 40)
-    assert need == (8 + 2 * 6 * 24) * 4  # counts of 6 heads, two lists of min(40, 64 - 40)
+    assert need == (8 + 6 * 2 + 2 * 6 * 24) * 4  # counts of 6 heads, starts of a block and its end, two lists of min(40, 64 - 40)
     assert call() == EINVAL and call(ws=FAKE, ws_bytes=need - 1) == EINVAL
     assert call(ws=ctypes.c_void_p(0x10008), ws_bytes=need) == EINVAL
     assert call(B=0, cache=None, tables=None, lens=None, w=None, p=None, nw=None, np=None, nl=None, ends=None) == 0
