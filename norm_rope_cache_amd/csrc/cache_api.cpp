@@ -330,7 +330,8 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
 int64_t nrc_context_kv_evict_workspace_bytes(int32_t B, int32_t H, int64_t width, int32_t budget) {
     if (B < 0 || H < 1 || budget < 1 || width < 0 || width > ((int64_t)1 << 31) - (1 << 17))
         return fail(NRC_EINVAL, "context_kv_evict: B >= 0, H >= 1, budget >= 1 and 0 <= width < 2^31 - 2^17 must hold");
-    return B == 0 ? 0 : nrc::kv_evict_workspace((int64_t)B * H, max_moves(width, budget), nrc::kv_evict_blocks(budget));
+    return B == 0 ? 0 : nrc::kv_evict_workspace((int64_t)B * H, width, max_moves(width, budget),
+                                                    nrc::kv_evict_blocks(budget));
 }
 
 int32_t nrc_context_kv_evict(uint16_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,

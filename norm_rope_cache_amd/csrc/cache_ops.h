@@ -136,7 +136,7 @@ struct KvEvictArgs {
 };
 
 // Bytes of KvEvictArgs::moves; workgroups along a list's places.
-int64_t kv_evict_workspace(int64_t lists, int64_t max_moves, int64_t blocks);
+int64_t kv_evict_workspace(int64_t lists, int64_t width, int64_t max_moves, int64_t blocks);
 int32_t kv_evict_blocks(int64_t budget);
 
 int launch_kv_evict(const KvEvictArgs& a, hipStream_t stream);

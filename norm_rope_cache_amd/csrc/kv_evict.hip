@@ -76,10 +76,44 @@ __device__ __forceinline__ int32_t cells_of(const KvEvictArgs& a, int32_t b) {
     return n < 0 ? 0 : (int32_t)n;
 }
 
+constexpr int kWholeMoves = 512;
+
+// The cells named by two lists in LDS: 16 lanes to a cell, GROUPS cells at a time, four times on the way.
+template <int GROUPS>
+__device__ __forceinline__ void move_cells(const PagedCache& kv, int32_t b, int32_t h, const int32_t* to_list,
+                                           const int32_t* from_list, int32_t count, uint32_t tid) {
+    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
+    uint16_t* head = kv.cache + (int64_t)h * kv.head_stride + 8 * (tid & 15u);
+    constexpr int kAtOnce = 4;
+    for (int32_t m0 = 0; m0 < count; m0 += GROUPS * kAtOnce) {
+        int64_t from[kAtOnce], to[kAtOnce];
+        U32x4 cell[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int32_t m = m0 + GROUPS * i + (int32_t)(tid >> 4);
+            from[i] = to[i] = -1;
+            if (m < count) {
+                to[i] = key_offset(kv, table, (uint32_t)to_list[m]);
+                from[i] = key_offset(kv, table, (uint32_t)from_list[m]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if ((from[i] | to[i]) >= 0) cell[i] = load16(head + from[i]);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if ((from[i] | to[i]) >= 0) store16(head + to[i], cell[i]);
+    }
+}
+
 // SLOTS > 0: a thread holds its cells' keys, at most SLOTS (<= 64) of them, 64
 // cells to a wave and slot; 0: they are worked out again in every pass.
-template <int SLOTS>
+// WHOLE (short lists with few moves): the workgroup also does kernel 2's work,
+// from the values it holds and lists in LDS; no second launch.
+template <int SLOTS, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
+    static_assert(!WHOLE || SLOTS == 8, "the values of 8 slots at most are held");
+    __shared__ int32_t hole[WHOLE ? kWholeMoves : 1], source[WHOLE ? kWholeMoves : 1];
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t wave_sum[kWaves], wave_sum2[kWaves];
     __shared__ uint32_t picked[3];  // the digit, how many are wanted among its cells, how many those are
@@ -87,13 +121,23 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
     const int32_t bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
     const int32_t n = cells_of(a, b);
     const Moves mv = moves_of(a, bh);
+    const float* __restrict__ weights = a.weights + (int64_t)b * a.w_bs + (int64_t)h * a.w_hs;
+    const int32_t* __restrict__ positions = a.positions + (int64_t)b * a.p_bs + (int64_t)h * a.p_hs;
+    float* __restrict__ new_w = a.new_weights + (int64_t)bh * a.budget;
+    int32_t* __restrict__ new_p = a.new_positions + (int64_t)bh * a.budget;
+    if (WHOLE && tid == 0 && h == 0) a.new_lens[b] = n < a.budget ? n : a.budget;
     if (n <= a.budget) {
-        if (tid == 0) *mv.count = 0;
+        if constexpr (WHOLE) {
+            for (int32_t j = (int32_t)tid; j < a.budget; j += kThreads) {
+                new_w[j] = j < n ? weights[j] : 0.0f;
+                new_p[j] = j < n ? positions[j] : -1;
+            }
+        } else if (tid == 0) {
+            *mv.count = 0;
+        }
         return;
     }
     const int32_t kept = a.budget;
-    const float* __restrict__ weights = a.weights + (int64_t)b * a.w_bs + (int64_t)h * a.w_hs;
-    const int32_t* __restrict__ positions = a.positions + (int64_t)b * a.p_bs + (int64_t)h * a.p_hs;
 
     // The wave's cells: slots of 64 from wave * per_wave * 64 on.
     const int32_t per_wave = (n + kThreads - 1) / kThreads;
@@ -107,23 +151,30 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
         return key_of(at, positions[in], weights[in]);
     };
     uint32_t held[SLOTS ? SLOTS : 1];
-    if constexpr (SLOTS > 0) {
+    auto load8 = [&](int i0, int32_t (&p)[8], float (&w)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int32_t at = base + (i0 + i) * 64, in = at < n ? at : n - 1;
+            p[i] = positions[in];
+            w[i] = weights[in];
+        }
+    };
+    int32_t p[WHOLE ? 8 : 1];
+    float w[WHOLE ? 8 : 1];
+    if constexpr (WHOLE) {
+        load8(0, p, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) held[i] = i < per_wave ? key_of(base + i * 64, p[i], w[i]) : 0u;
+    } else if constexpr (SLOTS > 0) {
         // eight slots' loads on the way together (a position decides only what its weight counts for)
 #pragma unroll
         for (int i0 = 0; i0 < SLOTS; i0 += 8) {
-            int32_t p[8];
-            float w[8];
-            if (i0 < per_wave) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t at = base + (i0 + i) * 64, in = at < n ? at : n - 1;
-                    p[i] = positions[in];
-                    w[i] = weights[in];
-                }
-            }
+            int32_t p8[8];
+            float w8[8];
+            if (i0 < per_wave) load8(i0, p8, w8);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                held[i0 + i] = i0 + i < per_wave ? key_of(base + (i0 + i) * 64, p[i], w[i]) : 0u;
+                held[i0 + i] = i0 + i < per_wave ? key_of(base + (i0 + i) * 64, p8[i], w8[i]) : 0u;
         }
     }
     // what the waves before this one add up to, of a sum each wave has left in LDS
@@ -224,25 +275,51 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(KvEvictArgs a) {
     __syncthreads();
     uint32_t count = 0;
     uint32_t hole0 = before_this(wave_sum, &count), source0 = before_this(wave_sum2, nullptr);
-    if (tid == 0) {
-        *mv.count = (int32_t)count;
-        mv.starts[a.blocks] = (int32_t)count;
+    if constexpr (!WHOLE) {
+        if (tid == 0) {
+            *mv.count = (int32_t)count;
+            mv.starts[a.blocks] = (int32_t)count;
+        }
+        walk([&](int i, bool is_hole, bool is_source) {
+            const int32_t at = base + i * 64, group = (int32_t)wave * per_wave + i;
+            // 64 cells a slot: every fourth begins a block of places
+            if ((group & 3) == 0 && group * 64 < kept && lane == 0) mv.starts[group >> 2] = (int32_t)hole0;
+            const uint64_t hm = __ballot(is_hole), sm = __ballot(is_source);
+            if (is_hole) mv.holes[hole0 + bits_below(hm, lane)] = at;
+            if (is_source) mv.sources[source0 + bits_below(sm, lane)] = at;
+            hole0 += (uint32_t)__popcll(hm);
+            source0 += (uint32_t)__popcll(sm);
+        });
+    } else {
+        int32_t rank[8];  // of the lane's sources, -1: none
+        walk([&](int i, bool is_hole, bool is_source) {
+            const int32_t at = base + i * 64;
+            const uint64_t hm = __ballot(is_hole), sm = __ballot(is_source);
+            if (is_hole) hole[hole0 + bits_below(hm, lane)] = at;
+            rank[i] = is_source ? (int32_t)(source0 + bits_below(sm, lane)) : -1;
+            if (is_source) source[rank[i]] = at;
+            hole0 += (uint32_t)__popcll(hm);
+            source0 += (uint32_t)__popcll(sm);
+            if (!is_hole && at < kept) {
+                new_w[at] = w[i];
+                new_p[at] = p[i];
+            }
+        });
+        __syncthreads();
+        each([&](int i, uint32_t) {
+            if (rank[i] >= 0) {
+                const int32_t to = hole[rank[i]];
+                new_w[to] = w[i];
+                new_p[to] = p[i];
+            }
+        });
+        move_cells<kThreads / 16>(a.kv, b, h, hole, source, (int32_t)count, tid);
     }
-    walk([&](int i, bool hole, bool source) {
-        const int32_t at = base + i * 64, group = (int32_t)wave * per_wave + i;
-        // 64 cells a slot: every fourth begins a block of places
-        if ((group & 3) == 0 && group * 64 < kept && lane == 0) mv.starts[group >> 2] = (int32_t)hole0;
-        const uint64_t hm = __ballot(hole), sm = __ballot(source);
-        if (hole) mv.holes[hole0 + bits_below(hm, lane)] = at;
-        if (source) mv.sources[source0 + bits_below(sm, lane)] = at;
-        hole0 += (uint32_t)__popcll(hm);
-        source0 += (uint32_t)__popcll(sm);
-    });
 }
 
 // One workgroup: 256 places of a list.
 __global__ __launch_bounds__(kPlaces) void evict_apply_kernel(KvEvictArgs a) {
-    __shared__ int32_t origin[kPlaces], hole[kPlaces];
+    __shared__ int32_t origin[kPlaces], hole[kPlaces], from_cell[kPlaces];
     const int32_t tid = (int32_t)threadIdx.x, j0 = (int32_t)blockIdx.x * kPlaces, j = j0 + tid;
     const int32_t bh = blockIdx.y, b = bh / a.H, h = bh - b * a.H;
     const int32_t n = cells_of(a, b), kept = n < a.budget ? n : a.budget;
@@ -264,7 +341,8 @@ __global__ __launch_bounds__(kPlaces) void evict_apply_kernel(KvEvictArgs a) {
         if (tid < moved) {
             const int32_t to = mv.holes[first + tid];
             hole[tid] = to;
-            origin[to - j0] = mv.sources[first + tid];
+            from_cell[tid] = mv.sources[first + tid];
+            origin[to - j0] = from_cell[tid];
         }
         __syncthreads();
     }
@@ -279,49 +357,36 @@ __global__ __launch_bounds__(kPlaces) void evict_apply_kernel(KvEvictArgs a) {
         a.new_positions[at] = position;
     }
     if (bh - b * a.H == 0 && j == 0) a.new_lens[b] = kept;
-    // 16 lanes to a cell, 16 cells at a time, four times on the way
-    const int32_t* table = a.kv.tables + (int64_t)b * a.kv.table_stride;
-    uint16_t* head = a.kv.cache + (int64_t)h * a.kv.head_stride + 8 * (tid & 15);
-    constexpr int kAtOnce = 4;
-    for (int32_t m0 = 0; m0 < moved; m0 += 16 * kAtOnce) {
-        int64_t from[kAtOnce], to[kAtOnce];
-        U32x4 cell[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int32_t m = m0 + 16 * i + (tid >> 4);
-            from[i] = to[i] = -1;
-            if (m < moved) {
-                const int32_t t = hole[m];
-                to[i] = key_offset(a.kv, table, (uint32_t)t);
-                from[i] = key_offset(a.kv, table, (uint32_t)origin[t - j0]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            if ((from[i] | to[i]) >= 0) cell[i] = load16(head + from[i]);
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            if ((from[i] | to[i]) >= 0) store16(head + to[i], cell[i]);
-    }
+    move_cells<kPlaces / 16>(a.kv, b, h, hole, from_cell, moved, threadIdx.x);
 }
 
 }  // namespace
 
-int64_t kv_evict_workspace(int64_t lists, int64_t max_moves, int64_t blocks) {
-    return max_moves == 0 ? 0 : ((lists + 3) / 4 * 4 + lists * (blocks + 1) + 2 * lists * max_moves) * 4;
+namespace {
+// Up to 8192 cells with up to 512 moves (128 KiB a list) take one launch: 256 lists of 4160 cells 12.6 us
+// against 21 in two.
+bool in_one(int64_t width, int64_t max_moves) { return max_moves <= kWholeMoves && width <= 8 * kThreads; }
+}  // namespace
+
+int64_t kv_evict_workspace(int64_t lists, int64_t width, int64_t max_moves, int64_t blocks) {
+    return max_moves == 0 || in_one(width, max_moves) ? 0 : ((lists + 3) / 4 * 4 + lists * (blocks + 1) + 2 * lists * max_moves) * 4;
 }
 
 int32_t kv_evict_blocks(int64_t budget) { return (int32_t)((budget + kPlaces - 1) / kPlaces); }
 
 int launch_kv_evict(const KvEvictArgs& a, hipStream_t stream) {
     const uint32_t lists = (uint32_t)a.B * a.H;
+    if (a.max_moves > 0 && in_one(a.width, a.max_moves)) {
+        hipLaunchKernelGGL((evict_select_kernel<8, true>), dim3(lists), dim3(kThreads), 0, stream, a);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
     if (a.max_moves > 0) {
         // what a thread can hold, by the longest sequence there may be
-        auto kernel = a.width <= 8 * kThreads    ? evict_select_kernel<8>
-                      : a.width <= 16 * kThreads ? evict_select_kernel<16>
-                      : a.width <= 32 * kThreads ? evict_select_kernel<32>
-                      : a.width <= 64 * kThreads ? evict_select_kernel<64>
-                                                 : evict_select_kernel<0>;
+        auto kernel = a.width <= 8 * kThreads    ? evict_select_kernel<8, false>
+                      : a.width <= 16 * kThreads ? evict_select_kernel<16, false>
+                      : a.width <= 32 * kThreads ? evict_select_kernel<32, false>
+                      : a.width <= 64 * kThreads ? evict_select_kernel<64, false>
+                                                 : evict_select_kernel<0, false>;
         hipLaunchKernelGGL(kernel, dim3(lists), dim3(kThreads), 0, stream, a);
     }
     hipLaunchKernelGGL(evict_apply_kernel, dim3((uint32_t)a.blocks, lists), dim3(kPlaces), 0, stream, a);

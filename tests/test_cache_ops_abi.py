@@ -135,10 +135,11 @@ def test_kv_evict(lib):
                               dict(ends=None), dict(nw=MISALIGNED), dict(np=MISALIGNED), dict(nl=MISALIGNED),
                               dict(lens=MISALIGNED), dict(ends=MISALIGNED)]:
         assert call(**kw, **({"ws": FAKE, "ws_bytes": 1 << 40} if "ws" not in kw else {})) == EINVAL, kw
-    need = lib.nrc_context_kv_evict_workspace_bytes(3, 2, 64, 40)
-    assert need == (8 + 6 * 2 + 2 * 6 * 24) * 4  # counts of 6 heads, starts of a block and its end, two lists of min(40, 64 - 40)
-    assert call() == EINVAL and call(ws=FAKE, ws_bytes=need - 1) == EINVAL
-    assert call(ws=ctypes.c_void_p(0x10008), ws_bytes=need) == EINVAL
+    long = dict(width=20000, wb=40000, wh=20000, pb=40000, ph=20000, budget=5000, tw=2000)
+    need = lib.nrc_context_kv_evict_workspace_bytes(3, 2, 20000, 5000)
+    assert need >= 2 * 6 * 5000 * 4  # two lists of as many cells as can move
+    assert call(**long) == EINVAL and call(**long, ws=FAKE, ws_bytes=need - 1) == EINVAL
+    assert call(**long, ws=ctypes.c_void_p(0x10008), ws_bytes=need) == EINVAL
     assert call(B=0, cache=None, tables=None, lens=None, w=None, p=None, nw=None, np=None, nl=None, ends=None) == 0
     f = lib.nrc_context_kv_evict_workspace_bytes
     assert f(3, 2, 64, 64) == 0 and f(3, 2, 64, 100) == 0 and f(0, 2, 64, 4) == 0
