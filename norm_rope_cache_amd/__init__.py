@@ -59,6 +59,17 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libnrc.so")
 _lib = None
 
+_torch = None  # the module, once a call has needed it (importing the package does not)
+
+
+def _get_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -173,8 +184,7 @@ def _ptr(t):
 def _stream(stream, ref):
     """The HIP stream for a call on ref's GPU: the given torch stream, which
     must belong to that GPU, or that GPU's current stream."""
-    import torch
-
+    torch = _torch or _get_torch()
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(ref.get_device())  # the handle alone, without a stream object
     if stream.device != ref.device:
@@ -186,8 +196,7 @@ def _call(ref, fn, *args):
     """One C-ABI call with ref's GPU as the current device (the library sizes
     its launches and finds its scratch on the current device), raising
     NrcError on a non-zero status."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev = ref.get_device()
     if dev >= 0 and dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -824,8 +833,7 @@ def _empty(shape, dtype, device, stream):
     """An uninitialized tensor of the call's stream: as under
     torch.cuda.stream(stream) when one is given, so that its memory is not one that
     another stream still uses."""
-    import torch
-
+    torch = _torch or _get_torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if stream.device != device:
@@ -834,11 +842,10 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _fits32(**values):
-    """Raise unless every value is an integer of 32 bits (ctypes would cut it)."""
-    for name, v in values.items():
-        if not isinstance(v, int) or not -(1 << 31) <= v < 1 << 31:
-            raise ValueError(f"{name} must be an integer of 32 bits, not {v!r}")
+def _fits32(v, name):
+    """Raise unless v is an integer of 32 bits (ctypes would cut it)."""
+    if not isinstance(v, int) or not -0x80000000 <= v <= 0x7FFFFFFF:
+        raise ValueError(f"{name} must be an integer of 32 bits, not {v!r}")
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
@@ -846,8 +853,7 @@ ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 
 
 def _dtype_code(dtype, name, table=False):
-    import torch
-
+    torch = _torch or _get_torch()
     if dtype == torch.bfloat16:
         return 0
     if dtype == torch.float32:
@@ -871,12 +877,12 @@ def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, orig
                 original_max in between: by their turns, or by their index)
     magnitude   factor of cos and sin
     """
-    import torch
-
+    torch = _torch or _get_torch()
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling is one of {', '.join(ROPE_SCALINGS)}")
     width = rotary_dim if width is None else width
-    _fits32(rotary_dim=rotary_dim, width=width)
+    _fits32(rotary_dim, "rotary_dim")
+    _fits32(width, "width")
     if out is None:
         if count < 0 or width < 0:
             raise ValueError("count and width must not be negative")
@@ -909,8 +915,7 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
     inverse    turn back: the gradient of the rotation
     out        x itself, or a tensor apart from it (default: a new one)
     """
-    import torch
-
+    torch = _torch or _get_torch()
     code = _dtype_code(x.dtype, "x")
     dev = x.get_device()
     if dev < 0:
@@ -945,16 +950,14 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
 
 def _at(t, dev, name):
     """Raise unless t is a tensor on GPU `dev`."""
-    import torch
-
+    torch = _torch or _get_torch()
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         where = "not a tensor" if not isinstance(t, torch.Tensor) else str(t.device)
         raise ValueError(f"{name} must be a tensor on cuda:{dev} ({where})")
 
 
 def _int32(t, name, dev, shape):
-    import torch
-
+    torch = _torch or _get_torch()
     _at(t, dev, name)
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
@@ -963,8 +966,7 @@ def _int32(t, name, dev, shape):
 def _paged_operands(cache, tables):
     """Checks of one layer's cache view and its block tables; the GPU, and the
     C ABI's arguments from `cache` to `B`."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev = cache.get_device()
     if cache.dtype != torch.bfloat16 or dev < 0:
         raise TypeError(f"cache must be a bfloat16 GPU tensor, not {cache.dtype} on {cache.device}")
@@ -987,11 +989,10 @@ def _paged_operands(cache, tables):
 def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap):
     """Checks shared by the attention and its received weights; the GPU, T, Hq, H,
     B, max_ctx and the C ABI's arguments from `q` to `softcap`."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev, paged = _paged_operands(cache, tables)
     bs, H, width, B = paged[2], paged[6], paged[9], paged[10]
-    _fits32(max_nodes=max_nodes)
+    _fits32(max_nodes, "max_nodes")
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q must be bfloat16, not {q.dtype}")
     _at(q, dev, "q")
@@ -1041,8 +1042,7 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
               softcap tanh(score / softcap) when it is not 0
     A row that sees no key gets 0 and -inf. The keys of long contexts are split
     over workgroups, with a workspace from torch's allocator."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
                                                       tree_mask, scale, softcap)
     if out is None:
@@ -1071,8 +1071,7 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
 
 
 def _float_lse(lse, dev, shape):
-    import torch
-
+    torch = _torch or _get_torch()
     _at(lse, dev, "lse")
     if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
@@ -1099,8 +1098,7 @@ def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes,
     width    cells a head (default: weights' or out's, else what the tables hold)
     out      may be weights itself (default: a new tensor)
     Other arguments as context_tree_attention."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
                                                       tree_mask, scale, softcap)
     _float_lse(lse, dev, (T, Hq))
@@ -1138,11 +1136,12 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
     sinks, recent  positions below sinks, and from ends - recent on, come first
     Equal weights: the lower index stays. Kept cells past the new length move
     into the holes before it; weights and positions follow them."""
-    import torch
-
+    torch = _torch or _get_torch()
     dev, paged = _paged_operands(cache, tables)
     H, B = paged[6], paged[10]
-    _fits32(budget=budget, sinks=sinks, recent=recent)
+    _fits32(budget, "budget")
+    _fits32(sinks, "sinks")
+    _fits32(recent, "recent")
     if budget < 1:
         raise ValueError("budget must be at least 1")
     _int32(lens, "lens", dev, (B,))
