@@ -62,6 +62,37 @@ def test_long_heads(nrc, n, budget):
     check(nrc, make([n, n // 3], H=1, seed=n), budget, sinks=4, recent=100)
 
 
+@pytest.mark.parametrize("n,budget,H", [(12000, 6000, 1), (33000, 32000, 33), (33000, 500, 2), (65536, 32768, 1),
+                                        (65537, 1, 2), (140000, 70001, 1)])
+def test_lists_of_one_and_of_many_workgroups(nrc, n, budget, H):
+    """Each way of selecting: the lists shorter than the array too, of a length that leaves parts empty."""
+    c = make([n, n // 2 + 77] if H < 3 else [n], H=H, bs=64, seed=n)
+    check(nrc, c, budget, sinks=4, recent=33)
+    if H < 3:
+        c["lens"][1] = min(budget + 3, n)
+        check(nrc, c, budget)
+
+
+@pytest.mark.parametrize("kind", ["one", "few", "signs", "close", "nan"])
+def test_ties_over_many_workgroups(nrc, kind):
+    n = 40000
+    c = make([n, n - 4097], H=2, bs=64, seed=12)
+    gen = torch.Generator().manual_seed(13)
+    w = c["weights"]
+    if kind == "one":
+        w.fill_(0.25)
+    elif kind == "few":
+        w.copy_(torch.randint(0, 5, w.shape, generator=gen).float())
+    elif kind == "signs":
+        w.copy_(torch.randint(-2, 3, w.shape, generator=gen).float() * 0.0)
+    elif kind == "close":  # differ in the last digit alone, many times each
+        w.copy_((torch.randint(0, 700, w.shape, generator=gen).int() + 0x3F800000).view(torch.float32))
+    else:
+        w[torch.rand(w.shape, generator=gen) < 0.6] = math.nan
+    for budget in (1, 9999, 20480, n - 1):
+        check(nrc, c, budget, sinks=2, recent=5)
+
+
 def test_ties_keep_the_first(nrc):
     c = make([500, 500, 500], seed=2)
     c["weights"][0] = 0.0
