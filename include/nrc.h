@@ -533,8 +533,8 @@ int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int3
  *              q_starts[b] + i set: node i sees node j of its sequence. NULL
  *              (mask_words 0): a chain, node i sees nodes 0 .. i. Every
  *              node sees the whole context.
- *   scale      factor of the scores, > 0. softcap: 0, or scores become
- *              softcap tanh(score / softcap).
+ *   scale      factor of the scores, 2^-40 .. 2^40. softcap: 0, or 2^-10 ..
+ *              2^10: scores become softcap tanh(score / softcap).
  *   out        [T, Hq, 64] bf16, contiguous, 16-byte aligned.
  *   lse        [T, Hq] float: the log of the row's sum of e^score.
  *   workspace  nrc_context_tree_attention_workspace_bytes(...) bytes,
@@ -549,7 +549,7 @@ int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int3
  * no row and not read. T == 0 or B == 0 returns NRC_OK.
  * Errors: NRC_EINVAL (NULL or misaligned operands, shapes, strides, scale,
  * softcap, a small workspace), NRC_ENOTSUP (Hq not a multiple of H, more than
- * 2^31 slots, shapes too large for one call).
+ * 2^31 slots, shapes too large for one call, scale or softcap out of range).
  */
 int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
                                    int32_t Hq, const uint16_t* cache, int64_t num_blocks, int64_t block_size,
@@ -581,7 +581,7 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
  *   lse        [T, Hq] float from nrc_context_tree_attention. Rows with -inf
  *              add nothing.
  *   weights    [B, H, width] float, batch and head strides in elements, or
- *              NULL (0); may be out itself.
+ *              NULL (0); out itself (same strides), or apart from out.
  *   decay      factor of the earlier weights.
  *   out        [B, H, width] float, batch and head strides in elements.
  * FP32 sums in one fixed order. B == 0 or width == 0 returns NRC_OK.
@@ -615,9 +615,9 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
  *   ends       [B] int32: one past the newest token's position.
  *   sinks, recent, budget  >= 0, >= 0, >= 1.
  *   new_weights, new_positions  [B, H, budget] contiguous: of the kept cells in
- *              their new places; 0 and -1 from new_lens[b] on. Apart from
- *              weights and positions, which are not written.
- *   new_lens   [B] int32: min(lens[b], budget).
+ *              their new places; 0 and -1 from new_lens[b] on.
+ *   new_lens   [B] int32: min(lens[b], budget). These three must lie apart from
+ *              weights, positions, lens and ends, which are not written.
  *   workspace  nrc_context_kv_evict_workspace_bytes(B, H, width, budget) bytes,
  *              16-byte aligned; unused (may be NULL) when that is 0. Contents on
  *              return unspecified; calls that share one must not overlap.

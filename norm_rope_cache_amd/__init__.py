@@ -881,6 +881,8 @@ def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, orig
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling is one of {', '.join(ROPE_SCALINGS)}")
     width = rotary_dim if width is None else width
+    if not -1 << 63 <= start < 1 << 63:  # (ctypes would cut it)
+        raise ValueError("start does not fit 64 bits")
     _fits32(rotary_dim, "rotary_dim")
     _fits32(width, "width")
     if out is None:
@@ -926,14 +928,14 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
     T, H, d = shape
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout is 'interleaved' or 'half'")
+    _at(positions, dev, "positions")
+    _at(cos_sin, dev, "cos_sin")
     tcode = _dtype_code(cos_sin.dtype, "cos_sin", table=True)
     table = cos_sin.shape
     if len(table) != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous [max_position, R]")
     if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int64 [T] tensor")
-    _at(positions, dev, "positions")
-    _at(cos_sin, dev, "cos_sin")
     if out is None:
         out = _empty(shape, x.dtype, x.device, stream)
         ost = (H * d, d)
@@ -1016,6 +1018,8 @@ def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tr
             words = 0  # (no row to read)
     if max_ctx is None:
         max_ctx = width * bs
+    elif not 0 <= max_ctx < 1 << 63:  # (ctypes would cut it)
+        raise ValueError("max_ctx must not be negative and fit 64 bits")
     return dev, T, Hq, H, B, max_ctx, (
         q.data_ptr(), st[0] if T > 1 else 0, st[1] if Hq > 1 else 0, T, Hq, *paged, ctx_lens.data_ptr(),
         q_starts.data_ptr(), max_nodes, max_ctx, mask, words, HEAD_DIM ** -0.5 if scale is None else scale, softcap)
@@ -1039,7 +1043,7 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
     tree_mask [T, words] int64: bit j set, the row sees node j of its
               sequence; None: a chain (each node sees those up to itself)
     scale     factor of the scores (1/8); softcap: scores become
-              softcap tanh(score / softcap) when it is not 0
+              softcap tanh(score / softcap) when it is not 0 (2^-10 .. 2^10)
     A row that sees no key gets 0 and -inf. The keys of long contexts are split
     over workgroups, with a workspace from torch's allocator."""
     torch = _torch or _get_torch()
@@ -1096,7 +1100,7 @@ def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes,
     lse      [T, Hq] float32 from context_tree_attention on the same operands
     weights  [B, H, width] float32 (any batch and head strides) or None (0)
     width    cells a head (default: weights' or out's, else what the tables hold)
-    out      may be weights itself (default: a new tensor)
+    out      weights itself, or a tensor apart from it (default: a new one)
     Other arguments as context_tree_attention."""
     torch = _torch or _get_torch()
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
@@ -1135,7 +1139,8 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
     ends       [B] int32: one past the newest token's position
     sinks, recent  positions below sinks, and from ends - recent on, come first
     Equal weights: the lower index stays. Kept cells past the new length move
-    into the holes before it; weights and positions follow them."""
+    into the holes before it; weights and positions follow them, into tensors
+    apart from the given ones."""
     torch = _torch or _get_torch()
     dev, paged = _paged_operands(cache, tables)
     H, B = paged[6], paged[10]

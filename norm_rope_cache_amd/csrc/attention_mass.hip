@@ -10,9 +10,10 @@
 // order and no atomics. Bound by the vector unit: an FMA, an exponential and an
 // FMA a score (16 cycles a wave's 64).
 // e^(s - lse) = 2^(c s + m) with c = scale log2 e and m = -c lse / scale rounded
-// to FP32: what the rounding lost, 2^(lost) = 1 + lost ln 2, is the factor of the
-// last FMA. c's own rounding then meets s - lse alone, which is small near the
-// largest weights, so the weights keep FP32's relative accuracy.
+// to FP32: what the rounding lost, 2^(lost), is the factor of the last FMA. c's own rounding then meets s - lse alone, which is small near the
+// largest weights, so the weights keep FP32's relative accuracy. (Past 2^30 the
+// lost part alone would overflow, while scores that differ at all are 2^7 apart and
+// more: c's power of two takes its place, exact where a score equals lse.)
 // Few keys (less than two workgroups a CU): KT 1, for twice the workgroups.
 #include <type_traits>
 
@@ -151,11 +152,11 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
     }
 
     const float inv_cap = CAP ? tq.scale / tq.softcap : 0.0f, inv_scale = 1.0f / tq.scale;
-    const float c = tq.scale * kLog2E;
+    const float c = tq.scale * kLog2E, c_power = __uint_as_float(__float_as_uint(c) & 0x7F800000u);
     if (any) {
         // Of 32 rows at row0: the factors of their weights, and Q as B operands.
         struct Part {
-            float m, f;
+            float c, m, f;
             int32_t row;
             bool masked, live;
         };
@@ -173,8 +174,17 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
             x.live = x.row < rows && l != -__builtin_inff();  // rows past the end, and rows that saw nothing, add 0
             x.masked = !plain || __any(!x.live);
             const float at = -l * inv_scale;
+            x.c = c;
             x.m = CAP ? -l : at * c;
-            x.f = CAP ? 1.0f : __builtin_fmaf(__builtin_fmaf(at, c, -x.m), kLn2, 1.0f);
+            x.f = 1.0f;
+            if constexpr (!CAP) {
+                if (__builtin_fabsf(x.m) > 0x1p30f) {
+                    x.c = c_power;
+                    x.m = at * c_power;
+                } else {
+                    x.f = exp2_hw(__builtin_fmaf(at, c, -x.m));
+                }
+            }
             const uint8_t* from = &stage[buf][part * 4096];
 #pragma unroll
             for (int j = 0; j < 4; ++j) q[j] = load16(from + (q_place ^ j * 32));
@@ -206,7 +216,7 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
                 for (int j = 0; j < 16; ++j) p[j] = exp2_hw(__builtin_fmaf(tq.softcap, t[j], x.m) * kLog2E);
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) p[j] = exp2_hw(__builtin_fmaf(s[j], c, x.m));
+                for (int j = 0; j < 16; ++j) p[j] = exp2_hw(__builtin_fmaf(s[j], x.c, x.m));
             }
             if (x.masked) {
                 uint32_t seen = 0u;

@@ -216,6 +216,10 @@ int32_t queries(const char* what, const uint16_t* q, int64_t q_rs, int64_t q_hs,
                     max_nodes);
     if (!(scale > 0.0f) || !isfinite(scale)) return fail(NRC_EINVAL, "%s: scale must be positive", what);
     if (!(softcap >= 0.0f) || !isfinite(softcap)) return fail(NRC_EINVAL, "%s: softcap must be 0 or positive", what);
+    // (the factors worked out from them stay finite; a cap's scores are off by 2^-22 of it)
+    if (scale < 0x1p-40f || scale > 0x1p40f) return fail(NRC_ENOTSUP, "%s: scale is outside [2^-40, 2^40]", what);
+    if (softcap != 0.0f && (softcap < 0x1p-10f || softcap > 0x1p10f))
+        return fail(NRC_ENOTSUP, "%s: softcap is neither 0 nor in [2^-10, 2^10]", what);
     if (B > 0 && T > 0 && (!q || !ctx_lens || !q_starts)) return fail(NRC_EINVAL, "%s: NULL q, ctx_lens or q_starts", what);
     if (!aligned(q, 16) || !aligned(ctx_lens, 4) || !aligned(q_starts, 4) || !aligned(mask, 8))
         return fail(NRC_EINVAL, "%s: q must be 16-byte, ctx_lens and q_starts 4-byte, tree_mask 8-byte aligned", what);
@@ -231,6 +235,12 @@ int32_t per_cell(const char* what, const char* name, const void* p, int64_t bs, 
     if (bs < 0 || hs < 0 || bs > kBig || hs > kBig)
         return fail(NRC_EINVAL, "%s: strides of %s must lie in [0, 2^40]", what, name);
     return NRC_OK;
+}
+
+// Do 4-byte elements [p, p + n) and [q, q + m) meet?
+bool meet(const void* p, int64_t n, const void* q, int64_t m) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return n > 0 && m > 0 && a < b + 4 * (uint64_t)m && b < a + 4 * (uint64_t)n;
 }
 
 int32_t max_moves(int64_t width, int32_t budget) {
@@ -314,6 +324,9 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
     if (!heads_in_rows && !rows_in_heads) return fail(NRC_EINVAL, "%s: out's heads overlap", what);
     if (weights && weights == out && (w_batch_stride != out_batch_stride || w_head_stride != out_head_stride))
         return fail(NRC_EINVAL, "%s: weights that are out must have its strides", what);
+    if (weights && weights != out && meet(weights, span(B, H, width, w_batch_stride, w_head_stride), out,
+                                          span(B, H, width, out_batch_stride, out_head_stride)))
+        return fail(NRC_EINVAL, "%s: weights must be out itself or lie apart from it", what);
     a.lse = lse;
     a.weights = weights;
     a.w_bs = w_batch_stride;
@@ -361,6 +374,19 @@ int32_t nrc_context_kv_evict(uint16_t* cache, int64_t num_blocks, int64_t block_
     if (!lens || !ends || !new_lens) return fail(NRC_EINVAL, "%s: NULL lens, ends or new_lens", what);
     if (!aligned(lens, 4) || !aligned(ends, 4) || !aligned(new_lens, 4))
         return fail(NRC_EINVAL, "%s: lens, ends and new_lens must be 4-byte aligned", what);
+    // other workgroups still read these when one writes those
+    const int64_t w_span = cells ? span(B, H, width, w_batch_stride, w_head_stride) : 0;
+    const int64_t p_span = cells ? span(B, H, width, p_batch_stride, p_head_stride) : 0;
+    const int64_t kept = (int64_t)B * H * budget;
+    const struct {
+        const void* p;
+        int64_t n;
+    } written[] = {{new_weights, kept}, {new_positions, kept}, {new_lens, B}},
+      read[] = {{weights, w_span}, {positions, p_span}, {lens, B}, {ends, B}};
+    for (const auto& w : written)
+        for (const auto& r : read)
+            if (meet(w.p, w.n, r.p, r.n))
+                return fail(NRC_EINVAL, "%s: new_weights, new_positions and new_lens must lie apart from the inputs", what);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
     a.B = B;

@@ -34,8 +34,7 @@ struct Nodes {
 };
 __device__ __forceinline__ Nodes nodes_of(const TreeQueries& t, int32_t b) {
     const int32_t lo = t.q_starts[b], hi = t.q_starts[b + 1];
-    Nodes n{lo, hi - lo};
-    if (lo < 0 || hi > t.T || n.count < 0) n.count = 0;
+    Nodes n{lo, lo < 0 || hi > t.T || hi < lo ? 0 : hi - lo};
     if (n.count > t.max_nodes) n.count = t.max_nodes;
     return n;
 }
@@ -69,7 +68,7 @@ __device__ __forceinline__ uint32_t bits_of_scores(uint32_t word, uint32_t half)
 
 // 16 bytes a lane from global memory to LDS at lds + 16 lane, without a register. As inline assembly, so
 // that the kernel alone accounts for it (a wait for all of them before the barrier) instead of a wait before
-// every LDS read. An LDS DMA right after a write of M0 needs a wait state in between.
+// every LDS read (M0 is reserved: the compiler keeps nothing in it). An LDS DMA right after a write of M0 needs a wait state in between.
 __device__ __forceinline__ void to_lds(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds) : "memory");
 }

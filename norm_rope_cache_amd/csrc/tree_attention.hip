@@ -5,26 +5,23 @@
 // A sequence's keys are its context, which every node sees, and its nodes,
 // seen as the tree mask says.
 //
-// One pass over the keys with a running maximum m and sum l per query row.
-// A tile is 32 keys by 16 query rows (rows = nodes x the query heads of one KV
-// head, so every cached byte is fetched once for all of them):
-//   S^T = K Q^T   4 v_mfma_f32_16x16x32_bf16; A is K as it lies (lane: key
-//                 l % 16, 8 elements of d), so K goes from memory to the matrix
-//                 core without LDS. A lane then holds, for query row l % 16, the
-//                 keys 4 (l / 16) + r of both halves of the tile.
-//   O^T += V^T P^T  4 more. P^T's lane needs 8 keys of query row l % 16: the
-//                 ones it holds, when slot 8 g + 4 t + r of the sum stands for
-//                 key 16 t + 4 g + r. V's lane loads those same 8 keys, 4 elements of
-//                 d each (8 bytes), and 16 byte permutes turn them into the 4
-//                 operands (operand c: d = 4 (l % 16) + c).
-// The statistics of a row and its column of O^T thus live in the lanes that
-// hold its scores. P is rounded to bf16 for the second product (relative 2^-9
-// each, independent between keys, so the error of the sum stays near the bf16
-// output's own rounding); m, l, O and the scores are FP32.
+// One pass over the keys with a running reference m (near the row's maximum)
+// and sum l per query row; rows = nodes x the query heads of one KV head, so
+// every cached byte is fetched once for all of them. S^T = K Q^T takes K as it
+// lies as the A operand, and O^T += V^T P^T takes P^T from the lanes that hold the
+// scores: a row's statistics and its column of O^T live in the lanes with its
+// scores, and P never leaves registers. P is rounded to bf16 for the second
+// product (relative 2^-8 at most each, independent between keys, so the error
+// of the sum stays near the bf16 output's own rounding); m, l, O and the scores
+// are FP32. m moves only when a lane's weights of a tile sum to more than 2^8 (the
+// lanes vote): between, p, l and O grow by up to that factor, which FP32 and bf16
+// hold at full precision, and no lane waits for another's maximum.
 //
-// m moves only when a score passes it by 2^8 (the lanes vote): between, p and
-// l and O grow by up to that factor, which FP32 and bf16 hold at full precision,
-// and no lane waits for another lane's maximum.
+// Up to 64 rows (few_rows_kernel) the cache's bytes bound it: K and V go from
+// memory to the matrix core through registers, each wave its own tiles of 32
+// keys. More rows (many_rows_kernel) are bound by the vector unit (the
+// exponentials and what feeds the matrix instructions): keys are staged in LDS
+// and shared by a workgroup's waves, 32 or 64 rows each.
 #include "cache_ops.h"
 #include "kernels.h"
 #include "paged.h"
@@ -72,8 +69,8 @@ template <int R>
 struct Rows {
     U32x4 q[R][2];   // S's B operand: row l % 16, halves of d
     f32x4 o[R][4];   // O^T: row l % 16, d = 4 (4 (l / 16) + r) + c at [c][r]
-    float limit[R];  // the running maximum and the slack, raw scores (-inf: no key yet)
-    float base[R];   // what is subtracted from the scores in base 2: the maximum's, or 0 without one
+    float base[R];   // subtracted from the scores in base 2; kNone: no key yet
+    float c[R];      // raw scores to base 2, see rebase
     float l[R];      // this lane's share of the sum
 };
 
@@ -83,21 +80,41 @@ __device__ __forceinline__ float in_base2(float raw, float c, float capped) {
     return raw * c;
 }
 
-// Moves row rq's maximum up to the lanes' largest score `top`, and l and O with it.
-// (slack: 8 in base 2 as raw scores; the cap only brings scores nearer to each other.)
+// Weights are taken against base as it stands; where a lane's sum passes kMost (or is NaN: the lanes vote), base moves
+// to the row's largest score of the tile, and they are taken again. Under kNone any score's weight is +inf, that of
+// -inf 0, so a row's first key moves it.
+constexpr float kNone = -3.402823466e38f, kMost = 256.0f;
+
+// Row's base moved up to its largest score `top`, if that is above it; what l and O shrink by.
+// Past 2^30 the rounding of top c alone would overflow the exponential (2^6 and more), while scores that differ at all
+// are 2^7 apart and more: there c's power of two takes its place, with which the largest score meets base exactly.
+template <bool CAP>
+__device__ __forceinline__ float rebase(float top, float& base, float& c, float whole_c, float capped) {
+    const float at = CAP ? in_base2<CAP>(top, whole_c, capped) : top * c;
+    if (top == -__builtin_inff() || !(at > base)) return 1.0f;
+    const float shrink = exp2_hw(base - at);
+    if constexpr (!CAP) {
+        const float power = __uint_as_float(__float_as_uint(whole_c) & 0x7F800000u);
+        c = __builtin_fabsf(top * whole_c) > 0x1p30f ? power : whole_c;
+    }
+    base = CAP ? at : top * c;
+    return shrink;
+}
+
+// Of a row, for the join and lse: its base in base 2, -inf without a key.
+template <bool CAP>
+__device__ __forceinline__ float base_of(float base, float c, float whole_c) {
+    return base == kNone ? -__builtin_inff() : CAP || c == whole_c ? base : base * (whole_c / c);
+}
+
 template <int R, bool CAP>
-__device__ __forceinline__ void raise(Rows<R>& w, int rq, float top, float c, float capped, float slack) {
-    const float limit = __builtin_fmaxf(w.limit[rq], group_max(top) + slack);
-    const float base = limit == -__builtin_inff() ? 0.0f : in_base2<CAP>(limit - slack, c, capped);
-    // -inf before: no key yet, l and O are 0
-    const float shrink = w.limit[rq] == -__builtin_inff() ? 1.0f : exp2_hw(w.base[rq] - base);
+__device__ __forceinline__ void raise(Rows<R>& w, int rq, float top, float c, float capped) {
+    const float shrink = rebase<CAP>(group_max(top), w.base[rq], w.c[rq], c, capped);
     w.l[rq] *= shrink;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) w.o[rq][i][r] *= shrink;
-    w.limit[rq] = limit;
-    w.base[rq] = base;
 }
 
 __device__ __forceinline__ float max8(const f32x4 (&s)[2]) {
@@ -126,7 +143,7 @@ __device__ __forceinline__ float open_weights(const f32x4 (&s)[2], float base, f
 // latencies and the exponentials of one hide behind the other's, and their
 // scores leave room in the registers.
 template <int R, bool CAP>
-__device__ __forceinline__ void open_tile(Rows<R>& w, const Keys& kv, float c, float capped, float slack) {
+__device__ __forceinline__ void open_tile(Rows<R>& w, const Keys& kv, float c, float capped) {
     constexpr int P = R < 2 ? 1 : 2;
 #pragma unroll
     for (int r0 = 0; r0 < R; r0 += P) {
@@ -139,20 +156,23 @@ __device__ __forceinline__ void open_tile(Rows<R>& w, const Keys& kv, float c, f
         for (int j = 0; j < P; ++j)
 #pragma unroll
             for (int t = 0; t < 2; ++t) s[j][t] = mfma16(kv.k[t][1], w.q[r0 + j][1], s[j][t]);
-        float top[P];
+        U32x4 pb[P];
+        float sum[P];
         bool up = false;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            top[j] = max8(s[j]);
-            up = up || top[j] > w.limit[r0 + j];
+            sum[j] = open_weights<CAP>(s[j], w.base[r0 + j], CAP ? c : w.c[r0 + j], capped, pb[j]);
+            up = up || !(sum[j] <= kMost);
         }
         if (__any(up)) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) raise<R, CAP>(w, r0 + j, top[j], c, capped, slack);
+            for (int j = 0; j < P; ++j) {
+                raise<R, CAP>(w, r0 + j, max8(s[j]), c, capped);
+                sum[j] = open_weights<CAP>(s[j], w.base[r0 + j], CAP ? c : w.c[r0 + j], capped, pb[j]);
+            }
         }
-        U32x4 pb[P];
 #pragma unroll
-        for (int j = 0; j < P; ++j) w.l[r0 + j] += open_weights<CAP>(s[j], w.base[r0 + j], c, capped, pb[j]);
+        for (int j = 0; j < P; ++j) w.l[r0 + j] += sum[j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const U32x4 va = v_operand(kv, i);
@@ -166,7 +186,7 @@ __device__ __forceinline__ void open_tile(Rows<R>& w, const Keys& kv, float c, f
 // exponent of tanh (2 scale log2 e / cap), capped then being cap log2 e.
 // seen[rq]: this lane's rows' bits of the tile's keys.
 template <int R, bool CAP>
-__device__ __forceinline__ void masked_tile(Rows<R>& w, const Keys& kv, float c, float capped, float slack,
+__device__ __forceinline__ void masked_tile(Rows<R>& w, const Keys& kv, float c, float capped,
                                             const uint32_t (&seen)[R], uint32_t lane) {
     const uint32_t g = lane >> 4;
     U32x4 va[4];
@@ -185,25 +205,32 @@ __device__ __forceinline__ void masked_tile(Rows<R>& w, const Keys& kv, float c,
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) s[t][r] = -__builtin_inff();
-        const float top = max8(s);
-        if (__any(top > w.limit[rq])) raise<R, CAP>(w, rq, top, c, capped, slack);
-        float p[8];
+        U32x4 pb;
+        auto weights = [&]() {
+            float p[8];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float e;
-                if constexpr (CAP) {
-                    e = __builtin_fmaf(rcp_hw(exp2_hw(s[t][r] * c) + 1.0f), -2.0f * capped, capped - w.base[rq]);
-                    if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) e = -__builtin_inff();
-                } else {
-                    e = __builtin_fmaf(s[t][r], c, -w.base[rq]);
+                for (int r = 0; r < 4; ++r) {
+                    float e;
+                    if constexpr (CAP) {
+                        e = __builtin_fmaf(rcp_hw(exp2_hw(s[t][r] * c) + 1.0f), -2.0f * capped, capped - w.base[rq]);
+                        if (!(seen[rq] >> (16 * t + 4 * g + r) & 1u)) e = -__builtin_inff();
+                    } else {
+                        e = __builtin_fmaf(s[t][r], w.c[rq], -w.base[rq]);
+                    }
+                    p[4 * t + r] = exp2_hw(e);
                 }
-                p[4 * t + r] = exp2_hw(e);
-            }
-        w.l[rq] += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-        const U32x4 pb{pack_bf16_pair_hw(p[0], p[1]), pack_bf16_pair_hw(p[2], p[3]), pack_bf16_pair_hw(p[4], p[5]),
+            pb = U32x4{pack_bf16_pair_hw(p[0], p[1]), pack_bf16_pair_hw(p[2], p[3]), pack_bf16_pair_hw(p[4], p[5]),
                        pack_bf16_pair_hw(p[6], p[7])};
+            return ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+        };
+        float sum = weights();
+        if (__any(!(sum <= kMost))) {
+            raise<R, CAP>(w, rq, max8(s), c, capped);
+            sum = weights();
+        }
+        w.l[rq] += sum;
 #pragma unroll
         for (int i = 0; i < 4; ++i) w.o[rq][i] = mfma16(va[i], pb, w.o[rq][i]);
     }
@@ -328,7 +355,7 @@ __device__ __forceinline__ int32_t last_tile(const TreeQueries& tq, const Span& 
 // The lane's rows row0 + 16 rq + l % 16: their queries, and their nodes (-1 past the last row).
 template <int R>
 __device__ __forceinline__ void load_rows(Rows<R>& w, int32_t (&node)[R], const TreeQueries& tq, const Span& s, int32_t h,
-                                          int32_t row0, uint32_t lane) {
+                                          int32_t row0, uint32_t lane, float c) {
 #pragma unroll
     for (int rq = 0; rq < R; ++rq) {
         const int32_t r = row0 + 16 * rq + (int32_t)(lane & 15u);
@@ -343,8 +370,8 @@ __device__ __forceinline__ void load_rows(Rows<R>& w, int32_t (&node)[R], const 
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) w.o[rq][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        w.limit[rq] = -__builtin_inff();
-        w.base[rq] = 0.0f;
+        w.base[rq] = kNone;
+        w.c[rq] = c;
         w.l[rq] = 0.0f;
     }
 }
@@ -363,12 +390,11 @@ __device__ __forceinline__ void seen_rows(uint32_t (&seen)[R], const int32_t (&n
 }
 
 struct Factors {
-    float c, capped, slack;
+    float c, capped;
 };
 template <bool CAP>
 __device__ __forceinline__ Factors factors(const TreeQueries& tq) {
-    return Factors{CAP ? 2.0f * kLog2E * tq.scale / tq.softcap : kLog2E * tq.scale, CAP ? tq.softcap * kLog2E : 0.0f,
-                   8.0f / (kLog2E * tq.scale)};
+    return Factors{CAP ? 2.0f * kLog2E * tq.scale / tq.softcap : kLog2E * tq.scale, CAP ? tq.softcap * kLog2E : 0.0f};
 }
 
 // Where a row's results go: out and lse of row `at`, or, of one of several splits, its partial sums at
@@ -400,9 +426,18 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
 
 // Few rows (up to 16 R, R <= 4): one workgroup per (sequence, KV head,
 // split); its WAVES waves hold the same rows and take the split's tiles in turn, and
-// join their sums in LDS. Bound by the cache's bytes: a wave keeps the next
-// tile's K and V on the way while it works on one, the tile after that's block
-// numbers too.
+// join their sums in LDS. A tile is 32 keys by 16 R rows:
+//   S^T = K Q^T   4 v_mfma_f32_16x16x32_bf16 a query tile; K's lane: key l % 16, 8
+//                 elements of d, straight from memory. A lane then holds, for
+//                 query row l % 16, the keys 4 (l / 16) + r of both halves.
+//   O^T += V^T P^T  4 more. P^T's lane needs 8 keys of query row l % 16: the
+//                 ones it holds, when slot 8 g + 4 t + r of the sum stands for
+//                 key 16 t + 4 g + r. V's lane loads those same 8 keys, 4 elements of
+//                 d each (8 bytes), and 16 byte permutes turn them into the 4
+//                 operands (operand c: d = 4 (l % 16) + c).
+// Bound by the cache's bytes: a wave keeps the next tile's K and V on the way
+// while it works on one, the tile after that's block numbers too (64 sequences of
+// up to 8192 keys, 8 heads: 685 MB in 139 us, 4.9 TB/s, a copy reaches 5.2).
 // PAGE16 (block_size a multiple of 16, page rows near each other): the 16
 // keys of half a tile lie in one page, so a tile's two bases are scalars.
 template <int R, int WAVES, bool CAP, bool PAGE16>
@@ -465,13 +500,13 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
         int64_t off = offsets(t), off1 = offsets(t + WAVES);
         bool cur_whole = whole(t, off);
         if (cur_whole) fetch(keys[0], off);
-        load_rows<R>(w, node, tq, s, h, 0, lane);
+        load_rows<R>(w, node, tq, s, h, 0, lane, f.c);
         auto step = [&](Keys& cur, Keys& next) {
             const bool next_whole = whole(t + WAVES, off1);
             if (next_whole) fetch(next, off1);
             off1 = offsets(t + 2 * WAVES);
             if (cur_whole)
-                open_tile<R, CAP>(w, cur, f.c, f.capped, f.slack);
+                open_tile<R, CAP>(w, cur, f.c, f.capped);
             else
                 left_out = true;
             cur_whole = next_whole;
@@ -492,7 +527,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
         seen_rows<R>(seen, node, (uint32_t)__ballot(off >= 0), tq, s, t - s.ctx_tiles);
         const bool odd = t >= s.ctx_tiles && any_odd(keys);
         if (odd) drop_odd(keys);
-        masked_tile<R, CAP>(w, keys, f.c, f.capped, f.slack, seen, lane);
+        masked_tile<R, CAP>(w, keys, f.c, f.capped, seen, lane);
         if (odd) {
             load_keys(keys, head, off, lane);
             add_odd<R>(w, keys, seen, lane);
@@ -508,7 +543,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
         const float l = group_sum(w.l[rq]);
         const uint32_t row = wave * 16 * R + 16 * rq + n16;
         if (g == 0) {
-            sm[row] = w.limit[rq] == -__builtin_inff() ? -__builtin_inff() : w.base[rq];
+            sm[row] = base_of<CAP>(w.base[rq], w.c[rq], f.c);
             sl[row] = l;
         }
 #pragma unroll
@@ -553,15 +588,13 @@ template <int R>
 struct Rows32 {
     U32x4 q[R][4];   // row l % 32, d = 16 i + 8 (l / 32) ...
     f32x16 o[R][2];  // O^T: row l % 32, d = 32 c + 8 (i / 4) + 4 (l / 32) + i % 4 at [c][i]
-    float base[R];   // subtracted from the scores in base 2
-    float most[R];   // weights that sum to more than this move base; -1 while the row has met no key
-    float l[R];
+    float base[R], c[R], l[R];  // as Rows'
+
 };
 struct Keys32 {
     U32x4 k[4];     // key l % 32, d as q's
     U32x4 v[2][2];  // [c][ks]: d = 32 c + l % 32, the keys of slots 8 (l / 32) .. + 7 of step ks
 };
-constexpr float kMost = 256.0f;
 
 template <int R, bool CAP>
 __device__ __forceinline__ void raise32(Rows32<R>& w, int rt, const f32x16& s, float c, float capped) {
@@ -569,18 +602,12 @@ __device__ __forceinline__ void raise32(Rows32<R>& w, int rt, const f32x16& s, f
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = __builtin_fmaxf(top, s[i]);
     top = __builtin_fmaxf(top, lane_xor<32>(top));
-    if (top == -__builtin_inff()) return;  // (for these lanes)
-    const bool none = w.most[rt] < 0.0f;
-    const float at = in_base2<CAP>(top, c, capped);
-    const float base = none ? at : __builtin_fmaxf(w.base[rt], at);
-    const float shrink = none ? 1.0f : exp2_hw(w.base[rt] - base);
+    const float shrink = rebase<CAP>(top, w.base[rt], w.c[rt], c, capped);
     w.l[rt] *= shrink;
 #pragma unroll
     for (int d = 0; d < 2; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) w.o[rt][d][i] *= shrink;
-    w.base[rt] = base;
-    w.most[rt] = kMost;
 }
 
 // The weights of 16 scores, as the second product's operands, and their sum.
@@ -612,21 +639,20 @@ __device__ __forceinline__ void scores32(f32x16& s, const Rows32<R>& w, int rt, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = mfma32(kv.k[i], w.q[rt][i], s);
 }
-// Weights of row tile rt's scores, its sum, and V by them. Weights are taken against base as it stands;
-// where their sum passes `most` (rare), base moves up and they are taken again.
+// Weights of row tile rt's scores, its sum, and V by them.
 template <int R, bool CAP, bool MASKED>
 __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Keys32& kv, const Factors& f,
                                       uint32_t seen) {
     U32x4 pb[2];
-    float sum = weights32<CAP, MASKED>(s, w.base[rt], f.c, f.capped, seen, pb);
-    if (__any(!(sum <= w.most[rt]))) {
+    float sum = weights32<CAP, MASKED>(s, w.base[rt], CAP ? f.c : w.c[rt], f.capped, seen, pb);
+    if (__any(!(sum <= kMost))) {
         if constexpr (MASKED) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (!(seen >> i & 1u)) s[i] = -__builtin_inff();
         }
         raise32<R, CAP>(w, rt, s, f.c, f.capped);
-        sum = weights32<CAP, MASKED>(s, w.base[rt], f.c, f.capped, seen, pb);
+        sum = weights32<CAP, MASKED>(s, w.base[rt], CAP ? f.c : w.c[rt], f.capped, seen, pb);
     }
     w.l[rt] += sum;
 #pragma unroll
@@ -640,7 +666,9 @@ __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Key
 // one tile the next one comes in (global_load_lds, no registers), and one barrier
 // a tile. Bound by what the vector unit issues: a matrix instruction takes it 8
 // cycles and keeps the matrix core 32, an exponential takes 8, other operations
-// 4; of 32 keys and 32 rows that is 8, 16 and about 50.
+// 4; of 32 keys and 32 rows that is 8, 16 and about 50. Measured: 600 TFLOP/s of
+// a large matrix product's 1212 (32768 keys, 512 rows a head), 490 with a softcap
+// (an exponential and a reciprocal more a score).
 // LDS: K rows of 128 bytes whose 16-byte chunk c lies at c ^ (key & 7), so
 // that 8 lanes reading one chunk of 8 keys meet all banks; V rows with c at
 // c ^ 4 in every second pair of keys, so that the 4 keys and 64 bytes that half a wave
@@ -853,8 +881,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
             for (int i = 0; i < 4; ++i) w.q[rt][i] = load16(q + 16 * i);
         }
         w.o[rt][0] = w.o[rt][1] = f32x16{0.f};
-        w.base[rt] = w.l[rt] = 0.0f;
-        w.most[rt] = -1.0f;
+        w.base[rt] = kNone;
+        w.c[rt] = f.c;
+        w.l[rt] = 0.0f;
     }
 
     // The tiles that every row sees whole. One row tile's scores are on the way in the matrix cores while the
@@ -1028,7 +1057,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
 #pragma unroll
     for (int rt = 0; rt < R; ++rt) {
         const float l = w.l[rt] + lane_xor<32>(w.l[rt]);
-        const float top = w.most[rt] < 0.0f ? -__builtin_inff() : w.base[rt];
+        const float top = base_of<CAP>(w.base[rt], w.c[rt], f.c);
         if (node[rt] < 0) continue;
         const int32_t r = row0 + 32 * rt + (int32_t)n32;
         const int64_t at = splits > 1 ? part0 + r
@@ -1043,7 +1072,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
 }
 
 // The splits of a row joined: 16 lanes a row, 4 elements of d a lane, eight splits' loads on the way at a
-// time.
+// time. Bound by the latency of one row's loads.
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq, AttentionPlan plan,
                                                                   const float* __restrict__ part,
                                                                   const int32_t* __restrict__ shares,

@@ -70,7 +70,8 @@ PAGED_NOTSUP = [dict(nb=1 << 27), dict(bst=4), dict(pst=132), dict(hst=1), dict(
 PAGED_EINVAL = [dict(H=0), dict(B=-1), dict(nb=0), dict(bs=0), dict(bst=-8), dict(pst=-8), dict(hst=1 << 41), dict(tw=0),
                 dict(tw=1 << 40), dict(ts=-1), dict(cache=None), dict(tables=None), dict(cache=ctypes.c_void_p(0x10008)),
                 dict(tables=MISALIGNED)]
-QUERY_NOTSUP = [dict(Hq=7), dict(T=1 << 31), dict(B=60000, nodes=60000)]
+QUERY_NOTSUP = [dict(Hq=7), dict(T=1 << 31), dict(B=60000, nodes=60000), dict(scale=1e-13), dict(scale=2e12),
+                dict(cap=9e-4), dict(cap=1025.0)]
 QUERY_EINVAL = [dict(T=-1), dict(Hq=0), dict(nodes=0), dict(nodes=65536), dict(max_ctx=-1), dict(max_ctx=1 << 31), dict(qr=4),
                 dict(qh=-8), dict(words=1), dict(mask=FAKE), dict(mask=FAKE, words=-1), dict(mask=FAKE, words=1, nodes=65),
                 dict(mask=MISALIGNED, words=1), dict(mask=FAKE, words=1025), dict(scale=0.0), dict(scale=-1.0),
@@ -116,7 +117,8 @@ def test_attention_mass(lib):
     for kw in PAGED_EINVAL + QUERY_EINVAL + [dict(lse=None), dict(out=None), dict(w=MISALIGNED), dict(out=MISALIGNED),
                                              dict(lse=MISALIGNED), dict(wb=-1), dict(oh=-1), dict(width=-1),
                                              dict(width=1 << 31), dict(decay=math.inf), dict(oh=63), dict(ob=100),
-                                             dict(w=FAR, wh=101)]:
+                                             dict(w=FAR, wh=101), dict(w=ctypes.c_void_p(FAR.value + 4)),
+                                             dict(w=ctypes.c_void_p(FAR.value + 4 * 563))]:
         assert call(**kw) == EINVAL, kw
         assert b"context_attention_mass" in lib.nrc_last_error()
     assert call(B=0, cache=None, tables=None, q=None, ctx=None, starts=None, lse=None, out=None) == 0
@@ -135,6 +137,14 @@ def test_kv_evict(lib):
                               dict(ends=None), dict(nw=MISALIGNED), dict(np=MISALIGNED), dict(nl=MISALIGNED),
                               dict(lens=MISALIGNED), dict(ends=MISALIGNED)]:
         assert call(**kw, **({"ws": FAKE, "ws_bytes": 1 << 40} if "ws" not in kw else {})) == EINVAL, kw
+    # what is written lies apart from what is read
+    at = [ctypes.c_void_p(0x100000 * i) for i in range(1, 8)]
+    apart = dict(lens=at[0], w=at[1], p=at[2], ends=at[3], nw=at[4], np=at[5], nl=at[6])
+    for out, size in (("nw", 3 * 2 * 40), ("np", 3 * 2 * 40), ("nl", 3)):
+        for name, cells in (("w", 2 * 128 + 64 + 64), ("p", 2 * 128 + 64 + 64), ("lens", 3), ("ends", 3)):
+            for place in (apart[name].value + 4 * (cells - 1), apart[name].value, apart[name].value - 4 * (size - 1)):
+                kw = dict(apart, **{out: ctypes.c_void_p(place)})
+                assert call(**kw) == EINVAL and b"apart" in lib.nrc_last_error(), (out, name, hex(place))
     long = dict(width=20000, wb=40000, wh=20000, pb=40000, ph=20000, budget=5000, tw=2000)
     need = lib.nrc_context_kv_evict_workspace_bytes(3, 2, 20000, 5000)
     assert need >= 2 * 6 * 5000 * 4  # two lists of as many cells as can move

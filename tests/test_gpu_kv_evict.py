@@ -210,7 +210,9 @@ def test_refusals(nrc):
            dict(positions=d["positions"].long()), dict(positions=d["positions"][:, :, :50]), dict(lens=d["lens"][:1]),
            dict(ends=d["ends"].long()), dict(cache=d["cache"].float()), dict(cache=d["cache"][..., :120]),
            dict(tables=d["tables"].long()), dict(new_weights=torch.empty(2, 2, 39, device="cuda")),
-           dict(new_positions=torch.empty(2, 2, 40, device="cuda")), dict(new_lens=torch.empty(2, device="cuda"))]
+           dict(new_positions=torch.empty(2, 2, 40, device="cuda")), dict(new_lens=torch.empty(2, device="cuda")),
+           dict(new_lens=d["lens"]), dict(new_lens=d["ends"]),
+           dict(new_weights=d["weights"].view(-1)[:160].view(2, 2, 40))]
     for kw in bad:
         with pytest.raises((ValueError, TypeError, nrc.NrcError)):
             nrc.context_kv_evict(**{**ok, **kw})

@@ -213,7 +213,7 @@ def test_refusals(nrc):
     pos = torch.zeros(4, dtype=torch.int64, device="cuda")
     cs = nrc.rope_table(10, 64)
     bad = [dict(x=x.double()), dict(x=x.cpu()), dict(x=x[0]), dict(x=x.transpose(1, 2)), dict(positions=pos.int()),
-           dict(positions=pos[:3]), dict(positions=pos.cpu()), dict(cos_sin=cs.half()), dict(cos_sin=cs.cpu()),
+           dict(positions=pos[:3]), dict(positions=pos.cpu()), dict(positions=None), dict(cos_sin=None), dict(cos_sin=cs.half()), dict(cos_sin=cs.cpu()),
            dict(cos_sin=cs[:, ::2]), dict(cos_sin=nrc.rope_table(10, 128)), dict(layout="pairs"),
            dict(out=torch.zeros(4, 2, 64, device="cuda")), dict(out=x[:3])]
     for kw in bad:
@@ -227,7 +227,7 @@ def test_refusals(nrc):
     for kw in (dict(count=-1), dict(rotary_dim=3), dict(rotary_dim=0), dict(rotary_dim=258), dict(width=62), dict(width=65),
                dict(base=1.0), dict(base=math.nan), dict(scaling="other"), dict(scaling="linear", factor=0.0),
                dict(scaling="ramp", factor=2.0, original_max=0), dict(scaling="bands", factor=2.0, original_max=9, low=2.0, high=1.0),
-               dict(magnitude=math.inf), dict(start=-1), dict(start=2 ** 28), dict(dtype=torch.float16), dict(device="cpu"),
+               dict(magnitude=math.inf), dict(start=-1), dict(start=2 ** 28), dict(start=2 ** 64), dict(dtype=torch.float16), dict(device="cpu"),
                dict(out=torch.zeros(4, 64, device="cuda"))):
         with pytest.raises((ValueError, TypeError, RuntimeError, nrc.NrcError)):
             nrc.rope_table(**{**dict(count=10, rotary_dim=64), **kw})

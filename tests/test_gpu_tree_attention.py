@@ -91,6 +91,37 @@ def test_scale(nrc):
     check(nrc, ref.Batch([90, 33], [6, 4], seed=4), scale=0.031)
 
 
+@pytest.mark.parametrize("scale,cap", [(2.0 ** -40, 0.0), (2.0 ** 40, 0.0), (0.125, 2.0 ** -10), (0.125, 2.0 ** 10),
+                                       (2.0 ** -40, 2.0 ** 10), (2.0 ** 40, 2.0 ** -10), (2.0 ** 40, 2.0 ** 10)])
+@pytest.mark.parametrize("nodes", [5, 40])
+def test_ends_of_the_scales(nrc, scale, cap, nodes):
+    # (scores of 2^40 and FP32's lse of them are 2^17 apart at the nearest, or equal: no weight to compare)
+    check(nrc, ref.Batch([90, 33], [nodes, 6], seed=38), scale=scale, cap=cap, mass=cap > 0 or scale < 1)
+
+
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e10, 1e15])
+@pytest.mark.parametrize("nodes", [5, 40])
+def test_scores_whose_spacing_passes_the_exponent(nrc, size, nodes):
+    """Scores of up to 1e30, where FP32's neighbours differ by more than an exponential holds: one key takes a row, or
+    equal ones share it; the sums are exact (one element of q and k each), so the same key as in 64 bits."""
+    bt = ref.Batch([90, 33], [nodes, 6], seed=39, tree=False)
+    q, k = bt.q[..., :1].clone(), bt.cache[..., :1].clone()
+    bt.q.zero_()
+    bt.cache[..., :64] = 0
+    bt.q[..., :1], bt.cache[..., :1] = q * size, k * size
+    out, lse, args, d = run(nrc, bt)
+    o, l, _, _ = ref.attention(bt)
+    big = (l.abs() > 2.0 ** 32)[..., None]
+    # beyond 2^32 the next score is e^-250 away at least: out is V itself, or the mean of equal keys' V (bf16 weights
+    # that are all 1, an FP32 sum, a reciprocal and the product with it, one rounding)
+    off = torch.where(big, (out.double().cpu() - o).abs() - o.abs() * 2.0 ** -8 - 2.0 ** -18 * 6, -1.0)
+    assert bool((off <= 0).all()) and bool(torch.isfinite(out).all())
+    # lse: base (two roundings), its factors (three) and 24 of log2's own steps
+    assert bool(((lse.double().cpu() - l).abs() <= l.abs() * 6 * 2.0 ** -24 + 1e-3 + 64 * 2.0 ** -23 * l.abs()).all())
+    m = nrc.context_attention_mass(*args, lse, d["max_nodes"])
+    assert bool((m >= 0).all())
+
+
 def test_ragged_batch_with_empty_sequences(nrc):
     check(nrc, ref.Batch([0, 40, 7, 0, 200], [0, 3, 0, 5, 1], seed=5))
 
@@ -370,7 +401,8 @@ def test_refusals(nrc):
            dict(ctx_lens=d["ctx_lens"][:1]), dict(q_starts=d["q_starts"][:2]), dict(ctx_lens=d["ctx_lens"].long()),
            dict(max_nodes=0), dict(max_nodes=65), dict(max_nodes=2 ** 32 + 5), dict(max_nodes=70000),
            dict(tree_mask=d["tree_mask"][:3]), dict(tree_mask=d["tree_mask"].int()), dict(scale=0.0), dict(scale=-1.0),
-           dict(scale=math.nan), dict(softcap=-1.0), dict(softcap=math.inf), dict(max_ctx=-1), dict(max_ctx=2 ** 31),
+           dict(scale=math.nan), dict(scale=1e-13), dict(softcap=-1.0), dict(softcap=math.inf), dict(softcap=2000.0),
+           dict(max_ctx=2 ** 64 + 7), dict(max_ctx=-1), dict(max_ctx=2 ** 31),
            dict(out=torch.empty(8, 8, 64, device="cuda")), dict(lse=torch.empty(8, 7, device="cuda")),
            dict(stream=None, out=torch.empty(8, 8, 64, dtype=torch.bfloat16))]
     for kw in bad:
