@@ -256,7 +256,11 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
                                                    int64_t max_ctx) {
     if (int32_t rc = query_sizes("context_tree_attention", B, T, Hq, H, max_nodes, max_ctx)) return rc;
     if (B == 0 || T == 0) return 0;
-    return nrc::tree_attention_workspace(nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, num_cus()), T, Hq, B);
+    int64_t bytes[2];  // without and with a softcap
+    for (int capped = 0; capped < 2; ++capped)
+        bytes[capped] = nrc::tree_attention_workspace(
+            nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, capped, num_cus()), T, Hq, B);
+    return bytes[0] > bytes[1] ? bytes[0] : bytes[1];
 }
 
 int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
@@ -279,7 +283,7 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
     if (!work) return NRC_OK;
     if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
-    a.plan = nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, num_cus());
+    a.plan = nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, softcap > 0.0f, num_cus());
     const int64_t bytes = nrc::tree_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);

@@ -85,7 +85,8 @@ struct AttentionPlan {
     int32_t q_tiles, waves, row_blocks, splits, split_tiles, groups;
 };
 
-AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t num_cus);
+AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, bool capped,
+                                  int32_t num_cus);
 // Bytes of TreeAttentionArgs::part and, behind it, shares.
 int64_t tree_attention_workspace(const AttentionPlan& p, int64_t T, int64_t heads, int32_t B);
 

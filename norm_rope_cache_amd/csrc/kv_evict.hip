@@ -32,25 +32,6 @@ __device__ __forceinline__ uint32_t ordered(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sums over the lanes up to each one: within rows of 16 by shifts, then the
-// rows' totals handed on (DPP: no LDS).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp_or_0(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
-    v += dpp_or_0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
-    v += dpp_or_0<0x112, 0xF>(v);
-    v += dpp_or_0<0x114, 0xF>(v);
-    v += dpp_or_0<0x118, 0xF>(v);
-    v += dpp_or_0<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
-    v += dpp_or_0<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
-    return v;
-}
-__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_readlane((int)wave_inclusive(v), 63);
-}
-
 __device__ __forceinline__ uint32_t bits_below(uint64_t m, uint32_t lane) {
     return (uint32_t)__popcll(m & (((uint64_t)1 << lane) - 1));
 }

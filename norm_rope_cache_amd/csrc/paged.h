@@ -76,13 +76,54 @@ __device__ __forceinline__ void to_lds(const void* src, uint32_t lds) {
 __device__ __forceinline__ void to_lds4(const void* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(lds) : "memory");
 }
+// At most N of this wave's loads to LDS are still on the way (they land in order).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | (N >> 4) << 14 | 0x0F70);
+    asm volatile("" ::: "memory");  // (LDS reads stay behind it)
+}
+// A barrier that waits for LDS accesses alone, not for loads on the way.
+__device__ __forceinline__ void barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 // This wave's loads to LDS have landed, and everybody's after the barrier.
 __device__ __forceinline__ void landed() {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt 0
+    wait_vmcnt<0>();
     __syncthreads();
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// Sums over the lanes up to each one: within rows of 16 by shifts, then the
+// rows' totals handed on (DPP: no LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_0(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
+    v += dpp_or_0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += dpp_or_0<0x112, 0xF>(v);
+    v += dpp_or_0<0x114, 0xF>(v);
+    v += dpp_or_0<0x118, 0xF>(v);
+    v += dpp_or_0<0x142, 0xA>(v);  // row_bcast 15 into rows 1 and 3
+    v += dpp_or_0<0x143, 0xC>(v);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_total(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)wave_inclusive(v), 63);
+}
+// The largest of the lanes', by the same steps.
+__device__ __forceinline__ uint32_t wave_most(uint32_t v) {
+    auto up = [&](uint32_t o) { v = v > o ? v : o; };
+    up(dpp_or_0<0x111, 0xF>(v));
+    up(dpp_or_0<0x112, 0xF>(v));
+    up(dpp_or_0<0x114, 0xF>(v));
+    up(dpp_or_0<0x118, 0xF>(v));
+    up(dpp_or_0<0x142, 0xA>(v));
+    up(dpp_or_0<0x143, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // e^x and log in base 2, the hardware's (relative error about 2^-23).

@@ -687,11 +687,6 @@ struct Shares {
     int32_t b, h, split, splits;    // of group g (b < 0: there is none)
     int32_t first;                  // of the sequence: its first group
 };
-__device__ __forceinline__ int32_t wave_sum_of(int32_t v) {
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d, 64);
-    return v;
-}
 __device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const AttentionPlan& plan, int32_t g, uint32_t lane) {
     constexpr int kMost = 8;
     int32_t tiles[kMost];
@@ -707,18 +702,14 @@ __device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const Attenti
         sum += tiles[j];
         longest = longest > tiles[j] ? longest : tiles[j];
     }
-    sum = wave_sum_of(sum);
-#pragma unroll
-    for (int d = 32; d > 0; d /= 2) {
-        const int32_t o = __shfl_xor(longest, d, 64);
-        longest = longest > o ? longest : o;
-    }
+    sum = (int32_t)wave_total((uint32_t)sum);
+    longest = (int32_t)wave_most((uint32_t)longest);
     auto count = [&](int32_t c) {
         int32_t n = 0;
 #pragma unroll
         for (int j = 0; j < kMost; ++j)
             if (64 * j < tq.B) n += (tiles[j] + c - 1) / c;
-        return wave_sum_of(n) * tq.H;
+        return (int32_t)wave_total((uint32_t)n) * tq.H;
     };
     int32_t lo = (int32_t)(((int64_t)sum * tq.H + plan.groups - 1) / plan.groups), hi = longest;
     if (lo < plan.split_tiles) lo = plan.split_tiles;  // (no share is smaller)
@@ -735,13 +726,7 @@ __device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const Attenti
     for (int j = 0; j < kMost; ++j) {
         if (64 * j >= tq.B) break;
         const int32_t n = (tiles[j] + lo - 1) / lo * tq.H;
-        int32_t upto = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int32_t o = __shfl_up(upto, d, 64);
-            if ((int32_t)lane >= d) upto += o;
-        }
-        upto += before;
+        const int32_t upto = before + (int32_t)wave_inclusive((uint32_t)n);
         const uint64_t past = __ballot(upto > g);
         if (r.b < 0 && past != 0) {
             const int32_t l = __builtin_ctzll(past);
@@ -757,15 +742,20 @@ __device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const Attenti
     r.groups = before;
     return r;
 }
-constexpr int kManyLds = 2 * (kStage * 256 + kStage * 4);
+// Buffers: as many as one workgroup of 8 waves, or two of 4, have room for.
+constexpr int buffers_of(int waves) { return waves == 8 ? 4 : 2; }
+constexpr int many_lds(int waves) { return buffers_of(waves) * (kStage * 256 + kStage * 4) + waves * 512; }
 template <int R, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse,
                                                                   float* __restrict__ part, int32_t* __restrict__ shares,
                                                                   uint32_t groups) {
     constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
+    constexpr int kBufs = buffers_of(WAVES);
+    static_assert(kBufs * 8 * kRuns == 64, "a wave's block numbers of kBufs tiles are one load");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    uint32_t* present = reinterpret_cast<uint32_t*>(lds + 2 * kStage * 256);  // [2][kStage]
+    uint32_t* present = reinterpret_cast<uint32_t*>(lds + kBufs * kStage * 256);  // [kBufs][kStage]
+    uint32_t* pages = present + kBufs * kStage;                                   // [WAVES][2][64]
     const uint32_t lds0 = lds_address(lds);
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t hl = lane >> 5, n32 = lane & 31u;
@@ -822,7 +812,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
         }
     };
     // (a key that is not there is read from the cache's first cell, and masked)
-    auto bring = [&](int buf) {
+    auto bring = [&](int buf, const int64_t (&off)[kRuns]) {
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             const uint32_t at = lds0 + buf * (kStage * 256) + (kRuns * wave + i) * 1024;
@@ -895,16 +885,57 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
         Keys32 k;
         f32x16 s0, s1;  // scores: of row tile 0 and 1 (of one row tile: of even and odd 32 keys)
         uint64_t exists[kStage / 64];
-        find(first, full_end);
-        bring(0);
-        find(first + 1, full_end);
-        landed();
-        if (first + 1 < full_end) bring(1);
-        find(first + 2, full_end);
+        // Block numbers go to LDS too, kBufs tiles of the wave's keys in one load and two such sets: a load to a register
+        // would have the compiler wait for it, and with it for the tiles on the way.
+        const int32_t all = full_end - first;
+        uint32_t* own_pages = pages + wave * 128;
+        auto find_pages = [&](int32_t set) {
+            const int32_t t = first + set * kBufs + (int32_t)(lane / (8 * kRuns));
+            const uint32_t key = (uint32_t)(t < full_end ? t : full_end - 1) * kStage + 8 * kRuns * wave + lane % (8 * kRuns);
+            const uint32_t blk = block_of(key, kv);
+            to_lds4(table + (blk < kv.table_width ? blk : kv.table_width - 1), lds_address(own_pages + (set & 1) * 64));
+        };
+        uint32_t page[kRuns];
+        auto read_pages = [&](int32_t i) {
+#pragma unroll
+            for (int r = 0; r < kRuns; ++r) page[r] = own_pages[(i % (2 * kBufs)) * 8 * kRuns + 8 * r + row8];
+        };
+        auto bring_whole = [&](int32_t i) {
+            int64_t offs[kRuns];
+#pragma unroll
+            for (int r = 0; r < kRuns; ++r) {
+                const uint32_t key = (uint32_t)(first + i) * kStage + 8 * (kRuns * wave + r) + row8, blk = block_of(key, kv);
+                offs[r] = blk < kv.table_width && page[r] < kv.num_blocks
+                              ? (int64_t)page[r] * kv.block_stride + (int64_t)(key - blk * kv.block_size) * kv.page_stride
+                              : -1;
+            }
+            bring(i % kBufs, offs);
+        };
+        // All but the loads of `later` tiles have landed; everybody's after the barrier.
+        auto landed_but = [&](int32_t later) {
+            if (later >= 3)
+                wait_vmcnt<6 * kRuns>();
+            else if (later == 2)
+                wait_vmcnt<4 * kRuns>();
+            else if (later == 1)
+                wait_vmcnt<2 * kRuns>();
+            else
+                wait_vmcnt<0>();
+            barrier();
+        };
+        find_pages(0);
+        find_pages(1);
+        wait_vmcnt<0>();
+        for (int32_t i = 0; i < kBufs && i < all; ++i) {
+            read_pages(i);
+            bring_whole(i);
+        }
+        landed_but((all < kBufs ? all : kBufs) - 1);
         bool whole = ballots(0, exists), primed = false;
-        for (int32_t t = first; t < full_end; ++t) {
-            const int buf = (t - first) & 1;
+        for (int32_t i = 0; i < all; ++i) {
+            const int buf = i % kBufs, next = (i + 1) % kBufs;
             const bool work = whole && active;
+            read_pages(i + kBufs);
             if (work) {
                 if (!primed) {
                     read_k(k, buf, 0);
@@ -929,26 +960,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                 }
             }
             // the wave has what it needs of this buffer
-            landed();
-            if (t + 2 < full_end) bring(buf);
-            find(t + 3, full_end);
-            const bool next_whole = t + 1 < full_end && ballots(buf ^ 1, exists);
+            const int32_t last_on_way = i + kBufs - 1 < all ? i + kBufs - 1 : all - 1;
+            landed_but(last_on_way - (i + 1));
+            if (i + kBufs < all) bring_whole(i + kBufs);
+            if (buf == 0) find_pages(i / kBufs + 2);
+            const bool next_whole = i + 1 < all && ballots(next, exists);
             primed = work && next_whole;
             if (primed) {
-                read_k(k, buf ^ 1, 0);
+                read_k(k, next, 0);
                 scores32<R>(s0, w, 0, k);
             }
             if (work) add32<R, CAP, false>(w, R - 1, s1, k, f, 0u);
             if (!whole) left_out = true;
             whole = next_whole;
         }
-        __syncthreads();  // (nobody reads the buffers any more)
+        landed();  // (nobody reads the buffers any more, and no block numbers are on the way)
     }
     // the others: the context's last, the nodes', those left out
     const int32_t rest = left_out || first > full_end ? first : full_end;
     if (rest < end) {
         find(rest, end);
-        bring(0);
+        bring(0, off);
         find(rest + 1, end);
         for (int32_t t = rest; t < end; ++t) {
             const int buf = (t - rest) & 1;
@@ -964,7 +996,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                                                                   kSubs * in_tree + sub);
             }
             landed();
-            if (t + 1 < end) bring(buf ^ 1);
+            if (t + 1 < end) bring(buf ^ 1, off);
             find(t + 2, end);
             uint64_t exists[kStage / 64];
             const bool whole = ballots(buf, exists);
@@ -1164,30 +1196,33 @@ int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     return page16 ? launch_few<R, WAVES, false, true>(a, stream) : launch_few<R, WAVES, false, false>(a, stream);
 }
 
-template <int R, int WAVES>
+template <int R, int WAVES, bool CAP>
 int launch_many(const TreeAttentionArgs& a, hipStream_t stream) {
     const uint32_t groups = a.plan.splits > 1 ? (uint32_t)a.plan.groups : (uint32_t)a.tq.B * a.tq.H;
     const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
-    auto kernel = a.tq.softcap > 0.0f ? many_rows_kernel<R, WAVES, true> : many_rows_kernel<R, WAVES, false>;
-    static std::atomic<int> done[2][64] = {};
-    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), kManyLds, done[a.tq.softcap > 0.0f]) != 0) return -1;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), kManyLds, stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
+    auto kernel = many_rows_kernel<R, WAVES, CAP>;
+    static std::atomic<int> done[64] = {};
+    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
                        a.shares, groups);
     return 0;
 }
 
 }  // namespace
 
-AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx,
+AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, bool capped,
                                   int32_t num_cus) {
     AttentionPlan p{};
     const int64_t rows = (int64_t)max_nodes * G;
     p.many = rows > 64;
     p.splits = 1;
     if (p.many) {
-        // 128, 256 or 512 rows a workgroup; two, two or one of them a CU
-        p.waves = rows > 256 ? 8 : 4;
-        p.q_tiles = rows > 128 ? 4 : 2;
+        // 128 rows a workgroup, two of them a CU; above, 256 and one, with more keys on the way (32768 keys of 4
+        // sequences and 8 heads, 256 rows: 111 us against 188 with waves of 64 rows). Above 256 rows of capped scores,
+        // whose exponentials leave the registers for it, 512 and waves of 64 rows (512 rows: 279 against 308 us;
+        // uncapped 288 against 221).
+        p.waves = rows > 128 ? 8 : 4;
+        p.q_tiles = capped && rows > 256 ? 4 : 2;
         const int64_t block_rows = 16 * p.q_tiles * p.waves;
         p.row_blocks = (int32_t)((rows + block_rows - 1) / block_rows);
         const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2);
@@ -1227,10 +1262,12 @@ int64_t tree_attention_workspace(const AttentionPlan& p, int64_t T, int64_t head
 
 int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
     int rc;
+    const bool capped = a.tq.softcap > 0.0f;
     if (a.plan.many)
-        rc = a.plan.waves == 8     ? launch_many<2, 8>(a, stream)
-             : a.plan.q_tiles == 4 ? launch_many<2, 4>(a, stream)
-                                   : launch_many<1, 4>(a, stream);
+        rc = a.plan.q_tiles == 4 ? launch_many<2, 8, true>(a, stream)
+             : a.plan.waves == 8 ? (capped ? launch_many<1, 8, true>(a, stream) : launch_many<1, 8, false>(a, stream))
+             : capped            ? launch_many<1, 4, true>(a, stream)
+                                 : launch_many<1, 4, false>(a, stream);
     else if (a.plan.waves == 16)
         rc = launch_few<1, 16>(a, stream);
     else
