@@ -43,20 +43,6 @@ __device__ __forceinline__ float tanh_of(float x) {
     return __builtin_fabsf(x) < 2.0f ? near : far;
 }
 
-// Bits 0 .. 31: does node i (row `row`) see keys key0 .. key0 + 31 of a
-// sequence with ctx keys of context and n nodes.
-__device__ __forceinline__ uint32_t seen32(const TreeQueries& t, int32_t row, int32_t i, int32_t n, int32_t ctx,
-                                           int32_t key0) {
-    const int32_t j0 = key0 - ctx;
-    if (j0 <= -32) return 0xFFFFFFFFu;
-    if (j0 >= n) return 0u;
-    if (j0 < 0) return ((1u << -j0) - 1u) | seen_word(t, row, i, n, 0) << -j0;
-    const int32_t w = j0 >> 5, s = j0 & 31;
-    uint32_t bits = seen_word(t, row, i, n, w) >> s;
-    if (s) bits |= seen_word(t, row, i, n, w + 1) << (32 - s);
-    return bits;
-}
-
 // Grid (blocks of keys, H, B), 4 waves of 32 KT keys each.
 constexpr int kStage = 64, kRuns = kStage / 32;  // query rows; runs of 8 of them a wave brings in
 template <int KT, bool CAP>
@@ -221,8 +207,9 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
             if (x.masked) {
                 uint32_t seen = 0u;
                 if (x.live) {
-                    const int32_t node = x.row / tq.G;
-                    seen = exists[kt] & seen32(tq, nodes.first + node, node, nodes.count, ctx, key0 + 32 * kt);
+                    uint32_t word[1];
+                    seen_keys<1>(word, tq, nodes, ctx, x.row / tq.G, key0 + 32 * kt);
+                    seen = exists[kt] & word[0];
                 }
                 seen = bits_of_scores(seen, hl);
 #pragma unroll

@@ -18,14 +18,23 @@ __device__ __forceinline__ uint32_t block_of(uint32_t key, const PagedCache& c) 
     return c.bs_shift >= 0 ? key >> c.bs_shift : key / c.block_size;
 }
 
-// Element offset of the key's 128-element run within head 0, or -1 where
-// there is no such key.
+// The key's entry of the table, an entry at all past its end.
+__device__ __forceinline__ uint32_t page_of(const PagedCache& c, const int32_t* table, uint32_t key) {
+    const uint32_t blk = block_of(key, c);
+    return (uint32_t)table[blk < c.table_width ? blk : c.table_width - 1];
+}
+// Element offset of the key's 128-element run within head 0, by its entry, or -1
+// where there is no such key.
+__device__ __forceinline__ int64_t key_offset(const PagedCache& c, uint32_t key, uint32_t page) {
+    const uint32_t blk = block_of(key, c);
+    return blk < c.table_width && page < c.num_blocks
+               ? (int64_t)page * c.block_stride + (int64_t)(key - blk * c.block_size) * c.page_stride
+               : -1;
+}
 __device__ __forceinline__ int64_t key_offset(const PagedCache& c, const int32_t* table, uint32_t key) {
     const uint32_t blk = block_of(key, c);
     if (blk >= c.table_width) return -1;
-    const uint32_t page = (uint32_t)table[blk];
-    if (page >= c.num_blocks) return -1;
-    return (int64_t)page * c.block_stride + (int64_t)(key - blk * c.block_size) * c.page_stride;
+    return key_offset(c, key, (uint32_t)table[blk]);
 }
 
 // A sequence's rows of q: the first, and how many (both within [0, T]).
@@ -43,15 +52,36 @@ __device__ __forceinline__ int32_t context_of(const TreeQueries& t, int32_t b) {
     return c < 0 ? 0 : c > t.max_ctx ? t.max_ctx : c;
 }
 
-// Which of the nodes 32 w .. 32 w + 31 of a sequence of n node i (row `row`
-// of q) sees, as bits.
-__device__ __forceinline__ uint32_t seen_word(const TreeQueries& t, int32_t row, int32_t i, int32_t n, int32_t w) {
-    const int32_t first = 32 * w;
-    const int32_t last = t.mask ? n - 1 : i;  // the last node that can be seen
-    if (last < first) return 0u;
-    const uint32_t there = last - first >= 31 ? 0xFFFFFFFFu : (2u << (last - first)) - 1u;
-    if (!t.mask) return there;
-    return w < t.mask_words ? t.mask[(int64_t)row * t.mask_words + w] & there : 0u;
+// Bits 0 .. 31 of words[i]: does node `node` (< 0: no row) see keys key0 + 32 i .. of a sequence with ctx keys of
+// context before its nodes.
+template <int N>
+__device__ __forceinline__ void seen_keys(uint32_t (&words)[N], const TreeQueries& t, const Nodes& nodes, int32_t ctx,
+                                          int32_t node, int32_t key0) {
+    const int32_t w0 = (key0 - ctx) >> 5;  // of the nodes' words of 32 (rounded down: the context's come before 0)
+    uint32_t bits[N + 1];
+#pragma unroll
+    for (int i = 0; i <= N; ++i) bits[i] = 0xFFFFFFFFu;
+    if (t.mask) {  // (every word on the way before the first is looked at)
+        const uint32_t* row = t.mask + (int64_t)(nodes.first + (node < 0 ? 0 : node)) * t.mask_words;
+#pragma unroll
+        for (int i = 0; i <= N; ++i) {
+            const int32_t w = w0 + i < t.mask_words ? w0 + i : t.mask_words - 1;
+            bits[i] = row[w < 0 ? 0 : w];
+        }
+    }
+    const int32_t last = t.mask ? nodes.count - 1 : node;  // the last node that can be seen
+    auto word = [&](int i) {
+        const int32_t behind = last - 32 * (w0 + i);  // how far it lies behind the word's first
+        const uint32_t there = behind < 0 ? 0u : behind >= 31 ? 0xFFFFFFFFu : (2u << behind) - 1u;
+        return node < 0 ? 0u : w0 + i < 0 ? 0xFFFFFFFFu : bits[i] & there;
+    };
+    uint32_t low = word(0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t high = word(i + 1);
+        words[i] = __builtin_amdgcn_alignbit(high, low, (uint32_t)(key0 - ctx) & 31u);
+        low = high;
+    }
 }
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));

@@ -321,11 +321,10 @@ __device__ __forceinline__ void add_odd(Rows<R>& w, const Keys& kv, const uint32
     }
 }
 
-// What a workgroup works on.
+// What a workgroup works on. Nodes' keys follow the context's, in the same tiles.
 struct Span {
     Nodes nodes;
-    int32_t ctx, rows;             // of the sequence; rows = nodes x heads per KV head
-    int32_t ctx_tiles, all_tiles;  // of TILE keys: the context's, and with the nodes' after them
+    int32_t ctx, rows, all_tiles;  // of the sequence; rows = nodes x heads per KV head; tiles of TILE keys
 };
 template <int TILE>
 __device__ __forceinline__ Span span_of(const TreeQueries& tq, int32_t b) {
@@ -333,23 +332,19 @@ __device__ __forceinline__ Span span_of(const TreeQueries& tq, int32_t b) {
     s.nodes = nodes_of(tq, b);
     s.ctx = context_of(tq, b);
     s.rows = s.nodes.count * tq.G;
-    s.ctx_tiles = (s.ctx + TILE - 1) / TILE;
-    s.all_tiles = s.ctx_tiles + (s.nodes.count + TILE - 1) / TILE;
+    s.all_tiles = (s.ctx + s.nodes.count + TILE - 1) / TILE;
     return s;
 }
-// A tile's first key, and how many keys it has at most.
+// How many keys a tile has at most.
 template <int TILE>
-__device__ __forceinline__ void tile_keys(const Span& s, int32_t t, uint32_t& key0, uint32_t& there) {
-    const int32_t in_tree = t - s.ctx_tiles;
-    key0 = in_tree < 0 ? (uint32_t)t * TILE : (uint32_t)(s.ctx + in_tree * TILE);
-    there = in_tree < 0 ? (uint32_t)(s.ctx - t * TILE) : (uint32_t)(s.nodes.count - in_tree * TILE);
+__device__ __forceinline__ uint32_t keys_from(const Span& s, int32_t t) {
+    return (uint32_t)(s.ctx + s.nodes.count - t * TILE);
 }
 // One past the last tile that rows up to `last_row` look at (a chain's nodes end with their own).
 template <int TILE>
 __device__ __forceinline__ int32_t last_tile(const TreeQueries& tq, const Span& s, int32_t last_row) {
-    if (tq.mask) return s.all_tiles;
-    if (last_row >= s.rows) last_row = s.rows - 1;
-    return s.ctx_tiles + last_row / tq.G / TILE + 1;
+    if (tq.mask || last_row >= s.rows) return s.all_tiles;
+    return (s.ctx + last_row / tq.G) / TILE + 1;
 }
 
 // The lane's rows row0 + 16 rq + l % 16: their queries, and their nodes (-1 past the last row).
@@ -376,16 +371,15 @@ __device__ __forceinline__ void load_rows(Rows<R>& w, int32_t (&node)[R], const 
     }
 }
 
-// Which keys of a tile each of the lane's rows sees. word: the tile's place among the nodes' 32-key
-// words, negative for the context.
+// Which of the 32 keys from key0 on each of the lane's rows sees.
 template <int R>
 __device__ __forceinline__ void seen_rows(uint32_t (&seen)[R], const int32_t (&node)[R], uint32_t exists,
-                                          const TreeQueries& tq, const Span& s, int32_t word) {
+                                          const TreeQueries& tq, const Span& s, int32_t key0) {
 #pragma unroll
     for (int rq = 0; rq < R; ++rq) {
-        seen[rq] = exists;
-        if (word >= 0)
-            seen[rq] &= node[rq] < 0 ? 0u : seen_word(tq, s.nodes.first + node[rq], node[rq], s.nodes.count, word);
+        uint32_t word[1];
+        seen_keys<1>(word, tq, s.nodes, s.ctx, node[rq], key0);
+        seen[rq] = exists & word[0];
     }
 }
 
@@ -450,8 +444,13 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
     const int32_t split = blockIdx.x % plan.splits;
     const uint32_t bh = blockIdx.x / plan.splits;
     const int32_t h = bh % tq.H, b = bh / tq.H;
-    const Span s = span_of<kTile>(tq, b);
+    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
     const int32_t first = split * plan.split_tiles;
+    int32_t t = first + (int32_t)wave;
+    // the first two tiles' table entries on the way before the lengths are known (key numbers stay below 2^32)
+    const uint32_t page0 = page_of(kv, table, (uint32_t)t * kTile + (lane & (kTile - 1)));
+    const uint32_t page1 = page_of(kv, table, (uint32_t)(t + WAVES) * kTile + (lane & (kTile - 1)));
+    const Span s = span_of<kTile>(tq, b);
     if (s.rows == 0 || first >= s.all_tiles) return;  // (nor does the join look at such a split)
     int32_t end = first + plan.split_tiles;
     const int32_t last = last_tile<kTile>(tq, s, 16 * R - 1);
@@ -459,13 +458,13 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
     const int32_t ctx_full = s.ctx / kTile;
 
     const uint16_t* head = kv.cache + (int64_t)h * kv.head_stride;
-    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
     const Factors f = factors<CAP>(tq);
+    auto in_tile = [&](int32_t t) { return t < end && lane < kTile && lane < keys_from<kTile>(s, t); };
     auto offsets = [&](int32_t t) -> int64_t {
-        uint32_t key0, there;
-        if (t >= end) return -1;
-        tile_keys<kTile>(s, t, key0, there);
-        return lane < kTile && lane < there ? key_offset(kv, table, key0 + lane) : -1;
+        return in_tile(t) ? key_offset(kv, table, (uint32_t)t * kTile + lane) : -1;
+    };
+    auto offsets_by = [&](int32_t t, uint32_t page) -> int64_t {
+        return in_tile(t) ? key_offset(kv, (uint32_t)t * kTile + lane, page) : -1;
     };
     // a whole tile of context, every key there
     auto whole = [&](int32_t t, int64_t off) { return t < end && t < ctx_full && (uint32_t)__ballot(off >= 0) == 0xFFFFFFFFu; };
@@ -491,13 +490,12 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
     Rows<R> w;
     int32_t node[R];
     uint32_t seen[R];
-    int32_t t = first + (int32_t)wave;
     const int32_t full_end = end < ctx_full ? end : ctx_full;
     bool left_out = false;  // a tile of the context with a key that is not there
     {
         // the tiles whose every key is there and seen by all
         Keys keys[2];
-        int64_t off = offsets(t), off1 = offsets(t + WAVES);
+        int64_t off = offsets_by(t, page0), off1 = offsets_by(t + WAVES, page1);
         bool cur_whole = whole(t, off);
         if (cur_whole) fetch(keys[0], off);
         load_rows<R>(w, node, tq, s, h, 0, lane, f.c);
@@ -524,8 +522,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
         if (whole(t, off)) continue;
         Keys keys;
         load_keys(keys, head, off, lane);
-        seen_rows<R>(seen, node, (uint32_t)__ballot(off >= 0), tq, s, t - s.ctx_tiles);
-        const bool odd = t >= s.ctx_tiles && any_odd(keys);
+        seen_rows<R>(seen, node, (uint32_t)__ballot(off >= 0), tq, s, t * kTile);
+        const bool odd = (t + 1) * kTile > s.ctx && any_odd(keys);
         if (odd) drop_odd(keys);
         masked_tile<R, CAP>(w, keys, f.c, f.capped, seen, lane);
         if (odd) {
@@ -579,6 +577,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, Tre
 }
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 // What a wave of the many-rows kernel carries for R query tiles of 32 rows.
 // Scores come as S^T = K Q^T by v_mfma_f32_32x32x16_bf16: lane l holds, for
@@ -621,7 +620,8 @@ __device__ __forceinline__ float weights32(const f32x16& s, float base, float c,
     for (int i = 0; i < 16; ++i) {
         p[i] = exp2_hw(CAP ? __builtin_fmaf(rcp_hw(exp2_hw(s[i] * c) + 1.0f), -2.0f * capped, from)
                            : __builtin_fmaf(s[i], c, from));
-        if (MASKED && !(seen >> i & 1u)) p[i] = 0.0f;
+        // (bit i over the whole word, and its float)
+        if (MASKED) p[i] = __uint_as_float(__float_as_uint(p[i]) & (uint32_t)__builtin_amdgcn_sbfe((int)seen, i, 1));
     }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
@@ -662,13 +662,15 @@ __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Key
 }
 
 // Many rows: the WAVES waves of a workgroup hold 32 R rows each and share the
-// keys, staged in LDS kStage at a time in two buffers: while the waves work on
-// one tile the next one comes in (global_load_lds, no registers), and one barrier
-// a tile. Bound by what the vector unit issues: a matrix instruction takes it 8
-// cycles and keeps the matrix core 32, an exponential takes 8, other operations
-// 4; of 32 keys and 32 rows that is 8, 16 and about 50. Measured: 600 TFLOP/s of
-// a large matrix product's 1212 (32768 keys, 512 rows a head), 490 with a softcap
-// (an exponential and a reciprocal more a score).
+// keys, staged in LDS kStage at a time in four buffers (of two workgroups a CU, two
+// each): while the waves work on one tile the next ones come in (global_load_lds, no
+// registers), and one barrier a tile. Bound by what the vector unit issues: a
+// matrix instruction takes it 8 cycles and keeps the matrix core 32, an
+// exponential takes 8, other operations 4; of 32 keys and 32 rows that is 8, 16 and
+// about 50. Measured: 620 TFLOP/s (4 sequences of 32768 keys, 8 heads, 512 rows
+// a head: 221 us; a large matrix product 1212), 490 with a softcap (an
+// exponential and a reciprocal more a score). Short shares are bound by their
+// loads' latency one after the other: lengths, block numbers, keys, masks.
 // LDS: K rows of 128 bytes whose 16-byte chunk c lies at c ^ (key & 7), so
 // that 8 lanes reading one chunk of 8 keys meet all banks; V rows with c at
 // c ^ 4 in every second pair of keys, so that the 4 keys and 64 bytes that half a wave
@@ -803,12 +805,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
     const uint32_t row8 = lane >> 3, c8 = lane & 7u;
     auto find = [&](int32_t t, int32_t stop) {
         if (t >= stop) return;
-        uint32_t key0, there;
-        tile_keys<kStage>(s, t, key0, there);
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             const uint32_t k = 8 * (kRuns * wave + i) + row8;
-            off[i] = k < there ? key_offset(kv, table, key0 + k) : -1;
+            off[i] = k < keys_from<kStage>(s, t) ? key_offset(kv, table, (uint32_t)t * kStage + k) : -1;
         }
     };
     // (a key that is not there is read from the cache's first cell, and masked)
@@ -904,10 +904,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
             int64_t offs[kRuns];
 #pragma unroll
             for (int r = 0; r < kRuns; ++r) {
-                const uint32_t key = (uint32_t)(first + i) * kStage + 8 * (kRuns * wave + r) + row8, blk = block_of(key, kv);
-                offs[r] = blk < kv.table_width && page[r] < kv.num_blocks
-                              ? (int64_t)page[r] * kv.block_stride + (int64_t)(key - blk * kv.block_size) * kv.page_stride
-                              : -1;
+                offs[r] = key_offset(kv, (uint32_t)(first + i) * kStage + 8 * (kRuns * wave + r) + row8, page[r]);
             }
             bring(i % kBufs, offs);
         };
@@ -984,17 +981,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
         find(rest + 1, end);
         for (int32_t t = rest; t < end; ++t) {
             const int buf = (t - rest) & 1;
-            const int32_t in_tree = t - s.ctx_tiles;
-            uint32_t words[kSubs][R];  // what the lane's rows see of the tile's nodes
-            if (in_tree >= 0) {
+            const bool has_nodes = (t + 1) * kStage > s.ctx;
+            uint32_t words[R][kSubs];  // what the lane's rows see of the tile
 #pragma unroll
-                for (int sub = 0; sub < kSubs; ++sub)
-#pragma unroll
-                    for (int rt = 0; rt < R; ++rt)
-                        words[sub][rt] = node[rt] < 0 ? 0u
-                                                      : seen_word(tq, s.nodes.first + node[rt], node[rt], s.nodes.count,
-                                                                  kSubs * in_tree + sub);
-            }
+            for (int rt = 0; rt < R; ++rt) seen_keys<kSubs>(words[rt], tq, s.nodes, s.ctx, node[rt], t * kStage);
             landed();
             if (t + 1 < end) bring(buf ^ 1, off);
             find(t + 2, end);
@@ -1003,19 +993,18 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
             if (!active || (whole && t < ctx_full)) continue;
 #pragma unroll 1
             for (int sub = 0; sub < kSubs; ++sub) {
-                const uint32_t there = (uint32_t)(exists[sub / 2] >> (32 * (sub & 1)));
+                const uint32_t there = (uint32_t)((sub & 2 ? exists[1] : exists[0]) >> (32 * (sub & 1)));
                 uint32_t word[R];
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
-                    word[rt] = words[0][rt];
+                    word[rt] = words[rt][0];
 #pragma unroll
-                    for (int i = 1; i < kSubs; ++i) words[i - 1][rt] = words[i][rt];
+                    for (int i = 1; i < kSubs; ++i) words[rt][i - 1] = words[rt][i];
                 }
                 if (there == 0u) continue;
                 Keys32 k;
                 const uint32_t mine = bits_of_scores(there, hl);
-                auto v_there = [&]() {
-                    read_v(k, buf, sub);
+                auto clear_absent = [&]() {
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -1029,12 +1018,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                         }
                 };
                 read_k(k, buf, sub);
-                v_there();
+                read_v(k, buf, sub);
+                if (there != 0xFFFFFFFFu) clear_absent();
                 bool odd = false;  // infinities and NaN in nodes' V: see add_odd
-                if (in_tree >= 0) {
+                if (has_nodes) {
+                    u16x2 most{0, 0};
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) odd = odd || inf_or_nan_pair((&k.v[i / 8][i / 4 % 2].x)[i % 4]);
-                    odd = __any(odd);
+                    for (int i = 0; i < 16; ++i)
+                        most = __builtin_elementwise_max(
+                            most, __builtin_bit_cast(u16x2, (&k.v[i / 8][i / 4 % 2].x)[i % 4] & 0x7FFF7FFFu));
+                    odd = __any(most.x >= 0x7F80 || most.y >= 0x7F80);
                     if (odd) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -1046,13 +1039,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
                 uint32_t seen[R];
 #pragma unroll
                 for (int rt = 0; rt < R; ++rt) {
-                    seen[rt] = bits_of_scores(in_tree >= 0 ? there & word[rt] : there, hl);
+                    seen[rt] = bits_of_scores(there & word[rt], hl);
                     f32x16 sc;
                     scores32<R>(sc, w, rt, k);
                     add32<R, CAP, true>(w, rt, sc, k, f, seen[rt]);
                 }
                 if (!odd) continue;
-                v_there();
+                read_v(k, buf, sub);
+                clear_absent();
 #pragma unroll 1
                 for (int kind = 0; kind < 3; ++kind) {
                     const float adds = kind == 0 ? __builtin_inff() : kind == 1 ? -__builtin_inff() : __builtin_nanf("");
@@ -1128,7 +1122,7 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq
         ml = part + (int64_t)plan.groups * step * kHeadDim;
     } else {
         const int32_t ctx = context_of(tq, b);
-        const int32_t tiles = (ctx + kTile - 1) / kTile + (nodes.count + kTile - 1) / kTile;
+        const int32_t tiles = (ctx + nodes.count + kTile - 1) / kTile;
         splits = (tiles + plan.split_tiles - 1) / plan.split_tiles;
         if (splits > plan.splits) splits = plan.splits;
         step = (int64_t)tq.T * heads;
@@ -1226,7 +1220,7 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
         const int64_t block_rows = 16 * p.q_tiles * p.waves;
         p.row_blocks = (int32_t)((rows + block_rows - 1) / block_rows);
         const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2);
-        const int64_t tiles = (max_ctx + kStage - 1) / kStage + (max_nodes + kStage - 1) / kStage;
+        const int64_t tiles = (max_ctx + max_nodes + kStage - 1) / kStage;
         p.split_tiles = 2;
         p.groups = (int32_t)(at_once / p.row_blocks);
         // split when the chip has room for twice the workgroups, by what the lengths turn out to be
@@ -1236,11 +1230,12 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
     p.q_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.waves = 4;
     p.row_blocks = 1;
-    const int64_t tiles = (max_ctx + kTile - 1) / kTile + (max_nodes + kTile - 1) / kTile;
+    const int64_t tiles = (max_ctx + max_nodes + kTile - 1) / kTile;
     const int64_t base = (int64_t)B * H;
     if (p.q_tiles == 1 && tiles <= 64 && base <= num_cus) {
-        // short and few: 16 waves, 4 tiles each at most, and no second launch
-        p.waves = 16;
+        // Short and few: 8 waves, 8 tiles each at most, and no second launch (8 heads: 1000 keys 10.5 us a launch, 16
+        // waves of half the registers 11.7; a call at 2000 keys 18 us, split in two launches 21; at 4000 split 21, one 27).
+        p.waves = 8;
         p.split_tiles = (int32_t)tiles;
         return p;
     }
@@ -1268,8 +1263,8 @@ int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
              : a.plan.waves == 8 ? (capped ? launch_many<1, 8, true>(a, stream) : launch_many<1, 8, false>(a, stream))
              : capped            ? launch_many<1, 4, true>(a, stream)
                                  : launch_many<1, 4, false>(a, stream);
-    else if (a.plan.waves == 16)
-        rc = launch_few<1, 16>(a, stream);
+    else if (a.plan.waves == 8)
+        rc = launch_few<1, 8>(a, stream);
     else
         rc = a.plan.q_tiles == 1   ? launch_few<1, 4>(a, stream)
              : a.plan.q_tiles == 2 ? launch_few<2, 4>(a, stream)
