@@ -960,9 +960,11 @@ def _at(t, dev, name):
 
 def _int32(t, name, dev, shape):
     torch = _torch or _get_torch()
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype == torch.int32 and t.shape == shape
+            and t.is_contiguous()):
+        return
     _at(t, dev, name)
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+    raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
 def _paged_operands(cache, tables):
@@ -1076,15 +1078,18 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
 
 def _float_lse(lse, dev, shape):
     torch = _torch or _get_torch()
+    if (isinstance(lse, torch.Tensor) and lse.get_device() == dev and lse.dtype == torch.float32 and lse.shape == shape
+            and lse.is_contiguous()):
+        return
     _at(lse, dev, "lse")
-    if lse.dtype != torch.float32 or lse.shape != shape or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
+    raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
 
 
 def _cells(t, name, dev, dtype, shape):
     """A [B, H, width] tensor of per-cell values with unit last stride; its strides."""
-    _at(t, dev, name)
-    if t.dtype != dtype or t.shape != shape:
+    torch = _torch or _get_torch()
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _at(t, dev, name)
         raise ValueError(f"{name} must be a {dtype} {list(shape)} tensor")
     st = t.stride()
     if shape[2] > 1 and st[2] != 1:
