@@ -237,10 +237,10 @@ int32_t per_cell(const char* what, const char* name, const void* p, int64_t bs, 
     return NRC_OK;
 }
 
-// Do 4-byte elements [p, p + n) and [q, q + m) meet?
-bool meet(const void* p, int64_t n, const void* q, int64_t m) {
+// Do elements [p, p + n) and [q, q + m), of 4 bytes unless said otherwise, meet?
+bool meet(const void* p, int64_t n, const void* q, int64_t m, int p_bytes = 4, int q_bytes = 4) {
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return n > 0 && m > 0 && a < b + 4 * (uint64_t)m && b < a + 4 * (uint64_t)n;
+    return n > 0 && m > 0 && a < b + q_bytes * (uint64_t)m && b < a + p_bytes * (uint64_t)n;
 }
 
 int32_t max_moves(int64_t width, int32_t budget) {
@@ -283,6 +283,9 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
     if (!work) return NRC_OK;
     if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
+    if (const int64_t q_span = span(T, Hq, 64, q_row_stride, q_head_stride);
+        meet(q, q_span, out, T * Hq * 64, 2, 2) || meet(q, q_span, lse, T * Hq, 2) || meet(out, T * Hq * 64, lse, T * Hq, 2))
+        return fail(NRC_EINVAL, "%s: q, out and lse must lie apart from each other", what);
     a.plan = nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, softcap > 0.0f, num_cus());
     const int64_t bytes = nrc::tree_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))

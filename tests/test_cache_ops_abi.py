@@ -81,13 +81,17 @@ QUERY_EINVAL = [dict(T=-1), dict(Hq=0), dict(nodes=0), dict(nodes=65536), dict(m
 
 
 def test_tree_attention(lib):
-    call = caller(lib.nrc_context_tree_attention, dict(QUERIES, out=FAKE, lse=FAKE, ws=None, ws_bytes=0, stream=None))
+    call = caller(lib.nrc_context_tree_attention, dict(QUERIES, out=FAR, lse=ctypes.c_void_p(0x20000000), ws=None,
+                                                       ws_bytes=0, stream=None))
     for kw in PAGED_NOTSUP + QUERY_NOTSUP:
         assert call(**kw) == ENOTSUP, kw
     for kw in PAGED_EINVAL + QUERY_EINVAL + [dict(out=None), dict(lse=None), dict(out=ctypes.c_void_p(0x10008)),
                                              dict(lse=MISALIGNED)]:
         assert call(**kw) == EINVAL, kw
         assert b"context_tree_attention" in lib.nrc_last_error()
+    for kw in (dict(out=FAKE), dict(lse=FAKE), dict(out=ctypes.c_void_p(FAKE.value + 2 * (5 * 512 + 7 * 64 + 56))),
+               dict(lse=ctypes.c_void_p(FAR.value + 6 * 8 * 64 * 2 - 4))):
+        assert call(**kw) == EINVAL and b"apart" in lib.nrc_last_error(), kw
     # a long context needs a workspace
     long = dict(max_ctx=100000, B=1, tw=10000)
     need = lib.nrc_context_tree_attention_workspace_bytes(1, 6, 8, 2, 2, 100000)
