@@ -73,7 +73,7 @@ __device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, uint
     }
 }
 
-constexpr int kWholeMoves = 512;
+constexpr int kWholeMoves = 1024;
 
 // The cells named by two lists in LDS: 16 lanes to a cell, GROUPS cells at a time, four times on the way.
 template <int GROUPS>
@@ -551,9 +551,13 @@ __global__ __launch_bounds__(kPlaces) void evict_apply_kernel(KvEvictArgs a) {
 }  // namespace
 
 namespace {
-// Up to 8192 cells with up to 512 moves (128 KiB a list) take one launch: 256 lists of 4160 cells 12.6 us
-// against 21 in two.
-bool in_one(int64_t width, int64_t max_moves) { return max_moves <= kWholeMoves && width <= 8 * kThreads; }
+// Up to 8192 cells with up to 1024 moves (256 KiB a list; half of that where there are more lists than CUs) take one
+// launch: a call on 256 lists of 4160 cells, 64 of them gone, 15 us against 21 in two launches; of 2048 cells, half of
+// them, 20.8 against 25.3; 64 lists of 1548 cells, half, 16.7 against 22.2. At 2048 moves 512 lists of 4096 cells took
+// 87 against 73.
+bool in_one(int64_t lists, int64_t width, int64_t max_moves) {
+    return max_moves <= (lists <= 256 ? kWholeMoves : kWholeMoves / 2) && width <= 8 * kThreads;
+}
 // A list takes one launch of one workgroup, or four of 16 (its cells read again in each): past what a workgroup
 // holds, always (8 lists of 131072 cells 60 us in all, 358 when one workgroup reads again); past half of that where few
 // lists would leave most CUs idle (65536 cells: 16 lists 57 against 87 us, 32 lists 102 against 113, 64 lists 202 against
@@ -564,7 +568,7 @@ bool in_parts(int64_t lists, int64_t width) {
 }  // namespace
 
 int64_t kv_evict_workspace(int64_t lists, int64_t width, int64_t max_moves, int64_t blocks) {
-    if (max_moves == 0 || in_one(width, max_moves)) return 0;
+    if (max_moves == 0 || in_one(lists, width, max_moves)) return 0;
     int64_t words = padded4(lists * (blocks + 1)) + padded4(2 * lists * max_moves);
     if (in_parts(lists, width)) words += lists * (16 + kParts + 2 * kParts * kBins);
     return words * 4;
@@ -574,7 +578,7 @@ int32_t kv_evict_blocks(int64_t budget) { return (int32_t)((budget + kPlaces - 1
 
 int launch_kv_evict(const KvEvictArgs& a, hipStream_t stream) {
     const uint32_t lists = (uint32_t)a.B * a.H;
-    if (a.max_moves > 0 && in_one(a.width, a.max_moves)) {
+    if (a.max_moves > 0 && in_one(lists, a.width, a.max_moves)) {
         hipLaunchKernelGGL((evict_select_kernel<8, true>), dim3(lists), dim3(kThreads), 0, stream, a);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }

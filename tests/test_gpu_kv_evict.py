@@ -62,7 +62,7 @@ def test_long_heads(nrc, n, budget):
     check(nrc, make([n, n // 3], H=1, seed=n), budget, sinks=4, recent=100)
 
 
-@pytest.mark.parametrize("n,budget,H", [(12000, 6000, 1), (33000, 32000, 33), (33000, 500, 2), (65536, 32768, 1),
+@pytest.mark.parametrize("n,budget,H", [(8000, 4000, 2), (1500, 750, 260), (12000, 6000, 1), (33000, 32000, 33), (33000, 500, 2), (65536, 32768, 1),
                                         (65537, 1, 2), (140000, 70001, 1)])
 def test_lists_of_one_and_of_many_workgroups(nrc, n, budget, H):
     """Each way of selecting: the lists shorter than the array too, of a length that leaves parts empty."""
