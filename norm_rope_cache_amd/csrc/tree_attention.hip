@@ -17,7 +17,7 @@
 // lanes vote): between, p, l and O grow by up to that factor, which FP32 and bf16
 // hold at full precision, and no lane waits for another's maximum.
 //
-// Up to 64 rows (few_rows_kernel) the cache's bytes bound it: K and V go from
+// Up to 32 rows (few_rows_kernel) the cache's bytes bound it: K and V go from
 // memory to the matrix core through registers, each wave its own tiles of 32
 // keys. More rows (many_rows_kernel) are bound by the vector unit (the
 // exponentials and what feeds the matrix instructions): keys are staged in LDS
@@ -418,7 +418,7 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
     }
 }
 
-// Few rows (up to 16 R, R <= 4): one workgroup per (sequence, KV head,
+// Few rows (up to 16 R, R <= 2): one workgroup per (sequence, KV head,
 // split); its WAVES waves hold the same rows and take the split's tiles in turn, and
 // join their sums in LDS. A tile is 32 keys by 16 R rows:
 //   S^T = K Q^T   4 v_mfma_f32_16x16x32_bf16 a query tile; K's lane: key l % 16, 8
@@ -434,8 +434,10 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
 // up to 8192 keys, 8 heads: 685 MB in 139 us, 4.9 TB/s, a copy reaches 5.2).
 // PAGE16 (block_size a multiple of 16, page rows near each other): the 16
 // keys of half a tile lie in one page, so a tile's two bases are scalars.
+// Two workgroups of 4 waves a CU, as the splits are planned: R 2 keeps to half the registers for it (32 rows over
+// 30000 keys of 4 sequences, 8 heads: 62 -> 42 us); a third of R 1 would leave other CUs short.
 template <int R, int WAVES, bool CAP, bool PAGE16>
-__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
+__global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                               uint16_t* __restrict__ out, float* __restrict__ lse,
                                                               float* __restrict__ part) {
     extern __shared__ float smem[];
@@ -1173,10 +1175,8 @@ __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq
 template <int R, int WAVES, bool CAP, bool PAGE16>
 int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
-    static std::atomic<int> done[64] = {};
-    auto kernel = few_rows_kernel<R, WAVES, CAP, PAGE16>;
-    if (kLds > 65536 && raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, done) != 0) return -1;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)a.tq.B * a.tq.H * a.plan.splits), dim3(64 * WAVES), kLds, stream, a.kv,
+    static_assert(kLds <= 65536, "above, the limit would have to be raised");
+    hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3((uint32_t)a.tq.B * a.tq.H * a.plan.splits), dim3(64 * WAVES), kLds, stream, a.kv,
                        a.tq, a.plan, a.out, a.lse, a.part);
     return 0;
 }
@@ -1208,7 +1208,8 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
                                   int32_t num_cus) {
     AttentionPlan p{};
     const int64_t rows = (int64_t)max_nodes * G;
-    p.many = rows > 64;
+    // 64 sequences of 4096 keys and 8 heads: 32 rows 67 us as few, 64 rows 90 as many (135 in tiles of 64 rows as few).
+    p.many = rows > 32;
     p.splits = 1;
     if (p.many) {
         // 128 rows a workgroup, two of them a CU; above, 256 and one, with more keys on the way (32768 keys of 4
@@ -1227,7 +1228,7 @@ AttentionPlan plan_tree_attention(int32_t B, int32_t H, int32_t G, int32_t max_n
         if (2 * (int64_t)B * H <= p.groups && tiles > p.split_tiles) p.splits = 2;
         return p;
     }
-    p.q_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.q_tiles = rows <= 16 ? 1 : 2;
     p.waves = 4;
     p.row_blocks = 1;
     const int64_t tiles = (max_ctx + max_nodes + kTile - 1) / kTile;
@@ -1266,9 +1267,7 @@ int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
     else if (a.plan.waves == 8)
         rc = launch_few<1, 8>(a, stream);
     else
-        rc = a.plan.q_tiles == 1   ? launch_few<1, 4>(a, stream)
-             : a.plan.q_tiles == 2 ? launch_few<2, 4>(a, stream)
-                                   : launch_few<4, 4>(a, stream);
+        rc = a.plan.q_tiles == 1 ? launch_few<1, 4>(a, stream) : launch_few<2, 4>(a, stream);
     if (rc) return rc;
     if (a.plan.splits > 1) {
         const dim3 grid((uint32_t)(((int64_t)a.tq.max_nodes * a.tq.H * a.tq.G + 15) / 16), (uint32_t)a.tq.B);
