@@ -57,12 +57,24 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t hl = lane >> 5, n32 = lane & 31u;
     const int32_t h = blockIdx.y, b = blockIdx.z;
-    const Nodes nodes = nodes_of(tq, b);
-    const int32_t ctx = context_of(tq, b);
-    const int32_t rows = nodes.count * tq.G, total = ctx + nodes.count, heads = tq.H * tq.G;
     const int32_t block0 = (int32_t)blockIdx.x * 128 * KT, key0 = block0 + (int32_t)wave * 32 * KT;
     const uint16_t* head = kv.cache + (int64_t)h * kv.head_stride;
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
+    // On the way before the lengths are known: the keys' table entries, and the earlier weights (of few query rows a
+    // workgroup's time is its chain of loads).
+    const int64_t at_w = b * w_bs + h * w_hs, at_o = b * out_bs + h * out_hs;
+    const int32_t own = (int32_t)(8 * (lane >> 3 & 3u) + 4 * hl + (lane >> 1 & 3u));  // of 32 keys, the lane's in the end
+    uint32_t page[KT];
+    float earlier[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+        page[kt] = page_of(kv, table, (uint32_t)(key0 + 32 * kt) + n32);
+        const int64_t key = key0 + 32 * kt + own;
+        earlier[kt] = weights && key < width ? weights[at_w + key] : 0.0f;
+    }
+    const Nodes nodes = nodes_of(tq, b);
+    const int32_t ctx = context_of(tq, b);
+    const int32_t rows = nodes.count * tq.G, total = ctx + nodes.count, heads = tq.H * tq.G;
     const bool any = block0 < total && rows > 0;  // (the same in the workgroup)
 
     // Rows of the stage that the lane brings in: of Q, in run i of the wave (8 rows), row lane / 8 and the chunk that
@@ -128,7 +140,7 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
     for (int kt = 0; kt < KT; ++kt) {
         const int32_t key = key0 + 32 * kt + (int32_t)n32;
         int64_t off = -1;
-        if (key < total) off = key_offset(kv, table, (uint32_t)key);
+        if (key < total) off = key_offset(kv, (uint32_t)key, page[kt]);
         exists[kt] = (uint32_t)__ballot(off >= 0);
         plain &= exists[kt] == 0xFFFFFFFFu;
         // (a key that is not there is read from the cache's first cell, and masked)
@@ -248,7 +260,6 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
     }
     // The sums over the 32 lanes of a half: each exchange halves the keys a lane
     // holds; bits 4 .. 1 of the lane name the one it ends with.
-    const int64_t at_w = b * w_bs + h * w_hs, at_o = b * out_bs + h * out_hs;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) {
         float v[16];
@@ -269,14 +280,13 @@ __global__ __launch_bounds__(256, CAP ? (KT == 1 ? 3 : 2) : (KT == 1 ? 4 : 3)) v
         halve(std::integral_constant<int, 4>{}, 2);
         halve(std::integral_constant<int, 2>{}, 1);
         float mass = v[0] + lane_xor<1>(v[0]);
-        const int32_t i = (int32_t)(lane >> 1 & 15u);
         // (halving: bit 4 chose i's bit 3, bit 3 its bit 2, bit 2 its bit 1, bit 1 its bit 0)
-        const int64_t key = key0 + 32 * kt + 8 * (i / 4) + 4 * (int32_t)hl + i % 4;
+        const int64_t key = key0 + 32 * kt + own;
         if ((lane & 1u) == 0u && key < width) {
             if (key >= total)
                 mass = 0.0f;
             else if (weights)
-                mass = __builtin_fmaf(weights[at_w + key], decay, mass);
+                mass = __builtin_fmaf(earlier[kt], decay, mass);
             out[at_o + key] = mass;
         }
     }
