@@ -487,7 +487,7 @@ int32_t nrc_rope_table(int64_t start, int64_t count, int32_t rotary_dim, int32_t
  *              T <= 2^23. 16-byte aligned heads take 16-byte accesses, others
  *              single elements.
  *   positions  [T] int64; a row whose position is outside [0, max_position)
- *              is left as it is.
+ *              is left as it is in out.
  *   cos_sin    [max_position, rotary_dim] of table_dtype (bf16 or FP32),
  *              contiguous: cos of the rotary_dim / 2 pairs, then sin.
  *   layout     NRC_ROPE_INTERLEAVED or NRC_ROPE_HALF; elements from
@@ -504,6 +504,19 @@ int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int3
                         int64_t x_head_stride, const int64_t* positions, const void* cos_sin, int32_t table_dtype,
                         int64_t max_position, int32_t rotary_dim, int32_t layout, int32_t inverse, void* out,
                         int64_t out_row_stride, int64_t out_head_stride, void* stream);
+
+/* Flags of nrc_rope_rotate_ex. */
+#define NRC_ROPE_PASS_OUTSIDE 1u /* a row whose position is outside the table is copied from x */
+
+/*
+ * nrc_rope_rotate_ex - nrc_rope_rotate with flags (NRC_ROPE_*; 0: the same).
+ * NRC_ROPE_PASS_OUTSIDE is for an out whose memory holds nothing yet: padded
+ * rows (a position of -1) come out as they went in. Unknown flags: NRC_EINVAL.
+ */
+int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, int32_t head_dim, int64_t x_row_stride,
+                           int64_t x_head_stride, const int64_t* positions, const void* cos_sin, int32_t table_dtype,
+                           int64_t max_position, int32_t rotary_dim, int32_t layout, int32_t inverse, void* out,
+                           int64_t out_row_stride, int64_t out_head_stride, uint32_t flags, void* stream);
 
 /*
  * nrc_context_tree_attention - drafted tokens attending to their sequence's

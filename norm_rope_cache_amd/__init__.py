@@ -150,6 +150,8 @@ def _load():
     L.nrc_rope_rotate.restype = _i32
     L.nrc_rope_rotate.argtypes = [_vp, _i32, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp,
                                   _i64, _i64, _vp]
+    L.nrc_rope_rotate_ex.restype = _i32
+    L.nrc_rope_rotate_ex.argtypes = L.nrc_rope_rotate.argtypes[:-1] + [ctypes.c_uint32, _vp]
     paged = [_vp, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _i64, _i32]
     queries = [_vp, _i64, _i64, _i64, _i32] + paged + [_vp, _vp, _i32, _i64, _vp, _i32, _f32, _f32]
     L.nrc_context_tree_attention.restype = _i32
@@ -850,6 +852,7 @@ def _fits32(v, name):
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_PASS_OUTSIDE = 1
 
 
 def _dtype_code(dtype, name, table=False):
@@ -910,7 +913,8 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
     first R = cos_sin.shape[1] elements of each head turned by its row's
     position; the rest is copied.
 
-    positions  [T] int64; a row outside the table is left as it is
+    positions  [T] int64; a row outside the table is left as it is in a given
+               out, and comes out as it went in otherwise
     cos_sin    [max_position, R] bf16 or float32 (rope_table)
     layout     "interleaved" (pairs 2j, 2j + 1, as context_kv_store turns its
                keys) or "half" (pairs j, j + R / 2)
@@ -938,15 +942,15 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
         raise ValueError("positions must be a contiguous int64 [T] tensor")
     if out is None:
         out = _empty(shape, x.dtype, x.device, stream)
-        ost = (H * d, d)
+        ost, flags = (H * d, d), ROPE_PASS_OUTSIDE
     else:
-        ost = out.stride()
+        ost, flags = out.stride(), 0
         if out.dtype != x.dtype or out.shape != shape or ost[2] != 1:
             raise ValueError("out must be shaped like x, of its dtype, with unit last stride")
         _at(out, dev, "out")
-    _call(x, _load().nrc_rope_rotate, x.data_ptr(), code, T, H, d, st[0], st[1], positions.data_ptr(),
+    _call(x, _load().nrc_rope_rotate_ex, x.data_ptr(), code, T, H, d, st[0], st[1], positions.data_ptr(),
           cos_sin.data_ptr(), tcode, table[0], table[1], ROPE_LAYOUTS[layout], 1 if inverse else 0, out.data_ptr(), ost[0],
-          ost[1], _stream(stream, x))
+          ost[1], flags, _stream(stream, x))
     return out
 
 

@@ -107,7 +107,16 @@ int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int3
                         int64_t x_head_stride, const int64_t* positions, const void* cos_sin, int32_t table_dtype,
                         int64_t max_position, int32_t rotary_dim, int32_t layout, int32_t inverse, void* out,
                         int64_t out_row_stride, int64_t out_head_stride, void* stream) {
+    return nrc_rope_rotate_ex(x, dtype, T, H, head_dim, x_row_stride, x_head_stride, positions, cos_sin, table_dtype,
+                              max_position, rotary_dim, layout, inverse, out, out_row_stride, out_head_stride, 0, stream);
+}
+
+int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, int32_t head_dim, int64_t x_row_stride,
+                           int64_t x_head_stride, const int64_t* positions, const void* cos_sin, int32_t table_dtype,
+                           int64_t max_position, int32_t rotary_dim, int32_t layout, int32_t inverse, void* out,
+                           int64_t out_row_stride, int64_t out_head_stride, uint32_t flags, void* stream) {
     const char* what = "rope_rotate";
+    if (flags & ~(uint32_t)NRC_ROPE_PASS_OUTSIDE) return fail(NRC_EINVAL, "%s: unknown flags 0x%x", what, flags);
     if (dtype < NRC_DTYPE_BF16 || dtype > NRC_DTYPE_F32)
         return fail(NRC_ENOTSUP, "%s: type %d (0 bf16, 1 FP16, 2 FP32)", what, dtype);
     if (table_dtype != NRC_DTYPE_BF16 && table_dtype != NRC_DTYPE_F32)
@@ -146,7 +155,7 @@ int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int3
     }
     nrc::RopeRotateArgs a{x, dtype, T, H, head_dim, x_row_stride, x_head_stride, positions, cos_sin,
                           table_dtype == NRC_DTYPE_F32, max_position, rotary_dim, layout == NRC_ROPE_HALF, inverse != 0,
-                          out, out_row_stride, out_head_stride};
+                          (flags & NRC_ROPE_PASS_OUTSIDE) != 0 && !in_place, out, out_row_stride, out_head_stride};
     return launch_status(nrc::launch_rope_rotate(a, (hipStream_t)stream), what);
 }
 

@@ -39,6 +39,7 @@ struct RopeRotateArgs {
     int64_t max_position;
     int32_t rotary_dim;
     bool half, inverse;
+    bool pass;  // rows without a row of the table are copied
     void* out;
     int64_t out_rs, out_hs;
 };

@@ -164,6 +164,7 @@ struct RotateDims {
     uint32_t units_per_row;
     SmallDiv per_row, per_head;
     float sign;  // of the sine: -1 for the inverse
+    bool pass;   // rows without a table row are copied, not left as they are
 };
 
 // Blocks: x the groups of rows_per_block rows, y the parts of a group. One
@@ -184,8 +185,24 @@ __global__ __launch_bounds__(256) void rope_rotate_kernel(const typename E::T* x
     const int64_t pos = positions[t];
     const typename E::T* src = x + t * d.x_rs + (int64_t)h * d.x_hs;
     typename E::T* dst = out + t * d.out_rs + (int64_t)h * d.out_hs;
-    if (pos < 0 || pos >= d.max_position) return;  // a row without a table row is left as it is
     const int32_t R = d.rotary_dim;
+    if (pos < 0 || pos >= d.max_position) {
+        if (!d.pass) return;
+        // the elements of the unit, as they are (a turn by 0 would make NaN of infinities)
+        if constexpr (VEC) {
+            constexpr int N = E::N;
+            const int32_t turning = HALF ? R / 2 / N : 0;
+            const int32_t e = (int32_t)u < turning ? (int32_t)u * N : (HALF ? R : 0) + ((int32_t)u - turning) * N;
+            store16(dst + e, load16(src + e));
+            if ((int32_t)u < turning) store16(dst + R / 2 + e, load16(src + R / 2 + e));
+        } else if ((int32_t)u < R / 2) {
+            dst[2 * u] = src[2 * u];
+            dst[2 * u + 1] = src[2 * u + 1];
+        } else {
+            dst[R / 2 + u] = src[R / 2 + u];
+        }
+        return;
+    }
     const int64_t cs = pos * R;
 
     if constexpr (VEC && HALF) {
@@ -257,6 +274,7 @@ void rotate(const RopeRotateArgs& a, hipStream_t stream) {
     d.T = a.T, d.x_rs = a.x_rs, d.x_hs = a.x_hs, d.out_rs = a.out_rs, d.out_hs = a.out_hs;
     d.max_position = a.max_position, d.rotary_dim = R;
     d.sign = a.inverse ? -1.0f : 1.0f;
+    d.pass = a.pass;
     const dim3 grid((uint32_t)((a.T + d.rows_per_block - 1) / d.rows_per_block),
                     (d.rows_per_block * d.units_per_row + 255) / 256);
     hipLaunchKernelGGL((rope_rotate_kernel<E, F32T, HALF, VEC>), grid, dim3(256), 0, stream,

@@ -1,0 +1,18 @@
+"""Calls of the operators around the cache that are refused on the host (no GPU)."""
+
+import ctypes
+import math
+
+import pytest
+
+from test_cache_ops_abi import EINVAL, ENOTSUP, FAKE, FAR, QUERIES, caller, lib  # noqa: F401
+
+
+def test_rope_rotate_flags(lib):
+    call = caller(lib.nrc_rope_rotate_ex, dict(x=FAKE, dtype=0, T=4, H=2, d=64, xr=128, xh=64, pos=FAKE, cs=FAKE, tdtype=0,
+                                               maxp=10, R=64, layout=0, inverse=0, out=FAR, orr=128, oh=64, flags=1,
+                                               stream=None))
+    for flags in (2, 3, 1 << 31):
+        assert call(flags=flags) == EINVAL and b"flags" in lib.nrc_last_error()
+    assert call(layout=2) == EINVAL and call(dtype=3) == ENOTSUP
+    assert call(T=0, x=None, pos=None, cs=None, out=None) == 0
