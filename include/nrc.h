@@ -574,6 +574,26 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
                                    float softcap, uint16_t* out, float* lse, void* workspace,
                                    int64_t workspace_bytes, void* stream);
 
+/* Flags of nrc_context_tree_attention_ex. */
+#define NRC_ATTENTION_FILL_OUT 1u /* out 0 in rows that are no sequence's nodes */
+#define NRC_ATTENTION_FILL_LSE 2u /* lse -inf there */
+
+/*
+ * nrc_context_tree_attention_ex - nrc_context_tree_attention with flags
+ * (NRC_ATTENTION_*; 0: the same). They are for outputs whose memory holds
+ * nothing yet: the rows before the first sequence, behind the last and past
+ * max_nodes (or all, with B == 0) are written too, in the same launch.
+ * Unknown flags: NRC_EINVAL.
+ */
+int32_t nrc_context_tree_attention_ex(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
+                                      int32_t Hq, const uint16_t* cache, int64_t num_blocks, int64_t block_size,
+                                      int64_t block_stride, int64_t page_stride, int64_t head_stride, int32_t H,
+                                      const int32_t* tables, int64_t table_stride, int64_t table_width, int32_t B,
+                                      const int32_t* ctx_lens, const int32_t* q_starts, int32_t max_nodes,
+                                      int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale,
+                                      float softcap, uint16_t* out, float* lse, void* workspace,
+                                      int64_t workspace_bytes, uint32_t flags, void* stream);
+
 /*
  * nrc_context_tree_attention_workspace_bytes - the workspace of
  * nrc_context_tree_attention for these sizes on the current device: 0 when

@@ -156,6 +156,8 @@ def _load():
     queries = [_vp, _i64, _i64, _i64, _i32] + paged + [_vp, _vp, _i32, _i64, _vp, _i32, _f32, _f32]
     L.nrc_context_tree_attention.restype = _i32
     L.nrc_context_tree_attention.argtypes = queries + [_vp, _vp, _vp, _i64, _vp]
+    L.nrc_context_tree_attention_ex.restype = _i32
+    L.nrc_context_tree_attention_ex.argtypes = L.nrc_context_tree_attention.argtypes[:-1] + [ctypes.c_uint32, _vp]
     L.nrc_context_tree_attention_workspace_bytes.restype = _i64
     L.nrc_context_tree_attention_workspace_bytes.argtypes = [_i32, _i64, _i32, _i32, _i32, _i64]
     L.nrc_context_attention_mass.restype = _i32
@@ -1031,6 +1033,9 @@ def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tr
         q_starts.data_ptr(), max_nodes, max_ctx, mask, words, HEAD_DIM ** -0.5 if scale is None else scale, softcap)
 
 
+ATTENTION_FILL_OUT, ATTENTION_FILL_LSE = 1, 2
+
+
 def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx=None, tree_mask=None, scale=None,
                            softcap=0.0, out=None, lse=None, stream=None):
     """Drafted tokens attending to the cache of one layer -> (out [T, Hq, 64]
@@ -1050,19 +1055,24 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
               sequence; None: a chain (each node sees those up to itself)
     scale     factor of the scores (1/8); softcap: scores become
               softcap tanh(score / softcap) when it is not 0 (2^-10 .. 2^10)
-    A row that sees no key gets 0 and -inf. The keys of long contexts are split
+    A row that sees no key gets 0 and -inf; so does, in an output that is not
+    given, a row of no sequence or past max_nodes (in a given one it stays as it
+    is). The keys of long contexts are split
     over workgroups, with a workspace from torch's allocator."""
     torch = _torch or _get_torch()
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
                                                       tree_mask, scale, softcap)
+    flags = 0
     if out is None:
         out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
+        flags = ATTENTION_FILL_OUT
     else:
         _at(out, dev, "out")
         if out.dtype != torch.bfloat16 or out.shape != (T, Hq, HEAD_DIM) or not out.is_contiguous():
             raise ValueError("out must be a contiguous bfloat16 [T, Hq, 64]")
     if lse is None:
         lse = _empty((T, Hq), torch.float32, q.device, stream)
+        flags |= ATTENTION_FILL_LSE
     else:
         _float_lse(lse, dev, (T, Hq))
     lib = _load()
@@ -1075,8 +1085,8 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
     if need < 0:
         _check(need)
     ws = _empty((need,), torch.uint8, q.device, stream) if need > 0 else None
-    _call(q, lib.nrc_context_tree_attention, *args, out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(),
-          need, _stream(stream, q))
+    _call(q, lib.nrc_context_tree_attention_ex, *args, out.data_ptr(), lse.data_ptr(),
+          None if ws is None else ws.data_ptr(), need, flags, _stream(stream, q))
     return out, lse
 
 

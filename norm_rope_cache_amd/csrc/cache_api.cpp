@@ -280,7 +280,23 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
                                    int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale,
                                    float softcap, uint16_t* out, float* lse, void* workspace,
                                    int64_t workspace_bytes, void* stream) {
+    return nrc_context_tree_attention_ex(q, q_row_stride, q_head_stride, T, Hq, cache, num_blocks, block_size, block_stride,
+                                         page_stride, head_stride, H, tables, table_stride, table_width, B, ctx_lens,
+                                         q_starts, max_nodes, max_ctx, tree_mask, mask_words, scale, softcap, out, lse,
+                                         workspace, workspace_bytes, 0, stream);
+}
+
+int32_t nrc_context_tree_attention_ex(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T,
+                                      int32_t Hq, const uint16_t* cache, int64_t num_blocks, int64_t block_size,
+                                      int64_t block_stride, int64_t page_stride, int64_t head_stride, int32_t H,
+                                      const int32_t* tables, int64_t table_stride, int64_t table_width, int32_t B,
+                                      const int32_t* ctx_lens, const int32_t* q_starts, int32_t max_nodes,
+                                      int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale,
+                                      float softcap, uint16_t* out, float* lse, void* workspace,
+                                      int64_t workspace_bytes, uint32_t flags, void* stream) {
     const char* what = "context_tree_attention";
+    if (flags & ~(uint32_t)(NRC_ATTENTION_FILL_OUT | NRC_ATTENTION_FILL_LSE))
+        return fail(NRC_EINVAL, "%s: unknown flags 0x%x", what, flags);
     const bool work = B > 0 && T > 0;
     nrc::TreeAttentionArgs a{};
     if (int32_t rc = paged_cache(what, cache, num_blocks, block_size, block_stride, page_stride, head_stride, H, tables,
@@ -289,18 +305,20 @@ int32_t nrc_context_tree_attention(const uint16_t* q, int64_t q_row_stride, int6
     if (int32_t rc = queries(what, q, q_row_stride, q_head_stride, T, Hq, H, B, ctx_lens, q_starts, max_nodes, max_ctx,
                              tree_mask, mask_words, scale, softcap, &a.tq))
         return rc;
-    if (!work) return NRC_OK;
+    if (!work && (T == 0 || flags == 0)) return NRC_OK;
     if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
     if (const int64_t q_span = span(T, Hq, 64, q_row_stride, q_head_stride);
-        meet(q, q_span, out, T * Hq * 64, 2, 2) || meet(q, q_span, lse, T * Hq, 2) || meet(out, T * Hq * 64, lse, T * Hq, 2))
+        (q && (meet(q, q_span, out, T * Hq * 64, 2, 2) || meet(q, q_span, lse, T * Hq, 2))) || meet(out, T * Hq * 64, lse, T * Hq, 2))
         return fail(NRC_EINVAL, "%s: q, out and lse must lie apart from each other", what);
+    a.fill = flags;
+    a.out = out;
+    a.lse = lse;
+    if (!work) return launch_status(nrc::launch_tree_attention(a, (hipStream_t)stream), what);
     a.plan = nrc::plan_tree_attention(B, H, Hq / H, max_nodes, max_ctx, softcap > 0.0f, num_cus());
     const int64_t bytes = nrc::tree_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
-    a.out = out;
-    a.lse = lse;
     a.part = static_cast<float*>(workspace);
     if (bytes > 0 && a.plan.many)  // the last [B, 2] of it
         a.shares = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + bytes) - 2 * (int64_t)B;

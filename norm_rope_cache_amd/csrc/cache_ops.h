@@ -99,6 +99,7 @@ struct TreeAttentionArgs {
     float* part;      // splits > 1: the partial sums' rows, [., 64] then [., 2]
     int32_t* shares;  // many rows: [B, 2], each sequence's first group and its splits
     AttentionPlan plan;
+    uint32_t fill;  // NRC_ATTENTION_FILL_*
 };
 
 int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream);

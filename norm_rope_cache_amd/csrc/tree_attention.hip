@@ -22,6 +22,7 @@
 // keys. More rows (many_rows_kernel) are bound by the vector unit (the
 // exponentials and what feeds the matrix instructions): keys are staged in LDS
 // and shared by a workgroup's waves, 32 or 64 rows each.
+#include "../../include/nrc.h"
 #include "cache_ops.h"
 #include "kernels.h"
 #include "paged.h"
@@ -418,6 +419,34 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
     }
 }
 
+// The rows that no sequence's nodes are: out 0 and lse -inf where `fill` asks for it (an out whose memory holds nothing
+// yet). Those before the first sequence and behind the last over all workgroups, those past max_nodes (or of a range
+// that does not lie in [0, T]) by one a sequence. No workgroup writes another's rows, so nothing is waited for.
+__device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, uint16_t* out, float* lse) {
+    if (fill == 0u) return;
+    const int32_t heads = tq.H * tq.G, tid = (int32_t)threadIdx.x, threads = (int32_t)blockDim.x;
+    auto rows = [&](int32_t from, int32_t to, int32_t step) {
+#pragma unroll 1
+        for (int64_t r = from; r < to; r += step) {
+            if (fill & NRC_ATTENTION_FILL_OUT)
+                for (int32_t i = tid; i < heads * 8; i += threads)
+                    store16(out + r * heads * kHeadDim + 8 * i, U32x4{0u, 0u, 0u, 0u});
+            if (fill & NRC_ATTENTION_FILL_LSE)
+                for (int32_t i = tid; i < heads; i += threads) lse[r * heads + i] = -__builtin_inff();
+        }
+    };
+    const int32_t group = (int32_t)blockIdx.x, groups = (int32_t)gridDim.x;
+    const int32_t begin = tq.B > 0 ? tq.q_starts[0] : tq.T, end = tq.B > 0 ? tq.q_starts[tq.B] : tq.T;
+    const int32_t before = begin > tq.T ? tq.T : begin;
+    rows(group, before, groups);
+    const int32_t behind = end < 0 ? 0 : end;
+    if (behind < tq.T && group < tq.T - behind) rows(behind + group, tq.T, groups);
+    for (int32_t b = group; b < tq.B; b += groups) {
+        const int32_t lo = tq.q_starts[b], hi = tq.q_starts[b + 1];
+        rows((lo < 0 ? 0 : lo) + nodes_of(tq, b).count, hi > tq.T ? tq.T : hi, 1);
+    }
+}
+
 // Few rows (up to 16 R, R <= 2): one workgroup per (sequence, KV head,
 // split); its WAVES waves hold the same rows and take the split's tiles in turn, and
 // join their sums in LDS. A tile is 32 keys by 16 R rows:
@@ -439,8 +468,9 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
 template <int R, int WAVES, bool CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                               uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                              float* __restrict__ part) {
+                                                              float* __restrict__ part, uint32_t fill) {
     extern __shared__ float smem[];
+    fill_rows(tq, fill, out, lse);
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
     const int32_t split = blockIdx.x % plan.splits;
@@ -753,7 +783,8 @@ template <int R, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse,
                                                                   float* __restrict__ part, int32_t* __restrict__ shares,
-                                                                  uint32_t groups) {
+                                                                  uint32_t groups, uint32_t fill) {
+    fill_rows(tq, fill, out, lse);
     constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
     constexpr int kBufs = buffers_of(WAVES);
     static_assert(kBufs * 8 * kRuns == 64, "a wave's block numbers of kBufs tiles are one load");
@@ -1099,6 +1130,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
     }
 }
 
+// Without a sequence every row is one of nobody's.
+__global__ __launch_bounds__(256) void fill_rows_kernel(TreeQueries tq, uint32_t fill, uint16_t* __restrict__ out,
+                                                        float* __restrict__ lse) {
+    fill_rows(tq, fill, out, lse);
+}
+
 // The splits of a row joined: 16 lanes a row, 4 elements of d a lane, eight splits' loads on the way at a
 // time. Bound by the latency of one row's loads.
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq, AttentionPlan plan,
@@ -1177,7 +1214,7 @@ int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
     static_assert(kLds <= 65536, "above, the limit would have to be raised");
     hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3((uint32_t)a.tq.B * a.tq.H * a.plan.splits), dim3(64 * WAVES), kLds, stream, a.kv,
-                       a.tq, a.plan, a.out, a.lse, a.part);
+                       a.tq, a.plan, a.out, a.lse, a.part, a.fill);
     return 0;
 }
 
@@ -1198,7 +1235,7 @@ int launch_many(const TreeAttentionArgs& a, hipStream_t stream) {
     static std::atomic<int> done[64] = {};
     if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
-                       a.shares, groups);
+                       a.shares, groups, a.fill);
     return 0;
 }
 
@@ -1259,6 +1296,11 @@ int64_t tree_attention_workspace(const AttentionPlan& p, int64_t T, int64_t head
 int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
     int rc;
     const bool capped = a.tq.softcap > 0.0f;
+    if (a.tq.B == 0) {
+        hipLaunchKernelGGL(fill_rows_kernel, dim3((uint32_t)(a.tq.T < 1024 ? a.tq.T : 1024)), dim3(256), 0, stream, a.tq,
+                           a.fill, a.out, a.lse);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
     if (a.plan.many)
         rc = a.plan.q_tiles == 4 ? launch_many<2, 8, true>(a, stream)
              : a.plan.waves == 8 ? (capped ? launch_many<1, 8, true>(a, stream) : launch_many<1, 8, false>(a, stream))

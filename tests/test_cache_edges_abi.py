@@ -16,3 +16,13 @@ def test_rope_rotate_flags(lib):
         assert call(flags=flags) == EINVAL and b"flags" in lib.nrc_last_error()
     assert call(layout=2) == EINVAL and call(dtype=3) == ENOTSUP
     assert call(T=0, x=None, pos=None, cs=None, out=None) == 0
+
+
+def test_tree_attention_flags(lib):
+    call = caller(lib.nrc_context_tree_attention_ex, dict(QUERIES, out=FAR, lse=ctypes.c_void_p(0x20000000), ws=None,
+                                                          ws_bytes=0, flags=3, stream=None))
+    for flags in (4, 7, 1 << 31):
+        assert call(flags=flags) == EINVAL and b"flags" in lib.nrc_last_error()
+    assert call(Hq=7) == ENOTSUP and call(q=None) == EINVAL and call(out=FAKE) == EINVAL
+    assert call(B=0, out=None) == EINVAL and call(B=0, lse=None) == EINVAL  # every row is to be written
+    assert call(T=0, q=None, cache=None, tables=None, out=None, lse=None) == 0

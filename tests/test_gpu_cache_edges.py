@@ -51,3 +51,90 @@ def test_rotate_padded_rows_come_out_as_they_went_in(nrc, dtype, layout, H, d, R
     assert torch.equal(out.view(bits)[outside.cuda()], x.view(bits)[outside.cuda()])
     inside = nrc.rope_rotate(x[~outside.cuda()], pos[~outside].cuda(), table, layout=layout, inverse=inverse)
     assert torch.equal(out[~outside.cuda()], inside)
+
+
+# few and many rows, each in one piece and split over workgroups
+@pytest.mark.parametrize("ctx,nodes,H,G", [([20, 30], [3, 6], 2, 4), ([5000, 1300], [3, 2], 1, 2), ([900, 130], [30, 12], 1, 4),
+                                           ([40, 33] * 40, [9, 12] * 40, 8, 4)])
+def test_attention_rows_of_no_sequence(nrc, ctx, nodes, H, G):
+    """Rows before the first sequence, behind the last and past max_nodes, in outputs of the call's own: 0 and -inf; the
+    others' bits are those without such rows."""
+    bt = ref.Batch(ctx, nodes, H=H, G=G, seed=50)
+    d = bt.dev()
+    before, behind = 5, 300
+    q = torch.cat([d["q"][:1].expand(before, -1, -1), d["q"], d["q"][:1].expand(behind, -1, -1)])
+    mask = torch.cat([d["tree_mask"][:1].expand(before, -1), d["tree_mask"], d["tree_mask"][:1].expand(behind, -1)])
+    starts = d["q_starts"] + before
+    T, Hq = q.shape[:2]
+    want, want_l = nrc.context_tree_attention(d["q"], d["cache"], d["tables"], d["ctx_lens"], d["q_starts"], max(nodes),
+                                              tree_mask=d["tree_mask"], max_ctx=max(ctx))
+    for most in (max(nodes), min(nodes)):
+        owned = torch.zeros(T, dtype=torch.bool)
+        for b, n in enumerate(nodes):
+            lo = before + int(bt.q_starts[b])
+            owned[lo:lo + min(n, most)] = True
+        owned = owned.cuda()
+        call = lambda **kw: nrc.context_tree_attention(q, d["cache"], d["tables"], d["ctx_lens"], starts, most,
+                                                       tree_mask=mask, max_ctx=max(ctx), **kw)
+        poison(T * Hq * 128, T * Hq * 4)
+        out, lse = call()
+        assert bool((out[~owned] == 0).all()) and bool((lse[~owned] == -math.inf).all())
+        if most == max(nodes):
+            assert torch.equal(out[owned], want) and torch.equal(lse[owned], want_l)
+        given = torch.full_like(out, 5.0)
+        same, l2 = call(out=given)
+        assert bool((given[~owned] == 5).all()) and torch.equal(given[owned], out[owned]) and torch.equal(l2, lse)
+        given = torch.full_like(lse, 6.0)
+        o2, same = call(lse=given)
+        assert bool((given[~owned] == 6).all()) and torch.equal(given[owned], lse[owned]) and torch.equal(o2, out)
+
+
+def test_attention_rows_of_ranges_outside(nrc):
+    """Ranges of rows outside q write nothing of their own: their rows are rows of no sequence."""
+    bt = ref.Batch([20, 30], [3, 6], seed=51)
+    d = bt.dev()
+    args = lambda starts: (d["q"], d["cache"], d["tables"], d["ctx_lens"],
+                           torch.tensor(starts, dtype=torch.int32, device="cuda"), 6)
+    want = nrc.context_tree_attention(*args([0, 3, 9]), tree_mask=d["tree_mask"])
+    for starts, owned in (([0, 3, 99], slice(0, 3)), ([-2, 3, 9], slice(3, 9)), ([0, 3, 2 ** 31 - 1], slice(0, 3)),
+                          ([50, 60, 70], slice(0, 0)), ([-9, -5, -2], slice(0, 0)), ([5, 5, 5], slice(0, 0))):
+        poison(9 * 8 * 128, 9 * 8 * 4)
+        out, lse = nrc.context_tree_attention(*args(starts), tree_mask=d["tree_mask"])
+        rest = torch.ones(9, dtype=torch.bool, device="cuda")
+        rest[owned] = False
+        assert bool((out[rest] == 0).all()) and bool((lse[rest] == -math.inf).all()), starts
+        assert torch.equal(out[owned], want[0][owned]) and torch.equal(lse[owned], want[1][owned]), starts
+
+
+def test_attention_without_a_sequence(nrc):
+    bt = ref.Batch([20, 30], [3, 6], seed=52)
+    d = bt.dev()
+    poison(9 * 8 * 128, 9 * 8 * 4)
+    out, lse = nrc.context_tree_attention(d["q"], d["cache"], d["tables"][:0], d["ctx_lens"][:0], d["q_starts"][:1], 1)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    given = torch.full_like(out, 5.0)
+    nrc.context_tree_attention(d["q"], d["cache"], d["tables"][:0], d["ctx_lens"][:0], d["q_starts"][:1], 1, out=given)
+    assert bool((given == 5).all())
+
+
+def test_captured_attention_of_a_padded_batch(nrc):
+    """T fixed at capture, sequences' rows moved under it: each replay leaves the rows of nobody at 0 and -inf."""
+    bt = ref.Batch([300, 200], [3, 6], seed=53)
+    d = bt.dev()
+    q = torch.cat([d["q"], d["q"]])
+    starts = torch.tensor([0, 3, 9], dtype=torch.int32, device="cuda")
+    call = lambda: nrc.context_tree_attention(q, d["cache"], d["tables"], d["ctx_lens"], starts, 6, max_ctx=300)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = call()
+    for s in ([0, 3, 9], [2, 4, 7], [0, 0, 1], [9, 12, 18]):
+        starts.copy_(torch.tensor(s, dtype=torch.int32))
+        out.fill_(3.0)
+        lse.fill_(3.0)
+        g.replay()
+        eager = call()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+        assert bool((out[:s[0]] == 0).all()) and bool((lse[s[2]:] == -math.inf).all())
