@@ -910,6 +910,34 @@ def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, orig
     return out
 
 
+_rotation = None  # the rotation as a torch.autograd.Function, once an x that requires grad has needed it
+
+
+def _get_rotation():
+    global _rotation
+    import torch
+
+    class Rotation(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, cos_sin, layout, inverse, stream):
+            ctx.save_for_backward(positions, cos_sin)
+            ctx.layout, ctx.inverse = layout, inverse
+            return rope_rotate(x, positions, cos_sin, layout, inverse, stream=stream)
+
+        @staticmethod
+        def backward(ctx, grad):
+            positions, cos_sin = ctx.saved_tensors
+            if grad.stride(2) != 1:  # (of a sum: one value for all)
+                grad = grad.clone(memory_format=torch.contiguous_format)
+            # the map is linear and orthogonal up to the table's magnitude: its transposed is the turn by the negative
+            # angles, and rows that came through as they were pass their gradient
+            back = rope_rotate(grad, positions, cos_sin, ctx.layout, not ctx.inverse)
+            return back, None, None, None, None, None
+
+    _rotation = Rotation
+    return Rotation
+
+
 def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=None, stream=None):
     """x [T, H, d] (bf16, float16 or float32; any row and head strides) with the
     first R = cos_sin.shape[1] elements of each head turned by its row's
@@ -922,6 +950,8 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
                keys) or "half" (pairs j, j + R / 2)
     inverse    turn back: the gradient of the rotation
     out        x itself, or a tensor apart from it (default: a new one)
+    An x that requires grad gets its gradient (by the inverse, on the current
+    stream of the forward call); it takes no out, and cos_sin gets none.
     """
     torch = _torch or _get_torch()
     code = _dtype_code(x.dtype, "x")
@@ -942,6 +972,12 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
         raise ValueError("cos_sin must be a contiguous [max_position, R]")
     if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int64 [T] tensor")
+    if (x.requires_grad or cos_sin.requires_grad) and torch.is_grad_enabled():
+        if cos_sin.requires_grad:
+            raise ValueError("cos_sin gets no gradient: detach it")
+        if out is not None:
+            raise ValueError("an x that requires grad takes no out: detach it, or call under torch.no_grad()")
+        return (_rotation or _get_rotation()).apply(x, positions, cos_sin, layout, inverse, stream)
     if out is None:
         out = _empty(shape, x.dtype, x.device, stream)
         ost, flags = (H * d, d), ROPE_PASS_OUTSIDE

@@ -138,3 +138,106 @@ def test_captured_attention_of_a_padded_batch(nrc):
         torch.cuda.synchronize()
         assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
         assert bool((out[:s[0]] == 0).all()) and bool((lse[s[2]:] == -math.inf).all())
+
+
+def turned(x, pos, table, layout, inverse):
+    """The rotation in 64 bits, of a tensor that may carry a graph; rows outside the table as they are."""
+    R = table.shape[1]
+    row = table[pos.clamp(0, table.shape[0] - 1)][:, None, :]
+    c, s = row[..., :R // 2], row[..., R // 2:] * (-1 if inverse else 1)
+    a, b = (x[..., 0:R:2], x[..., 1:R:2]) if layout == "interleaved" else (x[..., :R // 2], x[..., R // 2:R])
+    y, z = a * c - b * s, b * c + a * s
+    y = torch.stack([y, z], -1).flatten(-2) if layout == "interleaved" else torch.cat([y, z], -1)
+    inside = ((pos >= 0) & (pos < table.shape[0]))[:, None, None]
+    return torch.where(inside, torch.cat([y, x[..., R:]], -1), x)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotate_carries_the_gradient(nrc, dtype, layout, inverse):
+    """Against the formula's gradient in 64 bits and against differences; a padded row's passes through."""
+    T, H, d, R = 7, 3, 24, 16
+    gen = torch.Generator().manual_seed(54)
+    x = torch.randn(T, H, d, generator=gen).to(dtype)
+    g = torch.randn(T, H, d, generator=gen).to(dtype)
+    pos = torch.randint(0, 40, (T,), generator=gen)
+    pos[4] = -1
+    table = nrc.rope_table(40, R, dtype=torch.float32, magnitude=1.25)
+    table64 = table.double().cpu()
+    leaf = x.cuda().requires_grad_()
+    y = nrc.rope_rotate(leaf, pos.cuda(), table, layout=layout, inverse=inverse)
+    assert y.requires_grad
+    y.backward(g.cuda())
+    leaf64 = x.double().requires_grad_()
+    turned(leaf64, pos, table64, layout, inverse).backward(g.double())
+    # two products and sums of FP32 (2^-24 each of the terms' size, up to 2 sqrt(2) x 1.25 g) and half a step of the type
+    want = leaf64.grad
+    tol = want.abs() * torch.finfo(dtype).eps / 2 + 4 * 2.0 ** -24 * 3.6 * float(g.double().abs().max())
+    assert bool(((leaf.grad.double().cpu() - want).abs() <= tol).all())
+    assert torch.equal(leaf.grad[4].cpu(), g[4])
+    if dtype == torch.float32:
+        # the map is linear: differences of its own outputs over steps of 1
+        f = lambda t: float((nrc.rope_rotate(t.cuda(), pos.cuda(), table, layout=layout, inverse=inverse).double().cpu()
+                             * g.double()).sum())
+        for at in ((2, 1, 0), (2, 1, 9), (2, 1, 20), (4, 0, 3)):
+            e = torch.zeros_like(x)
+            e[at] = 1.0
+            assert abs((f(e) - f(-e)) / 2 - float(want[at])) <= 8 * 2.0 ** -24 * float(g.abs().max()) * 1.25
+    # a sum's gradient is one value without strides; a second derivative is the rotation again
+    leaf.grad = None
+    nrc.rope_rotate(leaf, pos.cuda(), table, layout=layout, inverse=inverse).sum().backward()
+    ones = nrc.rope_rotate(torch.ones_like(leaf).detach(), pos.cuda(), table, layout=layout, inverse=not inverse)
+    assert torch.equal(leaf.grad, ones)
+    go = g.cuda().requires_grad_()
+    grad, = torch.autograd.grad(nrc.rope_rotate(leaf, pos.cuda(), table, layout=layout, inverse=inverse), leaf, go,
+                                create_graph=True)
+    again, = torch.autograd.grad(grad, go, x.cuda())
+    assert torch.equal(again, nrc.rope_rotate(x.cuda(), pos.cuda(), table, layout=layout, inverse=inverse))
+
+
+def test_rotate_gradient_is_refused_or_not_wanted(nrc):
+    x = torch.randn(5, 2, 64, device="cuda", requires_grad=True)
+    pos = torch.arange(5, device="cuda")
+    table = nrc.rope_table(10, 64, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        nrc.rope_rotate(x, pos, table, out=torch.empty_like(x))
+    with pytest.raises(ValueError):
+        nrc.rope_rotate(x, pos, table, out=x)
+    with pytest.raises(ValueError):
+        nrc.rope_rotate(x.detach(), pos, table.clone().requires_grad_())
+    with torch.no_grad():
+        y = nrc.rope_rotate(x, pos, table, out=torch.empty_like(x))
+        z = nrc.rope_rotate(x, pos, table.clone().requires_grad_())
+    assert not y.requires_grad and torch.equal(y, z)
+    assert not nrc.rope_rotate(x.detach(), pos, table).requires_grad
+    empty = nrc.rope_rotate(x[:0], pos[:0], table)
+    empty.sum().backward()
+    assert bool((x.grad == 0).all())
+
+
+def test_rotate_gradient_captured_and_on_a_stream(nrc):
+    gen = torch.Generator().manual_seed(55)
+    x = torch.randn(50, 4, 64, generator=gen).cuda().requires_grad_()
+    g = torch.randn(50, 4, 64, generator=gen).cuda()
+    pos = torch.arange(50, device="cuda")
+    table = nrc.rope_table(50, 64)
+    step = lambda **kw: torch.autograd.grad(nrc.rope_rotate(x, pos, table, **kw), x, g)[0]
+    want = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        on_stream = step()
+    s.synchronize()
+    assert torch.equal(on_stream, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(3):
+        g.mul_(2.0)
+        out.zero_()
+        graph.replay()
+        eager = step()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(out, want * 2.0 ** (k + 1))
