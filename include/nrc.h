@@ -494,10 +494,11 @@ int32_t nrc_rope_table(int64_t start, int64_t count, int32_t rotary_dim, int32_t
  *              rotary_dim on are copied.
  *   inverse    1: turns by the negative angles (the transposed, for gradients).
  *   out        the same shape and type, its own strides; x itself (same
- *              pointer and strides), or memory apart from x's.
+ *              pointer and strides), or memory apart from x's; apart from
+ *              positions and cos_sin.
  * (a, b) -> (a c - b s, b c + a s), each an FP32 product and one FMA, rounded to
  * the type once. T == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or
- * misaligned operands, shapes, strides, an out that overlaps x or itself),
+ * misaligned operands, shapes, strides, an out that overlaps x, itself or the others),
  * NRC_ENOTSUP (types, too many rows or elements for one call).
  */
 int32_t nrc_rope_rotate(const void* x, int32_t dtype, int64_t T, int32_t H, int32_t head_dim, int64_t x_row_stride,

@@ -67,6 +67,12 @@ int64_t type_bytes(int32_t dtype) { return dtype == NRC_DTYPE_F32 ? 4 : 2; }
 // Elements from the first to the last of a [T, H, d] view, plus one.
 int64_t span(int64_t T, int64_t H, int64_t d, int64_t rs, int64_t hs) { return (T - 1) * rs + (H - 1) * hs + d; }
 
+// Do elements [p, p + n) and [q, q + m), of 4 bytes unless said otherwise, meet?
+bool meet(const void* p, int64_t n, const void* q, int64_t m, int p_bytes = 4, int q_bytes = 4) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    return n > 0 && m > 0 && a < b + q_bytes * (uint64_t)m && b < a + p_bytes * (uint64_t)n;
+}
+
 }  // namespace
 
 extern "C" {
@@ -147,12 +153,15 @@ int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, i
         return fail(NRC_EINVAL, "%s: out's heads overlap", what);
     const bool in_place = x == out && x_row_stride == out_row_stride && x_head_stride == out_head_stride;
     if (!in_place) {
-        const char* x0 = (const char*)x;
-        const char* o0 = (const char*)out;
-        if (x0 < o0 + span(T, H, head_dim, out_row_stride, out_head_stride) * eb &&
-            o0 < x0 + span(T, H, head_dim, x_row_stride, x_head_stride) * eb)
+        if (meet(x, span(T, H, head_dim, x_row_stride, x_head_stride), out,
+                 span(T, H, head_dim, out_row_stride, out_head_stride), (int)eb, (int)eb))
             return fail(NRC_EINVAL, "%s: out must be x itself or lie apart from it", what);
     }
+    // other workgroups still read these
+    const int64_t out_span = span(T, H, head_dim, out_row_stride, out_head_stride);
+    if (meet(out, out_span, positions, T, (int)eb, 8) ||
+        meet(out, out_span, cos_sin, max_position * rotary_dim, (int)eb, (int)type_bytes(table_dtype)))
+        return fail(NRC_EINVAL, "%s: out must lie apart from positions and cos_sin", what);
     nrc::RopeRotateArgs a{x, dtype, T, H, head_dim, x_row_stride, x_head_stride, positions, cos_sin,
                           table_dtype == NRC_DTYPE_F32, max_position, rotary_dim, layout == NRC_ROPE_HALF, inverse != 0,
                           (flags & NRC_ROPE_PASS_OUTSIDE) != 0 && !in_place, out, out_row_stride, out_head_stride};
@@ -244,12 +253,6 @@ int32_t per_cell(const char* what, const char* name, const void* p, int64_t bs, 
     if (bs < 0 || hs < 0 || bs > kBig || hs > kBig)
         return fail(NRC_EINVAL, "%s: strides of %s must lie in [0, 2^40]", what, name);
     return NRC_OK;
-}
-
-// Do elements [p, p + n) and [q, q + m), of 4 bytes unless said otherwise, meet?
-bool meet(const void* p, int64_t n, const void* q, int64_t m, int p_bytes = 4, int q_bytes = 4) {
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return n > 0 && m > 0 && a < b + q_bytes * (uint64_t)m && b < a + p_bytes * (uint64_t)n;
 }
 
 int32_t max_moves(int64_t width, int32_t budget) {

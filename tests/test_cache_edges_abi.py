@@ -26,3 +26,18 @@ def test_tree_attention_flags(lib):
     assert call(Hq=7) == ENOTSUP and call(q=None) == EINVAL and call(out=FAKE) == EINVAL
     assert call(B=0, out=None) == EINVAL and call(B=0, lse=None) == EINVAL  # every row is to be written
     assert call(T=0, q=None, cache=None, tables=None, out=None, lse=None) == 0
+
+
+def at(p, offset):
+    return ctypes.c_void_p(p.value + offset)
+
+
+def test_rope_rotate_out_apart_from_what_it_reads(lib):
+    """Positions of 4 rows, a table [10, 64] bf16 (1280 bytes), out [4, 2, 64] bf16 (1024 bytes)."""
+    ok = dict(x=ctypes.c_void_p(0x1000000), dtype=0, T=4, H=2, d=64, xr=128, xh=64, pos=ctypes.c_void_p(0x2000000),
+              cs=ctypes.c_void_p(0x3000000), tdtype=0, maxp=10, R=64, layout=0, inverse=0, out=FAR, orr=128, oh=64,
+              stream=None)
+    call = caller(lib.nrc_rope_rotate, ok)
+    for out in (at(ok["pos"], 0), at(ok["pos"], 24), at(ok["pos"], -1022), at(ok["cs"], 0), at(ok["cs"], 1278),
+                at(ok["cs"], -1022)):
+        assert call(out=out) == EINVAL and b"apart" in lib.nrc_last_error(), hex(out.value)
