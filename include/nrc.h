@@ -550,8 +550,8 @@ int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, i
  *   scale      factor of the scores, 2^-40 .. 2^40. softcap: 0, or 2^-10 ..
  *              2^10: scores become softcap tanh(score / softcap).
  *   out        [T, Hq, 64] bf16, contiguous, 16-byte aligned.
- *   lse        [T, Hq] float: the log of the row's sum of e^score. q, out and lse
- *              lie apart from each other.
+ *   lse        [T, Hq] float: the log of the row's sum of e^score. out, lse and
+ *              the workspace lie apart from each other and from the inputs.
  *   workspace  nrc_context_tree_attention_workspace_bytes(...) bytes,
  *              16-byte aligned, caller-owned; unused (may be NULL) when that is
  *              0. Its contents on return are unspecified; calls that share one

@@ -255,6 +255,28 @@ int32_t per_cell(const char* what, const char* name, const void* p, int64_t bs, 
     return NRC_OK;
 }
 
+// Memory that a call reads or writes, in bytes.
+struct Range {
+    const void* p;
+    int64_t bytes;
+};
+template <int W, int R>
+bool any_meet(const Range (&written)[W], const Range (&read)[R]) {
+    for (const Range& w : written)
+        for (const Range& r : read)
+            if (w.p && r.p && meet(w.p, w.bytes, r.p, r.bytes, 1, 1)) return true;
+    return false;
+}
+// From the first of a layer's cells to the last (at most 2^62 bytes: strides go up to 2^40 elements).
+Range cells_range(const nrc::PagedCache& c, int32_t H) {
+    const __int128 elements = (__int128)(c.num_blocks - 1) * c.block_stride + (__int128)(c.block_size - 1) * c.page_stride +
+                              (__int128)(H - 1) * c.head_stride + 2 * NRC_HEAD_DIM;
+    return Range{c.cache, elements > ((int64_t)1 << 61) ? (int64_t)1 << 62 : 2 * (int64_t)elements};
+}
+Range tables_range(const nrc::PagedCache& c, int32_t B) {
+    return Range{c.tables, 4 * ((B - 1) * c.table_stride + (int64_t)c.table_width)};
+}
+
 int32_t max_moves(int64_t width, int32_t budget) {
     const int64_t over = width - budget;
     return over <= 0 ? 0 : (int32_t)(over < budget ? over : budget);
@@ -311,8 +333,9 @@ int32_t nrc_context_tree_attention_ex(const uint16_t* q, int64_t q_row_stride, i
     if (!work && (T == 0 || flags == 0)) return NRC_OK;
     if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
     if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
-    if (const int64_t q_span = span(T, Hq, 64, q_row_stride, q_head_stride);
-        (q && (meet(q, q_span, out, T * Hq * 64, 2, 2) || meet(q, q_span, lse, T * Hq, 2))) || meet(out, T * Hq * 64, lse, T * Hq, 2))
+    const Range out_range{out, T * Hq * 128}, lse_range{lse, T * Hq * 4},
+        q_range{q, 2 * span(T, Hq, 64, q_row_stride, q_head_stride)};
+    if (any_meet({out_range, lse_range}, {q_range}) || any_meet({out_range}, {lse_range}))
         return fail(NRC_EINVAL, "%s: q, out and lse must lie apart from each other", what);
     a.fill = flags;
     a.out = out;
@@ -322,6 +345,13 @@ int32_t nrc_context_tree_attention_ex(const uint16_t* q, int64_t q_row_stride, i
     const int64_t bytes = nrc::tree_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
+    // other workgroups still read these
+    const Range ws_range{workspace, bytes};
+    if (any_meet({out_range, lse_range, ws_range},
+                 {cells_range(a.kv, H), tables_range(a.kv, B), {ctx_lens, 4 * (int64_t)B}, {q_starts, 4 * ((int64_t)B + 1)},
+                  {tree_mask, 8 * T * mask_words}}) ||
+        any_meet({ws_range}, {q_range, out_range, lse_range}))
+        return fail(NRC_EINVAL, "%s: out, lse and the workspace must lie apart from each other and the inputs", what);
     a.part = static_cast<float*>(workspace);
     if (bytes > 0 && a.plan.many)  // the last [B, 2] of it
         a.shares = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + bytes) - 2 * (int64_t)B;

@@ -41,3 +41,33 @@ def test_rope_rotate_out_apart_from_what_it_reads(lib):
     for out in (at(ok["pos"], 0), at(ok["pos"], 24), at(ok["pos"], -1022), at(ok["cs"], 0), at(ok["cs"], 1278),
                 at(ok["cs"], -1022)):
         assert call(out=out) == EINVAL and b"apart" in lib.nrc_last_error(), hex(out.value)
+
+
+# the operands of QUERIES, each in memory of its own, with their bytes: 6 rows of 8 heads, a cache of 8 blocks of 2 heads
+# of 16 cells, 3 sequences of up to 4 blocks, a mask of a word a row
+APART = dict(q=0x1000000, cache=0x2000000, tables=0x3000000, ctx=0x4000000, starts=0x5000000, mask=0x6000000)
+SIZES = dict(q=6 * 512 * 2, cache=8 * 2 * 16 * 128 * 2, tables=3 * 4 * 4, ctx=12, starts=16, mask=6 * 8)
+
+
+def places(start, size, own, unit):
+    """Where `own` bytes, in steps of `unit`, meet [start, start + size): at its first byte, its last, from before it."""
+    return start, start + (size - 1) // unit * unit, start - own + unit
+
+
+def test_tree_attention_outputs_apart_from_the_inputs(lib):
+    kw = {k: ctypes.c_void_p(v) for k, v in APART.items()}
+    call = caller(lib.nrc_context_tree_attention, dict(QUERIES, out=FAR, lse=ctypes.c_void_p(0x20000000), ws=None,
+                                                       ws_bytes=0, stream=None))
+    for name in APART:
+        for out in places(APART[name], SIZES[name], 6 * 8 * 128, 16):
+            assert call(**kw, words=1, out=ctypes.c_void_p(out)) == EINVAL and b"apart" in lib.nrc_last_error(), (name, hex(out))
+        for lse in places(APART[name], SIZES[name], 6 * 8 * 4, 4):
+            assert call(**kw, words=1, lse=ctypes.c_void_p(lse)) == EINVAL and b"apart" in lib.nrc_last_error(), (name, hex(lse))
+    # a split context's workspace
+    long = dict(kw, max_ctx=100000, words=1)
+    need = lib.nrc_context_tree_attention_workspace_bytes(3, 6, 8, 2, 2, 100000)
+    assert need > 0
+    inside = [p for name in APART for p in places(APART[name], SIZES[name], need, 16)]
+    for ws in inside + [FAR.value, FAR.value + 6 * 8 * 128 - 16, FAR.value - need + 16, 0x20000000]:
+        if ws > 0:
+            assert call(**long, ws=ctypes.c_void_p(ws), ws_bytes=need) == EINVAL and b"apart" in lib.nrc_last_error(), hex(ws)
