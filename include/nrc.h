@@ -618,7 +618,8 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
  *   weights    [B, H, width] float, batch and head strides in elements, or
  *              NULL (0); out itself (same strides), or apart from out.
  *   decay      factor of the earlier weights.
- *   out        [B, H, width] float, batch and head strides in elements.
+ *   out        [B, H, width] float, batch and head strides in elements; apart
+ *              from every other input.
  * FP32 sums in one fixed order. B == 0 or width == 0 returns NRC_OK.
  * Errors as nrc_context_tree_attention.
  */

@@ -394,6 +394,12 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
     if (weights && weights != out && meet(weights, span(B, H, width, w_batch_stride, w_head_stride), out,
                                           span(B, H, width, out_batch_stride, out_head_stride)))
         return fail(NRC_EINVAL, "%s: weights must be out itself or lie apart from it", what);
+    // other workgroups still read these
+    if (any_meet({{out, 4 * span(B, H, width, out_batch_stride, out_head_stride)}},
+                 {{q, T > 0 ? 2 * span(T, Hq, 64, q_row_stride, q_head_stride) : 0}, cells_range(a.kv, H), tables_range(a.kv, B),
+                  {ctx_lens, 4 * (int64_t)B}, {q_starts, 4 * ((int64_t)B + 1)}, {tree_mask, 8 * T * mask_words},
+                  {lse, 4 * T * Hq}}))
+        return fail(NRC_EINVAL, "%s: out must lie apart from the inputs other than weights", what);
     a.lse = lse;
     a.weights = weights;
     a.w_bs = w_batch_stride;

@@ -71,3 +71,14 @@ def test_tree_attention_outputs_apart_from_the_inputs(lib):
     for ws in inside + [FAR.value, FAR.value + 6 * 8 * 128 - 16, FAR.value - need + 16, 0x20000000]:
         if ws > 0:
             assert call(**long, ws=ctypes.c_void_p(ws), ws_bytes=need) == EINVAL and b"apart" in lib.nrc_last_error(), hex(ws)
+
+
+def test_attention_mass_out_apart_from_the_inputs(lib):
+    """out [3, 2, 64] of strides 200 and 100: 564 floats from the first to the last."""
+    kw = {k: ctypes.c_void_p(v) for k, v in APART.items()}
+    lse = 0x7000000
+    call = caller(lib.nrc_context_attention_mass, dict(QUERIES, lse=ctypes.c_void_p(lse), w=None, wb=0, wh=0, decay=1.0,
+                                                       out=FAR, ob=200, oh=100, width=64, stream=None))
+    for name, start in {**APART, "lse": lse}.items():
+        for out in places(start, {**SIZES, "lse": 6 * 8 * 4}[name], 564 * 4, 4):
+            assert call(**kw, words=1, out=ctypes.c_void_p(out)) == EINVAL and b"apart" in lib.nrc_last_error(), (name, hex(out))
