@@ -652,8 +652,9 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
  *   sinks, recent, budget  >= 0, >= 0, >= 1.
  *   new_weights, new_positions  [B, H, budget] contiguous: of the kept cells in
  *              their new places; 0 and -1 from new_lens[b] on.
- *   new_lens   [B] int32: min(lens[b], budget). These three must lie apart from
- *              weights, positions, lens and ends, which are not written.
+ *   new_lens   [B] int32: min(lens[b], budget). These three, the
+ *              workspace and the cache must lie apart from each other and from
+ *              weights, positions, lens, ends and tables, which are not written.
  *   workspace  nrc_context_kv_evict_workspace_bytes(B, H, width, budget) bytes,
  *              16-byte aligned; unused (may be NULL) when that is 0. Contents on
  *              return unspecified; calls that share one must not overlap.

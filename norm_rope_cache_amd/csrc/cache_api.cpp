@@ -447,21 +447,24 @@ int32_t nrc_context_kv_evict(uint16_t* cache, int64_t num_blocks, int64_t block_
     if (!lens || !ends || !new_lens) return fail(NRC_EINVAL, "%s: NULL lens, ends or new_lens", what);
     if (!aligned(lens, 4) || !aligned(ends, 4) || !aligned(new_lens, 4))
         return fail(NRC_EINVAL, "%s: lens, ends and new_lens must be 4-byte aligned", what);
-    // other workgroups still read these when one writes those
-    const int64_t w_span = cells ? span(B, H, width, w_batch_stride, w_head_stride) : 0;
-    const int64_t p_span = cells ? span(B, H, width, p_batch_stride, p_head_stride) : 0;
-    const int64_t kept = (int64_t)B * H * budget;
-    const struct {
-        const void* p;
-        int64_t n;
-    } written[] = {{new_weights, kept}, {new_positions, kept}, {new_lens, B}},
-      read[] = {{weights, w_span}, {positions, p_span}, {lens, B}, {ends, B}};
-    for (const auto& w : written)
-        for (const auto& r : read)
-            if (meet(w.p, w.n, r.p, r.n))
-                return fail(NRC_EINVAL, "%s: new_weights, new_positions and new_lens must lie apart from the inputs", what);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
+    // other workgroups still read these when one writes those
+    const int64_t kept = 4 * (int64_t)B * H * budget;
+    const Range nw{new_weights, kept}, np{new_positions, kept}, nl{new_lens, 4 * (int64_t)B}, ws{workspace, bytes},
+        cells_moved = cells_range(a.kv, H);
+    if (any_meet({nw, np, nl, ws, cells_moved},
+                 {{weights, cells ? 4 * span(B, H, width, w_batch_stride, w_head_stride) : 0},
+                  {positions, cells ? 4 * span(B, H, width, p_batch_stride, p_head_stride) : 0},
+                  {lens, 4 * (int64_t)B},
+                  {ends, 4 * (int64_t)B},
+                  tables_range(a.kv, B)}) ||
+        any_meet({nw, np, nl, ws}, {cells_moved}) || any_meet({nw}, {np, nl, ws}) || any_meet({np}, {nl, ws}) ||
+        any_meet({nl}, {ws}))
+        return fail(NRC_EINVAL,
+                    "%s: new_weights, new_positions, new_lens, the workspace and the cache must lie apart from each "
+                    "other and from the inputs",
+                    what);
     a.B = B;
     a.H = H;
     a.lens = lens;

@@ -82,3 +82,26 @@ def test_attention_mass_out_apart_from_the_inputs(lib):
     for name, start in {**APART, "lse": lse}.items():
         for out in places(start, {**SIZES, "lse": 6 * 8 * 4}[name], 564 * 4, 4):
             assert call(**kw, words=1, out=ctypes.c_void_p(out)) == EINVAL and b"apart" in lib.nrc_last_error(), (name, hex(out))
+
+
+def test_kv_evict_outputs_apart_from_each_other_and_the_inputs(lib):
+    """3 sequences of 2 heads: 240 kept cells each of new_weights and new_positions, 3 new_lens, and a workspace."""
+    from test_cache_ops_abi import PAGED
+
+    names = ["cache", "tables", "lens", "w", "p", "ends", "nw", "np", "nl", "ws"]
+    at = {n: 0x10000000 * (i + 1) for i, n in enumerate(names)}
+    width, budget = 2400, 1200
+    need = lib.nrc_context_kv_evict_workspace_bytes(3, 2, width, budget)
+    assert need > 0
+    size = dict(SIZES, lens=12, ends=12, w=4 * 6 * width, p=4 * 6 * width, nw=4 * 6 * budget, np=4 * 6 * budget, nl=12, ws=need)
+    ok = dict(PAGED, lens=None, w=None, wb=2 * width, wh=width, p=None, pb=2 * width, ph=width, width=width, ends=None, sinks=0,
+              recent=0, budget=budget, nw=None, np=None, nl=None, ws=None, ws_bytes=need, stream=None)
+    ok.update({n: ctypes.c_void_p(a) for n, a in at.items()})
+    call = caller(lib.nrc_context_kv_evict, ok)
+    for out in ("nw", "np", "nl", "ws", "cache"):
+        for other in names:
+            if other == out:
+                continue
+            for place in places(at[other], size[other], size[out], 16 if out in ("ws", "cache") else 4):
+                got = call(**{out: ctypes.c_void_p(place)})
+                assert got == EINVAL and b"apart" in lib.nrc_last_error(), (out, other, hex(place))
