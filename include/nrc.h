@@ -642,8 +642,8 @@ int32_t nrc_context_attention_mass(const uint16_t* q, int64_t q_row_stride, int6
  * first into the first; the others stay where they are. Keys keep their
  * rotation, so attention over the kept cells needs no order.
  *
- *   cache      one layer's cache view as nrc_context_kv_store_ex's; cells
- *              move in place. A sequence's blocks must belong to it alone.
+ *   cache      one layer's cache view as nrc_context_kv_store_ex's, every cell
+ *              in memory of its own; cells move in place. A sequence's blocks must belong to it alone.
  *   tables, lens  as nrc_context_tree_attention: cells 0 .. lens[b] - 1.
  *   weights    [B, H, width] float and positions [B, H, width] int32, batch
  *              and head strides in elements; width >= every lens[b] (a longer

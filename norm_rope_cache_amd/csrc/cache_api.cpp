@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/nrc.h"
 #include "cache_ops.h"
 #include "status.h"
@@ -273,6 +275,21 @@ Range cells_range(const nrc::PagedCache& c, int32_t H) {
                               (__int128)(H - 1) * c.head_stride + 2 * NRC_HEAD_DIM;
     return Range{c.cache, elements > ((int64_t)1 << 61) ? (int64_t)1 << 62 : 2 * (int64_t)elements};
 }
+// Is every cell of a layer in memory of its own? So it is when each kind of step, from the smallest stride on, passes
+// all that the smaller ones reach.
+bool cells_apart(const nrc::PagedCache& c, int32_t H) {
+    struct Step {
+        int64_t stride, count;
+    } steps[] = {{c.page_stride, (int64_t)c.block_size}, {c.head_stride, H}, {c.block_stride, (int64_t)c.num_blocks}};
+    std::sort(steps, steps + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
+    __int128 reach = 2 * NRC_HEAD_DIM;
+    for (const Step& s : steps) {
+        if (s.count == 1) continue;
+        if (s.stride < reach) return false;
+        reach += (__int128)(s.count - 1) * s.stride;
+    }
+    return true;
+}
 Range tables_range(const nrc::PagedCache& c, int32_t B) {
     return Range{c.tables, 4 * ((B - 1) * c.table_stride + (int64_t)c.table_width)};
 }
@@ -438,6 +455,8 @@ int32_t nrc_context_kv_evict(uint16_t* cache, int64_t num_blocks, int64_t block_
                                  table_stride, table_width, B, work, &a.kv))
         return rc;
     if ((int64_t)B * H > 65535) return fail(NRC_ENOTSUP, "%s: more than 65535 heads of all sequences", what);
+    if (work && !cells_apart(a.kv, H))
+        return fail(NRC_EINVAL, "%s: cells of the cache overlap, and one's move would change another", what);
     const bool cells = work && width > 0;
     if (int32_t rc = per_cell(what, "weights", weights, w_batch_stride, w_head_stride, cells)) return rc;
     if (int32_t rc = per_cell(what, "positions", positions, p_batch_stride, p_head_stride, cells)) return rc;

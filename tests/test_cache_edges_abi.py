@@ -105,3 +105,22 @@ def test_kv_evict_outputs_apart_from_each_other_and_the_inputs(lib):
             for place in places(at[other], size[other], size[out], 16 if out in ("ws", "cache") else 4):
                 got = call(**{out: ctypes.c_void_p(place)})
                 assert got == EINVAL and b"apart" in lib.nrc_last_error(), (out, other, hex(place))
+
+
+def test_kv_evict_cells_in_memory_of_their_own(lib):
+    """Strides (block, page, head) of 8 blocks of 2 heads of 16 cells of 128."""
+    from test_cache_ops_abi import PAGED
+
+    at = [ctypes.c_void_p(0x10000000 * i) for i in range(1, 9)]
+    ok = dict(PAGED, cache=at[0], tables=at[1], lens=at[2], w=at[3], wb=128, wh=64, p=at[4], pb=128, ph=64, width=64,
+              ends=at[5], sinks=0, recent=0, budget=40, nw=at[6], np=at[7], nl=FAKE, ws=None, ws_bytes=0, stream=None)
+    call = caller(lib.nrc_context_kv_evict, ok)
+    for bst, pst, hst in ((4096, 128, 0), (4096, 0, 2048), (0, 128, 2048), (4096, 120, 2048), (4096, 128, 2040),
+                          (4088, 128, 2048), (2048, 128, 2048), (128, 128, 2048)):
+        assert call(bst=bst, pst=pst, hst=hst) == EINVAL and b"overlap" in lib.nrc_last_error(), (bst, pst, hst)
+    # one of a kind has no stride; an empty call is none
+    assert call(bst=4096, pst=128, hst=0, B=0) == 0
+    assert call(nb=1, bs=1, H=1, bst=0, pst=0, hst=0, nw=None) == EINVAL and b"NULL" in lib.nrc_last_error()
+    # pages, heads and blocks in any order: refused for what comes after
+    for kw in (dict(bst=4096, pst=256, hst=128), dict(bst=256, pst=2048, hst=128), dict(bst=128, pst=1024, hst=16384)):
+        assert call(**kw, nw=None) == EINVAL and b"NULL" in lib.nrc_last_error(), kw
