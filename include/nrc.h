@@ -471,7 +471,7 @@ int32_t nrc_context_kv_project_store(const uint16_t* normed, const uint16_t* w, 
  * Angles, cos and sin are in double; each element is rounded once.
  * count == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or misaligned out,
  * positions outside [0, NRC_ROPE_MAX_POSITION), a width or scaling argument
- * out of range), NRC_ENOTSUP (another type, rotary_dim out of range).
+ * out of range, angles or a magnitude that are not finite), NRC_ENOTSUP (another type, rotary_dim out of range).
  */
 int32_t nrc_rope_table(int64_t start, int64_t count, int32_t rotary_dim, int32_t width, double base, int32_t scaling,
                        double factor, double original_max, double low, double high, double magnitude, void* out,

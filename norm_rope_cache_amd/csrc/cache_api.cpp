@@ -59,6 +59,7 @@ const char* rope_angles(int32_t R, double base, int32_t scaling, double factor, 
             default:
                 break;
         }
+        if (!isfinite(v * (double)NRC_ROPE_MAX_POSITION)) return "the scaling's angles are not finite";
         f[j] = v;
     }
     return nullptr;
@@ -93,7 +94,7 @@ int32_t nrc_rope_table(int64_t start, int64_t count, int32_t rotary_dim, int32_t
                     4 * nrc::kMaxRotaryPairs);
     if (scaling < NRC_ROPE_SCALE_NONE || scaling > NRC_ROPE_SCALE_RAMP)
         return fail(NRC_EINVAL, "%s: scaling %d is unknown", what, scaling);
-    if (!isfinite(magnitude)) return fail(NRC_EINVAL, "%s: magnitude is not finite", what);
+    if (!isfinite((float)magnitude)) return fail(NRC_EINVAL, "%s: magnitude is not finite in FP32", what);
     if (start < 0 || count < 0 || start > NRC_ROPE_MAX_POSITION || count > NRC_ROPE_MAX_POSITION - start)
         return fail(NRC_EINVAL, "%s: positions %lld .. + %lld must lie in [0, %lld)", what, (long long)start,
                     (long long)count, (long long)NRC_ROPE_MAX_POSITION);

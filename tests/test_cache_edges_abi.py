@@ -124,3 +124,15 @@ def test_kv_evict_cells_in_memory_of_their_own(lib):
     # pages, heads and blocks in any order: refused for what comes after
     for kw in (dict(bst=4096, pst=256, hst=128), dict(bst=256, pst=2048, hst=128), dict(bst=128, pst=1024, hst=16384)):
         assert call(**kw, nw=None) == EINVAL and b"NULL" in lib.nrc_last_error(), kw
+
+
+def test_rope_table_of_finite_values(lib):
+    """Scalings and magnitudes that would make a table of NaN and infinities."""
+    call = caller(lib.nrc_rope_table, dict(start=0, count=8, R=64, width=64, base=1e4, scaling=0, factor=1.0, orig=4096.0,
+                                           low=1.0, high=2.0, magnitude=1.0, out=None, dtype=0, stream=None))
+    for kw in (dict(scaling=1, factor=1e-310), dict(scaling=1, factor=1e-303), dict(scaling=2, factor=1e-306),
+               dict(scaling=2, factor=1e-306, R=4, width=4), dict(scaling=3, factor=1e-309), dict(scaling=4, factor=1e-309),
+               dict(magnitude=1e39), dict(magnitude=-1e39)):
+        assert call(**kw) == EINVAL and b"finite" in lib.nrc_last_error(), kw
+    for kw in (dict(scaling=1, factor=1e-3), dict(scaling=1, factor=1e300), dict(scaling=4, factor=64.0), dict(magnitude=3e38)):
+        assert call(**kw) == EINVAL and b"NULL" in lib.nrc_last_error(), kw  # (refused for what comes after)
