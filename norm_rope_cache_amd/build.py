@@ -20,9 +20,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnrc.so")
 SOURCES = ["api.cpp", "context_norms.hip", "norms_ex.hip", "draft_boundary.hip", "kv_project.hip", "kv_store.hip", "selftest.hip",
            "cache_api.cpp", "rope.hip", "tree_attention.hip", "attention_mass.hip", "kv_evict.hip"]
-# the chain's kernels: what the stored counter measurements were taken of
-CHAIN_SOURCES = ["context_norms.hip", "device_common.h", "draft_boundary.hip", "kernels.h", "kv_project.hip", "kv_store.hip",
-                 "norms_ex.hip", "selftest.hip"]
+# the chain's kernels and the entry points that choose among them: what the stored counter measurements were taken of
+CHAIN_SOURCES = ["api.cpp", "context_norms.hip", "device_common.h", "draft_boundary.hip", "kernels.h", "kv_project.hip",
+                 "kv_store.hip", "norms_ex.hip", "selftest.hip", "status.h"]
 
 ARCH = "gfx950"
 COMMON = [
@@ -88,10 +88,9 @@ def _code_only(text):
 
 
 def source_hash():
-    """Hash of the chain's kernel sources and headers with comments and layout
-    removed (identifies the kernels that a stored counter measurement belongs
-    to; a change to comments, to host-side checks or to other operators keeps
-    it)."""
+    """Hash of the chain's sources and headers, kernels and entry points, with
+    comments and layout removed (identifies what a stored counter measurement
+    belongs to; a change to comments or to other operators keeps it)."""
     import hashlib
 
     h = hashlib.sha256()
