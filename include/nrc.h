@@ -465,7 +465,9 @@ int32_t nrc_context_kv_project_store(const uint16_t* normed, const uint16_t* w, 
  *                 RAMP    v_j (1 - m + m / factor), m = (j - a) / (b - a) held
  *                         to [0, 1], a and b the pair indexes where the turns
  *                         are `high` (rounded down, at least 0) and `low`
- *                         (rounded up, at most R / 2 - 1)
+ *                         (rounded up, at most R / 2 - 1, the last pair; the
+ *                         form in publications holds it to R - 1, other
+ *                         values where original_max > 2 pi low base^(1 - 2 / R))
  *   magnitude     factor of the turning pairs' cos and sin.
  *   out           [count, width] of dtype NRC_DTYPE_BF16 or NRC_DTYPE_F32.
  * Angles, cos and sin are in double; each element is rounded once.
@@ -558,8 +560,8 @@ int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, i
  *              must not overlap.
  * A row that sees no key gets out 0 and lse -inf. K and V of keys that a row does
  * not see do not reach it, NaN and infinities included. Scores, maxima and
- * sums are FP32; the weights are rounded to bf16 for the product with V, the
- * output once.
+ * sums are FP32 (a capped score is off by up to 2^-22 softcap, and lse with it);
+ * the weights are rounded to bf16 for the product with V, the output once.
  * Keys whose block is outside [0, num_blocks) or past the table are seen by
  * no row and not read. T == 0 or B == 0 returns NRC_OK.
  * Errors: NRC_EINVAL (NULL or misaligned operands, shapes, strides, scale,
@@ -614,7 +616,9 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
  *
  *   q .. softcap  as nrc_context_tree_attention.
  *   lse        [T, Hq] float from nrc_context_tree_attention. Rows with -inf
- *              add nothing.
+ *              add nothing. Its own rounding (2^-24 |lse|) is the weights'
+ *              relative error: scores of 2^17 leave them within a hundredth,
+ *              far beyond that they say nothing (0 or +inf).
  *   weights    [B, H, width] float, batch and head strides in elements, or
  *              NULL (0); out itself (same strides), or apart from out.
  *   decay      factor of the earlier weights.

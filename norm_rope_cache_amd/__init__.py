@@ -23,6 +23,8 @@ and the operators that use the cache the chain fills:
     context_tree_attention(q, cache, tables, ...)  drafted tokens attending to the cache -> (out, lse)
     context_attention_mass(q, cache, tables, ..., lse, ...)   the weight each cached cell receives
     context_kv_evict(cache, tables, lens, weights, ...)       the cells of most weight kept (in place)
+
+Of these rope_rotate records a gradient; the others' outputs carry no graph.
 """
 
 import ctypes
@@ -879,7 +881,8 @@ def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, orig
     scaling     "none"; "linear" (angles divided by factor); "base" (base
                 times factor^(R / (R - 2))); "bands" and "ramp" (slow pairs
                 divided, fast ones kept, those between `low` and `high` turns over
-                original_max in between: by their turns, or by their index)
+                original_max in between: by their turns, or by their index;
+                the ramp's upper index is held to the last pair)
     magnitude   factor of cos and sin
     """
     torch = _torch or _get_torch()
@@ -1091,6 +1094,7 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
               sequence; None: a chain (each node sees those up to itself)
     scale     factor of the scores (1/8); softcap: scores become
               softcap tanh(score / softcap) when it is not 0 (2^-10 .. 2^10)
+    The weights are rounded to bf16 for the product with V.
     A row that sees no key gets 0 and -inf; so does, in an output that is not
     given, a row of no sequence or past max_nodes (in a given one it stays as it
     is). The keys of long contexts are split
@@ -1193,7 +1197,8 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
                and head strides), width >= every length
     ends       [B] int32: one past the newest token's position
     sinks, recent  positions below sinks, and from ends - recent on, come first
-    Equal weights: the lower index stays. Kept cells past the new length move
+    Equal weights: the lower index stays, among more protected cells than the
+    budget too (the newest go: recent <= budget - sinks keeps them). Kept cells past the new length move
     into the holes before it; weights and positions follow them, into tensors
     apart from the given ones."""
     torch = _torch or _get_torch()

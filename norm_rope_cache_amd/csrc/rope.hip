@@ -12,14 +12,14 @@
 // by turning it by the pair's step (4 double operations, each step adding
 // about 1e-16). Bound by the double sincos where there are few positions (a
 // run of 1), by the double operations and 2-byte stores of a long table (131072
-// positions of 64: 17 MB in 9.2 us).
+// positions of 64: 17 MB in 8.0 us).
 //
 // Rotation: reads x, writes as much, and 3 operations per element: bound by
 // memory. One thread takes 16 bytes (interleaved: a run of whole pairs; half:
 // 16 bytes of the first halves and the 16 that go with them) of one head of
 // one row, so a wave covers whole heads with contiguous accesses. Products
 // and sums in FP32, one rounding to the output type. 16384 rows of 64 heads of 64:
-// 273 MB in 50.7 us (5.4 TB/s, as fast as a copy).
+// 273 MB in 54.3 us (5.0 TB/s; a copy of 1 GiB reaches 5.1 to 5.2).
 #include <type_traits>
 
 #include "../../include/nrc.h"

@@ -20,7 +20,7 @@
 // Up to 32 rows (few_rows_kernel) the cache's bytes bound it: K and V go from
 // memory to the matrix core through registers, each wave its own tiles of 32
 // keys. More rows (many_rows_kernel) are bound by the vector unit (the
-// exponentials and what feeds the matrix instructions): keys are staged in LDS
+// exponentials and what feeds the matrix instructions) and the matrix cores, which mostly take turns: keys are staged in LDS
 // and shared by a workgroup's waves, 32 or 64 rows each.
 #include "../../include/nrc.h"
 #include "cache_ops.h"
@@ -460,7 +460,7 @@ __device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, 
 //                 operands (operand c: d = 4 (l % 16) + c).
 // Bound by the cache's bytes: a wave keeps the next tile's K and V on the way
 // while it works on one, the tile after that's block numbers too (64 sequences of
-// up to 8192 keys, 8 heads: 685 MB in 139 us, 4.9 TB/s, a copy reaches 5.2).
+// up to 8192 keys, 8 heads: 685 MB in 137 us, 5.0 TB/s, a copy reaches 5.2).
 // PAGE16 (block_size a multiple of 16, page rows near each other): the 16
 // keys of half a tile lie in one page, so a tile's two bases are scalars.
 // Two workgroups of 4 waves a CU, as the splits are planned: R 2 keeps to half the registers for it (32 rows over
@@ -696,12 +696,13 @@ __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Key
 // Many rows: the WAVES waves of a workgroup hold 32 R rows each and share the
 // keys, staged in LDS kStage at a time in four buffers (of two workgroups a CU, two
 // each): while the waves work on one tile the next ones come in (global_load_lds, no
-// registers), and one barrier a tile. Bound by what the vector unit issues: a
+// registers), and one barrier a tile. Bound by what the vector unit issues and, uncapped, by the matrix cores in turn: a
 // matrix instruction takes it 8 cycles and keeps the matrix core 32, an
 // exponential takes 8, other operations 4; of 32 keys and 32 rows that is 8, 16 and
 // about 50. Measured: 620 TFLOP/s (4 sequences of 32768 keys, 8 heads, 512 rows
 // a head: 221 us; a large matrix product 1212), 490 with a softcap (an
-// exponential and a reciprocal more a score). Short shares are bound by their
+// exponential and a reciprocal more a score). By counters the vector unit is busy 65% of that time and the matrix
+// cores 36%, with a softcap 81% and 26%. Short shares are bound by their
 // loads' latency one after the other: lengths, block numbers, keys, masks.
 // LDS: K rows of 128 bytes whose 16-byte chunk c lies at c ^ (key & 7), so
 // that 8 lanes reading one chunk of 8 keys meet all banks; V rows with c at
