@@ -420,10 +420,11 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
 }
 
 // The rows that no sequence's nodes are: out 0 and lse -inf where `fill` asks for it (an out whose memory holds nothing
-// yet). Those before the first sequence and behind the last over all workgroups, those past max_nodes (or of a range
-// that does not lie in [0, T]) by one a sequence. No workgroup writes another's rows, so nothing is waited for.
-__device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, uint16_t* out, float* lse) {
-    if (fill == 0u) return;
+// yet). Those before the first sequence and behind the last over all `groups` workgroups that fill, those past
+// max_nodes (or of a range that does not lie in [0, T]) by one a sequence. No workgroup writes another's rows, so nothing is
+// waited for.
+__device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, uint16_t* out, float* lse, int32_t group,
+                                          int32_t groups) {
     const int32_t heads = tq.H * tq.G, tid = (int32_t)threadIdx.x, threads = (int32_t)blockDim.x;
     auto rows = [&](int32_t from, int32_t to, int32_t step) {
 #pragma unroll 1
@@ -435,7 +436,6 @@ __device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, 
                 for (int32_t i = tid; i < heads; i += threads) lse[r * heads + i] = -__builtin_inff();
         }
     };
-    const int32_t group = (int32_t)blockIdx.x, groups = (int32_t)gridDim.x;
     const int32_t begin = tq.B > 0 ? tq.q_starts[0] : tq.T, end = tq.B > 0 ? tq.q_starts[tq.B] : tq.T;
     const int32_t before = begin > tq.T ? tq.T : begin;
     rows(group, before, groups);
@@ -445,6 +445,24 @@ __device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, 
         const int32_t lo = tq.q_starts[b], hi = tq.q_starts[b + 1];
         rows((lo < 0 ? 0 : lo) + nodes_of(tq, b).count, hi > tq.T ? tq.T : hi, 1);
     }
+}
+// The attention's workgroups fill beside their work, or, where that would be more than kFillBytes each, ones of their own
+// behind them, from workgroup `apart` on, on CUs that have nothing else to do (one token of one sequence in 1024 rows of 64
+// heads: 20.9 us by the 8 that attend, 11.3 by 132 more; the one row alone 10.6). Is this one of the latter?
+constexpr int64_t kFillBytes = 65536;
+__device__ __forceinline__ bool fills_alone(const TreeQueries& tq, uint32_t fill, uint32_t apart, uint16_t* out, float* lse) {
+    if (fill == 0u || blockIdx.x < apart) return false;
+    fill_rows(tq, fill, out, lse, (int32_t)(blockIdx.x - apart), (int32_t)(gridDim.x - apart));
+    return apart > 0u;
+}
+// How many of their own, beside `groups`: by the rows that cannot be a sequence's (most others are in proportion to the
+// workgroups).
+uint32_t fill_groups(const TreeAttentionArgs& a, int64_t groups) {
+    const int64_t rows = a.tq.T - (int64_t)a.tq.B * a.tq.max_nodes, heads = (int64_t)a.tq.H * a.tq.G;
+    const int64_t bytes = a.fill && rows > 0 ? rows * heads * (2 * kHeadDim + 4) : 0;
+    if (bytes <= groups * kFillBytes) return 0;
+    const int64_t n = (bytes + kFillBytes - 1) / kFillBytes;
+    return (uint32_t)(n < 1024 ? n : 1024);
 }
 
 // Few rows (up to 16 R, R <= 2): one workgroup per (sequence, KV head,
@@ -468,9 +486,9 @@ __device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, 
 template <int R, int WAVES, bool CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                               uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                              float* __restrict__ part, uint32_t fill) {
+                                                              float* __restrict__ part, uint32_t fill, uint32_t apart) {
     extern __shared__ float smem[];
-    fill_rows(tq, fill, out, lse);
+    if (fills_alone(tq, fill, apart, out, lse)) return;
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
     const int32_t split = blockIdx.x % plan.splits;
@@ -784,8 +802,8 @@ template <int R, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse,
                                                                   float* __restrict__ part, int32_t* __restrict__ shares,
-                                                                  uint32_t groups, uint32_t fill) {
-    fill_rows(tq, fill, out, lse);
+                                                                  uint32_t groups, uint32_t fill, uint32_t apart) {
+    if (fills_alone(tq, fill, apart, out, lse)) return;
     constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
     constexpr int kBufs = buffers_of(WAVES);
     static_assert(kBufs * 8 * kRuns == 64, "a wave's block numbers of kBufs tiles are one load");
@@ -1134,7 +1152,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
 // Without a sequence every row is one of nobody's.
 __global__ __launch_bounds__(256) void fill_rows_kernel(TreeQueries tq, uint32_t fill, uint16_t* __restrict__ out,
                                                         float* __restrict__ lse) {
-    fill_rows(tq, fill, out, lse);
+    fill_rows(tq, fill, out, lse, (int32_t)blockIdx.x, (int32_t)gridDim.x);
 }
 
 // The splits of a row joined: 16 lanes a row, 4 elements of d a lane, eight splits' loads on the way at a
@@ -1214,8 +1232,9 @@ template <int R, int WAVES, bool CAP, bool PAGE16>
 int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
     static_assert(kLds <= 65536, "above, the limit would have to be raised");
-    hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3((uint32_t)a.tq.B * a.tq.H * a.plan.splits), dim3(64 * WAVES), kLds, stream, a.kv,
-                       a.tq, a.plan, a.out, a.lse, a.part, a.fill);
+    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits, more = fill_groups(a, groups);
+    hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3(groups + more), dim3(64 * WAVES), kLds, stream, a.kv,
+                       a.tq, a.plan, a.out, a.lse, a.part, a.fill, more ? groups : 0u);
     return 0;
 }
 
@@ -1235,8 +1254,9 @@ int launch_many(const TreeAttentionArgs& a, hipStream_t stream) {
     auto kernel = many_rows_kernel<R, WAVES, CAP>;
     static std::atomic<int> done[64] = {};
     if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
-                       a.shares, groups, a.fill);
+    const uint32_t more = fill_groups(a, grid);
+    hipLaunchKernelGGL(kernel, dim3(grid + more), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse,
+                       a.part, a.shares, groups, a.fill, more ? grid : 0u);
     return 0;
 }
 

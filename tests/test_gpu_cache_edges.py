@@ -241,3 +241,25 @@ def test_rotate_gradient_captured_and_on_a_stream(nrc):
         eager = step()
         torch.cuda.synchronize()
         assert torch.equal(out, eager) and torch.equal(out, want * 2.0 ** (k + 1))
+
+
+@pytest.mark.parametrize("ctx,nodes,H,G", [([100], [1], 2, 4), ([9000], [3], 1, 2), ([700, 30], [40, 9], 1, 4), ([2000], [80], 2, 8)])
+def test_attention_in_a_large_padded_buffer(nrc, ctx, nodes, H, G):
+    """So many rows of nobody that workgroups of their own fill them: the others' bits are as without."""
+    bt = ref.Batch(ctx, nodes, H=H, G=G, seed=56, tree=False)
+    d = bt.dev()
+    rest = (d["cache"], d["tables"], d["ctx_lens"])
+    want, want_l = nrc.context_tree_attention(d["q"], *rest, d["q_starts"], max(nodes), max_ctx=max(ctx))
+    for before, behind in ((0, 20000), (20000, 0), (7001, 9000)):
+        q = torch.zeros(before + bt.T + behind, H * G, 64, dtype=torch.bfloat16, device="cuda")
+        q[before:before + bt.T] = d["q"]
+        poison(q.shape[0] * H * G * 128, q.shape[0] * H * G * 4)
+        out, lse = nrc.context_tree_attention(q, *rest, d["q_starts"] + before, max(nodes), max_ctx=max(ctx))
+        own = slice(before, before + bt.T)
+        assert torch.equal(out[own], want) and torch.equal(lse[own], want_l)
+        assert bool((out[:before] == 0).all()) and bool((out[before + bt.T:] == 0).all())
+        assert bool((lse[:before] == -math.inf).all()) and bool((lse[before + bt.T:] == -math.inf).all())
+        given = torch.full_like(out, 5.0)
+        _, l2 = nrc.context_tree_attention(q, *rest, d["q_starts"] + before, max(nodes), max_ctx=max(ctx), out=given)
+        assert bool((given[:before] == 5).all()) and bool((given[before + bt.T:] == 5).all())
+        assert torch.equal(given[own], want) and torch.equal(l2, lse)
