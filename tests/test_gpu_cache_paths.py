@@ -231,3 +231,61 @@ def test_table_of_runs(nrc, dtype, R, width, count, start, scaling, run):
     tol = want.abs() * (half_step(dtype) + 2.0 ** -24) + 1.1 * angle
     off = (got.double().cpu() - want).abs()
     assert bool((off <= tol).all()), float((off - tol).max())
+
+
+def whole_reference(q, run, ctx, words, step=2048):
+    """One sequence of one head in 64 bits on the GPU, some rows at a time, with cache_ref's bounds (attention's, and of
+    every key's received weight): out, lse, mass of the keys, and their bounds. run [keys, 128]; words: the mask or None."""
+    n, keys = q.shape[0], run.shape[0]
+    k, v = run[:, :64].double(), run[:, 64:].double()
+    kt, ka, va = k.T.contiguous(), k.abs().T.contiguous(), v.abs()
+    at = torch.arange(keys, device="cuda") - ctx
+    got = [torch.zeros(n, 64, dtype=torch.float64), torch.zeros(n, dtype=torch.float64), torch.zeros(n, 64, dtype=torch.float64),
+           torch.zeros(n, dtype=torch.float64)]
+    mass, bound = torch.zeros(keys, dtype=torch.float64, device="cuda"), torch.zeros(keys, dtype=torch.float64, device="cuda")
+    for lo in range(0, n, step):
+        qs = q[lo:lo + step].double()
+        s = torch.mm(qs, kt) * 0.125
+        e = 64 * 2.0 ** -23 * torch.mm(qs.abs(), ka) * 0.125 + s.abs() * 2.0 ** -21
+        if words is None:
+            sees = at[None, :] <= torch.arange(lo, lo + qs.shape[0], device="cuda")[:, None]
+        else:
+            w = words[lo:lo + step].gather(1, (at.clamp(min=0) // 64).expand(qs.shape[0], -1))
+            sees = ((w >> (at.clamp(min=0) % 64)) & 1 == 1) | (at < 0)
+        s = s.masked_fill(~sees, -math.inf)
+        l = torch.logsumexp(s, 1)
+        p = torch.exp(s - l[:, None])
+        o, A = torch.mm(p, v), torch.mm(p, va)
+        eps = e.masked_fill(~sees, 0.0).amax(1) + 2.0 ** -22 + keys * 2.0 ** -24
+        part = (o, l, o.abs() * 2.0 ** -8 + (2 * eps[:, None] + 2.0 ** -8) * A * 1.01, eps * 1.01 + (l.abs() + 24) * 3 * 2.0 ** -24)
+        for g, x in zip(got, part):
+            g[lo:lo + step] = x.cpu()
+        # with lse rounded to FP32, as the call takes it
+        d = torch.where(sees, s - l.float().double()[:, None], 0.0)
+        w = torch.where(sees, torch.exp(d), 0.0)
+        mass += w.sum(0)
+        bound += (w * (e + d.abs() * 3 * 2.0 ** -24 + 2.0 ** -22 + n * 2.0 ** -24) * 1.01).sum(0)
+    return (*got, mass.cpu(), (bound + mass.abs() * 2.0 ** -22 + 1e-37).cpu())
+
+
+@pytest.mark.parametrize("nodes,ctx,tree", [(65535, 1001, False), (20011, 300, True)])
+def test_the_longest_chains_and_trees(nrc, nodes, ctx, tree):
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    normal = lambda *shape: torch.randn(shape, generator=gen, device="cuda")
+    keys, bs = ctx + nodes, 16
+    blocks = -(-keys // bs)
+    q = (2 * normal(nodes, 1, 64)).to(torch.bfloat16)
+    cache = normal(blocks + 2, 1, bs, 128).to(torch.bfloat16)
+    tables = torch.randperm(blocks + 2, generator=gen, device="cuda")[None, :blocks].int()
+    words = None
+    if tree:  # (a node here sees half of all)
+        words = torch.randint(-2 ** 62, 2 ** 62, (nodes, (nodes + 63) // 64 + 1), generator=gen, device="cuda")
+    run_of = cache[tables[0].long()].transpose(1, 2).reshape(-1, 128)[:keys]
+    o, l, to, tl, m, tm = whole_reference(q[:, 0], run_of, ctx, words)
+    args = (q, cache, tables, torch.tensor([ctx], dtype=torch.int32, device="cuda"),
+            torch.tensor([0, nodes], dtype=torch.int32, device="cuda"))
+    out, lse = nrc.context_tree_attention(*args, nodes, tree_mask=words)
+    assert_within(out[:, 0], o, to, "out")
+    assert_within(lse[:, 0], l, tl, "lse")
+    got = nrc.context_attention_mass(*args, l.float().cuda()[:, None].contiguous(), nodes, tree_mask=words, width=keys)
+    assert_within(got[0, 0], m, tm, "mass")
