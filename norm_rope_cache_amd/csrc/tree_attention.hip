@@ -420,49 +420,50 @@ __device__ __forceinline__ void put_row4(const Results& t, int64_t at, int32_t d
 }
 
 // The rows that no sequence's nodes are: out 0 and lse -inf where `fill` asks for it (an out whose memory holds nothing
-// yet). Those before the first sequence and behind the last over all `groups` workgroups that fill, those past
-// max_nodes (or of a range that does not lie in [0, T]) by one a sequence. No workgroup writes another's rows, so nothing is
-// waited for.
-__device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, uint16_t* out, float* lse, int32_t group,
-                                          int32_t groups) {
-    const int32_t heads = tq.H * tq.G, tid = (int32_t)threadIdx.x, threads = (int32_t)blockDim.x;
-    auto rows = [&](int32_t from, int32_t to, int32_t step) {
-#pragma unroll 1
-        for (int64_t r = from; r < to; r += step) {
-            if (fill & NRC_ATTENTION_FILL_OUT)
-                for (int32_t i = tid; i < heads * 8; i += threads)
-                    store16(out + r * heads * kHeadDim + 8 * i, U32x4{0u, 0u, 0u, 0u});
-            if (fill & NRC_ATTENTION_FILL_LSE)
-                for (int32_t i = tid; i < heads; i += threads) lse[r * heads + i] = -__builtin_inff();
-        }
+// yet), by workgroups of their own behind the attending ones, number `group` of `groups`. Those before the first
+// sequence and behind the last are two runs of memory; sequences with rows past max_nodes (or with a range that does
+// not lie in [0, T]) are looked for 64 at a time by every wave. No workgroup writes another's rows, so nothing is waited for.
+__device__ __forceinline__ void fill_rows(const TreeQueries& tq, uint32_t fill, uint16_t* out, float* lse, uint32_t group,
+                                          uint32_t groups) {
+    const int64_t heads = tq.H * tq.G;
+    // rows from .. to - 1, 16 bytes a thread, by `among` threads of which this is number `me`
+    auto rows = [&](int64_t from, int64_t to, int64_t me, int64_t among) {
+        if (fill & NRC_ATTENTION_FILL_OUT)
+            for (int64_t i = from * heads * 8 + me; i < to * heads * 8; i += among) store16(out + 8 * i, U32x4{0u, 0u, 0u, 0u});
+        if (fill & NRC_ATTENTION_FILL_LSE)
+            for (int64_t i = from * heads + me; i < to * heads; i += among) lse[i] = -__builtin_inff();
     };
+    const int64_t me = (int64_t)group * blockDim.x + threadIdx.x, among = (int64_t)groups * blockDim.x;
     const int32_t begin = tq.B > 0 ? tq.q_starts[0] : tq.T, end = tq.B > 0 ? tq.q_starts[tq.B] : tq.T;
-    const int32_t before = begin > tq.T ? tq.T : begin;
-    rows(group, before, groups);
-    const int32_t behind = end < 0 ? 0 : end;
-    if (behind < tq.T && group < tq.T - behind) rows(behind + group, tq.T, groups);
-    for (int32_t b = group; b < tq.B; b += groups) {
-        const int32_t lo = tq.q_starts[b], hi = tq.q_starts[b + 1];
-        rows((lo < 0 ? 0 : lo) + nodes_of(tq, b).count, hi > tq.T ? tq.T : hi, 1);
+    rows(0, begin > tq.T ? tq.T : begin, me, among);
+    rows(end < 0 ? 0 : end, tq.T, me, among);
+    const int32_t lane = (int32_t)(threadIdx.x & 63u);
+    for (int64_t b0 = me - lane; b0 < tq.B; b0 += among) {
+        int32_t from = 0, to = 0;
+        if (b0 + lane < tq.B) {
+            const int32_t b = (int32_t)b0 + lane, lo = tq.q_starts[b], hi = tq.q_starts[b + 1];
+            from = (lo < 0 ? 0 : lo) + nodes_of(tq, b).count;
+            to = hi > tq.T ? tq.T : hi;
+        }
+        for (uint64_t left = __ballot(from < to); left != 0; left &= left - 1) {
+            const int l = __builtin_ctzll(left);
+            rows(__builtin_amdgcn_readlane(from, l), __builtin_amdgcn_readlane(to, l), lane, 64);
+        }
     }
 }
-// The attention's workgroups fill beside their work, or, where that would be more than kFillBytes each, ones of their own
-// behind them, from workgroup `apart` on, on CUs that have nothing else to do (one token of one sequence in 1024 rows of 64
-// heads: 20.9 us by the 8 that attend, 11.3 by 132 more; the one row alone 10.6). Is this one of the latter?
-constexpr int64_t kFillBytes = 65536;
-__device__ __forceinline__ bool fills_alone(const TreeQueries& tq, uint32_t fill, uint32_t apart, uint16_t* out, float* lse) {
-    if (fill == 0u || blockIdx.x < apart) return false;
-    fill_rows(tq, fill, out, lse, (int32_t)(blockIdx.x - apart), (int32_t)(gridDim.x - apart));
-    return apart > 0u;
-}
-// How many of their own, beside `groups`: by the rows that cannot be a sequence's (most others are in proportion to the
-// workgroups).
-uint32_t fill_groups(const TreeAttentionArgs& a, int64_t groups) {
-    const int64_t rows = a.tq.T - (int64_t)a.tq.B * a.tq.max_nodes, heads = (int64_t)a.tq.H * a.tq.G;
-    const int64_t bytes = a.fill && rows > 0 ? rows * heads * (2 * kHeadDim + 4) : 0;
-    if (bytes <= groups * kFillBytes) return 0;
-    const int64_t n = (bytes + kFillBytes - 1) / kFillBytes;
+// How many workgroups fill: one to 64 KiB of all rows, 1 to 1024. They run on CUs that have nothing else to do, or behind the
+// others: one token of one sequence 10.0 -> 10.2 us, in 1024 rows of 64 heads 11.3, in 16384 19; 64 sequences of up to 8192
+// keys 137.0 -> 137.3. (By the attending workgroups beside their work 10.5, 20.3, 133 and 138.0.)
+uint32_t fill_groups(const TreeAttentionArgs& a) {
+    if (a.fill == 0u) return 0u;
+    const int64_t n = ((int64_t)a.tq.T * a.tq.H * a.tq.G * (2 * kHeadDim + 4) + 65535) / 65536;
     return (uint32_t)(n < 1024 ? n : 1024);
+}
+
+// The filling alone, of a call without a sequence.
+__global__ __launch_bounds__(256) void fill_rows_kernel(TreeQueries tq, uint32_t fill, uint16_t* __restrict__ out,
+                                                        float* __restrict__ lse) {
+    fill_rows(tq, fill, out, lse, blockIdx.x, gridDim.x);
 }
 
 // Few rows (up to 16 R, R <= 2): one workgroup per (sequence, KV head,
@@ -486,9 +487,12 @@ uint32_t fill_groups(const TreeAttentionArgs& a, int64_t groups) {
 template <int R, int WAVES, bool CAP, bool PAGE16>
 __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void few_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                               uint16_t* __restrict__ out, float* __restrict__ lse,
-                                                              float* __restrict__ part, uint32_t fill, uint32_t apart) {
+                                                              float* __restrict__ part, uint32_t groups, uint32_t fill) {
     extern __shared__ float smem[];
-    if (fills_alone(tq, fill, apart, out, lse)) return;
+    if (blockIdx.x >= groups) {
+        fill_rows(tq, fill, out, lse, blockIdx.x - groups, gridDim.x - groups);
+        return;
+    }
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
     const int32_t split = blockIdx.x % plan.splits;
@@ -802,8 +806,11 @@ template <int R, int WAVES, bool CAP>
 __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv, TreeQueries tq, AttentionPlan plan,
                                                                   uint16_t* __restrict__ out, float* __restrict__ lse,
                                                                   float* __restrict__ part, int32_t* __restrict__ shares,
-                                                                  uint32_t groups, uint32_t fill, uint32_t apart) {
-    if (fills_alone(tq, fill, apart, out, lse)) return;
+                                                                  uint32_t groups, uint32_t grid, uint32_t fill) {
+    if (blockIdx.x >= grid) {
+        fill_rows(tq, fill, out, lse, blockIdx.x - grid, gridDim.x - grid);
+        return;
+    }
     constexpr int kRuns = kStage / 8 / WAVES;  // of 8 rows of K, and of V, that a wave brings in
     constexpr int kBufs = buffers_of(WAVES);
     static_assert(kBufs * 8 * kRuns == 64, "a wave's block numbers of kBufs tiles are one load");
@@ -1149,12 +1156,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
     }
 }
 
-// Without a sequence every row is one of nobody's.
-__global__ __launch_bounds__(256) void fill_rows_kernel(TreeQueries tq, uint32_t fill, uint16_t* __restrict__ out,
-                                                        float* __restrict__ lse) {
-    fill_rows(tq, fill, out, lse, (int32_t)blockIdx.x, (int32_t)gridDim.x);
-}
-
 // The splits of a row joined: 16 lanes a row, 4 elements of d a lane, eight splits' loads on the way at a
 // time. Bound by the latency of one row's loads.
 __global__ __launch_bounds__(256) void tree_attention_join_kernel(TreeQueries tq, AttentionPlan plan,
@@ -1232,9 +1233,9 @@ template <int R, int WAVES, bool CAP, bool PAGE16>
 int launch_few(const TreeAttentionArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
     static_assert(kLds <= 65536, "above, the limit would have to be raised");
-    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits, more = fill_groups(a, groups);
-    hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3(groups + more), dim3(64 * WAVES), kLds, stream, a.kv,
-                       a.tq, a.plan, a.out, a.lse, a.part, a.fill, more ? groups : 0u);
+    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
+    hipLaunchKernelGGL((few_rows_kernel<R, WAVES, CAP, PAGE16>), dim3(groups + fill_groups(a)), dim3(64 * WAVES), kLds, stream, a.kv,
+                       a.tq, a.plan, a.out, a.lse, a.part, groups, a.fill);
     return 0;
 }
 
@@ -1254,9 +1255,8 @@ int launch_many(const TreeAttentionArgs& a, hipStream_t stream) {
     auto kernel = many_rows_kernel<R, WAVES, CAP>;
     static std::atomic<int> done[64] = {};
     if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
-    const uint32_t more = fill_groups(a, grid);
-    hipLaunchKernelGGL(kernel, dim3(grid + more), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse,
-                       a.part, a.shares, groups, a.fill, more ? grid : 0u);
+    hipLaunchKernelGGL(kernel, dim3(grid + fill_groups(a)), dim3(64 * WAVES), many_lds(WAVES), stream, a.kv, a.tq, a.plan, a.out, a.lse, a.part,
+                       a.shares, groups, grid, a.fill);
     return 0;
 }
 
@@ -1318,8 +1318,7 @@ int launch_tree_attention(const TreeAttentionArgs& a, hipStream_t stream) {
     int rc;
     const bool capped = a.tq.softcap > 0.0f;
     if (a.tq.B == 0) {
-        hipLaunchKernelGGL(fill_rows_kernel, dim3((uint32_t)(a.tq.T < 1024 ? a.tq.T : 1024)), dim3(256), 0, stream, a.tq,
-                           a.fill, a.out, a.lse);
+        hipLaunchKernelGGL(fill_rows_kernel, dim3(fill_groups(a)), dim3(256), 0, stream, a.tq, a.fill, a.out, a.lse);
         return hipGetLastError() == hipSuccess ? 0 : -1;
     }
     if (a.plan.many)
