@@ -12,7 +12,7 @@
 // by turning it by the pair's step (4 double operations, each step adding
 // about 1e-16). Bound by the double sincos where there are few positions (a
 // run of 1), by the double operations and 2-byte stores of a long table (131072
-// positions of 64: 17 MB in 8.0 us).
+// positions of 64: 17 MB in 8.1 us).
 //
 // Rotation: reads x, writes as much, and 3 operations per element: bound by
 // memory. One thread takes 16 bytes (interleaved: a run of whole pairs; half:
