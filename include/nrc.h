@@ -522,6 +522,70 @@ int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, i
                            int64_t out_row_stride, int64_t out_head_stride, uint32_t flags, void* stream);
 
 /*
+ * nrc_qk_norm_rotate - the draft's own queries and keys made ready for the
+ * cache: each head normed (with gains or without) and turned by its row's
+ * position, in one pass (page "...cutedsl.draft.context", _sum_squares_64 and
+ * _rope: the same steps on the context's keys).
+ *
+ *   q, k       [T, Hq, head_dim] and [T, Hk, head_dim] of dtype (NRC_DTYPE_*), unit
+ *              stride in the head, row and head strides in elements. Hk = 0: no
+ *              keys (k and out_k may be NULL). head_dim 2 .. 256, T (Hq + Hk) <=
+ *              2^25. Heads that are whole 16-byte units, 16-byte aligned, take
+ *              16-byte accesses, others single elements.
+ *   q_weight, k_weight  [head_dim] gains of their dtype (NRC_DTYPE_*), or NULL: 1.
+ *   eps        at least 0.
+ *   positions, cos_sin, table_dtype, max_position, rotary_dim, layout
+ *              as nrc_rope_rotate: the first rotary_dim elements turn, a row whose
+ *              position is outside [0, max_position) is left as it is in the outputs
+ *              (NRC_ROPE_PASS_OUTSIDE in flags: is copied, without the norm).
+ *   out_q, out_k  like q and k, their own strides: the input itself (same pointer
+ *              and strides), or apart from q, k and each other. Parts of the rows
+ *              of one wider tensor lie apart.
+ * y = rot(x w / sqrt(mean x^2 + eps)) in FP32, rounded to the type once (nrc_context_kv_store
+ * rounds its keys between the norm and the turn too). T == 0 returns
+ * NRC_OK. Errors: NRC_EINVAL (NULL or misaligned operands, shapes, strides,
+ * outputs that overlap something, eps, unknown flags), NRC_ENOTSUP (types, head_dim, too
+ * many heads for one call).
+ */
+int32_t nrc_qk_norm_rotate(const void* q, int64_t q_row_stride, int64_t q_head_stride, int32_t Hq, const void* k,
+                           int64_t k_row_stride, int64_t k_head_stride, int32_t Hk, int32_t dtype, int64_t T,
+                           int32_t head_dim, const void* q_weight, int32_t q_weight_dtype, const void* k_weight,
+                           int32_t k_weight_dtype, float eps, const int64_t* positions, const void* cos_sin,
+                           int32_t table_dtype, int64_t max_position, int32_t rotary_dim, int32_t layout, void* out_q,
+                           int64_t oq_row_stride, int64_t oq_head_stride, void* out_k, int64_t ok_row_stride,
+                           int64_t ok_head_stride, uint32_t flags, void* stream);
+
+/*
+ * nrc_qk_norm_rotate_grad - the gradients of nrc_qk_norm_rotate's inputs and
+ * gains from those of its outputs.
+ *
+ *   grad_q, grad_k  gradients of out_q and out_k, strided like q and k.
+ *   dq, dk     [T, Hq, head_dim], [T, Hk, head_dim] of dtype, contiguous.
+ *   dq_weight, dk_weight  [head_dim] of the gains' types, exactly where there
+ *              are gains: sums over all rows and heads in FP32, in one fixed order. With
+ *              T == 0 they are 0.
+ *   workspace  nrc_qk_norm_rotate_grad_workspace_bytes(head_dim, with_gains) bytes,
+ *              16-byte aligned (0 without gains: may be NULL). Contents on return
+ *              unspecified; calls that share one must not overlap.
+ * Rows outside the table: dq and dk are left as they are, or with
+ * NRC_ROPE_PASS_OUTSIDE copied from grad_q and grad_k; the gains get nothing from them. Gradients
+ * and the workspace lie apart from the inputs and each other. The rest, and
+ * errors, as nrc_qk_norm_rotate (and NRC_EINVAL for a small workspace).
+ */
+int32_t nrc_qk_norm_rotate_grad(const void* grad_q, int64_t gq_row_stride, int64_t gq_head_stride, const void* grad_k,
+                                int64_t gk_row_stride, int64_t gk_head_stride, const void* q, int64_t q_row_stride,
+                                int64_t q_head_stride, int32_t Hq, const void* k, int64_t k_row_stride,
+                                int64_t k_head_stride, int32_t Hk, int32_t dtype, int64_t T, int32_t head_dim,
+                                const void* q_weight, int32_t q_weight_dtype, const void* k_weight,
+                                int32_t k_weight_dtype, float eps, const int64_t* positions, const void* cos_sin,
+                                int32_t table_dtype, int64_t max_position, int32_t rotary_dim, int32_t layout, void* dq,
+                                void* dk, void* dq_weight, void* dk_weight, void* workspace, int64_t workspace_bytes,
+                                uint32_t flags, void* stream);
+
+/* Bytes of nrc_qk_norm_rotate_grad's workspace on the current device; negative status for a bad head_dim. */
+int64_t nrc_qk_norm_rotate_grad_workspace_bytes(int32_t head_dim, int32_t with_gains);
+
+/*
  * nrc_context_tree_attention - drafted tokens attending to their sequence's
  * cached keys: one token (decoding), a chain, or a tree (an ancestor mask),
  * over the cache that nrc_context_kv_store fills (page

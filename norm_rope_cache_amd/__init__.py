@@ -44,6 +44,8 @@ __all__ = [
     "context_kv_project_noalloc",
     "rope_table",
     "rope_rotate",
+    "qk_norm_rotate",
+    "qk_norm_rotate_grad",
     "context_tree_attention",
     "context_attention_mass",
     "context_kv_evict",
@@ -169,6 +171,16 @@ def _load():
                                                _vp, _vp, _vp, _i64, _vp]
     L.nrc_context_kv_evict_workspace_bytes.restype = _i64
     L.nrc_context_kv_evict_workspace_bytes.argtypes = [_i32, _i32, _i64, _i32]
+    head3 = [_vp, _i64, _i64]  # a [T, H, d] view: pointer, row and head strides
+    table = [_f32, _vp, _vp, _i32, _i64, _i32, _i32]
+    gains = [_vp, _i32, _vp, _i32]
+    qk = head3 + [_i32] + head3 + [_i32, _i32, _i64, _i32] + gains + table
+    L.nrc_qk_norm_rotate.restype = _i32
+    L.nrc_qk_norm_rotate.argtypes = qk + head3 + head3 + [ctypes.c_uint32, _vp]
+    L.nrc_qk_norm_rotate_grad.restype = _i32
+    L.nrc_qk_norm_rotate_grad.argtypes = head3 + head3 + qk + [_vp] * 5 + [_i64, ctypes.c_uint32, _vp]
+    L.nrc_qk_norm_rotate_grad_workspace_bytes.restype = _i64
+    L.nrc_qk_norm_rotate_grad_workspace_bytes.argtypes = [_i32, _i32]
     _lib = L
     return L
 
@@ -993,6 +1005,158 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
           cos_sin.data_ptr(), tcode, table[0], table[1], ROPE_LAYOUTS[layout], 1 if inverse else 0, out.data_ptr(), ost[0],
           ost[1], flags, _stream(stream, x))
     return out
+
+
+_norm_rotation = None  # qk_norm_rotate as a torch.autograd.Function, once an input that requires grad has needed it
+
+
+def _get_norm_rotation():
+    global _norm_rotation
+    import torch
+
+    class NormRotation(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, q_weight, k_weight, positions, cos_sin, eps, layout, stream):
+            ctx.save_for_backward(q, k, q_weight, k_weight, positions, cos_sin)
+            ctx.eps, ctx.layout = eps, layout
+            return qk_norm_rotate(q, k, positions, cos_sin, q_weight, k_weight, eps, layout, stream=stream)
+
+        @staticmethod
+        def backward(ctx, grad_q, grad_k):
+            q, k, q_weight, k_weight, positions, cos_sin = ctx.saved_tensors
+            # (a gradient of a sum is one value for all: no unit stride)
+            whole = lambda g: g.clone(memory_format=torch.contiguous_format) if g is not None and g.stride(2) != 1 else g
+            back = qk_norm_rotate_grad(whole(grad_q), whole(grad_k), q, k, positions, cos_sin, q_weight, k_weight, ctx.eps,
+                                       ctx.layout)
+            return back + (None,) * 5
+
+    _norm_rotation = NormRotation
+    return NormRotation
+
+
+def _heads(t, name, code, dev, shape=None):
+    """Checks of a [T, H, d] tensor with unit last stride: its pointer, row and head strides."""
+    torch = _torch or _get_torch()
+    _at(t, dev, name)
+    st = t.stride()
+    if t.dim() != 3 or st[2] != 1 and t.shape[2] != 1 or shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {'[T, H, d]' if shape is None else list(shape)} with unit last stride")
+    if _dtype_code(t.dtype, name) != code:
+        raise TypeError(f"{name} must be of q's dtype")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _gains(w, name, dev, d):
+    if w is None:
+        return None, 0
+    _at(w, dev, name)
+    if w.shape != (d,) or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{d}] tensor")
+    return w.data_ptr(), _dtype_code(w.dtype, name)
+
+
+def _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout):
+    """Checks that both directions share; the GPU, q's type and the C ABI's arguments from q to the layout."""
+    torch = _torch or _get_torch()
+    dev = q.get_device()
+    if dev < 0:
+        raise TypeError("q must be a GPU tensor")
+    code = _dtype_code(q.dtype, "q")
+    qs = _heads(q, "q", code, dev)
+    T, Hq, d = q.shape
+    ks, Hk = (None, 0, 0), 0
+    if k is not None:
+        ks = _heads(k, "k", code, dev)
+        Hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("k must have q's rows and head_dim")
+    elif k_weight is not None:
+        raise ValueError("k_weight without k")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout is 'interleaved' or 'half'")
+    _at(positions, dev, "positions")
+    _at(cos_sin, dev, "cos_sin")
+    tcode = _dtype_code(cos_sin.dtype, "cos_sin", table=True)
+    table = cos_sin.shape
+    if len(table) != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_position, R]")
+    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 [T] tensor")
+    return dev, code, (*qs, Hq, *ks, Hk, code, T, d, *_gains(q_weight, "q_weight", dev, d), *_gains(k_weight, "k_weight", dev, d),
+                       eps, positions.data_ptr(), cos_sin.data_ptr(), tcode, table[0], table[1], ROPE_LAYOUTS[layout])
+
+
+def qk_norm_rotate(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, layout="interleaved", out_q=None,
+                   out_k=None, stream=None):
+    """Queries [T, Hq, d] and keys [T, Hk, d] with each head normed and its first
+    R = cos_sin.shape[1] elements turned by its row's position, in one pass ->
+    (q', k').
+
+    q, k       bf16, float16 or float32, d 2 .. 256, any row and head strides; k
+               may be None (then so is k')
+    positions, cos_sin, layout  as rope_rotate; a row outside the table is left as it
+               is in given outputs, and comes out as it went in otherwise
+    q_weight, k_weight  [d] gains (bf16, float16 or float32) or None (1)
+    out_q, out_k  q or k itself, or a tensor apart from both (default: new ones)
+    x w / sqrt(mean x^2 + eps), turned, in float32 and rounded once. Inputs and
+    gains that require grad get their gradients (qk_norm_rotate_grad, on the current
+    stream of the backward pass); such a call takes no outputs, and cos_sin gets none."""
+    torch = _torch or _get_torch()
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight, cos_sin)):
+        if cos_sin.requires_grad:
+            raise ValueError("cos_sin gets no gradient: detach it")
+        if out_q is not None or out_k is not None:
+            raise ValueError("inputs that require grad take no outputs: detach them, or call under torch.no_grad()")
+        _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout)
+        return (_norm_rotation or _get_norm_rotation()).apply(q, k, q_weight, k_weight, positions, cos_sin, eps, layout, stream)
+    dev, code, args = _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout)
+    if k is None and out_k is not None:
+        raise ValueError("out_k without k")
+    if (out_q is None) != (out_k is None) and k is not None:
+        raise ValueError("give both outputs or none")
+    flags = 0
+    if out_q is None:
+        flags = ROPE_PASS_OUTSIDE
+        out_q = _empty(q.shape, q.dtype, q.device, stream)
+        out_k = None if k is None else _empty(k.shape, k.dtype, k.device, stream)
+    oq = _heads(out_q, "out_q", code, dev, q.shape)
+    ok = (None, 0, 0) if k is None else _heads(out_k, "out_k", code, dev, k.shape)
+    _call(q, _load().nrc_qk_norm_rotate, *args, *oq, *ok, flags, _stream(stream, q))
+    return out_q, out_k
+
+
+def qk_norm_rotate_grad(grad_q, grad_k, q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
+                        layout="interleaved", stream=None):
+    """The gradients of qk_norm_rotate's inputs and gains from those of its outputs
+    -> (dq, dk, dq_weight, dk_weight), None where there is no such input.
+
+    grad_q, grad_k  like q and k (unit last stride); a None counts as 0
+    Rows outside the table pass their gradient, and add nothing to the gains'. The
+    gains' gradients are float32 sums in one fixed order, rounded to the gains' types."""
+    torch = _torch or _get_torch()
+    dev, code, args = _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout)
+    if grad_q is None:
+        grad_q = torch.zeros_like(q, memory_format=torch.contiguous_format)
+    if grad_k is None and k is not None:
+        grad_k = torch.zeros_like(k, memory_format=torch.contiguous_format)
+    gq = _heads(grad_q, "grad_q", code, dev, q.shape)
+    gk = (None, 0, 0) if k is None else _heads(grad_k, "grad_k", code, dev, k.shape)
+    new = lambda t: None if t is None else _empty(t.shape, t.dtype, t.device, stream)
+    dq, dk, dqw, dkw = new(q), new(k), new(q_weight), new(k_weight)
+    lib = _load()
+    need, ws = 0, None
+    if q_weight is not None or k_weight is not None:
+        if dev != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                need = lib.nrc_qk_norm_rotate_grad_workspace_bytes(q.shape[2], 1)
+        else:
+            need = lib.nrc_qk_norm_rotate_grad_workspace_bytes(q.shape[2], 1)
+        if need < 0:
+            _check(need)
+        ws = _empty((need,), torch.uint8, q.device, stream)
+    _call(q, lib.nrc_qk_norm_rotate_grad, *gq, *gk, *args, dq.data_ptr(), *(None if t is None else t.data_ptr() for t in (
+        dk, dqw, dkw, ws)), need, ROPE_PASS_OUTSIDE, _stream(stream, q))
+    return dq, dk, dqw, dkw
 
 
 def _at(t, dev, name):

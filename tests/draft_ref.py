@@ -1,0 +1,64 @@
+"""Plain 64-bit references of the operators on a drafted token's way to the cache
+and over it, with the bounds on the kernels' errors."""
+
+import torch
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def halves(x, R, layout):
+    return (x[..., 0:R:2], x[..., 1:R:2]) if layout == "interleaved" else (x[..., :R // 2], x[..., R // 2:R])
+
+
+def turn(x, pos, table, layout, sign=1.0):
+    """(x turned, the sum of the magnitudes of each element's terms)."""
+    R = table.shape[1]
+    row = table.double()[pos][:, None, :]
+    c, s = row[..., :R // 2], row[..., R // 2:] * sign
+    out, size = x.clone(), x.abs()
+    a, b = halves(x, R, layout)
+    oa, ob = halves(out, R, layout)
+    sa, sb = halves(size, R, layout)
+    oa.copy_(a * c - b * s), ob.copy_(b * c + a * s)
+    sa.copy_((a * c).abs() + (b * s).abs()), sb.copy_((b * c).abs() + (a * s).abs())
+    return out, size
+
+
+def norm_rotate(x, w, pos, table, layout, eps):
+    """(y, bound). In FP32 the sum of d squares is off by d 2^-24 of itself, the mean, eps and 1 / sqrt by
+    four roundings, and the root halves what the sum brings: with x r and times w (two roundings) and the turn's
+    product and FMA n is off by (d / 2 + 8) 2^-24 of its terms; then half a step of the type (a subnormal's:
+    half of the least value)."""
+    d, dt = x.shape[-1], x.dtype
+    x = x.double()
+    n = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps)
+    if w is not None:
+        n = n * w.double()
+    y, size = turn(n, pos, table, layout)
+    tol = size * (d / 2 + 8) * 2.0 ** -24 * 1.01 + y.abs() * half_step(dt) * 1.01
+    return y, tol + torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+
+
+def norm_rotate_grad(gy, x, w, pos, table, layout, eps):
+    """(dx, its bound, dw, its bound). With e = (d / 2 + 8) 2^-24 for x r: g is off by 2 2^-24 of its terms
+    G, a product g w x r by e + 4 2^-24 of G |w x r|, their mean by d 2^-24 more, dx by the sum of those times r
+    and half a step. dw sums N such products: N 2^-24 of their magnitudes, and half a step of the gains' type."""
+    T, H, d = x.shape
+    dt = x.dtype
+    x, gy = x.double(), gy.double()
+    r = 1.0 / torch.sqrt(x.square().mean(-1, keepdim=True) + eps)
+    u = x * r
+    g, G = turn(gy, pos, table, layout, -1.0)
+    gain = torch.ones(d, dtype=torch.float64) if w is None else w.double()
+    along = (g * gain * u).mean(-1, keepdim=True)
+    dx = r * (g * gain - u * along)
+    e = (d / 2 + 8) * 2.0 ** -24
+    mean = (G * gain.abs() * u.abs()).mean(-1, keepdim=True)
+    tol = r * (G * gain.abs() * (e + 6 * 2.0 ** -24) + u.abs() * mean * (3 * e + (d + 8) * 2.0 ** -24)) * 1.01
+    tol = tol + dx.abs() * half_step(dt) * 1.01 + torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    dw = (g * u).sum((0, 1))
+    wt = torch.float32 if w is None else w.dtype
+    dw_tol = (G * u.abs()).sum((0, 1)) * (e + (T * H + 6) * 2.0 ** -24) * 1.01 + dw.abs() * half_step(wt) * 1.01
+    return dx, tol, dw, dw_tol + torch.finfo(wt).smallest_normal * torch.finfo(wt).eps
