@@ -586,6 +586,65 @@ int32_t nrc_qk_norm_rotate_grad(const void* grad_q, int64_t gq_row_stride, int64
 int64_t nrc_qk_norm_rotate_grad_workspace_bytes(int32_t head_dim, int32_t with_gains);
 
 /*
+ * Paged caches of 4 bits. A page of a head holds the cells of its block_size
+ * places in nrc_fp4_page_bytes(block_size) bytes (68 a cell, up to a multiple of 16):
+ *   [block_size][32] K's codes, [block_size][32] V's codes, [block_size][4] scales.
+ * A code is 4 bits, the sign on top: 0 .5 1 1.5 2 3 4 6; element 2 i of a row is the
+ * low half of its byte i. A cell's scale bytes belong to elements 0 .. 31 and
+ * 32 .. 63 of K, then of V; an element stands for its code's value times 2^(byte -
+ * 127). nrc_context_fp4_store writes bytes 7 .. 252, and 255 in all four of a cell
+ * that had an infinity or NaN in K or V: such a cell stands for NaN. Others
+ * (3 of 4 bytes 255, 253, 254, 0 .. 6) mean nothing that is promised.
+ */
+
+/* Bytes of a page of a head: 68 block_size, rounded up to 16; NRC_EINVAL unless 1 <= block_size <= 2^24. */
+int64_t nrc_fp4_page_bytes(int64_t block_size);
+
+/*
+ * nrc_context_fp4_store - K and V rows into their slots' cells of 4 bits, all
+ * layers in one launch (page "...cutedsl.draft.context",
+ * _ContextKvStoreKernel: the insert by slot, into smaller cells).
+ *
+ *   k, v       [L, T, H, 64] bf16, unit stride in the row, the others in
+ *              elements, multiples of 8; 16-byte aligned. As nrc_qk_norm_rotate and
+ *              the projection leave them; they are stored as they are.
+ *   slots      [L, T] int64 in device memory, layer stride in elements (0: one list
+ *              for all); slot s is place s % block_size of block s / block_size.
+ *              Negative slots, and slots past the cache, are skipped; the others are
+ *              distinct within a layer.
+ *   caches     [L, num_blocks, H, nrc_fp4_page_bytes(block_size)], strides in
+ *              bytes, multiples of 16; 16-byte aligned; pages in memory of their
+ *              own, apart from the inputs.
+ * A group of 32 elements gets the least power of two with which none passes 6 (2^-120 ..
+ * 2^125; what passes 6 2^125 is stored as that), an element the nearest code, of two
+ * equally near the even one. T == 0 or L == 0 returns NRC_OK. Errors: NRC_EINVAL (NULL or
+ * misaligned operands, strides, overlaps), NRC_ENOTSUP (cache strides that are not
+ * multiples of 16, more than 2^31 slots, T H above 2^28).
+ */
+int32_t nrc_context_fp4_store(const uint16_t* k, int64_t k_layer_stride, int64_t k_row_stride, int64_t k_head_stride,
+                              const uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride, int64_t v_head_stride,
+                              const int64_t* slots, int64_t slots_layer_stride, int64_t T, int32_t H, int32_t L,
+                              uint8_t* caches, int64_t layer_stride, int64_t block_stride, int64_t head_stride,
+                              int64_t num_blocks, int64_t block_size, void* stream);
+
+/* Flag of nrc_context_fp4_load. */
+#define NRC_FP4_FILL 1u /* rows without a cell become 0 */
+
+/*
+ * nrc_context_fp4_load - the values of cells of 4 bits, as bf16 rows (every
+ * value is a bf16 number; 0x7FC0 for NaN).
+ * Operands as nrc_context_fp4_store, k and v being written: rows in memory of their
+ * own, apart from each other, the caches and slots. A row whose slot is negative or
+ * past the cache is left as it is (NRC_FP4_FILL in flags: becomes 0). A slot may come more
+ * than once.
+ */
+int32_t nrc_context_fp4_load(const uint8_t* caches, int64_t layer_stride, int64_t block_stride, int64_t head_stride,
+                             int64_t num_blocks, int64_t block_size, const int64_t* slots, int64_t slots_layer_stride,
+                             int64_t T, int32_t H, int32_t L, uint16_t* k, int64_t k_layer_stride, int64_t k_row_stride,
+                             int64_t k_head_stride, uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride,
+                             int64_t v_head_stride, uint32_t flags, void* stream);
+
+/*
  * nrc_context_tree_attention - drafted tokens attending to their sequence's
  * cached keys: one token (decoding), a chain, or a tree (an ancestor mask),
  * over the cache that nrc_context_kv_store fills (page

@@ -46,6 +46,9 @@ __all__ = [
     "rope_rotate",
     "qk_norm_rotate",
     "qk_norm_rotate_grad",
+    "fp4_page_bytes",
+    "context_fp4_store",
+    "context_fp4_load",
     "context_tree_attention",
     "context_attention_mass",
     "context_kv_evict",
@@ -181,6 +184,14 @@ def _load():
     L.nrc_qk_norm_rotate_grad.argtypes = head3 + head3 + qk + [_vp] * 5 + [_i64, ctypes.c_uint32, _vp]
     L.nrc_qk_norm_rotate_grad_workspace_bytes.restype = _i64
     L.nrc_qk_norm_rotate_grad_workspace_bytes.argtypes = [_i32, _i32]
+    rows4 = [_vp, _i64, _i64, _i64]  # an [L, T, H, 64] view: pointer, layer, row and head strides
+    pages = [_vp, _i64, _i64, _i64, _i64, _i64]
+    L.nrc_fp4_page_bytes.restype = _i64
+    L.nrc_fp4_page_bytes.argtypes = [_i64]
+    L.nrc_context_fp4_store.restype = _i32
+    L.nrc_context_fp4_store.argtypes = rows4 + rows4 + [_vp, _i64, _i64, _i32, _i32] + pages + [_vp]
+    L.nrc_context_fp4_load.restype = _i32
+    L.nrc_context_fp4_load.argtypes = pages + [_vp, _i64, _i64, _i32, _i32] + rows4 + rows4 + [ctypes.c_uint32, _vp]
     _lib = L
     return L
 
@@ -1405,6 +1416,108 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
           new_positions.data_ptr(), new_lens.data_ptr(), None if ws is None else ws.data_ptr(), need,
           _stream(stream, cache))
     return new_weights, new_positions, new_lens
+
+
+FP4_FILL = 1
+
+
+def fp4_page_bytes(block_size):
+    """Bytes of a page of a head in a cache of 4 bits, [num_blocks, H, fp4_page_bytes(block_size)] uint8: 68 a cell,
+    rounded up to 16."""
+    n = _load().nrc_fp4_page_bytes(block_size)
+    if n < 0:
+        _check(n)
+    return n
+
+
+def _fp4_block_size(page_bytes):
+    """The block_size whose pages have so many bytes."""
+    bs = page_bytes // 68
+    if bs < 1 or page_bytes != (68 * bs + 15) // 16 * 16:
+        raise ValueError(f"pages of {page_bytes} bytes: a cache of 4 bits has fp4_page_bytes(block_size)")
+    return bs
+
+
+def _fp4_caches(caches):
+    """Checks of [L, num_blocks, H, page] or [num_blocks, H, page] caches; the GPU, L, H and the C ABI's arguments."""
+    torch = _torch or _get_torch()
+    dev = caches.get_device()
+    if caches.dtype != torch.uint8 or dev < 0:
+        raise TypeError(f"caches must be a uint8 GPU tensor, not {caches.dtype} on {caches.device}")
+    shape, st = caches.shape, caches.stride()
+    if len(shape) == 3:
+        shape, st = (1, *shape), (0, *st)
+    if len(shape) != 4 or st[3] != 1:
+        raise ValueError("caches must be [L, num_blocks, H, page bytes] with unit last stride")
+    L, nb, H, page = shape
+    # (one of a kind has no stride)
+    return dev, L, H, (caches.data_ptr(), st[0] if L > 1 else 0, st[1] if nb > 1 else 0, st[2] if H > 1 else 0, nb,
+                       _fp4_block_size(page))
+
+
+def _fp4_rows(t, name, dev, shape):
+    """Checks of [L, T, H, 64] (or [T, H, 64]) rows; pointer and strides."""
+    torch = _torch or _get_torch()
+    _at(t, dev, name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
+    own, st = t.shape, t.stride()
+    if len(own) == 3:
+        own, st = (1, *own), (0, *st)
+    if tuple(own) != shape or st[3] != 1:
+        raise ValueError(f"{name} must be {list(shape)} with unit last stride")
+    return t.data_ptr(), *(s if n > 1 else 0 for s, n in zip(st[:3], shape))
+
+
+def _fp4_slots(slots, dev, L):
+    torch = _torch or _get_torch()
+    _at(slots, dev, "slots")
+    if slots.dtype != torch.int64 or slots.dim() not in (1, 2) or slots.dim() == 2 and slots.shape[0] != L:
+        raise ValueError("slots must be an int64 [T] or [L, T] tensor")
+    if slots.shape[-1] > 1 and slots.stride(-1) != 1:
+        raise ValueError("slots must have unit last stride")
+    return slots.shape[-1], (slots.data_ptr(), slots.stride(0) if slots.dim() == 2 and L > 1 else 0)
+
+
+def context_fp4_store(k, v, slots, caches, stream=None):
+    """K and V rows into their slots' cells of 4 bits, in place.
+
+    k, v    [L, T, H, 64] bf16 (kv_views; or [T, H, 64] of one layer), strides
+            multiples of 8, stored as they are: normed and rotated before
+            (qk_norm_rotate)
+    slots   [T] int64 for all layers or [L, T]; negative ones are skipped
+    caches  [L, num_blocks, H, fp4_page_bytes(block_size)] uint8 (or without L), strides
+            multiples of 16
+    Groups of 32 elements share a power of two, with which none passes 6; elements
+    take the nearest of 0 .5 1 1.5 2 3 4 6. A cell with an infinity or NaN
+    stands for NaN."""
+    dev, L, H, pages = _fp4_caches(caches)
+    T, at = _fp4_slots(slots, dev, L)
+    shape = (L, T, H, HEAD_DIM)
+    _call(caches, _load().nrc_context_fp4_store, *_fp4_rows(k, "k", dev, shape), *_fp4_rows(v, "v", dev, shape), *at, T, H, L,
+          *pages, _stream(stream, caches))
+
+
+def context_fp4_load(caches, slots, out_k=None, out_v=None, stream=None):
+    """The values of the slots' cells of 4 bits -> (k, v) bf16, [L, T, H, 64] (or [T, H, 64]
+    of one layer's cache).
+
+    A row whose slot is negative or past the cache is left as it is in given
+    outputs, and 0 otherwise; slots may repeat."""
+    torch = _torch or _get_torch()
+    dev, L, H, pages = _fp4_caches(caches)
+    T, at = _fp4_slots(slots, dev, L)
+    if (out_k is None) != (out_v is None):
+        raise ValueError("give both outputs or none")
+    flags = 0
+    if out_k is None:
+        shape = (L, T, H, HEAD_DIM) if caches.dim() == 4 else (T, H, HEAD_DIM)
+        out_k, out_v = (_empty(shape, torch.bfloat16, caches.device, stream) for _ in range(2))
+        flags = FP4_FILL
+    shape = (L, T, H, HEAD_DIM)
+    _call(caches, _load().nrc_context_fp4_load, *pages, *at, T, H, L, *_fp4_rows(out_k, "out_k", dev, shape),
+          *_fp4_rows(out_v, "out_v", dev, shape), flags, _stream(stream, caches))
+    return out_k, out_v
 
 
 def context_kv_chain(x, hidden_w, pre_w, w_kv, positions, slots, cos_sin, caches, H, hidden_eps=1e-6,

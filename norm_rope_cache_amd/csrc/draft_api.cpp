@@ -4,6 +4,8 @@
 // enqueued.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "api_checks.h"
 #include "draft_ops.h"
 
@@ -89,6 +91,93 @@ bool rows_interleave(const Range& a, int64_t a_heads, int64_t a_hs, int64_t a_rs
     const int64_t row = a_rs * eb, in_a = ((a_heads - 1) * a_hs + d) * eb, in_b = ((b_heads - 1) * b_hs + d) * eb;
     const int64_t apart = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % row, behind = apart < 0 ? apart + row : apart;
     return behind >= in_a && in_b <= row - behind;
+}
+
+// A view of layers of 4-bit pages, checked (the pointer with need).
+int32_t fp4_cache(const char* what, const uint8_t* caches, int64_t layer_stride, int64_t block_stride, int64_t head_stride,
+                  int64_t num_blocks, int64_t block_size, int32_t H, bool need, Fp4Cache* out) {
+    if (H < 1) return fail(NRC_EINVAL, "%s: H = %d < 1", what, H);
+    if (num_blocks < 1 || block_size < 1) return fail(NRC_EINVAL, "%s: num_blocks and block_size must be >= 1", what);
+    if (H > 65535) return fail(NRC_ENOTSUP, "%s: more than 65535 heads", what);
+    if (num_blocks > (((int64_t)1 << 31) - 1) / block_size || block_size > ((int64_t)1 << 24))
+        return fail(NRC_ENOTSUP, "%s: %lld x %lld slots do not fit 31 bits (a block 24)", what, (long long)num_blocks,
+                    (long long)block_size);
+    for (int64_t s : {layer_stride, block_stride, head_stride}) {
+        if (s < 0 || s > kBig) return fail(NRC_EINVAL, "%s: cache strides must lie in [0, 2^40]", what);
+        if (s & 15) return fail(NRC_ENOTSUP, "%s: cache strides must be multiples of 16 bytes", what);
+    }
+    if (num_blocks * block_stride > (int64_t)1 << 60) return fail(NRC_EINVAL, "%s: cache strides too large", what);
+    if (need && !caches) return fail(NRC_EINVAL, "%s: NULL cache", what);
+    if (!aligned(caches, 16)) return fail(NRC_EINVAL, "%s: the cache must be 16-byte aligned", what);
+    int32_t shift = -1;
+    if ((block_size & (block_size - 1)) == 0)
+        for (shift = 0; ((int64_t)1 << shift) != block_size;) ++shift;
+    *out = Fp4Cache{const_cast<uint8_t*>(caches), layer_stride, block_stride, head_stride, (uint32_t)num_blocks,
+                    (uint32_t)block_size, shift};
+    return NRC_OK;
+}
+// From the first page's first byte to the last one's last.
+Range pages_range(const Fp4Cache& c, int32_t H, int32_t L) {
+    const __int128 bytes = (__int128)(L - 1) * c.layer_stride + (__int128)(c.num_blocks - 1) * c.block_stride +
+                           (__int128)(H - 1) * c.head_stride + fp4_page(c.block_size);
+    return Range{c.cache, bytes > ((int64_t)1 << 62) ? (int64_t)1 << 62 : (int64_t)bytes};
+}
+// Is every page in memory of its own?
+bool pages_apart(const Fp4Cache& c, int32_t H, int32_t L) {
+    struct Step {
+        int64_t stride, count;
+    } steps[] = {{c.layer_stride, L}, {c.block_stride, (int64_t)c.num_blocks}, {c.head_stride, H}};
+    std::sort(steps, steps + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
+    __int128 reach = fp4_page(c.block_size);
+    for (const Step& s : steps) {
+        if (s.count == 1) continue;
+        if (s.stride < reach) return false;
+        reach += (__int128)(s.count - 1) * s.stride;
+    }
+    return true;
+}
+
+// K's or V's rows, [L, T, H, 64] by strides in elements.
+struct Rows4 {
+    const char* name;
+    const uint16_t* p;
+    int64_t ls, rs, hs;
+};
+int32_t fp4_rows(const char* what, const Rows4& k, const Rows4& v, const int64_t* slots, int64_t slots_ls, int64_t T,
+                 int32_t H, int32_t L, bool need, Fp4Rows* out) {
+    if (T < 0 || L < 0) return fail(NRC_EINVAL, "%s: T >= 0 and L >= 0 must hold", what);
+    if (T > ((int64_t)1 << 28) || T * H > ((int64_t)1 << 28) || L > 65535)
+        return fail(NRC_ENOTSUP, "%s: too many rows or layers for one call", what);
+    for (const Rows4* r : {&k, &v}) {
+        if (need && !r->p) return fail(NRC_EINVAL, "%s: NULL %s", what, r->name);
+        if (!aligned(r->p, 16)) return fail(NRC_EINVAL, "%s: %s must be 16-byte aligned", what, r->name);
+        for (int64_t s : {r->ls, r->rs, r->hs})
+            if (s < 0 || s > kBig || s & 7)
+                return fail(NRC_EINVAL, "%s: strides of %s must be multiples of 8 elements in [0, 2^40]", what, r->name);
+    }
+    if (need && !slots) return fail(NRC_EINVAL, "%s: NULL slots", what);
+    if (!aligned(slots, 8) || slots_ls < 0 || slots_ls > kBig)
+        return fail(NRC_EINVAL, "%s: slots must be 8-byte aligned, their layer stride in [0, 2^40]", what);
+    *out = Fp4Rows{k.p, v.p, k.ls, k.rs, k.hs, v.ls, v.rs, v.hs, slots, slots_ls, T, H, L};
+    return NRC_OK;
+}
+Range rows4_range(const Rows4& r, int64_t T, int32_t H, int32_t L) {
+    const __int128 n = (__int128)(L - 1) * r.ls + (__int128)(T - 1) * r.rs + (__int128)(H - 1) * r.hs + NRC_HEAD_DIM;
+    return Range{r.p, n > ((int64_t)1 << 61) ? (int64_t)1 << 62 : 2 * (int64_t)n};
+}
+// Do rows that are written lie in places of their own (layers, rows and heads in any order)?
+bool rows4_apart(const Rows4& r, int64_t T, int32_t H, int32_t L) {
+    struct Step {
+        int64_t stride, count;
+    } steps[] = {{r.ls, L}, {r.rs, T}, {r.hs, H}};
+    std::sort(steps, steps + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
+    __int128 reach = NRC_HEAD_DIM;
+    for (const Step& s : steps) {
+        if (s.count == 1) continue;
+        if (s.stride < reach) return false;
+        reach += (__int128)(s.count - 1) * s.stride;
+    }
+    return true;
 }
 
 }  // namespace
@@ -208,6 +297,56 @@ int32_t nrc_qk_norm_rotate_grad(const void* grad_q, int64_t gq_row_stride, int64
                  gk_head_stride, dk_rs, head_dim, k_weight_dtype, Hk};
     a.part = static_cast<float*>(workspace);
     return launch_status(launch_qk_norm(a, (hipStream_t)stream), what);
+}
+
+int64_t nrc_fp4_page_bytes(int64_t block_size) {
+    if (block_size < 1 || block_size > ((int64_t)1 << 24))
+        return fail(NRC_EINVAL, "fp4_page_bytes: block_size = %lld must lie in [1, 2^24]", (long long)block_size);
+    return fp4_page(block_size);
+}
+
+int32_t nrc_context_fp4_store(const uint16_t* k, int64_t k_layer_stride, int64_t k_row_stride, int64_t k_head_stride,
+                              const uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride, int64_t v_head_stride,
+                              const int64_t* slots, int64_t slots_layer_stride, int64_t T, int32_t H, int32_t L,
+                              uint8_t* caches, int64_t layer_stride, int64_t block_stride, int64_t head_stride,
+                              int64_t num_blocks, int64_t block_size, void* stream) {
+    const char* what = "context_fp4_store";
+    const bool work = T > 0 && L > 0;
+    Fp4Cache c{};
+    Fp4Rows r{};
+    const Rows4 kr{"k", k, k_layer_stride, k_row_stride, k_head_stride}, vr{"v", v, v_layer_stride, v_row_stride, v_head_stride};
+    if (int32_t rc = fp4_cache(what, caches, layer_stride, block_stride, head_stride, num_blocks, block_size, H, work, &c))
+        return rc;
+    if (int32_t rc = fp4_rows(what, kr, vr, slots, slots_layer_stride, T, H, L, work, &r)) return rc;
+    if (!work) return NRC_OK;
+    if (!pages_apart(c, H, L)) return fail(NRC_EINVAL, "%s: pages of the caches overlap", what);
+    if (any_meet({pages_range(c, H, L)}, {rows4_range(kr, T, H, L), rows4_range(vr, T, H, L),
+                                          {slots, 8 * ((L - 1) * slots_layer_stride + T)}}))
+        return fail(NRC_EINVAL, "%s: the caches must lie apart from k, v and slots", what);
+    return launch_status(launch_fp4_store(r, c, (hipStream_t)stream), what);
+}
+
+int32_t nrc_context_fp4_load(const uint8_t* caches, int64_t layer_stride, int64_t block_stride, int64_t head_stride,
+                             int64_t num_blocks, int64_t block_size, const int64_t* slots, int64_t slots_layer_stride,
+                             int64_t T, int32_t H, int32_t L, uint16_t* k, int64_t k_layer_stride, int64_t k_row_stride,
+                             int64_t k_head_stride, uint16_t* v, int64_t v_layer_stride, int64_t v_row_stride,
+                             int64_t v_head_stride, uint32_t flags, void* stream) {
+    const char* what = "context_fp4_load";
+    if (flags & ~(uint32_t)NRC_FP4_FILL) return fail(NRC_EINVAL, "%s: unknown flags 0x%x", what, flags);
+    const bool work = T > 0 && L > 0;
+    Fp4Cache c{};
+    Fp4Rows r{};
+    const Rows4 kr{"k", k, k_layer_stride, k_row_stride, k_head_stride}, vr{"v", v, v_layer_stride, v_row_stride, v_head_stride};
+    if (int32_t rc = fp4_cache(what, caches, layer_stride, block_stride, head_stride, num_blocks, block_size, H, work, &c))
+        return rc;
+    if (int32_t rc = fp4_rows(what, kr, vr, slots, slots_layer_stride, T, H, L, work, &r)) return rc;
+    if (!work) return NRC_OK;
+    if (!rows4_apart(kr, T, H, L) || !rows4_apart(vr, T, H, L)) return fail(NRC_EINVAL, "%s: rows of k or v overlap", what);
+    const Range k_range = rows4_range(kr, T, H, L), v_range = rows4_range(vr, T, H, L);
+    if (any_meet({k_range, v_range}, {pages_range(c, H, L), {slots, 8 * ((L - 1) * slots_layer_stride + T)}}) ||
+        any_meet({k_range}, {v_range}))
+        return fail(NRC_EINVAL, "%s: k and v must lie apart from each other, the caches and slots", what);
+    return launch_status(launch_fp4_load(r, c, k, v, flags != 0, (hipStream_t)stream), what);
 }
 
 }  // extern "C"

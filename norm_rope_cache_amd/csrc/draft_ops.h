@@ -41,4 +41,28 @@ int64_t qk_norm_grad_workspace(int32_t head_dim, int32_t num_cus);
 
 int launch_qk_norm(const QkNormArgs& a, hipStream_t stream);
 
+// Paged caches of 4 bits, [layers, num_blocks, H, page] by strides in bytes.
+struct Fp4Cache {
+    uint8_t* cache;
+    int64_t layer_stride, block_stride, head_stride;
+    uint32_t num_blocks, block_size;
+    int32_t bs_shift;  // log2(block_size), or -1 when not a power of two
+};
+
+// K and V rows of L layers, [L, T, H, 64] by strides in elements, and their slots.
+struct Fp4Rows {
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t k_ls, k_rs, k_hs, v_ls, v_rs, v_hs;
+    const int64_t* slots;  // [L, T] by slots_ls
+    int64_t slots_ls;
+    int64_t T;
+    int32_t H, L;
+};
+
+int64_t fp4_page(int64_t block_size);  // bytes of a page of a head
+
+int launch_fp4_store(const Fp4Rows& r, const Fp4Cache& c, hipStream_t stream);
+int launch_fp4_load(const Fp4Rows& r, const Fp4Cache& c, uint16_t* k, uint16_t* v, bool fill, hipStream_t stream);
+
 }  // namespace nrc

@@ -62,3 +62,30 @@ def norm_rotate_grad(gy, x, w, pos, table, layout, eps):
     wt = torch.float32 if w is None else w.dtype
     dw_tol = (G * u.abs()).sum((0, 1)) * (e + (T * H + 6) * 2.0 ** -24) * 1.01 + dw.abs() * half_step(wt) * 1.01
     return dx, tol, dw, dw_tol + torch.finfo(wt).smallest_normal * torch.finfo(wt).eps
+
+
+STEPS = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def fp4_groups(x):
+    """[..., 32] -> (code numbers, exponents) by the definition, element by element in 64 bits: the least e in -120 ..
+    125 with which the largest is at most 6 2^e (125 at the most), and the nearest value, of two the even code."""
+    x = x.double()
+    most = x.abs().amax(-1)
+    e = torch.full(most.shape, -120, dtype=torch.int64)
+    for _ in range(246):
+        e = torch.where((most > 6 * torch.exp2(e.double())) & (e < 125), e + 1, e)
+    y = x.abs() * torch.exp2(-e.double())[..., None]  # (exact: a power of two)
+    far = torch.stack([(y - s).abs() for s in STEPS], -1)
+    least = far.amin(-1, keepdim=True)
+    order = torch.tensor([0, 2, 4, 6, 1, 3, 5, 7])  # even codes first
+    code = order[(far[..., order] == least).to(torch.int8).argmax(-1)]
+    return code, e
+
+
+def fp4_values(x):
+    """What a [..., 64] row of K or V stands for once stored."""
+    g = x.double().unflatten(-1, (2, 32))
+    code, e = fp4_groups(g)
+    sign = torch.where(torch.signbit(g), -1.0, 1.0)
+    return (torch.tensor(STEPS, dtype=torch.float64)[code] * sign * torch.exp2(e.double())[..., None]).flatten(-2)
