@@ -730,6 +730,60 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
                                                    int64_t max_ctx);
 
 /*
+ * nrc_context_window_attention - nrc_context_tree_attention_ex behind a sliding
+ * window: a row at position p sees key j of its context if j < sinks or j > p - window
+ * (page "...runtime.draft", DraftDecode._attention, of a draft layer that looks
+ * back so far only).
+ *
+ *   window     at least 1: the row's own key and the window - 1 before it.
+ *   sinks      at least 0: the first keys, which stay visible.
+ * Without tree_mask node i stands at ctx_lens[b] + i, and nodes are keys like the
+ * context's: node j is seen if j <= i and it lies in the window or among the sinks. With
+ * tree_mask a row stands at ctx_lens[b] + the nodes it sees - 1 (its depth in the
+ * tree), and over its nodes the mask alone decides. Keys that no row of a call can see are
+ * not read: a row costs its window, not its context.
+ * Prompts are chains too: max_nodes up to 65535, and rows far apart share no work.
+ * The other arguments, results and errors as nrc_context_tree_attention_ex, the workspace
+ * as nrc_context_window_attention_workspace_bytes says. Errors also: NRC_EINVAL for a
+ * window or sinks out of range.
+ */
+int32_t nrc_context_window_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int32_t Hq,
+                                     const uint16_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,
+                                     int64_t page_stride, int64_t head_stride, int32_t H, const int32_t* tables,
+                                     int64_t table_stride, int64_t table_width, int32_t B, const int32_t* ctx_lens,
+                                     const int32_t* q_starts, int32_t max_nodes, int64_t max_ctx, const int64_t* tree_mask,
+                                     int32_t mask_words, float scale, float softcap, int32_t window, int32_t sinks,
+                                     uint16_t* out, float* lse, void* workspace, int64_t workspace_bytes, uint32_t flags,
+                                     void* stream);
+
+/*
+ * nrc_context_window_attention_workspace_bytes - the workspace of nrc_context_window_attention, and (with window 0:
+ * none) of nrc_context_fp4_attention, for these sizes on the current device: 0 when the keys are not split. Negative
+ * status for sizes that they reject.
+ */
+int64_t nrc_context_window_attention_workspace_bytes(int32_t B, int64_t T, int32_t Hq, int32_t H, int32_t max_nodes,
+                                                     int64_t max_ctx, int32_t window, int32_t sinks);
+
+/*
+ * nrc_context_fp4_attention - nrc_context_tree_attention_ex over a cache of 4
+ * bits (nrc_context_fp4_store), with a window or without.
+ *
+ *   cache      one layer's [num_blocks, H, nrc_fp4_page_bytes(block_size)] pages, strides in
+ *              bytes, multiples of 16; 16-byte aligned.
+ *   window     0: none (sinks is not looked at), else as nrc_context_window_attention.
+ * K and V are the cells' values, which the matrix instructions take as they are; a row
+ * that sees a cell that stands for NaN gets NaN in out and lse. Cells that a row does not see do not
+ * reach it, whatever their bytes. The rest as nrc_context_window_attention.
+ */
+int32_t nrc_context_fp4_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int32_t Hq,
+                                  const uint8_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,
+                                  int64_t head_stride, int32_t H, const int32_t* tables, int64_t table_stride,
+                                  int64_t table_width, int32_t B, const int32_t* ctx_lens, const int32_t* q_starts,
+                                  int32_t max_nodes, int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words,
+                                  float scale, float softcap, int32_t window, int32_t sinks, uint16_t* out, float* lse,
+                                  void* workspace, int64_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
  * nrc_context_attention_mass - the attention weight that each cached cell
  * receives, by which nrc_context_kv_evict keeps cells:
  *   out[b, h, j] = decay weights[b, h, j] + sum over the rows of KV head h of

@@ -50,6 +50,8 @@ __all__ = [
     "context_fp4_store",
     "context_fp4_load",
     "context_tree_attention",
+    "context_window_attention",
+    "context_fp4_attention",
     "context_attention_mass",
     "context_kv_evict",
     "kv_views",
@@ -186,6 +188,13 @@ def _load():
     L.nrc_qk_norm_rotate_grad_workspace_bytes.argtypes = [_i32, _i32]
     rows4 = [_vp, _i64, _i64, _i64]  # an [L, T, H, 64] view: pointer, layer, row and head strides
     pages = [_vp, _i64, _i64, _i64, _i64, _i64]
+    near = [_i32, _i32, _vp, _vp, _vp, _i64, ctypes.c_uint32, _vp]  # window and sinks, then out to the stream
+    L.nrc_context_window_attention.restype = _i32
+    L.nrc_context_window_attention.argtypes = queries + near
+    L.nrc_context_fp4_attention.restype = _i32
+    L.nrc_context_fp4_attention.argtypes = queries[:9] + queries[10:] + near  # (pages have no page stride)
+    L.nrc_context_window_attention_workspace_bytes.restype = _i64
+    L.nrc_context_window_attention_workspace_bytes.argtypes = [_i32, _i64, _i32, _i32, _i32, _i64, _i32, _i32]
     L.nrc_fp4_page_bytes.restype = _i64
     L.nrc_fp4_page_bytes.argtypes = [_i64]
     L.nrc_context_fp4_store.restype = _i32
@@ -1210,12 +1219,37 @@ def _paged_operands(cache, tables):
                  tables.data_ptr(), tst[0], width, B)
 
 
-def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap):
-    """Checks shared by the attention and its received weights; the GPU, T, Hq, H,
-    B, max_ctx and the C ABI's arguments from `q` to `softcap`."""
+def _fp4_paged(cache, tables):
+    """_paged_operands of a cache of 4 bits (no page stride among the arguments)."""
     torch = _torch or _get_torch()
-    dev, paged = _paged_operands(cache, tables)
-    bs, H, width, B = paged[2], paged[6], paged[9], paged[10]
+    dev = cache.get_device()
+    if dev < 0:
+        raise TypeError(f"cache must be a GPU tensor, not on {cache.device}")
+    shape, st = cache.shape, cache.stride()
+    if len(shape) != 3 or st[2] != 1:
+        raise ValueError("cache must be a [num_blocks, H, page bytes] view with unit last stride")
+    _at(tables, dev, "tables")
+    if tables.dtype != torch.int32 or tables.dim() != 2:
+        raise ValueError("tables must be an int32 [B, blocks] tensor")
+    B, width = tables.shape
+    tst = tables.stride()
+    if width > 1 and tst[1] != 1:
+        raise ValueError("tables must have unit last stride")
+    nb, H, page = shape
+    return dev, (cache.data_ptr(), nb, _fp4_block_size(page), st[0] if nb > 1 else 0, st[1] if H > 1 else 0, H,
+                 tables.data_ptr(), tst[0], width, B)
+
+
+def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, scale, softcap):
+    """Checks shared by the attentions and their received weights (a uint8 cache: pages of 4 bits); the GPU, T, Hq,
+    H, B, max_ctx and the C ABI's arguments from `q` to `softcap`."""
+    torch = _torch or _get_torch()
+    if cache.dtype == torch.uint8:
+        dev, paged = _fp4_paged(cache, tables)
+        bs, H, width, B = paged[2], paged[5], paged[8], paged[9]
+    else:
+        dev, paged = _paged_operands(cache, tables)
+        bs, H, width, B = paged[2], paged[6], paged[9], paged[10]
     _fits32(max_nodes, "max_nodes")
     if q.dtype != torch.bfloat16:
         raise TypeError(f"q must be bfloat16, not {q.dtype}")
@@ -1250,6 +1284,31 @@ def _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx, tr
 ATTENTION_FILL_OUT, ATTENTION_FILL_LSE = 1, 2
 
 
+def _bf16_cache(cache):
+    torch = _torch or _get_torch()
+    if cache.dtype != torch.bfloat16:
+        raise TypeError(f"cache must be a bfloat16 GPU tensor, not {cache.dtype} on {cache.device}")
+
+
+def _attention_outputs(q, dev, T, Hq, out, lse, stream):
+    """An attention's out and lse, given or new, and the flags that fill the new ones' rows of no sequence."""
+    torch = _torch or _get_torch()
+    flags = 0
+    if out is None:
+        out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
+        flags = ATTENTION_FILL_OUT
+    else:
+        _at(out, dev, "out")
+        if out.dtype != torch.bfloat16 or out.shape != (T, Hq, HEAD_DIM) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bfloat16 [T, Hq, 64]")
+    if lse is None:
+        lse = _empty((T, Hq), torch.float32, q.device, stream)
+        flags |= ATTENTION_FILL_LSE
+    else:
+        _float_lse(lse, dev, (T, Hq))
+    return out, lse, flags
+
+
 def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx=None, tree_mask=None, scale=None,
                            softcap=0.0, out=None, lse=None, stream=None):
     """Drafted tokens attending to the cache of one layer -> (out [T, Hq, 64]
@@ -1275,21 +1334,10 @@ def context_tree_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, max_
     is). The keys of long contexts are split
     over workgroups, with a workspace from torch's allocator."""
     torch = _torch or _get_torch()
+    _bf16_cache(cache)
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
                                                       tree_mask, scale, softcap)
-    flags = 0
-    if out is None:
-        out = _empty((T, Hq, HEAD_DIM), torch.bfloat16, q.device, stream)
-        flags = ATTENTION_FILL_OUT
-    else:
-        _at(out, dev, "out")
-        if out.dtype != torch.bfloat16 or out.shape != (T, Hq, HEAD_DIM) or not out.is_contiguous():
-            raise ValueError("out must be a contiguous bfloat16 [T, Hq, 64]")
-    if lse is None:
-        lse = _empty((T, Hq), torch.float32, q.device, stream)
-        flags |= ATTENTION_FILL_LSE
-    else:
-        _float_lse(lse, dev, (T, Hq))
+    out, lse, flags = _attention_outputs(q, dev, T, Hq, out, lse, stream)
     lib = _load()
     # the split follows the device's size: asked with q's GPU as the current device
     if dev != torch.cuda.current_device():
@@ -1337,6 +1385,7 @@ def context_attention_mass(q, cache, tables, ctx_lens, q_starts, lse, max_nodes,
     out      weights itself, or a tensor apart from it (default: a new one)
     Other arguments as context_tree_attention."""
     torch = _torch or _get_torch()
+    _bf16_cache(cache)
     dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
                                                       tree_mask, scale, softcap)
     _float_lse(lse, dev, (T, Hq))
@@ -1416,6 +1465,64 @@ def context_kv_evict(cache, tables, lens, weights, positions, ends, budget, sink
           new_positions.data_ptr(), new_lens.data_ptr(), None if ws is None else ws.data_ptr(), need,
           _stream(stream, cache))
     return new_weights, new_positions, new_lens
+
+
+def _window_attention(entry, q, cache, tables, ctx_lens, q_starts, max_nodes, window, sinks, max_ctx, tree_mask, scale, softcap,
+                      out, lse, stream):
+    torch = _torch or _get_torch()
+    _fits32(window, "window")
+    _fits32(sinks, "sinks")
+    dev, T, Hq, H, B, max_ctx, args = _query_operands(q, cache, tables, ctx_lens, q_starts, max_nodes, max_ctx,
+                                                      tree_mask, scale, softcap)
+    out, lse, flags = _attention_outputs(q, dev, T, Hq, out, lse, stream)
+    sizes = _load().nrc_context_window_attention_workspace_bytes
+    # the split follows the device's size: asked with q's GPU as the current device
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            need = sizes(B, T, Hq, H, max_nodes, max_ctx, window, sinks)
+    else:
+        need = sizes(B, T, Hq, H, max_nodes, max_ctx, window, sinks)
+    if need < 0:
+        _check(need)
+    ws = _empty((need,), torch.uint8, q.device, stream) if need > 0 else None
+    _call(q, entry, *args, window, sinks, out.data_ptr(), lse.data_ptr(), None if ws is None else ws.data_ptr(), need, flags,
+          _stream(stream, q))
+    return out, lse
+
+
+def context_window_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, window, sinks=0, max_ctx=None, tree_mask=None,
+                             scale=None, softcap=0.0, out=None, lse=None, stream=None):
+    """context_tree_attention behind a sliding window with a few first keys that
+    stay visible -> (out [T, Hq, 64] bf16, lse [T, Hq] float32).
+
+    window  a row at position p sees the keys j > p - window of those it would see
+            without (its own is one of the window)
+    sinks   and the keys j < sinks
+    Without tree_mask node i stands at ctx_lens + i, and the window goes over the nodes too;
+    with it a row stands at ctx_lens + the nodes it sees - 1, and over its
+    nodes the mask alone decides. Keys that no row can see are not read. A prompt's
+    chunk is a chain of up to 65535 nodes. Other arguments and results as
+    context_tree_attention."""
+    _bf16_cache(cache)
+    if isinstance(window, int) and window < 1:
+        raise ValueError("window must be at least 1")
+    return _window_attention(_load().nrc_context_window_attention, q, cache, tables, ctx_lens, q_starts, max_nodes, window,
+                             sinks, max_ctx, tree_mask, scale, softcap, out, lse, stream)
+
+
+def context_fp4_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, window=0, sinks=0, max_ctx=None, tree_mask=None,
+                          scale=None, softcap=0.0, out=None, lse=None, stream=None):
+    """context_tree_attention over a cache of 4 bits ([num_blocks, H,
+    fp4_page_bytes(block_size)] uint8, one layer's of context_fp4_store), behind a window
+    (context_window_attention) or, with window 0, without -> (out, lse).
+
+    K and V are the cells' values; a row that sees a cell that stands for NaN gets NaN. Other
+    arguments and results as context_tree_attention."""
+    torch = _torch or _get_torch()
+    if cache.dtype != torch.uint8:
+        raise TypeError(f"cache must be a uint8 GPU tensor, not {cache.dtype} on {cache.device}")
+    return _window_attention(_load().nrc_context_fp4_attention, q, cache, tables, ctx_lens, q_starts, max_nodes, window, sinks,
+                             max_ctx, tree_mask, scale, softcap, out, lse, stream)
 
 
 FP4_FILL = 1

@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnrc.so")
 SOURCES = ["api.cpp", "context_norms.hip", "norms_ex.hip", "draft_boundary.hip", "kv_project.hip", "kv_store.hip", "selftest.hip",
            "cache_api.cpp", "rope.hip", "tree_attention.hip", "attention_mass.hip", "kv_evict.hip",
-           "draft_api.cpp", "qk_norm.hip", "fp4_cells.hip"]
+           "draft_api.cpp", "qk_norm.hip", "fp4_cells.hip", "window_attention.hip"]
 # the chain's kernels and the entry points that choose among them: what the stored counter measurements were taken of
 CHAIN_SOURCES = ["api.cpp", "context_norms.hip", "device_common.h", "draft_boundary.hip", "kernels.h", "kv_project.hip",
                  "kv_store.hip", "norms_ex.hip", "selftest.hip", "status.h"]

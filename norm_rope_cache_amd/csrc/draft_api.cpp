@@ -180,6 +180,47 @@ bool rows4_apart(const Rows4& r, int64_t T, int32_t H, int32_t L) {
     return true;
 }
 
+// The queries, outputs and workspace of both attentions; a->kv is set, cells what they read of the cache.
+int32_t attend(const char* what, WindowArgs a, const Range& cells, const uint16_t* q, int64_t q_rs, int64_t q_hs, int64_t T,
+               int32_t Hq, int32_t H, int32_t B, const int32_t* ctx_lens, const int32_t* q_starts, int32_t max_nodes,
+               int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words, float scale, float softcap, uint16_t* out,
+               float* lse, void* workspace, int64_t workspace_bytes, uint32_t flags, void* stream) {
+    if (flags & ~(uint32_t)(NRC_ATTENTION_FILL_OUT | NRC_ATTENTION_FILL_LSE))
+        return fail(NRC_EINVAL, "%s: unknown flags 0x%x", what, flags);
+    if (int32_t rc = queries(what, q, q_rs, q_hs, T, Hq, H, B, ctx_lens, q_starts, max_nodes, max_ctx, tree_mask, mask_words,
+                             scale, softcap, &a.tq))
+        return rc;
+    const bool work = B > 0 && T > 0;
+    if (!work && (T == 0 || flags == 0)) return NRC_OK;
+    if (!out || !lse) return fail(NRC_EINVAL, "%s: NULL out or lse", what);
+    if (!aligned(out, 16) || !aligned(lse, 4)) return fail(NRC_EINVAL, "%s: out must be 16-byte, lse 4-byte aligned", what);
+    const Range out_range{out, T * Hq * 128}, lse_range{lse, T * Hq * 4}, q_range{q, 2 * span(T, Hq, 64, q_rs, q_hs)};
+    if (any_meet({out_range, lse_range}, {q_range}) || any_meet({out_range}, {lse_range}))
+        return fail(NRC_EINVAL, "%s: q, out and lse must lie apart from each other", what);
+    a.fill = flags;
+    a.out = out;
+    a.lse = lse;
+    if (!work) return launch_status(launch_window_attention(a, (hipStream_t)stream), what);
+    a.plan = plan_window_attention(B, H, Hq / H, max_nodes, max_ctx, a.window, a.sinks, num_cus());
+    const int64_t bytes = window_attention_workspace(a.plan, T, Hq);
+    if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
+        return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
+    // other workgroups still read these
+    const Range ws_range{workspace, bytes};
+    if (any_meet({out_range, lse_range, ws_range},
+                 {cells, tables_range(a.kv, B), {ctx_lens, 4 * (int64_t)B}, {q_starts, 4 * ((int64_t)B + 1)},
+                  {tree_mask, 8 * T * mask_words}}) ||
+        any_meet({ws_range}, {q_range, out_range, lse_range}))
+        return fail(NRC_EINVAL, "%s: out, lse and the workspace must lie apart from each other and the inputs", what);
+    a.part = static_cast<float*>(workspace);
+    return launch_status(launch_window_attention(a, (hipStream_t)stream), what);
+}
+
+int32_t window_sizes(const char* what, int32_t window, int32_t sinks) {
+    if (window < 0 || sinks < 0) return fail(NRC_EINVAL, "%s: window and sinks must not be negative", what);
+    return NRC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -347,6 +388,62 @@ int32_t nrc_context_fp4_load(const uint8_t* caches, int64_t layer_stride, int64_
         any_meet({k_range}, {v_range}))
         return fail(NRC_EINVAL, "%s: k and v must lie apart from each other, the caches and slots", what);
     return launch_status(launch_fp4_load(r, c, k, v, flags != 0, (hipStream_t)stream), what);
+}
+
+int64_t nrc_context_window_attention_workspace_bytes(int32_t B, int64_t T, int32_t Hq, int32_t H, int32_t max_nodes,
+                                                     int64_t max_ctx, int32_t window, int32_t sinks) {
+    const char* what = "context_window_attention";
+    if (int32_t rc = query_sizes(what, B, T, Hq, H, max_nodes, max_ctx)) return rc;
+    if (int32_t rc = window_sizes(what, window, sinks)) return rc;
+    if (B == 0 || T == 0) return 0;
+    return window_attention_workspace(plan_window_attention(B, H, Hq / H, max_nodes, max_ctx, window ? window : INT32_MAX,
+                                                            window ? sinks : 0, num_cus()),
+                                      T, Hq);
+}
+
+int32_t nrc_context_window_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int32_t Hq,
+                                     const uint16_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,
+                                     int64_t page_stride, int64_t head_stride, int32_t H, const int32_t* tables,
+                                     int64_t table_stride, int64_t table_width, int32_t B, const int32_t* ctx_lens,
+                                     const int32_t* q_starts, int32_t max_nodes, int64_t max_ctx, const int64_t* tree_mask,
+                                     int32_t mask_words, float scale, float softcap, int32_t window, int32_t sinks,
+                                     uint16_t* out, float* lse, void* workspace, int64_t workspace_bytes, uint32_t flags,
+                                     void* stream) {
+    const char* what = "context_window_attention";
+    WindowArgs a{};
+    if (int32_t rc = paged_cache(what, cache, num_blocks, block_size, block_stride, page_stride, head_stride, H, tables,
+                                 table_stride, table_width, B, B > 0 && T > 0, &a.kv))
+        return rc;
+    if (int32_t rc = window_sizes(what, window, sinks)) return rc;
+    if (window < 1) return fail(NRC_EINVAL, "%s: window must be at least 1", what);
+    a.window = window;
+    a.sinks = sinks;
+    return attend(what, a, cells_range(a.kv, H), q, q_row_stride, q_head_stride, T, Hq, H, B, ctx_lens, q_starts, max_nodes,
+                  max_ctx, tree_mask, mask_words, scale, softcap, out, lse, workspace, workspace_bytes, flags, stream);
+}
+
+int32_t nrc_context_fp4_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int32_t Hq,
+                                  const uint8_t* cache, int64_t num_blocks, int64_t block_size, int64_t block_stride,
+                                  int64_t head_stride, int32_t H, const int32_t* tables, int64_t table_stride,
+                                  int64_t table_width, int32_t B, const int32_t* ctx_lens, const int32_t* q_starts,
+                                  int32_t max_nodes, int64_t max_ctx, const int64_t* tree_mask, int32_t mask_words,
+                                  float scale, float softcap, int32_t window, int32_t sinks, uint16_t* out, float* lse,
+                                  void* workspace, int64_t workspace_bytes, uint32_t flags, void* stream) {
+    const char* what = "context_fp4_attention";
+    const bool work = B > 0 && T > 0;
+    WindowArgs a{};
+    Fp4Cache c{};
+    if (int32_t rc = fp4_cache(what, cache, 0, block_stride, head_stride, num_blocks, block_size, H, work, &c)) return rc;
+    // (the table's checks; the pages' are done)
+    if (int32_t rc = paged_cache(what, reinterpret_cast<const uint16_t*>(cache), num_blocks, block_size, block_stride, 0,
+                                 head_stride, H, tables, table_stride, table_width, B, work, &a.kv))
+        return rc;
+    if (int32_t rc = window_sizes(what, window, sinks)) return rc;
+    a.fp4 = true;
+    a.window = window ? window : INT32_MAX;
+    a.sinks = window ? sinks : 0;
+    return attend(what, a, pages_range(c, H, 1), q, q_row_stride, q_head_stride, T, Hq, H, B, ctx_lens, q_starts, max_nodes,
+                  max_ctx, tree_mask, mask_words, scale, softcap, out, lse, workspace, workspace_bytes, flags, stream);
 }
 
 }  // extern "C"

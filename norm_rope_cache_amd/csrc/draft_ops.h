@@ -65,4 +65,30 @@ int64_t fp4_page(int64_t block_size);  // bytes of a page of a head
 int launch_fp4_store(const Fp4Rows& r, const Fp4Cache& c, hipStream_t stream);
 int launch_fp4_load(const Fp4Rows& r, const Fp4Cache& c, uint16_t* k, uint16_t* v, bool fill, hipStream_t stream);
 
+// How a shape is worked on: the kernel (many rows: keys shared through LDS), 16-row query tiles of a wave (few rows),
+// a workgroup's waves, workgroups along the rows, the most shares that a block's tiles are dealt into and the fewest tiles
+// of one.
+struct WindowPlan {
+    bool many;
+    int32_t q_tiles, waves, row_blocks, splits, min_tiles;
+};
+
+WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t window,
+                                 int32_t sinks, int32_t num_cus);
+int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads);
+
+struct WindowArgs {
+    PagedCache kv;  // fp4: pages of 4 bits, the strides in bytes (page_stride is not used)
+    TreeQueries tq;
+    int32_t window, sinks;  // window 2^31 - 1: none
+    bool fp4;
+    uint16_t* out;  // [T, H G, 64]
+    float* lse;     // [T, H G]
+    float* part;    // splits > 1: the partial sums, [splits, T, H G, 64] then [splits, T, H G, 2]
+    WindowPlan plan;
+    uint32_t fill;  // NRC_ATTENTION_FILL_*
+};
+
+int launch_window_attention(const WindowArgs& a, hipStream_t stream);
+
 }  // namespace nrc

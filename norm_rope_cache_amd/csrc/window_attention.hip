@@ -1,0 +1,832 @@
+// Attention of drafted tokens over the paged cache behind a sliding window with
+// a few first keys that stay visible, and over a cache held in 4 bits.
+//
+// The formulas, the running softmax and its roundings are those of
+// tree_attention.hip; what differs is which keys there are to look at and what a cell is.
+//
+// Window: a row at position p sees the keys j <= p with j > p - window or j <
+// sinks. A workgroup's rows stand at nearby positions, so the tiles it looks at are
+// those of the sinks and those from its first row's window to its last row's own
+// key: two runs, walked as one by their numbers. A tile that every row of a wave
+// sees whole (most of them) goes without a mask, others get one from each row's
+// first key, by shifts alone for a chain.
+//
+// 4 bits: K's and V's elements are bf16 numbers once opened (a code's value times a
+// power of two), so the matrix instructions take them as a bf16 cache's, with
+// nothing rounded on the way. The conversion takes two codes an instruction. A cell that
+// stands for NaN has NaN in K, so a row that sees it gets NaN scores and outputs; in a
+// tile that some rows do not see whole, V's scales are held to 2^125, so that 0
+// times a V that a row does not see is 0.
+//
+// Few rows a KV head (up to 32) are bound by the cache's bytes and, in 4 bits, by
+// the instructions that open them; many rows by the vector unit and the matrix cores.
+#include <atomic>
+
+#include "../../include/nrc.h"
+#include "attention_core.h"
+#include "draft_ops.h"
+#include "fp4.h"
+#include "kernels.h"
+
+namespace nrc {
+namespace {
+
+constexpr int32_t kNoWindow = 0x7FFFFFFF;
+
+// The keys that a block of rows looks at: key j if any row may see it lies in [0, sinks) or [lo_min, hi_max]; every row
+// sees those in [lo_max, hi_min], and the sinks up to hi_min.
+struct Keyspan {
+    int32_t lo_min, lo_max, hi_min, hi_max;
+};
+// Of rows first .. last (of the sequence's; last is cut to them). A tree's rows stand at ctx + the nodes they see - 1.
+__device__ __forceinline__ Keyspan keyspan(const TreeQueries& tq, const Span& s, int32_t window, int32_t first, int32_t last) {
+    if (last >= s.rows) last = s.rows - 1;
+    if (tq.mask) return Keyspan{s.ctx - window, s.ctx - window + s.nodes.count, s.ctx - 1, s.ctx + s.nodes.count - 1};
+    const int32_t n0 = first / tq.G, n1 = last / tq.G;
+    return Keyspan{s.ctx - window + 1 + n0, s.ctx - window + 1 + n1, s.ctx + n0, s.ctx + n1};
+}
+
+// The tiles of KEYS keys that a block of rows looks at: `sinks` from the first on, then those from `from` on, n in all.
+struct Tiles {
+    int32_t sinks, from, n;
+    __device__ __forceinline__ int32_t at(int32_t v) const { return v < sinks ? v : v - sinks + from; }
+};
+template <int KEYS>
+__device__ __forceinline__ Tiles tiles_of(const Keyspan& k, int32_t sinks) {
+    Tiles t;
+    t.from = (k.lo_min < 0 ? 0 : k.lo_min) / KEYS;
+    const int32_t first = sinks / KEYS + (sinks % KEYS != 0);
+    t.sinks = first < t.from ? first : t.from;
+    t.n = t.sinks + k.hi_max / KEYS + 1 - t.from;
+    return t;
+}
+// Tiles of one of up to `splits` shares, and how many shares there are.
+__device__ __forceinline__ int32_t share_of(int32_t n, const WindowPlan& plan) {
+    const int32_t share = (n + plan.splits - 1) / plan.splits;
+    return share < plan.min_tiles ? plan.min_tiles : share;
+}
+
+enum Seen { kNobody, kSome, kEverybody };
+template <int KEYS>
+__device__ __forceinline__ Seen seen_by(const Keyspan& k, int32_t sinks, int32_t key0) {
+    if (key0 > k.hi_max || (key0 + (KEYS - 1) < k.lo_min && key0 >= sinks)) return kNobody;
+    if (key0 + (KEYS - 1) <= k.hi_min && (key0 >= k.lo_max || key0 + (KEYS - 1) < sinks)) return kEverybody;
+    return kSome;
+}
+
+// Bits i of a word of 32 keys from key0 on with key0 + i >= first; < first.
+__device__ __forceinline__ uint32_t from_key(int32_t first, int32_t key0) {
+    if (first <= key0) return 0xFFFFFFFFu;
+    const int64_t k = (int64_t)first - key0;
+    return k >= 32 ? 0u : 0xFFFFFFFFu << k;
+}
+__device__ __forceinline__ uint32_t below_key(int32_t first, int32_t key0) { return ~from_key(first, key0); }
+
+// A lane's row: its node (-1: none) and the first key of its window.
+struct Row {
+    int32_t node, lo;
+};
+__device__ __forceinline__ Row row_of(const TreeQueries& tq, const Span& s, int32_t window, int32_t r) {
+    Row row{-1, 0};
+    if (r >= s.rows) return row;
+    row.node = r / tq.G;
+    row.lo = s.ctx - window + 1 + row.node;
+    if (tq.mask && window != kNoWindow) {
+        const uint32_t* words = tq.mask + (int64_t)(s.nodes.first + row.node) * tq.mask_words;
+        int32_t seen = 0;
+        for (int32_t w = 0; 32 * w < s.nodes.count; ++w) {
+            const int32_t left = s.nodes.count - 32 * w;
+            seen += __builtin_popcount(words[w] & (left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u));
+        }
+        row.lo = s.ctx - window + seen;
+    }
+    return row;
+}
+// Which of the 32 keys from key0 on the row sees.
+__device__ __forceinline__ uint32_t row_sees(const TreeQueries& tq, const Span& s, const Row& row, int32_t sinks, int32_t key0) {
+    uint32_t word[1] = {row.node < 0 ? 0u : 0xFFFFFFFFu};
+    if (!tq.mask || key0 + 31 >= s.ctx) seen_keys<1>(word, tq, s.nodes, s.ctx, row.node, key0);
+    uint32_t near = from_key(row.lo, key0) | below_key(sinks, key0);
+    if (tq.mask) near |= from_key(s.ctx, key0);  // a tree's mask alone decides over its nodes
+    return word[0] & near;
+}
+
+// Where a key's cell lies: byte (bf16: element) offset of its K within head 0, or -1, and its place in the page.
+struct Place {
+    int64_t off;
+    uint32_t at;
+};
+template <bool FP4>
+__device__ __forceinline__ Place place_of(const PagedCache& c, uint32_t key, uint32_t page) {
+    const uint32_t blk = block_of(key, c), at = key - blk * c.block_size;
+    const bool there = blk < c.table_width && page < c.num_blocks;
+    return Place{there ? (int64_t)page * c.block_stride + (FP4 ? (int64_t)at * kFp4Codes : (int64_t)at * c.page_stride) : -1, at};
+}
+
+// ---- few rows -----------------------------------------------------------------------------------------------------
+
+// A tile of 32 cells of 4 bits as a lane loads it: K's 16 codes of key l % 16 of each half (elements 16 (l / 16) ..,
+// the first 8 in .x), V's 4 codes (elements 4 (l % 16) ..) of the keys 16 t + 4 (l / 16) + r, the keys' scale dwords.
+struct Packed {
+    uint2 k[2];
+    uint32_t ks[2];
+    uint32_t v[8];
+    uint32_t vs[8];
+};
+template <bool FP4>
+struct RawOf {
+    typedef Keys T;
+};
+template <>
+struct RawOf<true> {
+    typedef Packed T;
+};
+
+__device__ __forceinline__ uint32_t rotate_right(uint32_t w, uint32_t n) { return __builtin_amdgcn_alignbit(w, w, n); }
+
+// Packed cells opened. HELD: V's scales at most 2^125 (of cells that not every row sees).
+template <bool HELD>
+__device__ __forceinline__ void open_keys(Keys& kv, const Packed& p, uint32_t lane) {
+    // the scale's byte to a float's exponent; the other bits are not looked at
+    const uint32_t k_turn = lane & 32u ? 17u : 9u, v_turn = lane & 8u ? 1u : 25u;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const float s = __uint_as_float(rotate_right(p.ks[t], k_turn));
+        kv.k[t][0] = fp4_open(p.k[t].x, s);
+        kv.k[t][1] = fp4_open(p.k[t].y, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t s = rotate_right(p.vs[i], v_turn);
+        if constexpr (HELD) {
+            s &= 0x7F800000u;
+            s = s < kScaleHigh << 23 ? s : kScaleHigh << 23;
+        }
+        kv.v[i] = uint2{fp4_pair<0>(p.v[i], __uint_as_float(s)), fp4_pair<1>(p.v[i], __uint_as_float(s))};
+    }
+}
+
+// One workgroup per (sequence, KV head, share); its WAVES waves hold the same rows and take the share's tiles of 32
+// keys in turn, from memory through registers, as few_rows_kernel of tree_attention.hip does.
+// PAGE16 (block_size a multiple of 16): half a tile lies in one page, so its base is a scalar.
+template <int R, int WAVES, bool CAP, bool FP4, bool PAGE16>
+__global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void window_few_kernel(WindowArgs a, uint32_t groups) {
+    extern __shared__ float smem[];
+    if (blockIdx.x >= groups) {
+        fill_rows(a.tq, a.fill, a.out, a.lse, blockIdx.x - groups, gridDim.x - groups);
+        return;
+    }
+    typedef typename RawOf<FP4>::T Raw;
+    const PagedCache& kv = a.kv;
+    const TreeQueries& tq = a.tq;
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t g = lane >> 4, n16 = lane & 15u;
+    const int32_t split = blockIdx.x % a.plan.splits;
+    const uint32_t bh = blockIdx.x / a.plan.splits;
+    const int32_t h = bh % tq.H, b = bh / tq.H;
+    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
+    const Span s = span_of<kTile>(tq, b);
+    if (s.rows == 0) return;
+    const Keyspan span = keyspan(tq, s, a.window, 0, s.rows - 1);
+    const Tiles tiles = tiles_of<kTile>(span, a.sinks);
+    const int32_t share = share_of(tiles.n, a.plan), first = split * share;
+    if (first >= tiles.n) return;  // (nor does the join look at such a share)
+    const int32_t end = tiles.n - first < share ? tiles.n : first + share;
+    const int32_t total = s.ctx + s.nodes.count;
+
+    const uint8_t* head = reinterpret_cast<const uint8_t*>(kv.cache) + (int64_t)h * kv.head_stride * (FP4 ? 1 : 2);
+    const Factors f = factors<CAP>(tq);
+    // the table's entry of the lane's key of tile number v (of the last one past the end)
+    auto entry = [&](int32_t v) {
+        return page_of(kv, table, (uint32_t)tiles.at(v < end ? v : end - 1) * kTile + (lane & (kTile - 1)));
+    };
+    auto place = [&](int32_t v, uint32_t page) -> Place {
+        if (v >= end) return Place{-1, 0u};
+        const uint32_t key = (uint32_t)tiles.at(v) * kTile + (lane & (kTile - 1));
+        Place p = place_of<FP4>(kv, key, page);
+        if (!PAGE16 && key >= (uint32_t)total) p.off = -1;  // (PAGE16 reads whole pages, and masks)
+        return p;
+    };
+    auto exists = [&](int32_t v, const Place& p) {
+        const uint32_t key = (uint32_t)tiles.at(v) * kTile + (lane & (kTile - 1));
+        return (uint32_t)__ballot(p.off >= 0 && key < (uint32_t)total);
+    };
+    const uint32_t codes = kFp4Codes * kv.block_size;  // bytes of a page's K codes
+    auto fetch = [&](Raw& raw, const Place& p) {
+        if constexpr (FP4 && PAGE16) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int32_t hi = __builtin_amdgcn_readlane((int)((uint64_t)p.off >> 32), 16 * t);
+                raw.k[t] = uint2{0u, 0u}, raw.ks[t] = 0u;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) raw.v[4 * t + r] = raw.vs[4 * t + r] = 0u;
+                if (hi < 0) continue;  // (no such page)
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)p.off, 16 * t);
+                const uint32_t at = __builtin_amdgcn_readlane(p.at, 16 * t);
+                const uint8_t* page = head + (int64_t)((uint64_t)(uint32_t)hi << 32 | lo);
+                const uint8_t* scales = page + 2 * codes - (kFp4Codes - 4) * at;
+                raw.k[t] = *reinterpret_cast<const uint2*>(page + n16 * kFp4Codes + 8 * g);
+                raw.ks[t] = *reinterpret_cast<const uint32_t*>(scales + 4 * n16);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    raw.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(page + codes + (4 * g + r) * kFp4Codes + 2 * n16);
+                const U32x4 vs = load16(scales + 16 * g);
+                raw.vs[4 * t] = vs.x, raw.vs[4 * t + 1] = vs.y, raw.vs[4 * t + 2] = vs.z, raw.vs[4 * t + 3] = vs.w;
+            }
+        } else if constexpr (FP4) {
+            auto of = [&](uint32_t key, int64_t* off, int64_t* scales) {
+                const int lo = __builtin_amdgcn_ds_bpermute((int)(key << 2), (int)(uint32_t)p.off);
+                const int hi = __builtin_amdgcn_ds_bpermute((int)(key << 2), (int)(uint32_t)((uint64_t)p.off >> 32));
+                const uint32_t at = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(key << 2), (int)p.at);
+                *off = (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+                *scales = *off + 2 * (int64_t)codes - (int64_t)(kFp4Codes - 4) * at;
+                return hi >= 0;
+            };
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                int64_t off, sc;
+                raw.k[t] = uint2{0u, 0u}, raw.ks[t] = 0u;
+                if (of(16 * t + n16, &off, &sc)) {
+                    const uint32_t* k = reinterpret_cast<const uint32_t*>(head + off + 8 * g);  // (pages are 16-byte aligned)
+                    raw.k[t] = uint2{k[0], k[1]};
+                    raw.ks[t] = *reinterpret_cast<const uint32_t*>(head + sc);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    raw.v[4 * t + r] = raw.vs[4 * t + r] = 0u;
+                    if (of(16 * t + 4 * g + r, &off, &sc)) {
+                        raw.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(head + off + codes + 2 * n16);
+                        raw.vs[4 * t + r] = *reinterpret_cast<const uint32_t*>(head + sc);
+                    }
+                }
+            }
+        } else if constexpr (PAGE16) {
+            const uint16_t* head16 = reinterpret_cast<const uint16_t*>(head);
+            const uint32_t k_at = n16 * (uint32_t)kv.page_stride + 8 * g;
+            const uint32_t v_at = 4 * g * (uint32_t)kv.page_stride + kHeadDim + 4 * n16;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int32_t hi = __builtin_amdgcn_readlane((int)((uint64_t)p.off >> 32), 16 * t);
+                raw.k[t][0] = raw.k[t][1] = U32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) raw.v[4 * t + r] = uint2{0u, 0u};
+                if (hi < 0) continue;
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)p.off, 16 * t);
+                const uint16_t* page = head16 + (int64_t)((uint64_t)(uint32_t)hi << 32 | lo);
+                raw.k[t][0] = load16(page + k_at);
+                raw.k[t][1] = load16(page + k_at + 32);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    raw.v[4 * t + r] = *reinterpret_cast<const uint2*>(page + v_at + r * (uint32_t)kv.page_stride);
+            }
+        } else {
+            load_keys(raw, reinterpret_cast<const uint16_t*>(head), p.off, lane);
+        }
+    };
+
+    Rows<R> w;
+    Row row[R];
+#pragma unroll
+    for (int rq = 0; rq < R; ++rq) {
+        const int32_t r = 16 * rq + (int32_t)n16;
+        row[rq] = row_of(tq, s, a.window, r);
+        w.q[rq][0] = w.q[rq][1] = U32x4{0u, 0u, 0u, 0u};
+        if (row[rq].node >= 0) {
+            const uint16_t* q = tq.q + (int64_t)(s.nodes.first + row[rq].node) * tq.q_rs +
+                                (int64_t)(h * tq.G + r - row[rq].node * tq.G) * tq.q_hs;
+            // in the order of d that K's operand has
+            w.q[rq][0] = load16(q + (FP4 ? 16 * g : 8 * g));
+            w.q[rq][1] = load16(q + (FP4 ? 16 * g + 8 : 32 + 8 * g));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.o[rq][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        w.base[rq] = kNone;
+        w.c[rq] = f.c;
+        w.l[rq] = 0.0f;
+    }
+
+    auto work = [&](int32_t v, Raw& raw, uint32_t there) {
+        const int32_t key0 = tiles.at(v) * kTile;
+        const Seen seen = seen_by<kTile>(span, a.sinks, key0);
+        if (seen == kEverybody && there == 0xFFFFFFFFu) {
+            if constexpr (FP4) {
+                Keys keys;
+                open_keys<false>(keys, raw, lane);
+                open_tile<R, CAP>(w, keys, f.c, f.capped);
+            } else {
+                open_tile<R, CAP>(w, raw, f.c, f.capped);
+            }
+        } else if (seen != kNobody && there != 0u) {
+            uint32_t sees[R];
+#pragma unroll
+            for (int rq = 0; rq < R; ++rq) sees[rq] = there & row_sees(tq, s, row[rq], a.sinks, key0);
+            Keys keys;
+            if constexpr (FP4) {
+                open_keys<true>(keys, raw, lane);
+                masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
+            } else {
+                keys = raw;
+                // (what lies in the places of keys that are not there may be anything)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!(there >> (16 * (i / 4) + 4 * g + i % 4) & 1u)) keys.v[i] = uint2{0u, 0u};
+                const bool odd = any_odd(keys);
+                if (odd) {
+                    Keys finite = keys;
+                    drop_odd(finite);
+                    masked_tile<R, CAP>(w, finite, f.c, f.capped, sees, lane);
+                    add_odd<R>(w, keys, sees, lane);
+                } else {
+                    masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
+                }
+            }
+        }
+    };
+    {
+        int32_t v = first + (int32_t)wave;
+        Raw raw[2];
+        const uint32_t page0 = entry(v), page1 = entry(v + WAVES);
+        Place p = place(v, page0);
+        uint32_t there = v < end ? exists(v, p) : 0u;
+        fetch(raw[0], p);
+        p = place(v + WAVES, page1);
+        auto step = [&](Raw& cur, Raw& next) {
+            const uint32_t page = entry(v + 2 * WAVES);  // (before the cells, so that nobody waits for those with it)
+            const uint32_t next_there = v + WAVES < end ? exists(v + WAVES, p) : 0u;
+            fetch(next, p);
+            work(v, cur, there);
+            v += WAVES;
+            there = next_there;
+            p = place(v + WAVES, page);
+        };
+        while (v < end) {
+            step(raw[0], raw[1]);
+            if (v >= end) break;
+            step(raw[1], raw[0]);
+        }
+    }
+
+    // Join the waves: each leaves m's base, l and O of its rows in LDS.
+    float* so = smem;                          // [WAVES][16 R][kPad]
+    float* sm = smem + WAVES * 16 * R * kPad;  // [WAVES][16 R]
+    float* sl = sm + WAVES * 16 * R;           // [WAVES][16 R]
+#pragma unroll
+    for (int rq = 0; rq < R; ++rq) {
+        const float l = group_sum(w.l[rq]);
+        const uint32_t r = wave * 16 * R + 16 * rq + n16;
+        if (g == 0) {
+            sm[r] = base_of<CAP>(w.base[rq], w.c[rq], f.c);
+            sl[r] = l;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<f32x4*>(so + r * kPad + 16 * g + 4 * i) =
+                f32x4{w.o[rq][0][i], w.o[rq][1][i], w.o[rq][2][i], w.o[rq][3][i]};
+    }
+    __syncthreads();
+    const int32_t heads = tq.H * tq.G;
+    const int64_t rows_all = (int64_t)tq.T * heads;
+    const Results to{a.out, a.lse, a.part + split * rows_all * kHeadDim,
+                     a.part + (a.plan.splits * kHeadDim + 2 * split) * rows_all, a.plan.splits == 1};
+    for (int32_t e = threadIdx.x; e < 16 * R * 16; e += 64 * WAVES) {
+        const int32_t r = e >> 4, d = (e & 15) * 4;
+        if (r >= s.rows) continue;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) top = __builtin_fmaxf(top, sm[k * 16 * R + r]);
+        const float base = top == -__builtin_inff() ? 0.0f : top;
+        float l = 0.0f;
+        f32x4 o{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < WAVES; ++k) {
+            const float x = exp2_hw(sm[k * 16 * R + r] - base);
+            l = __builtin_fmaf(sl[k * 16 * R + r], x, l);
+            const f32x4 p = *reinterpret_cast<const f32x4*>(so + (k * 16 * R + r) * kPad + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[i], x, o[i]);
+        }
+        const int32_t node = r / tq.G;
+        put_row4(to, (int64_t)(s.nodes.first + node) * heads + h * tq.G + (r - node * tq.G), d, top, l, o);
+    }
+}
+
+// ---- many rows ----------------------------------------------------------------------------------------------------
+
+// The WAVES waves of a workgroup hold 32 rows each and share the keys, staged as bf16 in LDS 16 WAVES at a time, in two
+// buffers: four threads a key bring a quarter of its cell each into registers while the waves work on the tile before, open it
+// where it is packed, and leave it in the other buffer; one barrier a tile. So a key is opened once for all rows of the
+// workgroup. LDS layout and matrix operands as many_rows_kernel of tree_attention.hip.
+template <int WAVES>
+constexpr int stage_of() { return 16 * WAVES; }
+constexpr int many_lds(int waves) { return 2 * 16 * waves * (256 + 4); }
+
+template <int WAVES, bool CAP, bool FP4>
+__global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a, uint32_t groups, uint32_t grid) {
+    if (blockIdx.x >= grid) {
+        fill_rows(a.tq, a.fill, a.out, a.lse, blockIdx.x - grid, gridDim.x - grid);
+        return;
+    }
+    constexpr int kStage = stage_of<WAVES>(), kSubs = kStage / 32;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    uint32_t* present = reinterpret_cast<uint32_t*>(lds + 2 * kStage * 256);  // [2][kStage]
+    const PagedCache& kv = a.kv;
+    const TreeQueries& tq = a.tq;
+    const uint32_t lds0 = lds_address(lds);
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const uint32_t hl = lane >> 5, n32 = lane & 31u;
+    // the row blocks of one share, which read the same keys, run on one XCD next to each other
+    uint32_t id = blockIdx.x, rb = 0;
+    if (a.plan.row_blocks > 1) {
+        const uint32_t slot = id >> 3;
+        rb = slot % a.plan.row_blocks;
+        id = slot / a.plan.row_blocks * 8 + (id & 7u);
+        if (id >= groups) return;
+    }
+    const int32_t split = id % a.plan.splits;
+    const uint32_t bh = id / a.plan.splits;
+    const int32_t h = bh % tq.H, b = bh / tq.H;
+    const Span s = span_of<kStage>(tq, b);
+    const int32_t block0 = rb * WAVES * 32;
+    if (block0 >= s.rows) return;
+    const Tiles tiles = tiles_of<kStage>(keyspan(tq, s, a.window, block0, block0 + WAVES * 32 - 1), a.sinks);
+    const int32_t share = share_of(tiles.n, a.plan), first = split * share;
+    if (first >= tiles.n) return;
+    const int32_t end = tiles.n - first < share ? tiles.n : first + share;
+    const int32_t total = s.ctx + s.nodes.count;
+    const int32_t row0 = block0 + (int32_t)wave * 32;
+    const bool active = row0 < s.rows;
+    const Keyspan span = keyspan(tq, s, a.window, row0, row0 + 31);  // of this wave's rows
+
+    const uint8_t* head = reinterpret_cast<const uint8_t*>(kv.cache) + (int64_t)h * kv.head_stride * (FP4 ? 1 : 2);
+    const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
+    const Factors f = factors<CAP>(tq);
+
+    // A thread's quarter (K's halves, V's halves) of its key's cell.
+    const uint32_t own_key = tid >> 2, quarter = tid & 3u;
+    U32x4 cell[FP4 ? 1 : 4];
+    uint32_t scales = 0;
+    bool there = false;
+    auto entry = [&](int32_t v) { return page_of(kv, table, (uint32_t)tiles.at(v < end ? v : end - 1) * kStage + own_key); };
+    auto fetch = [&](int32_t v, uint32_t page) {
+        const uint32_t key = (uint32_t)tiles.at(v) * kStage + own_key;
+        const Place p = place_of<FP4>(kv, key, page);
+        there = p.off >= 0 && key < (uint32_t)total;
+#pragma unroll
+        for (U32x4& c : cell) c = U32x4{0u, 0u, 0u, 0u};
+        scales = 0;
+        if (!there) return;
+        if constexpr (FP4) {
+            const int64_t codes = (int64_t)kFp4Codes * kv.block_size;
+            cell[0] = load16(head + p.off + (quarter >> 1) * codes + (quarter & 1u) * 16);
+            scales = *reinterpret_cast<const uint32_t*>(head + p.off + 2 * codes - (int64_t)(kFp4Codes - 4) * p.at);
+        } else {
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(head) + p.off + 32 * quarter;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cell[i] = load16(at + 8 * i);
+        }
+    };
+    auto put = [&](int buf) {
+        const uint32_t swizzle = quarter < 2 ? own_key & 7u : (own_key >> 1 & 1u) << 2;
+        uint8_t* at = lds + buf * (kStage * 256) + (quarter >> 1) * (kStage * 128) + own_key * 128;
+        if constexpr (FP4) {
+            uint32_t byte = scales >> (8 * quarter) & 0xFFu;
+            if (quarter >= 2) byte = byte < kScaleHigh ? byte : kScaleHigh;  // (V: see the top)
+            const float scale = __uint_as_float(byte << 23);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, fp4_open((&cell[0].x)[i], scale));
+        } else {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, cell[i]);
+        }
+        if (quarter == 0) present[buf * kStage + own_key] = there;
+    };
+
+    // this lane's places in a stage
+    const uint32_t k_at = n32 * 128, k_c = n32 & 7u, t16 = lane & 15u;
+    const uint32_t v_at = kStage * 128 + (4 * hl + (t16 >> 2)) * 128 +
+                          ((2 * (lane >> 4 & 1u) + (t16 >> 1 & 1u)) ^ (t16 >> 3) << 2) * 16 + (t16 & 1u) * 8;
+    auto read_k = [&](Keys32& k, int buf, int sub) {
+        const uint8_t* at = lds + buf * (kStage * 256) + sub * 4096 + k_at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k.k[i] = load16(at + (((2 * i + hl) ^ k_c) << 4));
+    };
+    auto read_v = [&](Keys32& k, int buf, int sub) {
+        const uint32_t at = buf * (kStage * 256) + sub * 4096;
+        auto four = [&](uint32_t o) {
+            typedef __attribute__((address_space(3))) i16x4 LdsFour;
+            return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour*)(uintptr_t)(lds0 + o)));
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const uint2 a = four(at + (v_at ^ c * 64) + ks * 2048), z = four(at + (v_at ^ c * 64) + ks * 2048 + 1024);
+                k.v[c][ks] = U32x4{a.x, a.y, z.x, z.y};
+            }
+    };
+
+    Rows32<1> w;
+    const int32_t r = row0 + (int32_t)n32;
+    const Row row = row_of(tq, s, a.window, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.q[0][i] = U32x4{0u, 0u, 0u, 0u};
+    if (row.node >= 0) {
+        const uint16_t* q = tq.q + (int64_t)(s.nodes.first + row.node) * tq.q_rs +
+                            (int64_t)(h * tq.G + r - row.node * tq.G) * tq.q_hs + 8 * hl;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.q[0][i] = load16(q + 16 * i);
+    }
+    w.o[0][0] = w.o[0][1] = f32x16{0.f};
+    w.base[0] = kNone;
+    w.c[0] = f.c;
+    w.l[0] = 0.0f;
+
+    auto masked = [&](int buf, int sub, int32_t key0, uint32_t keys_there) {
+        Keys32 k;
+        const uint32_t sees = bits_of_scores(keys_there & row_sees(tq, s, row, a.sinks, key0), hl);
+        read_k(k, buf, sub);
+        read_v(k, buf, sub);
+        bool odd = false;  // infinities and NaN in V: see add_odd
+        if constexpr (!FP4) {
+            u16x2 most{0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, (&k.v[i / 8][i / 4 % 2].x)[i % 4] & 0x7FFF7FFFu));
+            odd = __any(most.x >= 0x7F80 || most.y >= 0x7F80);
+            if (odd) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    uint32_t& v = (&k.v[i / 8][i / 4 % 2].x)[i % 4];
+                    v = finite_pair(v);
+                }
+            }
+        }
+        f32x16 sc;
+        scores32<1>(sc, w, 0, k);
+        add32<1, CAP, true>(w, 0, sc, k, f, sees);
+        if (!odd) return;
+        read_v(k, buf, sub);
+#pragma unroll 1
+        for (int kind = 0; kind < 3; ++kind) {
+            const float adds = kind == 0 ? __builtin_inff() : kind == 1 ? -__builtin_inff() : __builtin_nanf("");
+            const uint32_t which = kind == 0 ? 0x7F80u : kind == 1 ? 0xFF80u : 0u;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f32x16 met{0.f};
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    U32x4 ones, seen;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        (&ones.x)[j] = ones_of_kind((&k.v[c][ks].x)[j], which);
+                        const uint32_t two = sees >> (8 * ks + 2 * j);
+                        (&seen.x)[j] = (two & 1u ? 0x3F80u : 0u) | (two & 2u ? 0x3F800000u : 0u);
+                    }
+                    met = mfma32(ones, seen, met);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (met[i] > 0.0f) w.o[0][c][i] += adds;
+            }
+        }
+    };
+    auto work = [&](int32_t v, int buf) {
+        const int32_t key0 = tiles.at(v) * kStage;
+        uint64_t exists[kStage / 64];
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < kStage / 64; ++i) {
+            exists[i] = __ballot(present[buf * kStage + 64 * i + lane] != 0u);
+            all &= exists[i] == ~0ull;
+        }
+        if (all && seen_by<kStage>(span, a.sinks, key0) == kEverybody) {
+            // the next 32 keys' scores on the way while the vector unit takes these ones' exponentials
+            Keys32 k;
+            f32x16 sc[2];
+            read_k(k, buf, 0);
+            scores32<1>(sc[0], w, 0, k);
+#pragma unroll
+            for (int sub = 0; sub < kSubs; ++sub) {
+                read_v(k, buf, sub);
+                if (sub + 1 < kSubs) {
+                    read_k(k, buf, sub + 1);
+                    scores32<1>(sc[(sub + 1) % 2], w, 0, k);
+                }
+                add32<1, CAP, false>(w, 0, sc[sub % 2], k, f, 0u);
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int sub = 0; sub < kSubs; ++sub) {
+            const uint32_t keys_there = (uint32_t)((kStage > 64 && sub & 2 ? exists[kStage / 64 - 1] : exists[0]) >> (32 * (sub & 1)));
+            const int32_t at = key0 + 32 * sub;
+            const Seen seen = seen_by<32>(span, a.sinks, at);
+            if (seen == kNobody || keys_there == 0u) continue;
+            if (seen == kEverybody && keys_there == 0xFFFFFFFFu) {
+                Keys32 k;
+                f32x16 sc;
+                read_k(k, buf, sub);
+                read_v(k, buf, sub);
+                scores32<1>(sc, w, 0, k);
+                add32<1, CAP, false>(w, 0, sc, k, f, 0u);
+            } else {
+                masked(buf, sub, at, keys_there);
+            }
+        }
+    };
+
+    uint32_t page = entry(first);
+    fetch(first, page);
+    page = entry(first + 1);
+    put(0);
+    __syncthreads();
+    for (int32_t v = first; v < end; ++v) {
+        const int buf = (v - first) & 1;
+        const uint32_t after = entry(v + 2);  // (before the cells, so that nobody waits for those with it)
+        if (v + 1 < end) fetch(v + 1, page);
+        if (active) work(v, buf);
+        page = after;
+        if (v + 1 < end) {
+            put(buf ^ 1);  // (nobody reads it since the last barrier)
+            __syncthreads();
+        }
+    }
+    if (!active) return;
+    const int32_t heads = tq.H * tq.G;
+    const int64_t rows_all = (int64_t)tq.T * heads;
+    const Results to{a.out, a.lse, a.part + split * rows_all * kHeadDim,
+                     a.part + (a.plan.splits * kHeadDim + 2 * split) * rows_all, a.plan.splits == 1};
+    const float l = w.l[0] + lane_xor<32>(w.l[0]);
+    const float top = base_of<CAP>(w.base[0], w.c[0], f.c);
+    if (row.node < 0) return;
+    const int64_t at = (int64_t)(s.nodes.first + row.node) * heads + h * tq.G + r - row.node * tq.G;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            put_row4(to, at, 32 * c + 8 * i + 4 * (int32_t)hl, top, l,
+                     f32x4{w.o[0][c][4 * i], w.o[0][c][4 * i + 1], w.o[0][c][4 * i + 2], w.o[0][c][4 * i + 3]});
+}
+
+// The shares of a row joined: 16 lanes a row, 4 elements of d a lane, eight shares' loads on the way at a time.
+__global__ __launch_bounds__(256) void window_join_kernel(WindowArgs a) {
+    const TreeQueries& tq = a.tq;
+    const int32_t heads = tq.H * tq.G;
+    const int32_t row = blockIdx.x * 16 + (int32_t)(threadIdx.x >> 4), d = 4 * (int32_t)(threadIdx.x & 15u);
+    const int32_t b = blockIdx.y;
+    const Span s = span_of<kTile>(tq, b);
+    if (row >= s.nodes.count * heads) return;
+    // the tiles of the row's block, as the attending workgroup counted them
+    const int32_t node = row / heads, hq = row - node * heads, r = node * tq.G + hq % tq.G;
+    const int32_t block_rows = a.plan.many ? 32 * a.plan.waves : s.rows, block0 = r / block_rows * block_rows;
+    const Keyspan span = keyspan(tq, s, a.window, block0, block0 + block_rows - 1);
+    const int32_t n = !a.plan.many        ? tiles_of<kTile>(span, a.sinks).n
+                      : a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n
+                                          : tiles_of<stage_of<4>()>(span, a.sinks).n;
+    const int32_t share = share_of(n, a.plan), splits = (n + share - 1) / share;
+    const int64_t at = (int64_t)s.nodes.first * heads + row, step = (int64_t)tq.T * heads;
+    const float* po = a.part + at * kHeadDim + d;
+    const float* pm = a.part + a.plan.splits * step * kHeadDim + at * 2;
+    float base = -__builtin_inff(), l = 0.0f;  // the largest base so far
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    constexpr int kAtOnce = 8;
+    for (int32_t s0 = 0; s0 < splits; s0 += kAtOnce) {
+        f32x4 p[kAtOnce];
+        float2 ml[kAtOnce];
+        float top = base;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t k = s0 + j < splits ? s0 + j : s0;
+            p[j] = *reinterpret_cast<const f32x4*>(po + k * step * kHeadDim);
+            ml[j] = *reinterpret_cast<const float2*>(pm + k * step * 2);
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) top = __builtin_fmaxf(top, ml[j].x);  // (a repeated one changes nothing)
+        const float ref = top == -__builtin_inff() ? 0.0f : top;
+        const float keep = exp2_hw(base - ref);
+        l *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= keep;
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (s0 + j >= splits) break;
+            const float x = exp2_hw(ml[j].x - ref);
+            l = __builtin_fmaf(ml[j].y, x, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[j][i], x, o[i]);
+        }
+        base = top;
+    }
+    put_row4(Results{a.out, a.lse, nullptr, nullptr, true}, at, d, base, l, o);
+}
+
+__global__ __launch_bounds__(256) void window_fill_kernel(TreeQueries tq, uint32_t fill, uint16_t* __restrict__ out,
+                                                          float* __restrict__ lse) {
+    fill_rows(tq, fill, out, lse, blockIdx.x, gridDim.x);
+}
+// Workgroups that fill: one to 64 KiB of all rows, 1 to 1024.
+uint32_t fill_groups(const WindowArgs& a) {
+    if (a.fill == 0u) return 0u;
+    const int64_t n = ((int64_t)a.tq.T * a.tq.H * a.tq.G * (2 * kHeadDim + 4) + 65535) / 65536;
+    return (uint32_t)(n < 1024 ? n : 1024);
+}
+
+template <int R, int WAVES, bool FP4>
+void launch_few(const WindowArgs& a, hipStream_t stream) {
+    constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
+    static_assert(kLds <= 65536, "above, the limit would have to be raised");
+    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
+    const dim3 grid(groups + fill_groups(a)), block(64 * WAVES);
+    // (32-bit offsets of a page's rows)
+    const bool page16 = a.kv.block_size % 16 == 0 && (FP4 || a.kv.page_stride < (1 << 24));
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups); };
+    if (a.tq.softcap > 0.0f)
+        page16 ? go(window_few_kernel<R, WAVES, true, FP4, true>) : go(window_few_kernel<R, WAVES, true, FP4, false>);
+    else
+        page16 ? go(window_few_kernel<R, WAVES, false, FP4, true>) : go(window_few_kernel<R, WAVES, false, FP4, false>);
+}
+
+template <int WAVES, bool CAP, bool FP4>
+int launch_many(const WindowArgs& a, hipStream_t stream) {
+    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
+    const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
+    auto kernel = window_many_kernel<WAVES, CAP, FP4>;
+    static std::atomic<int> done[64] = {};
+    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
+    hipLaunchKernelGGL(kernel, dim3(grid + fill_groups(a)), dim3(64 * WAVES), many_lds(WAVES), stream, a, groups, grid);
+    return 0;
+}
+
+template <bool FP4>
+int launch(const WindowArgs& a, hipStream_t stream) {
+    const bool capped = a.tq.softcap > 0.0f;
+    if (a.plan.many)
+        return a.plan.waves == 8 ? (capped ? launch_many<8, true, FP4>(a, stream) : launch_many<8, false, FP4>(a, stream))
+                                 : (capped ? launch_many<4, true, FP4>(a, stream) : launch_many<4, false, FP4>(a, stream));
+    if (a.plan.waves == 8)
+        launch_few<1, 8, FP4>(a, stream);
+    else
+        a.plan.q_tiles == 1 ? launch_few<1, 4, FP4>(a, stream) : launch_few<2, 4, FP4>(a, stream);
+    return 0;
+}
+
+}  // namespace
+
+WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t window,
+                                 int32_t sinks, int32_t num_cus) {
+    WindowPlan p{};
+    const int64_t rows = (int64_t)max_nodes * G, base = (int64_t)B * H;
+    p.many = rows > 32;
+    p.waves = p.many && rows > 128 ? 8 : 4;
+    p.q_tiles = rows <= 16 ? 1 : 2;
+    const int64_t block_rows = p.many ? 32 * p.waves : rows, keys = p.many ? 16 * p.waves : kTile;
+    p.row_blocks = p.many ? (int32_t)((rows + block_rows - 1) / block_rows) : 1;
+    // the most tiles that a block of rows looks at
+    int64_t tiles = (max_ctx + max_nodes + keys - 1) / keys;
+    const int64_t nodes = block_rows / G + 1 < max_nodes ? block_rows / G + 1 : max_nodes;
+    const int64_t near = (int64_t)sinks / keys + 1 + ((int64_t)window + nodes + keys - 1) / keys + 1;
+    if (near < tiles) tiles = near;
+    p.splits = 1;
+    p.min_tiles = 1;
+    int64_t splits, most;
+    if (p.many) {
+        // until there is twice what the chip holds at once, of at least 4 tiles
+        const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2), groups = base * p.row_blocks;
+        splits = groups >= at_once ? 1 : (2 * at_once + groups - 1) / groups;
+        most = tiles / 4;
+        p.min_tiles = 4;
+    } else {
+        if (p.q_tiles == 1 && tiles <= 64 && base <= num_cus) {
+            p.waves = 8;  // short and few: no second launch
+            p.min_tiles = (int32_t)tiles;
+            return p;
+        }
+        // until there are two workgroups per CU, each of at least 4 tiles a wave
+        splits = (2 * num_cus + base - 1) / base;
+        most = tiles / (4 * p.waves);
+        p.min_tiles = 4 * p.waves;
+    }
+    if (splits > most) splits = most;
+    if (splits > 1) p.splits = (int32_t)splits;
+    return p;
+}
+
+int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads) {
+    return p.splits == 1 ? 0 : p.splits * T * heads * (kHeadDim + 2) * 4;
+}
+
+int launch_window_attention(const WindowArgs& a, hipStream_t stream) {
+    if (a.tq.B == 0) {
+        hipLaunchKernelGGL(window_fill_kernel, dim3(fill_groups(a)), dim3(256), 0, stream, a.tq, a.fill, a.out, a.lse);
+        return hipGetLastError() == hipSuccess ? 0 : -1;
+    }
+    if (int rc = a.fp4 ? launch<true>(a, stream) : launch<false>(a, stream)) return rc;
+    if (a.plan.splits > 1) {
+        const dim3 grid((uint32_t)(((int64_t)a.tq.max_nodes * a.tq.H * a.tq.G + 15) / 16), (uint32_t)a.tq.B);
+        hipLaunchKernelGGL(window_join_kernel, grid, dim3(256), 0, stream, a);
+    }
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace nrc

@@ -89,3 +89,52 @@ def fp4_values(x):
     code, e = fp4_groups(g)
     sign = torch.where(torch.signbit(g), -1.0, 1.0)
     return (torch.tensor(STEPS, dtype=torch.float64)[code] * sign * torch.exp2(e.double())[..., None]).flatten(-2)
+
+
+def make_batch():
+    """cache_ref.Batch with a window and sinks, and (after pack) with the values of a cache of 4 bits."""
+    import numpy as np
+
+    from cache_ref import Batch, bits
+
+    class WindowBatch(Batch):
+        window, sinks = None, 0
+
+        def behind(self, window, sinks=0):
+            self.window, self.sinks = window, sinks
+            return self
+
+        def sees(self, b, there):
+            s = super().sees(b, there).numpy().copy()
+            if self.window is None:
+                return torch.from_numpy(s)
+            ctx, n, lo = self.ctx[b], self.nodes[b], int(self.q_starts[b])
+            key = np.arange(ctx + n)
+            for i in range(n):
+                if self.mask is None:
+                    s[i] &= (key < self.sinks) | (key > ctx + i - self.window)
+                else:
+                    p = ctx + int(bits(self.mask[lo + i], n).sum()) - 1
+                    s[i, :ctx] &= ((key < self.sinks) | (key > p - self.window))[:ctx]
+            return torch.from_numpy(s)
+
+        def pack(self, nrc, fill=0xFF):
+            """The cache as cells of 4 bits on the GPU (bytes of no cell: fill); its values become the reference's cache."""
+            page = nrc.fp4_page_bytes(self.bs)
+            packed = torch.full((self.nb, self.H, page), fill, dtype=torch.uint8, device="cuda")
+            rows = self.cache.transpose(1, 2).reshape(-1, self.H, 128).cuda()
+            slots = torch.arange(self.nb * self.bs, device="cuda")
+            nrc.context_fp4_store(rows[..., :64], rows[..., 64:], slots, packed)
+            k, v = nrc.context_fp4_load(packed, slots)
+            self.cache = torch.cat([k, v], -1).unflatten(0, (self.nb, self.bs)).transpose(1, 2).cpu()
+            return packed
+
+        def wipe(self, packed, b, key, byte=None, gen=None):
+            """A key's cell filled with one byte, or with random ones."""
+            block, at = self.cell(b, key)
+            for first, width in ((0, 32), (32 * self.bs, 32), (64 * self.bs, 4)):
+                run = packed[block, :, first + at * width:first + (at + 1) * width]
+                run.copy_(torch.randint(0, 256, run.shape, generator=gen).to(torch.uint8) if byte is None
+                          else torch.full_like(run, byte))
+
+    return WindowBatch
