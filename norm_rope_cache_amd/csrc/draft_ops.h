@@ -66,11 +66,10 @@ int launch_fp4_store(const Fp4Rows& r, const Fp4Cache& c, hipStream_t stream);
 int launch_fp4_load(const Fp4Rows& r, const Fp4Cache& c, uint16_t* k, uint16_t* v, bool fill, hipStream_t stream);
 
 // How a shape is worked on: the kernel (many rows: keys shared through LDS), 16-row query tiles of a wave (few rows),
-// a workgroup's waves, workgroups along the rows, the most shares that a block's tiles are dealt into and the fewest tiles
-// of one.
+// a workgroup's waves, workgroups along the rows, the shares that a block's tiles are dealt into at most and the tiles of one.
 struct WindowPlan {
     bool many;
-    int32_t q_tiles, waves, row_blocks, splits, min_tiles;
+    int32_t q_tiles, waves, row_blocks, splits, share;
 };
 
 WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t window,

@@ -60,12 +60,6 @@ __device__ __forceinline__ Tiles tiles_of(const Keyspan& k, int32_t sinks) {
     t.n = t.sinks + k.hi_max / KEYS + 1 - t.from;
     return t;
 }
-// Tiles of one of up to `splits` shares, and how many shares there are.
-__device__ __forceinline__ int32_t share_of(int32_t n, const WindowPlan& plan) {
-    const int32_t share = (n + plan.splits - 1) / plan.splits;
-    return share < plan.min_tiles ? plan.min_tiles : share;
-}
-
 enum Seen { kNobody, kSome, kEverybody };
 template <int KEYS>
 __device__ __forceinline__ Seen seen_by(const Keyspan& k, int32_t sinks, int32_t key0) {
@@ -125,13 +119,11 @@ __device__ __forceinline__ Place place_of(const PagedCache& c, uint32_t key, uin
 
 // ---- few rows -----------------------------------------------------------------------------------------------------
 
-// A tile of 32 cells of 4 bits as a lane loads it: K's 16 codes of key l % 16 of each half (elements 16 (l / 16) ..,
-// the first 8 in .x), V's 4 codes (elements 4 (l % 16) ..) of the keys 16 t + 4 (l / 16) + r, the keys' scale dwords.
+// A tile of 32 cells of 4 bits as a lane loads it: of key 16 (l / 32) + l % 16 the 32 codes of K's group l / 16 % 2, V's,
+// and the scale dword.
 struct Packed {
-    uint2 k[2];
-    uint32_t ks[2];
-    uint32_t v[8];
-    uint32_t vs[8];
+    U32x4 k, v;
+    uint32_t scales;
 };
 template <bool FP4>
 struct RawOf {
@@ -142,41 +134,74 @@ struct RawOf<true> {
     typedef Packed T;
 };
 
-__device__ __forceinline__ uint32_t rotate_right(uint32_t w, uint32_t n) { return __builtin_amdgcn_alignbit(w, w, n); }
+// The wave's own part of LDS, through which V's codes and the scales of a packed tile reach the lanes that need them: 32
+// bytes a key, every 8 keys 32 bytes apart (so that the four rows of 32 bytes that a read touches lie in banks of their
+// own), then the keys' scale dwords.
+constexpr int kTurnScales = 4 * 288, kTurnBytes = kTurnScales + 4 * kTile;
 
-// Packed cells opened. HELD: V's scales at most 2^125 (of cells that not every row sees).
+// Packed cells opened as K's and V's operands: K's lane has key l % 16 of each half, elements 32 (l / 16 % 2) + 16 (l / 32) +
+// 8 h .., V's lane elements 4 (l % 16) .. of the keys 16 t + 4 (l / 16) + r.
+// HELD: V's scales at most 2^125 (of cells that not every row sees).
 template <bool HELD>
-__device__ __forceinline__ void open_keys(Keys& kv, const Packed& p, uint32_t lane) {
-    // the scale's byte to a float's exponent; the other bits are not looked at
-    const uint32_t k_turn = lane & 32u ? 17u : 9u, v_turn = lane & 8u ? 1u : 25u;
+__device__ __forceinline__ void open_keys(Keys& kv, const Packed& p, uint8_t* turn, uint32_t lane) {
+    const uint32_t g = lane >> 4, n16 = lane & 15u, key = 16 * (lane >> 5) + n16;
+    store16(turn + key * 32 + (key >> 3) * 32 + (g & 1u) * 16, p.v);
+    *reinterpret_cast<uint32_t*>(turn + kTurnScales + 4 * key) = p.scales;
+    __builtin_amdgcn_wave_barrier();  // (a wave's LDS accesses keep their order)
+    asm volatile("" ::: "memory");
+    uint32_t v[8];
+    U32x4 vs[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const float s = __uint_as_float(rotate_right(p.ks[t], k_turn));
-        kv.k[t][0] = fp4_open(p.k[t].x, s);
-        kv.k[t][1] = fp4_open(p.k[t].y, s);
+        vs[t] = load16(turn + kTurnScales + 64 * t + 16 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t of = 16 * t + 4 * g;  // (its key + r lies in the same 8)
+            v[4 * t + r] = *reinterpret_cast<const uint16_t*>(turn + of * 32 + (of >> 3) * 32 + r * 32 + 2 * n16);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+    // the halves of the wave trade dwords, so that each has both halves of the tile
+    const auto k0 = __builtin_amdgcn_permlane32_swap(p.k.x, p.k.z, false, false);
+    const auto k1 = __builtin_amdgcn_permlane32_swap(p.k.y, p.k.w, false, false);
+    const auto ks = __builtin_amdgcn_permlane32_swap(p.scales, p.scales, false, false);
+    // the scale's byte to a float's exponent; the other bits are not looked at
+    const uint32_t k_turn = g & 1u ? 17u : 9u, v_turn = lane & 8u ? 1u : 25u;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const float s = __uint_as_float(__builtin_amdgcn_alignbit(ks[t], ks[t], k_turn));
+        kv.k[t][0] = fp4_open(k0[t], s);
+        kv.k[t][1] = fp4_open(k1[t], s);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        uint32_t s = rotate_right(p.vs[i], v_turn);
+        const uint32_t w = (&vs[i / 4].x)[i % 4];
+        uint32_t s = __builtin_amdgcn_alignbit(w, w, v_turn);
         if constexpr (HELD) {
             s &= 0x7F800000u;
             s = s < kScaleHigh << 23 ? s : kScaleHigh << 23;
         }
-        kv.v[i] = uint2{fp4_pair<0>(p.v[i], __uint_as_float(s)), fp4_pair<1>(p.v[i], __uint_as_float(s))};
+        kv.v[i] = uint2{fp4_pair<0>(v[i], __uint_as_float(s)), fp4_pair<1>(v[i], __uint_as_float(s))};
     }
 }
 
 // One workgroup per (sequence, KV head, share); its WAVES waves hold the same rows and take the share's tiles of 32
-// keys in turn, from memory through registers, as few_rows_kernel of tree_attention.hip does.
-// PAGE16 (block_size a multiple of 16): half a tile lies in one page, so its base is a scalar.
-template <int R, int WAVES, bool CAP, bool FP4, bool PAGE16>
-__global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void window_few_kernel(WindowArgs a, uint32_t groups) {
+// keys in turn, from memory through registers. The matrix products and the order of their operands are those of
+// few_rows_kernel in tree_attention.hip (K's 16 packed codes of a lane are 16 neighbouring elements of d, and the queries'
+// operand is loaded in that order). Several tiles of a wave are on the way while it works on one (a packed tile is 2.2 KB: one
+// ahead would leave the memory waiting), and the block numbers of 32 tiles come in one load.
+// First the tiles that every row sees whole, without masks; then the others, which are few: the sinks' last, those in
+// which the rows' windows begin, those of the rows' own keys.
+template <int R, int WAVES, bool CAP, bool FP4, bool PAGES>
+__global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a, uint32_t groups) {
     extern __shared__ float smem[];
     if (blockIdx.x >= groups) {
         fill_rows(a.tq, a.fill, a.out, a.lse, blockIdx.x - groups, gridDim.x - groups);
         return;
     }
     typedef typename RawOf<FP4>::T Raw;
+    constexpr int kAhead = FP4 ? 4 : 2;  // tiles of a wave in registers
     const PagedCache& kv = a.kv;
     const TreeQueries& tq = a.tq;
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -189,98 +214,70 @@ __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void window_few_kernel(
     if (s.rows == 0) return;
     const Keyspan span = keyspan(tq, s, a.window, 0, s.rows - 1);
     const Tiles tiles = tiles_of<kTile>(span, a.sinks);
-    const int32_t share = share_of(tiles.n, a.plan), first = split * share;
+    const int32_t share = a.plan.share, first = split * share;
     if (first >= tiles.n) return;  // (nor does the join look at such a share)
     const int32_t end = tiles.n - first < share ? tiles.n : first + share;
     const int32_t total = s.ctx + s.nodes.count;
+    const int32_t v0 = first + (int32_t)wave;  // the wave's tiles: v0, v0 + WAVES ..
+    const int32_t count = v0 < end ? (end - v0 + WAVES - 1) / WAVES : 0;
 
     const uint8_t* head = reinterpret_cast<const uint8_t*>(kv.cache) + (int64_t)h * kv.head_stride * (FP4 ? 1 : 2);
     const Factors f = factors<CAP>(tq);
-    // the table's entry of the lane's key of tile number v (of the last one past the end)
-    auto entry = [&](int32_t v) {
-        return page_of(kv, table, (uint32_t)tiles.at(v < end ? v : end - 1) * kTile + (lane & (kTile - 1)));
+    const uint32_t codes = kFp4Codes * kv.block_size;  // bytes of a page's K codes
+    uint8_t* turn = reinterpret_cast<uint8_t*>(smem) + wave * kTurnBytes;  // FP4, until the waves join
+
+    // The block numbers of the wave's kAhead tiles from number j on. PAGES (bf16, block_size a multiple of 16, so that half a
+    // tile lies in one page): lane 2 i + t of half t of tile j + i; otherwise, at [i], of the lane's key of tile j + i.
+    constexpr int kVectors = PAGES ? 1 : kAhead;
+    const uint32_t own_key = FP4 ? 16 * (lane >> 5) + n16 : lane & 31u;
+    struct Blocks {
+        uint32_t page[kVectors];
     };
-    auto place = [&](int32_t v, uint32_t page) -> Place {
-        if (v >= end) return Place{-1, 0u};
-        const uint32_t key = (uint32_t)tiles.at(v) * kTile + (lane & (kTile - 1));
-        Place p = place_of<FP4>(kv, key, page);
-        if (!PAGE16 && key >= (uint32_t)total) p.off = -1;  // (PAGE16 reads whole pages, and masks)
+    auto key_of = [&](int32_t j, int i) {
+        const int32_t v = v0 + (j + (PAGES ? (int32_t)(lane >> 1) : i)) * WAVES;
+        return (uint32_t)tiles.at(v < end ? v : end - 1) * kTile + (PAGES ? (lane & 1u) * 16 : own_key);
+    };
+    auto blocks_of = [&](int32_t j) {
+        Blocks p;
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i) p.page[i] = page_of(kv, table, key_of(j, i));
         return p;
     };
-    auto exists = [&](int32_t v, const Place& p) {
-        const uint32_t key = (uint32_t)tiles.at(v) * kTile + (lane & (kTile - 1));
-        return (uint32_t)__ballot(p.off >= 0 && key < (uint32_t)total);
-    };
-    const uint32_t codes = kFp4Codes * kv.block_size;  // bytes of a page's K codes
-    auto fetch = [&](Raw& raw, const Place& p) {
-        if constexpr (FP4 && PAGE16) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int32_t hi = __builtin_amdgcn_readlane((int)((uint64_t)p.off >> 32), 16 * t);
-                raw.k[t] = uint2{0u, 0u}, raw.ks[t] = 0u;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) raw.v[4 * t + r] = raw.vs[4 * t + r] = 0u;
-                if (hi < 0) continue;  // (no such page)
-                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)p.off, 16 * t);
-                const uint32_t at = __builtin_amdgcn_readlane(p.at, 16 * t);
-                const uint8_t* page = head + (int64_t)((uint64_t)(uint32_t)hi << 32 | lo);
-                const uint8_t* scales = page + 2 * codes - (kFp4Codes - 4) * at;
-                raw.k[t] = *reinterpret_cast<const uint2*>(page + n16 * kFp4Codes + 8 * g);
-                raw.ks[t] = *reinterpret_cast<const uint32_t*>(scales + 4 * n16);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    raw.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(page + codes + (4 * g + r) * kFp4Codes + 2 * n16);
-                const U32x4 vs = load16(scales + 16 * g);
-                raw.vs[4 * t] = vs.x, raw.vs[4 * t + 1] = vs.y, raw.vs[4 * t + 2] = vs.z, raw.vs[4 * t + 3] = vs.w;
-            }
-        } else if constexpr (FP4) {
-            auto of = [&](uint32_t key, int64_t* off, int64_t* scales) {
-                const int lo = __builtin_amdgcn_ds_bpermute((int)(key << 2), (int)(uint32_t)p.off);
-                const int hi = __builtin_amdgcn_ds_bpermute((int)(key << 2), (int)(uint32_t)((uint64_t)p.off >> 32));
-                const uint32_t at = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(key << 2), (int)p.at);
-                *off = (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
-                *scales = *off + 2 * (int64_t)codes - (int64_t)(kFp4Codes - 4) * at;
-                return hi >= 0;
-            };
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                int64_t off, sc;
-                raw.k[t] = uint2{0u, 0u}, raw.ks[t] = 0u;
-                if (of(16 * t + n16, &off, &sc)) {
-                    const uint32_t* k = reinterpret_cast<const uint32_t*>(head + off + 8 * g);  // (pages are 16-byte aligned)
-                    raw.k[t] = uint2{k[0], k[1]};
-                    raw.ks[t] = *reinterpret_cast<const uint32_t*>(head + sc);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    raw.v[4 * t + r] = raw.vs[4 * t + r] = 0u;
-                    if (of(16 * t + 4 * g + r, &off, &sc)) {
-                        raw.v[4 * t + r] = *reinterpret_cast<const uint16_t*>(head + off + codes + 2 * n16);
-                        raw.vs[4 * t + r] = *reinterpret_cast<const uint32_t*>(head + sc);
-                    }
-                }
-            }
-        } else if constexpr (PAGE16) {
-            const uint16_t* head16 = reinterpret_cast<const uint16_t*>(head);
+    // The i-th of the tiles from number j on; which of its keys there are. A cell that is not there is read from the
+    // cache's first page, and masked.
+    auto fetch = [&](Raw& raw, const Blocks& p, int32_t j, int i) -> uint32_t {
+        const uint32_t key = key_of(j, i), blk = block_of(key, kv);
+        uint32_t at = key - blk * kv.block_size, page = p.page[PAGES ? 0 : i];
+        const bool is = blk < kv.table_width && page < kv.num_blocks && key < (uint32_t)total;
+        const uint64_t there = __ballot(is);
+        page = is ? page : 0u;
+        at = is ? at : 0u;
+        const uint8_t* base = head + (int64_t)page * kv.block_stride * (FP4 ? 1 : 2);
+        if constexpr (FP4) {
+            const uint8_t* k = base + (int64_t)(at * kFp4Codes + (g & 1u) * 16);
+            raw.k = load16(k);
+            raw.v = load16(k + codes);
+            raw.scales = *reinterpret_cast<const uint32_t*>(base + (int64_t)(2 * codes + 4 * at));
+            return (uint32_t)(there & 0xFFFFu) | (uint32_t)(there >> 16 & 0xFFFF0000u);
+        } else if constexpr (PAGES) {
+            const uint8_t* first_cell = base + (int64_t)at * kv.page_stride * 2;
             const uint32_t k_at = n16 * (uint32_t)kv.page_stride + 8 * g;
             const uint32_t v_at = 4 * g * (uint32_t)kv.page_stride + kHeadDim + 4 * n16;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int32_t hi = __builtin_amdgcn_readlane((int)((uint64_t)p.off >> 32), 16 * t);
-                raw.k[t][0] = raw.k[t][1] = U32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) raw.v[4 * t + r] = uint2{0u, 0u};
-                if (hi < 0) continue;
-                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)p.off, 16 * t);
-                const uint16_t* page = head16 + (int64_t)((uint64_t)(uint32_t)hi << 32 | lo);
-                raw.k[t][0] = load16(page + k_at);
-                raw.k[t][1] = load16(page + k_at + 32);
+                const uint64_t w = (uint64_t)(uintptr_t)first_cell;
+                const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)w, 2 * i + t), hi = __builtin_amdgcn_readlane((uint32_t)(w >> 32), 2 * i + t);
+                const uint16_t* cells = reinterpret_cast<const uint16_t*>((uintptr_t)((uint64_t)hi << 32 | lo));
+                raw.k[t][0] = load16(cells + k_at);
+                raw.k[t][1] = load16(cells + k_at + 32);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    raw.v[4 * t + r] = *reinterpret_cast<const uint2*>(page + v_at + r * (uint32_t)kv.page_stride);
+                    raw.v[4 * t + r] = *reinterpret_cast<const uint2*>(cells + v_at + r * (uint32_t)kv.page_stride);
             }
+            return (there >> (2 * i) & 1u ? 0xFFFFu : 0u) | (there >> (2 * i + 1) & 1u ? 0xFFFF0000u : 0u);
         } else {
-            load_keys(raw, reinterpret_cast<const uint16_t*>(head), p.off, lane);
+            load_keys(raw, reinterpret_cast<const uint16_t*>(head), is ? (int64_t)page * kv.block_stride + (int64_t)at * kv.page_stride : -1, lane);
+            return (uint32_t)there;
         }
     };
 
@@ -295,8 +292,8 @@ __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void window_few_kernel(
             const uint16_t* q = tq.q + (int64_t)(s.nodes.first + row[rq].node) * tq.q_rs +
                                 (int64_t)(h * tq.G + r - row[rq].node * tq.G) * tq.q_hs;
             // in the order of d that K's operand has
-            w.q[rq][0] = load16(q + (FP4 ? 16 * g : 8 * g));
-            w.q[rq][1] = load16(q + (FP4 ? 16 * g + 8 : 32 + 8 * g));
+            w.q[rq][0] = load16(q + (FP4 ? 32 * (g & 1u) + 16 * (g >> 1) : 8 * g));
+            w.q[rq][1] = load16(q + (FP4 ? 32 * (g & 1u) + 16 * (g >> 1) + 8 : 32 + 8 * g));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) w.o[rq][i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -305,68 +302,95 @@ __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void window_few_kernel(
         w.l[rq] = 0.0f;
     }
 
-    auto work = [&](int32_t v, Raw& raw, uint32_t there) {
-        const int32_t key0 = tiles.at(v) * kTile;
-        const Seen seen = seen_by<kTile>(span, a.sinks, key0);
-        if (seen == kEverybody && there == 0xFFFFFFFFu) {
-            if constexpr (FP4) {
+    // The numbers of the tiles that every row sees whole: below whole_sinks, and from `near` to `own` (a tile of
+    // the sinks' last keys, or one in which a row's window or own keys begin, is not whole).
+    const int32_t whole_sinks = a.sinks / kTile < tiles.sinks ? a.sinks / kTile : tiles.sinks;
+    int32_t near = (span.lo_max < 0 ? 0 : (int32_t)(((int64_t)span.lo_max + kTile - 1) / kTile)), own = (span.hi_min + 1) / kTile;
+    if (a.sinks / kTile >= near) near = tiles.from;  // (the sinks reach past the windows' beginnings)
+    near += tiles.sinks - tiles.from, own += tiles.sinks - tiles.from;
+    bool left_out = false;  // such a tile with a key that is not there
+    if (count > 0) {
+        // kAhead tiles to a round. Every load is made in every round (past the last tile, of some tile again), so that the
+        // compiler knows how many are on the way and waits for the oldest alone; block numbers come two rounds ahead.
+        Raw raw[kAhead];
+        uint32_t there[kAhead];
+        Blocks blocks = blocks_of(0), next = blocks_of(kAhead);
+        auto bring = [&](int slot, const Blocks& from, int32_t j) {
+            there[slot] = fetch(raw[slot], from, j, slot);
+            __builtin_amdgcn_sched_barrier(0);  // (the tiles' loads in their order)
+        };
+        auto work = [&](int32_t j, Raw& cur, bool all) {
+            const int32_t v = v0 + j * WAVES;
+            if (j >= count || v >= own || (v < near && v >= whole_sinks)) return;
+            if (!all) {
+                left_out = true;
+            } else if constexpr (FP4) {
                 Keys keys;
-                open_keys<false>(keys, raw, lane);
+                open_keys<false>(keys, cur, turn, lane);
                 open_tile<R, CAP>(w, keys, f.c, f.capped);
             } else {
-                open_tile<R, CAP>(w, raw, f.c, f.capped);
+                open_tile<R, CAP>(w, cur, f.c, f.capped);
             }
-        } else if (seen != kNobody && there != 0u) {
-            uint32_t sees[R];
+        };
 #pragma unroll
-            for (int rq = 0; rq < R; ++rq) sees[rq] = there & row_sees(tq, s, row[rq], a.sinks, key0);
-            Keys keys;
-            if constexpr (FP4) {
-                open_keys<true>(keys, raw, lane);
-                masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
+        for (int i = 0; i < kAhead - 1; ++i) bring(i, blocks, 0);
+#pragma unroll 1
+        for (int32_t q = 0; q * kAhead < count; ++q) {
+            const Blocks after = blocks_of((q + 2) * kAhead);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (i == 0)
+                    bring(kAhead - 1, blocks, q * kAhead);
+                else
+                    bring(i - 1, next, (q + 1) * kAhead);
+                work(q * kAhead + i, raw[i], there[i] == 0xFFFFFFFFu);
+            }
+            blocks = next;
+            next = after;
+        }
+    }
+    // the others
+    auto masked = [&](int32_t v, bool whole) {
+        const int32_t key0 = tiles.at(v) * kTile, j = (v - v0) / WAVES;
+        Raw raw;
+        const uint32_t there = below_key(total, key0) & fetch(raw, blocks_of(j), j, 0);
+        if (there == 0u || (whole && there == 0xFFFFFFFFu)) return;  // (nobody's, or done)
+        uint32_t sees[R];
+#pragma unroll
+        for (int rq = 0; rq < R; ++rq) sees[rq] = there & row_sees(tq, s, row[rq], a.sinks, key0);
+        Keys keys;
+        if constexpr (FP4) {
+            open_keys<true>(keys, raw, turn, lane);
+            masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
+        } else {
+            keys = raw;
+            // (what lies in the places of keys that are not there may be anything)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(there >> (16 * (i / 4) + 4 * g + i % 4) & 1u)) keys.v[i] = uint2{0u, 0u};
+            const bool odd = any_odd(keys);
+            if (odd) {
+                Keys finite = keys;
+                drop_odd(finite);
+                masked_tile<R, CAP>(w, finite, f.c, f.capped, sees, lane);
+                add_odd<R>(w, keys, sees, lane);
             } else {
-                keys = raw;
-                // (what lies in the places of keys that are not there may be anything)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!(there >> (16 * (i / 4) + 4 * g + i % 4) & 1u)) keys.v[i] = uint2{0u, 0u};
-                const bool odd = any_odd(keys);
-                if (odd) {
-                    Keys finite = keys;
-                    drop_odd(finite);
-                    masked_tile<R, CAP>(w, finite, f.c, f.capped, sees, lane);
-                    add_odd<R>(w, keys, sees, lane);
-                } else {
-                    masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
-                }
+                masked_tile<R, CAP>(w, keys, f.c, f.capped, sees, lane);
             }
         }
     };
-    {
-        int32_t v = first + (int32_t)wave;
-        Raw raw[2];
-        const uint32_t page0 = entry(v), page1 = entry(v + WAVES);
-        Place p = place(v, page0);
-        uint32_t there = v < end ? exists(v, p) : 0u;
-        fetch(raw[0], p);
-        p = place(v + WAVES, page1);
-        auto step = [&](Raw& cur, Raw& next) {
-            const uint32_t page = entry(v + 2 * WAVES);  // (before the cells, so that nobody waits for those with it)
-            const uint32_t next_there = v + WAVES < end ? exists(v + WAVES, p) : 0u;
-            fetch(next, p);
-            work(v, cur, there);
-            v += WAVES;
-            there = next_there;
-            p = place(v + WAVES, page);
-        };
-        while (v < end) {
-            step(raw[0], raw[1]);
-            if (v >= end) break;
-            step(raw[1], raw[0]);
-        }
+    // (all tiles where some were left out, else those that are not whole)
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+        const int32_t from = left_out ? (i == 0 ? 0 : tiles.n) : i == 0 ? whole_sinks : near < own ? own : near;
+        const int32_t upto = left_out ? tiles.n : i == 0 ? near : tiles.n;
+        int32_t v = from < first ? first : from;
+        v += ((int32_t)wave - (v - first) % WAVES + WAVES) % WAVES;
+        for (; v < upto && v < end; v += WAVES) masked(v, v < whole_sinks || (v >= near && v < own));
     }
 
     // Join the waves: each leaves m's base, l and O of its rows in LDS.
+    if (FP4) __syncthreads();
     float* so = smem;                          // [WAVES][16 R][kPad]
     float* sm = smem + WAVES * 16 * R * kPad;  // [WAVES][16 R]
     float* sl = sm + WAVES * 16 * R;           // [WAVES][16 R]
@@ -449,7 +473,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     const int32_t block0 = rb * WAVES * 32;
     if (block0 >= s.rows) return;
     const Tiles tiles = tiles_of<kStage>(keyspan(tq, s, a.window, block0, block0 + WAVES * 32 - 1), a.sinks);
-    const int32_t share = share_of(tiles.n, a.plan), first = split * share;
+    const int32_t share = a.plan.share, first = split * share;
     if (first >= tiles.n) return;
     const int32_t end = tiles.n - first < share ? tiles.n : first + share;
     const int32_t total = s.ctx + s.nodes.count;
@@ -684,7 +708,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(WindowArgs a) {
     const int32_t n = !a.plan.many        ? tiles_of<kTile>(span, a.sinks).n
                       : a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n
                                           : tiles_of<stage_of<4>()>(span, a.sinks).n;
-    const int32_t share = share_of(n, a.plan), splits = (n + share - 1) / share;
+    const int32_t splits = (n + a.plan.share - 1) / a.plan.share;
     const int64_t at = (int64_t)s.nodes.first * heads + row, step = (int64_t)tq.T * heads;
     const float* po = a.part + at * kHeadDim + d;
     const float* pm = a.part + a.plan.splits * step * kHeadDim + at * 2;
@@ -736,15 +760,16 @@ template <int R, int WAVES, bool FP4>
 void launch_few(const WindowArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
     static_assert(kLds <= 65536, "above, the limit would have to be raised");
+    static_assert(kTurnBytes <= 16 * R * (kPad + 2) * 4, "a wave's packed tile fits its part of the join's");
     const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
     const dim3 grid(groups + fill_groups(a)), block(64 * WAVES);
     // (32-bit offsets of a page's rows)
-    const bool page16 = a.kv.block_size % 16 == 0 && (FP4 || a.kv.page_stride < (1 << 24));
+    const bool pages = !FP4 && a.kv.block_size % 16 == 0 && a.kv.page_stride < (1 << 24);
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups); };
     if (a.tq.softcap > 0.0f)
-        page16 ? go(window_few_kernel<R, WAVES, true, FP4, true>) : go(window_few_kernel<R, WAVES, true, FP4, false>);
+        pages ? go(window_few_kernel<R, WAVES, true, FP4, !FP4>) : go(window_few_kernel<R, WAVES, true, FP4, false>);
     else
-        page16 ? go(window_few_kernel<R, WAVES, false, FP4, true>) : go(window_few_kernel<R, WAVES, false, FP4, false>);
+        pages ? go(window_few_kernel<R, WAVES, false, FP4, !FP4>) : go(window_few_kernel<R, WAVES, false, FP4, false>);
 }
 
 template <int WAVES, bool CAP, bool FP4>
@@ -788,27 +813,29 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     const int64_t near = (int64_t)sinks / keys + 1 + ((int64_t)window + nodes + keys - 1) / keys + 1;
     if (near < tiles) tiles = near;
     p.splits = 1;
-    p.min_tiles = 1;
+    p.share = (int32_t)tiles;
     int64_t splits, most;
     if (p.many) {
         // until there is twice what the chip holds at once, of at least 4 tiles
         const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2), groups = base * p.row_blocks;
         splits = groups >= at_once ? 1 : (2 * at_once + groups - 1) / groups;
         most = tiles / 4;
-        p.min_tiles = 4;
     } else {
         if (p.q_tiles == 1 && tiles <= 64 && base <= num_cus) {
             p.waves = 8;  // short and few: no second launch
-            p.min_tiles = (int32_t)tiles;
             return p;
         }
-        // until there are two workgroups per CU, each of at least 4 tiles a wave
-        splits = (2 * num_cus + base - 1) / base;
+        // until there are several workgroups per CU, each of at least 4 tiles a wave: over a window, of about equal lengths, 2;
+        // over contexts, more than run at once, which evens out ragged lengths
+        const bool ragged = window == kNoWindow;
+        splits = ((ragged ? 6 : 2) * num_cus + base - 1) / base;
         most = tiles / (4 * p.waves);
-        p.min_tiles = 4 * p.waves;
     }
     if (splits > most) splits = most;
-    if (splits > 1) p.splits = (int32_t)splits;
+    if (splits > 1) {
+        p.share = (int32_t)((tiles + splits - 1) / splits);
+        p.splits = (int32_t)((tiles + p.share - 1) / p.share);
+    }
     return p;
 }
 
