@@ -516,5 +516,71 @@ __device__ __forceinline__ void add32(Rows32<R>& w, int rt, f32x16& s, const Key
         for (int ks = 0; ks < 2; ++ks) w.o[rt][c] = mfma32(kv.v[c][ks], pb[ks], w.o[rt][c]);
 }
 
+// How a batch whose workgroups fit the chip at once is split: into shares of
+// at most `tiles` tiles of KEYS keys, the least for which all of them are at most
+// `most`, so that ragged sequences end together (no share is smaller than `least`). Worked out by every wave
+// from the lengths (B <= 512).
+struct Shares {
+    int32_t tiles, groups;          // of a share; of all sequences and heads
+    int32_t b, h, split, splits;    // of group g (b < 0: there is none)
+    int32_t first;                  // of the sequence: its first group
+};
+template <int KEYS>
+__device__ __forceinline__ Shares shares_of(const TreeQueries& tq, int32_t most, int32_t least, int32_t g, uint32_t lane) {
+    constexpr int kSets = 8;
+    int32_t tiles[kSets];
+    int32_t sum = 0, longest = 0;
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+        tiles[j] = 0;
+        const int32_t b = 64 * j + (int32_t)lane;
+        if (64 * j < tq.B && b < tq.B) {
+            const Span s = span_of<KEYS>(tq, b);
+            tiles[j] = s.rows > 0 ? s.all_tiles : 0;
+        }
+        sum += tiles[j];
+        longest = longest > tiles[j] ? longest : tiles[j];
+    }
+    sum = (int32_t)wave_total((uint32_t)sum);
+    longest = (int32_t)wave_most((uint32_t)longest);
+    auto count = [&](int32_t c) {
+        int32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < kSets; ++j)
+            if (64 * j < tq.B) n += (tiles[j] + c - 1) / c;
+        return (int32_t)wave_total((uint32_t)n) * tq.H;
+    };
+    int32_t lo = (int32_t)(((int64_t)sum * tq.H + most - 1) / most), hi = longest;
+    if (lo < least) lo = least;  // (no share is smaller)
+    while (lo < hi) {
+        const int32_t mid = (lo + hi) / 2;
+        if (count(mid) <= most)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    Shares r{lo, 0, -1, 0, 0, 1, 0};
+    int32_t before = 0;  // groups of the sequences before
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+        if (64 * j >= tq.B) break;
+        const int32_t n = (tiles[j] + lo - 1) / lo * tq.H;
+        const int32_t upto = before + (int32_t)wave_inclusive((uint32_t)n);
+        const uint64_t past = __ballot(upto > g);
+        if (r.b < 0 && past != 0) {
+            const int32_t l = __builtin_ctzll(past);
+            r.b = 64 * j + l;
+            const int32_t mine = __builtin_amdgcn_readlane(n, l);
+            r.first = __builtin_amdgcn_readlane(upto, l) - mine;
+            r.splits = mine / tq.H;
+            r.h = (g - r.first) / r.splits;
+            r.split = (g - r.first) - r.h * r.splits;
+        }
+        before = __builtin_amdgcn_readlane(upto, 63);
+    }
+    r.groups = before;
+    return r;
+}
+
 }  // namespace
 }  // namespace nrc

@@ -202,7 +202,7 @@ int32_t attend(const char* what, WindowArgs a, const Range& cells, const uint16_
     a.lse = lse;
     if (!work) return launch_status(launch_window_attention(a, (hipStream_t)stream), what);
     a.plan = plan_window_attention(B, H, Hq / H, max_nodes, max_ctx, a.window, a.sinks, num_cus());
-    const int64_t bytes = window_attention_workspace(a.plan, T, Hq);
+    const int64_t bytes = window_attention_workspace(a.plan, T, Hq, B);
     if (bytes > 0 && (!workspace || workspace_bytes < bytes || !aligned(workspace, 16)))
         return fail(NRC_EINVAL, "%s: needs a 16-byte aligned workspace of %lld bytes", what, (long long)bytes);
     // other workgroups still read these
@@ -213,6 +213,8 @@ int32_t attend(const char* what, WindowArgs a, const Range& cells, const uint16_
         any_meet({ws_range}, {q_range, out_range, lse_range}))
         return fail(NRC_EINVAL, "%s: out, lse and the workspace must lie apart from each other and the inputs", what);
     a.part = static_cast<float*>(workspace);
+    if (a.plan.by_lengths)  // the last [B, 3] of it
+        a.shares = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + bytes) - 3 * (int64_t)B;
     return launch_status(launch_window_attention(a, (hipStream_t)stream), what);
 }
 
@@ -398,7 +400,7 @@ int64_t nrc_context_window_attention_workspace_bytes(int32_t B, int64_t T, int32
     if (B == 0 || T == 0) return 0;
     return window_attention_workspace(plan_window_attention(B, H, Hq / H, max_nodes, max_ctx, window ? window : INT32_MAX,
                                                             window ? sinks : 0, num_cus()),
-                                      T, Hq);
+                                      T, Hq, B);
 }
 
 int32_t nrc_context_window_attention(const uint16_t* q, int64_t q_row_stride, int64_t q_head_stride, int64_t T, int32_t Hq,

@@ -67,14 +67,16 @@ int launch_fp4_load(const Fp4Rows& r, const Fp4Cache& c, uint16_t* k, uint16_t* 
 
 // How a shape is worked on: the kernel (many rows: keys shared through LDS), 16-row query tiles of a wave (few rows),
 // a workgroup's waves, workgroups along the rows, the shares that a block's tiles are dealt into at most and the tiles of one.
+// Many rows: the workgroups of all sequences, heads and shares to a row block; by_lengths: that many at most, their
+// shares of at least `share` tiles worked out from the lengths.
 struct WindowPlan {
-    bool many;
-    int32_t q_tiles, waves, row_blocks, splits, share;
+    bool many, by_lengths;
+    int32_t q_tiles, waves, row_blocks, splits, share, groups;
 };
 
 WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_nodes, int64_t max_ctx, int32_t window,
                                  int32_t sinks, int32_t num_cus);
-int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads);
+int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads, int32_t B);
 
 struct WindowArgs {
     PagedCache kv;  // fp4: pages of 4 bits, the strides in bytes (page_stride is not used)
@@ -83,7 +85,8 @@ struct WindowArgs {
     bool fp4;
     uint16_t* out;  // [T, H G, 64]
     float* lse;     // [T, H G]
-    float* part;    // splits > 1: the partial sums, [splits, T, H G, 64] then [splits, T, H G, 2]
+    float* part;      // splits > 1: the partial sums' rows, [., 64] then [., 2]
+    int32_t* shares;  // by_lengths: [B, 3], each sequence's first group, its shares and their tiles
     WindowPlan plan;
     uint32_t fill;  // NRC_ATTENTION_FILL_*
 };

@@ -229,70 +229,6 @@ __global__ __launch_bounds__(64 * WAVES, R == 2 ? 2 : 1) void few_rows_kernel(Pa
 // to each other (workgroup i runs on XCD i % 8): its L2 holds them for all.
 constexpr int kStage = 128;
 
-// How a batch whose workgroups fit the chip at once is split: into shares of
-// at most `tiles` tiles, the least for which all of them are at most
-// plan.groups, so that ragged sequences end together. Worked out by every wave
-// from the lengths (B <= 512).
-struct Shares {
-    int32_t tiles, groups;          // of a share; of all sequences and heads
-    int32_t b, h, split, splits;    // of group g (b < 0: there is none)
-    int32_t first;                  // of the sequence: its first group
-};
-__device__ __forceinline__ Shares shares_of(const TreeQueries& tq, const AttentionPlan& plan, int32_t g, uint32_t lane) {
-    constexpr int kMost = 8;
-    int32_t tiles[kMost];
-    int32_t sum = 0, longest = 0;
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        tiles[j] = 0;
-        const int32_t b = 64 * j + (int32_t)lane;
-        if (64 * j < tq.B && b < tq.B) {
-            const Span s = span_of<kStage>(tq, b);
-            tiles[j] = s.rows > 0 ? s.all_tiles : 0;
-        }
-        sum += tiles[j];
-        longest = longest > tiles[j] ? longest : tiles[j];
-    }
-    sum = (int32_t)wave_total((uint32_t)sum);
-    longest = (int32_t)wave_most((uint32_t)longest);
-    auto count = [&](int32_t c) {
-        int32_t n = 0;
-#pragma unroll
-        for (int j = 0; j < kMost; ++j)
-            if (64 * j < tq.B) n += (tiles[j] + c - 1) / c;
-        return (int32_t)wave_total((uint32_t)n) * tq.H;
-    };
-    int32_t lo = (int32_t)(((int64_t)sum * tq.H + plan.groups - 1) / plan.groups), hi = longest;
-    if (lo < plan.split_tiles) lo = plan.split_tiles;  // (no share is smaller)
-    while (lo < hi) {
-        const int32_t mid = (lo + hi) / 2;
-        if (count(mid) <= plan.groups)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    Shares r{lo, 0, -1, 0, 0, 1, 0};
-    int32_t before = 0;  // groups of the sequences before
-#pragma unroll
-    for (int j = 0; j < kMost; ++j) {
-        if (64 * j >= tq.B) break;
-        const int32_t n = (tiles[j] + lo - 1) / lo * tq.H;
-        const int32_t upto = before + (int32_t)wave_inclusive((uint32_t)n);
-        const uint64_t past = __ballot(upto > g);
-        if (r.b < 0 && past != 0) {
-            const int32_t l = __builtin_ctzll(past);
-            r.b = 64 * j + l;
-            const int32_t mine = __builtin_amdgcn_readlane(n, l);
-            r.first = __builtin_amdgcn_readlane(upto, l) - mine;
-            r.splits = mine / tq.H;
-            r.h = (g - r.first) / r.splits;
-            r.split = (g - r.first) - r.h * r.splits;
-        }
-        before = __builtin_amdgcn_readlane(upto, 63);
-    }
-    r.groups = before;
-    return r;
-}
 // Buffers: as many as one workgroup of 8 waves, or two of 4, have room for.
 constexpr int buffers_of(int waves) { return waves == 8 ? 4 : 2; }
 constexpr int many_lds(int waves) { return buffers_of(waves) * (kStage * 256 + kStage * 4) + waves * 512; }
@@ -323,7 +259,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void many_rows_kernel(PagedCache kv,
     }
     int32_t b, h, split, splits, share;
     if (plan.splits > 1) {
-        const Shares r = shares_of(tq, plan, (int32_t)id, lane);
+        const Shares r = shares_of<kStage>(tq, plan.groups, plan.split_tiles, (int32_t)id, lane);
         if (r.b < 0) return;
         b = r.b, h = r.h, split = r.split, splits = r.splits, share = r.tiles;
         // for the join: each sequence's first group and its splits

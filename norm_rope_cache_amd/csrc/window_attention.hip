@@ -68,13 +68,14 @@ __device__ __forceinline__ Seen seen_by(const Keyspan& k, int32_t sinks, int32_t
     return kSome;
 }
 
-// Bits i of a word of 32 keys from key0 on with key0 + i >= first; < first.
-__device__ __forceinline__ uint32_t from_key(int32_t first, int32_t key0) {
-    if (first <= key0) return 0xFFFFFFFFu;
-    const int64_t k = (int64_t)first - key0;
-    return k >= 32 ? 0u : 0xFFFFFFFFu << k;
+// The bits i of a word of 32 with i < n (any n).
+__device__ __forceinline__ uint32_t below(int32_t n) {
+    const int32_t k = n < 0 ? 0 : n;
+    return k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u;
 }
-__device__ __forceinline__ uint32_t below_key(int32_t first, int32_t key0) { return ~from_key(first, key0); }
+// Bits i of a word of 32 keys from key0 on with key0 + i < end (a key's number, or one past it: the difference fits 32 bits
+// where end is at least -2^31 + 2 and key0 below 2^31 - 2^17).
+__device__ __forceinline__ uint32_t below_key(int32_t end, int32_t key0) { return end <= key0 ? 0u : below(end - key0); }
 
 // A lane's row: its node (-1: none) and the first key of its window.
 struct Row {
@@ -98,10 +99,13 @@ __device__ __forceinline__ Row row_of(const TreeQueries& tq, const Span& s, int3
 }
 // Which of the 32 keys from key0 on the row sees.
 __device__ __forceinline__ uint32_t row_sees(const TreeQueries& tq, const Span& s, const Row& row, int32_t sinks, int32_t key0) {
+    uint32_t near = ~below_key(row.lo, key0) | below_key(sinks, key0);
+    if (!tq.mask) return row.node < 0 ? 0u : near & below_key(s.ctx + row.node + 1, key0);
     uint32_t word[1] = {row.node < 0 ? 0u : 0xFFFFFFFFu};
-    if (!tq.mask || key0 + 31 >= s.ctx) seen_keys<1>(word, tq, s.nodes, s.ctx, row.node, key0);
-    uint32_t near = from_key(row.lo, key0) | below_key(sinks, key0);
-    if (tq.mask) near |= from_key(s.ctx, key0);  // a tree's mask alone decides over its nodes
+    if (key0 + 31 >= s.ctx) {
+        seen_keys<1>(word, tq, s.nodes, s.ctx, row.node, key0);
+        near |= ~below_key(s.ctx, key0);  // the mask alone decides over the nodes
+    }
     return word[0] & near;
 }
 
@@ -466,14 +470,31 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         id = slot / a.plan.row_blocks * 8 + (id & 7u);
         if (id >= groups) return;
     }
-    const int32_t split = id % a.plan.splits;
-    const uint32_t bh = id / a.plan.splits;
-    const int32_t h = bh % tq.H, b = bh / tq.H;
+    int32_t b, h, split, share = a.plan.share;
+    if (a.plan.by_lengths) {
+        const Shares r = shares_of<kStage>(tq, a.plan.groups, share, (int32_t)id, lane);
+        if (r.b < 0) return;
+        b = r.b, h = r.h, split = r.split, share = r.tiles;
+        // for the join: each sequence's first group, its shares and their tiles
+        if (rb == 0 && h == 0 && split == 0 && tid == 0) {
+            a.shares[3 * b] = r.first;
+            a.shares[3 * b + 1] = r.splits;
+            a.shares[3 * b + 2] = r.tiles;
+        }
+    } else {
+        split = id % a.plan.splits;
+        b = id / a.plan.splits / tq.H, h = id / a.plan.splits - b * tq.H;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    h = __builtin_amdgcn_readfirstlane(h);
+    split = __builtin_amdgcn_readfirstlane(split);
+    share = __builtin_amdgcn_readfirstlane(share);
     const Span s = span_of<kStage>(tq, b);
     const int32_t block0 = rb * WAVES * 32;
     if (block0 >= s.rows) return;
-    const Tiles tiles = tiles_of<kStage>(keyspan(tq, s, a.window, block0, block0 + WAVES * 32 - 1), a.sinks);
-    const int32_t share = a.plan.share, first = split * share;
+    const Keyspan block_span = keyspan(tq, s, a.window, block0, block0 + WAVES * 32 - 1);
+    const Tiles tiles = tiles_of<kStage>(block_span, a.sinks);
+    const int32_t first = split * share;
     if (first >= tiles.n) return;
     const int32_t end = tiles.n - first < share ? tiles.n : first + share;
     const int32_t total = s.ctx + s.nodes.count;
@@ -615,7 +636,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             }
         }
     };
-    auto work = [&](int32_t v, int buf) {
+    // A tile that is not whole, or of which keys may not be there.
+    auto partial = [&](int32_t v, int buf) {
         const int32_t key0 = tiles.at(v) * kStage;
         uint64_t exists[kStage / 64];
         bool all = true;
@@ -624,67 +646,126 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             exists[i] = __ballot(present[buf * kStage + 64 * i + lane] != 0u);
             all &= exists[i] == ~0ull;
         }
-        if (all && seen_by<kStage>(span, a.sinks, key0) == kEverybody) {
-            // the next 32 keys' scores on the way while the vector unit takes these ones' exponentials
+        // the 32s that all the wave's rows see whole (but those of the sinks alone), from `from` to `upto`, with every key
+        // there; then the others
+        int32_t from = (span.lo_max <= key0 ? 0 : (span.lo_max - key0 + 31) >> 5), upto = (span.hi_min + 1 - key0) >> 5;
+        if (key0 + kStage <= a.sinks) from = 0;
+        if (upto > kSubs) upto = kSubs;
+        if (!all || from >= upto) from = upto = 0;
+        if (from < upto) {
             Keys32 k;
             f32x16 sc[2];
-            read_k(k, buf, 0);
+            read_k(k, buf, from);
             scores32<1>(sc[0], w, 0, k);
-#pragma unroll
-            for (int sub = 0; sub < kSubs; ++sub) {
+            auto step = [&](int32_t sub, f32x16& own, f32x16& next) {
                 read_v(k, buf, sub);
-                if (sub + 1 < kSubs) {
+                if (sub + 1 < upto) {
                     read_k(k, buf, sub + 1);
-                    scores32<1>(sc[(sub + 1) % 2], w, 0, k);
+                    scores32<1>(next, w, 0, k);
                 }
-                add32<1, CAP, false>(w, 0, sc[sub % 2], k, f, 0u);
+                add32<1, CAP, false>(w, 0, own, k, f, 0u);
+            };
+#pragma unroll 1
+            for (int32_t sub = from;;) {
+                step(sub, sc[0], sc[1]);
+                if (++sub >= upto) break;
+                step(sub, sc[1], sc[0]);
+                if (++sub >= upto) break;
             }
-            return;
         }
 #pragma unroll 1
-        for (int sub = 0; sub < kSubs; ++sub) {
+        for (int32_t sub = 0; sub < kSubs; ++sub) {
+            if (sub >= from && sub < upto) continue;
             const uint32_t keys_there = (uint32_t)((kStage > 64 && sub & 2 ? exists[kStage / 64 - 1] : exists[0]) >> (32 * (sub & 1)));
             const int32_t at = key0 + 32 * sub;
-            const Seen seen = seen_by<32>(span, a.sinks, at);
-            if (seen == kNobody || keys_there == 0u) continue;
-            if (seen == kEverybody && keys_there == 0xFFFFFFFFu) {
-                Keys32 k;
-                f32x16 sc;
-                read_k(k, buf, sub);
-                read_v(k, buf, sub);
-                scores32<1>(sc, w, 0, k);
-                add32<1, CAP, false>(w, 0, sc, k, f, 0u);
-            } else {
-                masked(buf, sub, at, keys_there);
-            }
+            if (seen_by<32>(span, a.sinks, at) != kNobody && keys_there != 0u) masked(buf, sub, at, keys_there);
         }
     };
 
-    uint32_t page = entry(first);
-    fetch(first, page);
-    page = entry(first + 1);
+    // First the tiles that every row of the workgroup sees whole, if every block of theirs is there (looked at 64 blocks a
+    // load, up to 1024 of them): nobody asks for single rows or keys in them. Then those before, and those behind.
+    int32_t whole0 = block_span.lo_max < 0 ? 0 : (int32_t)(((int64_t)block_span.lo_max + kStage - 1) / kStage);
+    int32_t whole1 = (block_span.hi_min + 1) / kStage;
+    whole0 += tiles.sinks - tiles.from, whole1 += tiles.sinks - tiles.from;
+    whole0 = whole0 < first ? first : whole0 > end ? end : whole0;
+    whole1 = whole1 > end ? end : whole1 < whole0 ? whole0 : whole1;
+    if (whole0 < whole1) {
+        const uint32_t block = block_of((uint32_t)tiles.at(whole0) * kStage, kv);
+        const uint32_t blocks = block_of((uint32_t)(tiles.at(whole1 - 1) + 1) * kStage - 1, kv) - block + 1;
+        bool is = blocks <= 1024;
+        for (uint32_t i = lane; is && i < blocks; i += 64)
+            is = block + i < kv.table_width && (uint32_t)table[block + i] < kv.num_blocks;
+        if (!__all(is)) whole1 = whole0;
+    }
+    const int32_t whole = whole1 - whole0, count = end - first;
+    auto number = [&](int32_t i) {  // of the i-th tile
+        if (i < whole) return whole0 + i;
+        return i - whole < whole0 - first ? first + i - whole : first + i;
+    };
+    // The tile after the next one's block numbers are on the way before the next one's cells, so that nobody waits for
+    // these with those.
+    uint32_t page = entry(number(1));
+    fetch(number(0), entry(number(0)));
+    auto bring = [&](int32_t i) {
+        const uint32_t after = entry(number(i + 1));
+        if (i < count) fetch(number(i), page);
+        page = after;
+    };
     put(0);
     __syncthreads();
-    for (int32_t v = first; v < end; ++v) {
-        const int buf = (v - first) & 1;
-        const uint32_t after = entry(v + 2);  // (before the cells, so that nobody waits for those with it)
-        if (v + 1 < end) fetch(v + 1, page);
-        if (active) work(v, buf);
-        page = after;
-        if (v + 1 < end) {
-            put(buf ^ 1);  // (nobody reads it since the last barrier)
+    if (whole > 0) {
+        // One 32 keys' scores are on the way in the matrix cores while the vector unit takes the last ones' exponentials,
+        // over the barrier too: a tile's last weights are taken behind it, with the next one's first scores on the way.
+        Keys32 k;
+        f32x16 sc[2];
+        if (active) {
+            read_k(k, 0, 0);
+            scores32<1>(sc[0], w, 0, k);
+        }
+#pragma unroll 1
+        for (int32_t i = 0; i < whole; ++i) {
+            const int buf = i & 1;
+            bring(i + 1);
+            if (active) {
+#pragma unroll
+                for (int sub = 0; sub < kSubs; ++sub) {
+                    read_v(k, buf, sub);
+                    if (sub + 1 < kSubs) {
+                        read_k(k, buf, sub + 1);
+                        scores32<1>(sc[(sub + 1) % 2], w, 0, k);
+                        add32<1, CAP, false>(w, 0, sc[sub % 2], k, f, 0u);
+                    }
+                }
+            }
+            if (i + 1 < count) put(buf ^ 1);  // (nobody reads it since the last barrier)
+            __syncthreads();
+            if (active) {
+                if (i + 1 < whole) {
+                    read_k(k, buf ^ 1, 0);
+                    scores32<1>(sc[0], w, 0, k);
+                }
+                add32<1, CAP, false>(w, 0, sc[1], k, f, 0u);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int32_t i = whole; i < count; ++i) {
+        bring(i + 1);
+        if (active) partial(number(i), i & 1);
+        if (i + 1 < count) {
+            put((i & 1) ^ 1);
             __syncthreads();
         }
     }
     if (!active) return;
     const int32_t heads = tq.H * tq.G;
-    const int64_t rows_all = (int64_t)tq.T * heads;
-    const Results to{a.out, a.lse, a.part + split * rows_all * kHeadDim,
-                     a.part + (a.plan.splits * kHeadDim + 2 * split) * rows_all, a.plan.splits == 1};
+    constexpr int kRows = WAVES * 32;
+    const int64_t part0 = ((int64_t)id * a.plan.row_blocks + rb) * kRows - block0;
+    const Results to{a.out, a.lse, a.part, a.part + (int64_t)a.plan.groups * a.plan.row_blocks * kRows * kHeadDim, a.plan.splits == 1};
     const float l = w.l[0] + lane_xor<32>(w.l[0]);
     const float top = base_of<CAP>(w.base[0], w.c[0], f.c);
     if (row.node < 0) return;
-    const int64_t at = (int64_t)(s.nodes.first + row.node) * heads + h * tq.G + r - row.node * tq.G;
+    const int64_t at = to.whole ? (int64_t)(s.nodes.first + row.node) * heads + h * tq.G + r - row.node * tq.G : part0 + r;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -701,17 +782,30 @@ __global__ __launch_bounds__(256) void window_join_kernel(WindowArgs a) {
     const int32_t b = blockIdx.y;
     const Span s = span_of<kTile>(tq, b);
     if (row >= s.nodes.count * heads) return;
-    // the tiles of the row's block, as the attending workgroup counted them
-    const int32_t node = row / heads, hq = row - node * heads, r = node * tq.G + hq % tq.G;
-    const int32_t block_rows = a.plan.many ? 32 * a.plan.waves : s.rows, block0 = r / block_rows * block_rows;
-    const Keyspan span = keyspan(tq, s, a.window, block0, block0 + block_rows - 1);
-    const int32_t n = !a.plan.many        ? tiles_of<kTile>(span, a.sinks).n
-                      : a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n
-                                          : tiles_of<stage_of<4>()>(span, a.sinks).n;
-    const int32_t splits = (n + a.plan.share - 1) / a.plan.share;
-    const int64_t at = (int64_t)s.nodes.first * heads + row, step = (int64_t)tq.T * heads;
-    const float* po = a.part + at * kHeadDim + d;
-    const float* pm = a.part + a.plan.splits * step * kHeadDim + at * 2;
+    // the row's block, its tiles as the attending workgroup counted them, its first share's place
+    const int32_t node = row / heads, hq = row - node * heads, h = hq / tq.G, r = node * tq.G + hq - h * tq.G;
+    const int64_t at = (int64_t)s.nodes.first * heads + row;
+    int32_t splits;
+    int64_t from, step, all;
+    if (a.plan.many) {
+        const int32_t rows = 32 * a.plan.waves, block0 = r / rows * rows;
+        const Keyspan span = keyspan(tq, s, a.window, block0, block0 + rows - 1);
+        const int32_t n = a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n : tiles_of<stage_of<4>()>(span, a.sinks).n;
+        int32_t group = b * tq.H * a.plan.splits, of_head = a.plan.splits, share = a.plan.share;
+        if (a.plan.by_lengths) group = a.shares[3 * b], of_head = a.shares[3 * b + 1], share = a.shares[3 * b + 2];
+        splits = (n + share - 1) / share;  // (a chain's first rows may end before the sequence's last share)
+        step = (int64_t)a.plan.row_blocks * rows;
+        from = (int64_t)(group + h * of_head) * step + r;
+        all = a.plan.groups * step;
+    } else {
+        const int32_t n = tiles_of<kTile>(keyspan(tq, s, a.window, 0, s.rows - 1), a.sinks).n;
+        splits = (n + a.plan.share - 1) / a.plan.share;
+        step = (int64_t)tq.T * heads;
+        from = at;
+        all = a.plan.splits * step;
+    }
+    const float* po = a.part + from * kHeadDim + d;
+    const float* pm = a.part + all * kHeadDim + from * 2;
     float base = -__builtin_inff(), l = 0.0f;  // the largest base so far
     f32x4 o{0.f, 0.f, 0.f, 0.f};
     constexpr int kAtOnce = 8;
@@ -774,7 +868,7 @@ void launch_few(const WindowArgs& a, hipStream_t stream) {
 
 template <int WAVES, bool CAP, bool FP4>
 int launch_many(const WindowArgs& a, hipStream_t stream) {
-    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
+    const uint32_t groups = (uint32_t)a.plan.groups;
     const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
     auto kernel = window_many_kernel<WAVES, CAP, FP4>;
     static std::atomic<int> done[64] = {};
@@ -802,8 +896,11 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
                                  int32_t sinks, int32_t num_cus) {
     WindowPlan p{};
     const int64_t rows = (int64_t)max_nodes * G, base = (int64_t)B * H;
+    const bool ragged = window == kNoWindow;  // lengths that differ as the contexts do; over a window they are about equal
     p.many = rows > 32;
     p.waves = p.many && rows > 128 ? 8 : 4;
+    // waves without rows are idle: blocks of 128 rows where those of 256 would be filled to less than four fifths as much
+    if (p.waves == 8 && 4 * ((rows + 255) / 256 * 256) > 5 * ((rows + 127) / 128 * 128)) p.waves = 4;
     p.q_tiles = rows <= 16 ? 1 : 2;
     const int64_t block_rows = p.many ? 32 * p.waves : rows, keys = p.many ? 16 * p.waves : kTile;
     p.row_blocks = p.many ? (int32_t)((rows + block_rows - 1) / block_rows) : 1;
@@ -816,8 +913,20 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     p.share = (int32_t)tiles;
     int64_t splits, most;
     if (p.many) {
-        // until there is twice what the chip holds at once, of at least 4 tiles
         const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2), groups = base * p.row_blocks;
+        p.groups = (int32_t)base;
+        if (ragged && B <= 512) {
+            // shares by the lengths, in one or two rounds of what the chip holds at once
+            const int64_t round = at_once / p.row_blocks, rounds = round >= 2 * base ? 1 : 2;
+            if (rounds * round >= 2 * base && tiles > 4) {
+                p.by_lengths = true;
+                p.groups = (int32_t)(rounds * round);
+                p.splits = 2;  // (or more)
+                p.share = 4;   // at least
+            }
+            return p;
+        }
+        // until there is twice what the chip holds at once, of at least 4 tiles
         splits = groups >= at_once ? 1 : (2 * at_once + groups - 1) / groups;
         most = tiles / 4;
     } else {
@@ -827,7 +936,6 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
         }
         // until there are several workgroups per CU, each of at least 4 tiles a wave: over a window, of about equal lengths, 2;
         // over contexts, more than run at once, which evens out ragged lengths
-        const bool ragged = window == kNoWindow;
         splits = ((ragged ? 6 : 2) * num_cus + base - 1) / base;
         most = tiles / (4 * p.waves);
     }
@@ -836,11 +944,15 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
         p.share = (int32_t)((tiles + splits - 1) / splits);
         p.splits = (int32_t)((tiles + p.share - 1) / p.share);
     }
+    if (p.many) p.groups = (int32_t)(base * p.splits);
     return p;
 }
 
-int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads) {
-    return p.splits == 1 ? 0 : p.splits * T * heads * (kHeadDim + 2) * 4;
+// The partial sums' rows, and of shares by the lengths each sequence's first group, shares and tiles of one.
+int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads, int32_t B) {
+    if (p.splits == 1) return 0;
+    const int64_t rows = p.many ? (int64_t)p.groups * p.row_blocks * 32 * p.waves : p.splits * T * heads;
+    return rows * (kHeadDim + 2) * 4 + (p.by_lengths ? (int64_t)B * 3 * 4 : 0);
 }
 
 int launch_window_attention(const WindowArgs& a, hipStream_t stream) {
