@@ -5,6 +5,7 @@
 #pragma once
 
 #include "cache_ops.h"
+#include "div.h"
 
 namespace nrc {
 
@@ -88,7 +89,8 @@ struct WindowArgs {
     float* part;      // splits > 1: the partial sums' rows, [., 64] then [., 2]
     int32_t* shares;  // by_lengths: [B, 3], each sequence's first group, its shares and their tiles
     WindowPlan plan;
-    uint32_t fill;  // NRC_ATTENTION_FILL_*
+    Div by_group, by_heads, by_splits, by_blocks;  // tq.G, tq.H, plan.splits, plan.row_blocks
+    uint32_t fill;                                 // NRC_ATTENTION_FILL_*
 };
 
 int launch_window_attention(const WindowArgs& a, hipStream_t stream);

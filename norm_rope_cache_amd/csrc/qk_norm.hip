@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "../../include/nrc.h"
+#include "div.h"
 #include "draft_ops.h"
 #include "element.h"
 
@@ -30,18 +31,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxHead = 256;
-
-// n / d for n < 2^31.
-struct Div {
-    uint32_t mul, shift;  // mul 0: d = 1
-};
-Div div_by(uint32_t d) {
-    if (d == 1) return Div{0, 0};
-    uint32_t s = 0;
-    while ((1ull << s) < d) ++s;
-    return Div{(uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d), s - 1};
-}
-__device__ __forceinline__ uint32_t quotient(uint32_t n, Div d) { return d.mul ? __umulhi(n, d.mul) >> d.shift : n; }
 
 struct Part {
     const void* x;

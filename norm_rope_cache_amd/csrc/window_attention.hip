@@ -39,27 +39,39 @@ struct Keyspan {
     int32_t lo_min, lo_max, hi_min, hi_max;
 };
 // Of rows first .. last (of the sequence's; last is cut to them). A tree's rows stand at ctx + the nodes they see - 1.
-__device__ __forceinline__ Keyspan keyspan(const TreeQueries& tq, const Span& s, int32_t window, int32_t first, int32_t last) {
+__device__ __forceinline__ Keyspan keyspan(const WindowArgs& a, const Span& s, int32_t first, int32_t last) {
     if (last >= s.rows) last = s.rows - 1;
-    if (tq.mask) return Keyspan{s.ctx - window, s.ctx - window + s.nodes.count, s.ctx - 1, s.ctx + s.nodes.count - 1};
-    const int32_t n0 = first / tq.G, n1 = last / tq.G;
-    return Keyspan{s.ctx - window + 1 + n0, s.ctx - window + 1 + n1, s.ctx + n0, s.ctx + n1};
+    if (a.tq.mask) return Keyspan{s.ctx - a.window, s.ctx - a.window + s.nodes.count, s.ctx - 1, s.ctx + s.nodes.count - 1};
+    const int32_t n0 = (int32_t)quotient((uint32_t)first, a.by_group), n1 = (int32_t)quotient((uint32_t)last, a.by_group);
+    return Keyspan{s.ctx - a.window + 1 + n0, s.ctx - a.window + 1 + n1, s.ctx + n0, s.ctx + n1};
 }
 
-// The tiles of KEYS keys that a block of rows looks at: `sinks` from the first on, then those from `from` on, n in all.
+// The keys that a block of rows looks at, one after the other: the sinks (as whole 32s; none where the windows reach back
+// to them), then those from `base` (a multiple of 32) to hi_max. They are dealt into tiles of KEYS, n in all.
 struct Tiles {
-    int32_t sinks, from, n;
-    __device__ __forceinline__ int32_t at(int32_t v) const { return v < sinks ? v : v - sinks + from; }
+    int32_t sinks, base, n;
+    // the key at place p, a multiple of 16 (the 16 from there on lie together)
+    __device__ __forceinline__ int32_t key(int32_t p) const { return p < sinks ? p : p - sinks + base; }
+    // the place of a key that is not before `base`
+    __device__ __forceinline__ int64_t place(int64_t key) const { return key - base + sinks; }
 };
 template <int KEYS>
 __device__ __forceinline__ Tiles tiles_of(const Keyspan& k, int32_t sinks) {
     Tiles t;
-    t.from = (k.lo_min < 0 ? 0 : k.lo_min) / KEYS;
-    const int32_t first = sinks / KEYS + (sinks % KEYS != 0);
-    t.sinks = first < t.from ? first : t.from;
-    t.n = t.sinks + k.hi_max / KEYS + 1 - t.from;
+    t.base = k.lo_min < 0 ? 0 : k.lo_min & ~31;
+    t.sinks = sinks > t.base ? t.base : (sinks + 31) & ~31;
+    if (t.sinks >= t.base) t.base = t.sinks = 0;
+    t.n = (int32_t)(t.place(k.hi_max) / KEYS) + 1;
     return t;
 }
+// The numbers of the tiles that every one of the rows sees whole, from .x to .y (but for some of the sinks alone).
+template <int KEYS>
+__device__ __forceinline__ int2 whole_tiles(const Keyspan& k, const Tiles& t, int32_t sinks) {
+    const int64_t from = k.lo_max <= t.base || (t.base == 0 && sinks >= k.lo_max) ? t.sinks : t.place(k.lo_max);
+    const int64_t upto = t.place(k.hi_min + 1) / KEYS, first = (from + KEYS - 1) / KEYS;
+    return int2{(int32_t)first, (int32_t)(upto < first ? first : upto)};
+}
+
 enum Seen { kNobody, kSome, kEverybody };
 template <int KEYS>
 __device__ __forceinline__ Seen seen_by(const Keyspan& k, int32_t sinks, int32_t key0) {
@@ -81,10 +93,12 @@ __device__ __forceinline__ uint32_t below_key(int32_t end, int32_t key0) { retur
 struct Row {
     int32_t node, lo;
 };
-__device__ __forceinline__ Row row_of(const TreeQueries& tq, const Span& s, int32_t window, int32_t r) {
+__device__ __forceinline__ Row row_of(const WindowArgs& a, const Span& s, int32_t r) {
+    const TreeQueries& tq = a.tq;
+    const int32_t window = a.window;
     Row row{-1, 0};
     if (r >= s.rows) return row;
-    row.node = r / tq.G;
+    row.node = (int32_t)quotient((uint32_t)r, a.by_group);
     row.lo = s.ctx - window + 1 + row.node;
     if (tq.mask && window != kNoWindow) {
         const uint32_t* words = tq.mask + (int64_t)(s.nodes.first + row.node) * tq.mask_words;
@@ -210,17 +224,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     const TreeQueries& tq = a.tq;
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
-    const int32_t split = blockIdx.x % a.plan.splits;
-    const uint32_t bh = blockIdx.x / a.plan.splits;
-    const int32_t h = bh % tq.H, b = bh / tq.H;
+    const uint32_t bh = quotient(blockIdx.x, a.by_splits);
+    const int32_t split = (int32_t)(blockIdx.x - bh * a.plan.splits);
+    const int32_t b = (int32_t)quotient(bh, a.by_heads), h = (int32_t)bh - b * tq.H;
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
     const Span s = span_of<kTile>(tq, b);
     if (s.rows == 0) return;
-    const Keyspan span = keyspan(tq, s, a.window, 0, s.rows - 1);
+    const Keyspan span = keyspan(a, s, 0, s.rows - 1);
     const Tiles tiles = tiles_of<kTile>(span, a.sinks);
     const int32_t share = a.plan.share, first = split * share;
     if (first >= tiles.n) return;  // (nor does the join look at such a share)
-    const int32_t end = tiles.n - first < share ? tiles.n : first + share;
+    const int32_t end = tiles.n - first < share || split == a.plan.splits - 1 ? tiles.n : first + share;
     const int32_t total = s.ctx + s.nodes.count;
     const int32_t v0 = first + (int32_t)wave;  // the wave's tiles: v0, v0 + WAVES ..
     const int32_t count = v0 < end ? (end - v0 + WAVES - 1) / WAVES : 0;
@@ -239,7 +253,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     };
     auto key_of = [&](int32_t j, int i) {
         const int32_t v = v0 + (j + (PAGES ? (int32_t)(lane >> 1) : i)) * WAVES;
-        return (uint32_t)tiles.at(v < end ? v : end - 1) * kTile + (PAGES ? (lane & 1u) * 16 : own_key);
+        return (uint32_t)tiles.key((v < end ? v : end - 1) * kTile) + (PAGES ? (lane & 1u) * 16 : own_key);
     };
     auto blocks_of = [&](int32_t j) {
         Blocks p;
@@ -290,7 +304,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
 #pragma unroll
     for (int rq = 0; rq < R; ++rq) {
         const int32_t r = 16 * rq + (int32_t)n16;
-        row[rq] = row_of(tq, s, a.window, r);
+        row[rq] = row_of(a, s, r);
         w.q[rq][0] = w.q[rq][1] = U32x4{0u, 0u, 0u, 0u};
         if (row[rq].node >= 0) {
             const uint16_t* q = tq.q + (int64_t)(s.nodes.first + row[rq].node) * tq.q_rs +
@@ -306,12 +320,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
         w.l[rq] = 0.0f;
     }
 
-    // The numbers of the tiles that every row sees whole: below whole_sinks, and from `near` to `own` (a tile of
-    // the sinks' last keys, or one in which a row's window or own keys begin, is not whole).
-    const int32_t whole_sinks = a.sinks / kTile < tiles.sinks ? a.sinks / kTile : tiles.sinks;
-    int32_t near = (span.lo_max < 0 ? 0 : (int32_t)(((int64_t)span.lo_max + kTile - 1) / kTile)), own = (span.hi_min + 1) / kTile;
-    if (a.sinks / kTile >= near) near = tiles.from;  // (the sinks reach past the windows' beginnings)
-    near += tiles.sinks - tiles.from, own += tiles.sinks - tiles.from;
+    // The tiles that every row sees whole, below whole_sinks and from `near` to `own`.
+    const int2 seen_whole = whole_tiles<kTile>(span, tiles, a.sinks);
+    const int32_t whole_sinks = tiles.sinks > 0 ? a.sinks / kTile : 0, near = seen_whole.x, own = seen_whole.y;
     bool left_out = false;  // such a tile with a key that is not there
     if (count > 0) {
         // kAhead tiles to a round. Every load is made in every round (past the last tile, of some tile again), so that the
@@ -355,7 +366,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     }
     // the others
     auto masked = [&](int32_t v, bool whole) {
-        const int32_t key0 = tiles.at(v) * kTile, j = (v - v0) / WAVES;
+        const int32_t key0 = tiles.key(v * kTile), j = (v - v0) / WAVES;
         Raw raw;
         const uint32_t there = below_key(total, key0) & fetch(raw, blocks_of(j), j, 0);
         if (there == 0u || (whole && there == 0xFFFFFFFFu)) return;  // (nobody's, or done)
@@ -386,7 +397,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     // (all tiles where some were left out, else those that are not whole)
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
-        const int32_t from = left_out ? (i == 0 ? 0 : tiles.n) : i == 0 ? whole_sinks : near < own ? own : near;
+        const int32_t from = left_out ? (i == 0 ? 0 : tiles.n) : i == 0 ? whole_sinks : own;
         const int32_t upto = left_out ? tiles.n : i == 0 ? near : tiles.n;
         int32_t v = from < first ? first : from;
         v += ((int32_t)wave - (v - first) % WAVES + WAVES) % WAVES;
@@ -433,7 +444,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[i], x, o[i]);
         }
-        const int32_t node = r / tq.G;
+        const int32_t node = (int32_t)quotient((uint32_t)r, a.by_group);
         put_row4(to, (int64_t)(s.nodes.first + node) * heads + h * tq.G + (r - node * tq.G), d, top, l, o);
     }
 }
@@ -465,9 +476,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     // the row blocks of one share, which read the same keys, run on one XCD next to each other
     uint32_t id = blockIdx.x, rb = 0;
     if (a.plan.row_blocks > 1) {
-        const uint32_t slot = id >> 3;
-        rb = slot % a.plan.row_blocks;
-        id = slot / a.plan.row_blocks * 8 + (id & 7u);
+        const uint32_t slot = id >> 3, of = quotient(slot, a.by_blocks);
+        rb = slot - of * a.plan.row_blocks;
+        id = of * 8 + (id & 7u);
         if (id >= groups) return;
     }
     int32_t b, h, split, share = a.plan.share;
@@ -482,8 +493,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             a.shares[3 * b + 2] = r.tiles;
         }
     } else {
-        split = id % a.plan.splits;
-        b = id / a.plan.splits / tq.H, h = id / a.plan.splits - b * tq.H;
+        const uint32_t bh = quotient(id, a.by_splits);
+        split = (int32_t)(id - bh * a.plan.splits);
+        b = (int32_t)quotient(bh, a.by_heads), h = (int32_t)bh - b * tq.H;
     }
     b = __builtin_amdgcn_readfirstlane(b);
     h = __builtin_amdgcn_readfirstlane(h);
@@ -492,15 +504,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     const Span s = span_of<kStage>(tq, b);
     const int32_t block0 = rb * WAVES * 32;
     if (block0 >= s.rows) return;
-    const Keyspan block_span = keyspan(tq, s, a.window, block0, block0 + WAVES * 32 - 1);
+    const Keyspan block_span = keyspan(a, s, block0, block0 + WAVES * 32 - 1);
     const Tiles tiles = tiles_of<kStage>(block_span, a.sinks);
     const int32_t first = split * share;
     if (first >= tiles.n) return;
-    const int32_t end = tiles.n - first < share ? tiles.n : first + share;
+    const int32_t end = tiles.n - first < share || (!a.plan.by_lengths && split == a.plan.splits - 1) ? tiles.n : first + share;
     const int32_t total = s.ctx + s.nodes.count;
     const int32_t row0 = block0 + (int32_t)wave * 32;
     const bool active = row0 < s.rows;
-    const Keyspan span = keyspan(tq, s, a.window, row0, row0 + 31);  // of this wave's rows
+    const Keyspan span = keyspan(a, s, row0, row0 + 31);  // of this wave's rows
 
     const uint8_t* head = reinterpret_cast<const uint8_t*>(kv.cache) + (int64_t)h * kv.head_stride * (FP4 ? 1 : 2);
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
@@ -511,9 +523,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     U32x4 cell[FP4 ? 1 : 4];
     uint32_t scales = 0;
     bool there = false;
-    auto entry = [&](int32_t v) { return page_of(kv, table, (uint32_t)tiles.at(v < end ? v : end - 1) * kStage + own_key); };
+    auto key_of = [&](int32_t v) {  // in tile number v
+        return (uint32_t)tiles.key(v * kStage + (int32_t)(own_key & ~31u)) + (own_key & 31u);
+    };
+    auto entry = [&](int32_t v) { return page_of(kv, table, key_of(v < end ? v : end - 1)); };
     auto fetch = [&](int32_t v, uint32_t page) {
-        const uint32_t key = (uint32_t)tiles.at(v) * kStage + own_key;
+        const uint32_t key = key_of(v);
         const Place p = place_of<FP4>(kv, key, page);
         there = p.off >= 0 && key < (uint32_t)total;
 #pragma unroll
@@ -573,7 +588,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
 
     Rows32<1> w;
     const int32_t r = row0 + (int32_t)n32;
-    const Row row = row_of(tq, s, a.window, r);
+    const Row row = row_of(a, s, r);
 #pragma unroll
     for (int i = 0; i < 4; ++i) w.q[0][i] = U32x4{0u, 0u, 0u, 0u};
     if (row.node >= 0) {
@@ -638,7 +653,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     };
     // A tile that is not whole, or of which keys may not be there.
     auto partial = [&](int32_t v, int buf) {
-        const int32_t key0 = tiles.at(v) * kStage;
         uint64_t exists[kStage / 64];
         bool all = true;
 #pragma unroll
@@ -646,10 +660,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             exists[i] = __ballot(present[buf * kStage + 64 * i + lane] != 0u);
             all &= exists[i] == ~0ull;
         }
-        // the 32s that all the wave's rows see whole (but those of the sinks alone), from `from` to `upto`, with every key
+        // the 32s that all the wave's rows see whole (but some of the sinks alone), from `from` to `upto`, with every key
         // there; then the others
-        int32_t from = (span.lo_max <= key0 ? 0 : (span.lo_max - key0 + 31) >> 5), upto = (span.hi_min + 1 - key0) >> 5;
-        if (key0 + kStage <= a.sinks) from = 0;
+        const int2 of_rows = whole_tiles<32>(span, tiles, a.sinks);
+        int32_t from = of_rows.x - v * kSubs, upto = of_rows.y - v * kSubs;
+        if (from < 0) from = 0;
         if (upto > kSubs) upto = kSubs;
         if (!all || from >= upto) from = upto = 0;
         if (from < upto) {
@@ -677,40 +692,43 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         for (int32_t sub = 0; sub < kSubs; ++sub) {
             if (sub >= from && sub < upto) continue;
             const uint32_t keys_there = (uint32_t)((kStage > 64 && sub & 2 ? exists[kStage / 64 - 1] : exists[0]) >> (32 * (sub & 1)));
-            const int32_t at = key0 + 32 * sub;
+            const int32_t at = tiles.key(v * kStage + 32 * sub);
             if (seen_by<32>(span, a.sinks, at) != kNobody && keys_there != 0u) masked(buf, sub, at, keys_there);
         }
     };
 
     // First the tiles that every row of the workgroup sees whole, if every block of theirs is there (looked at 64 blocks a
     // load, up to 1024 of them): nobody asks for single rows or keys in them. Then those before, and those behind.
-    int32_t whole0 = block_span.lo_max < 0 ? 0 : (int32_t)(((int64_t)block_span.lo_max + kStage - 1) / kStage);
-    int32_t whole1 = (block_span.hi_min + 1) / kStage;
-    whole0 += tiles.sinks - tiles.from, whole1 += tiles.sinks - tiles.from;
-    whole0 = whole0 < first ? first : whole0 > end ? end : whole0;
-    whole1 = whole1 > end ? end : whole1 < whole0 ? whole0 : whole1;
-    if (whole0 < whole1) {
-        const uint32_t block = block_of((uint32_t)tiles.at(whole0) * kStage, kv);
-        const uint32_t blocks = block_of((uint32_t)(tiles.at(whole1 - 1) + 1) * kStage - 1, kv) - block + 1;
-        bool is = blocks <= 1024;
-        for (uint32_t i = lane; is && i < blocks; i += 64)
-            is = block + i < kv.table_width && (uint32_t)table[block + i] < kv.num_blocks;
-        if (!__all(is)) whole1 = whole0;
-    }
-    const int32_t whole = whole1 - whole0, count = end - first;
+    const int2 block_whole = whole_tiles<kStage>(block_span, tiles, a.sinks);
+    int32_t whole0 = block_whole.x < first ? first : block_whole.x > end ? end : block_whole.x;
+    const int32_t whole1 = block_whole.y > end ? end : block_whole.y < whole0 ? whole0 : block_whole.y;
+    int32_t whole = whole1 - whole0;
+    const int32_t count = end - first;
     auto number = [&](int32_t i) {  // of the i-th tile
         if (i < whole) return whole0 + i;
         return i - whole < whole0 - first ? first + i - whole : first + i;
     };
     // The tile after the next one's block numbers are on the way before the next one's cells, so that nobody waits for
     // these with those.
-    uint32_t page = entry(number(1));
-    fetch(number(0), entry(number(0)));
+    uint32_t page = entry(number(0)), after = entry(number(1));
     auto bring = [&](int32_t i) {
-        const uint32_t after = entry(number(i + 1));
-        if (i < count) fetch(number(i), page);
         page = after;
+        after = entry(number(i + 1));
+        if (i < count) fetch(number(i), page);
     };
+    fetch(number(0), page);
+    if (whole > 0) {
+        const uint32_t block = block_of((uint32_t)tiles.key(whole0 * kStage), kv);
+        const uint32_t blocks = block_of((uint32_t)tiles.key((whole0 + whole) * kStage - 32) + 31, kv) - block + 1;
+        bool is = blocks <= 1024;
+        for (uint32_t i = lane; is && i < blocks; i += 64)
+            is = block + i < kv.table_width && (uint32_t)table[block + i] < kv.num_blocks;
+        if (!__all(is)) {
+            whole = 0;
+            fetch(number(0), entry(number(0)));
+            after = entry(number(1));
+        }
+    }
     put(0);
     __syncthreads();
     if (whole > 0) {
@@ -783,23 +801,25 @@ __global__ __launch_bounds__(256) void window_join_kernel(WindowArgs a) {
     const Span s = span_of<kTile>(tq, b);
     if (row >= s.nodes.count * heads) return;
     // the row's block, its tiles as the attending workgroup counted them, its first share's place
-    const int32_t node = row / heads, hq = row - node * heads, h = hq / tq.G, r = node * tq.G + hq - h * tq.G;
+    const int32_t node = row / heads, hq = row - node * heads, h = (int32_t)quotient((uint32_t)hq, a.by_group), r = node * tq.G + hq - h * tq.G;
     const int64_t at = (int64_t)s.nodes.first * heads + row;
     int32_t splits;
     int64_t from, step, all;
     if (a.plan.many) {
         const int32_t rows = 32 * a.plan.waves, block0 = r / rows * rows;
-        const Keyspan span = keyspan(tq, s, a.window, block0, block0 + rows - 1);
+        const Keyspan span = keyspan(a, s, block0, block0 + rows - 1);
         const int32_t n = a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n : tiles_of<stage_of<4>()>(span, a.sinks).n;
         int32_t group = b * tq.H * a.plan.splits, of_head = a.plan.splits, share = a.plan.share;
         if (a.plan.by_lengths) group = a.shares[3 * b], of_head = a.shares[3 * b + 1], share = a.shares[3 * b + 2];
         splits = (n + share - 1) / share;  // (a chain's first rows may end before the sequence's last share)
+        if (!a.plan.by_lengths && splits > a.plan.splits) splits = a.plan.splits;
         step = (int64_t)a.plan.row_blocks * rows;
         from = (int64_t)(group + h * of_head) * step + r;
         all = a.plan.groups * step;
     } else {
-        const int32_t n = tiles_of<kTile>(keyspan(tq, s, a.window, 0, s.rows - 1), a.sinks).n;
+        const int32_t n = tiles_of<kTile>(keyspan(a, s, 0, s.rows - 1), a.sinks).n;
         splits = (n + a.plan.share - 1) / a.plan.share;
+        if (splits > a.plan.splits) splits = a.plan.splits;
         step = (int64_t)tq.T * heads;
         from = at;
         all = a.plan.splits * step;
@@ -904,10 +924,10 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     p.q_tiles = rows <= 16 ? 1 : 2;
     const int64_t block_rows = p.many ? 32 * p.waves : rows, keys = p.many ? 16 * p.waves : kTile;
     p.row_blocks = p.many ? (int32_t)((rows + block_rows - 1) / block_rows) : 1;
-    // the most tiles that a block of rows looks at
+    // the tiles that a block of rows looks at (a tree's last share takes what there are more)
     int64_t tiles = (max_ctx + max_nodes + keys - 1) / keys;
     const int64_t nodes = block_rows / G + 1 < max_nodes ? block_rows / G + 1 : max_nodes;
-    const int64_t near = (int64_t)sinks / keys + 1 + ((int64_t)window + nodes + keys - 1) / keys + 1;
+    const int64_t near = ((int64_t)sinks + 31 + window + nodes + 31) / keys + 1;
     if (near < tiles) tiles = near;
     p.splits = 1;
     p.share = (int32_t)tiles;
@@ -955,7 +975,10 @@ int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads
     return rows * (kHeadDim + 2) * 4 + (p.by_lengths ? (int64_t)B * 3 * 4 : 0);
 }
 
-int launch_window_attention(const WindowArgs& a, hipStream_t stream) {
+int launch_window_attention(const WindowArgs& args, hipStream_t stream) {
+    WindowArgs a = args;
+    a.by_group = div_by((uint32_t)a.tq.G), a.by_heads = div_by((uint32_t)a.tq.H);
+    a.by_splits = div_by((uint32_t)a.plan.splits), a.by_blocks = div_by((uint32_t)a.plan.row_blocks);
     if (a.tq.B == 0) {
         hipLaunchKernelGGL(window_fill_kernel, dim3(fill_groups(a)), dim3(256), 0, stream, a.tq, a.fill, a.out, a.lse);
         return hipGetLastError() == hipSuccess ? 0 : -1;
