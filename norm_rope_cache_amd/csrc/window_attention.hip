@@ -123,18 +123,6 @@ __device__ __forceinline__ uint32_t row_sees(const TreeQueries& tq, const Span& 
     return word[0] & near;
 }
 
-// Where a key's cell lies: byte (bf16: element) offset of its K within head 0, or -1, and its place in the page.
-struct Place {
-    int64_t off;
-    uint32_t at;
-};
-template <bool FP4>
-__device__ __forceinline__ Place place_of(const PagedCache& c, uint32_t key, uint32_t page) {
-    const uint32_t blk = block_of(key, c), at = key - blk * c.block_size;
-    const bool there = blk < c.table_width && page < c.num_blocks;
-    return Place{there ? (int64_t)page * c.block_stride + (FP4 ? (int64_t)at * kFp4Codes : (int64_t)at * c.page_stride) : -1, at};
-}
-
 // ---- few rows -----------------------------------------------------------------------------------------------------
 
 // A tile of 32 cells of 4 bits as a lane loads it: of key 16 (l / 32) + l % 16 the 32 codes of K's group l / 16 % 2, V's,
@@ -324,52 +312,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     const int2 seen_whole = whole_tiles<kTile>(span, tiles, a.sinks);
     const int32_t whole_sinks = tiles.sinks > 0 ? a.sinks / kTile : 0, near = seen_whole.x, own = seen_whole.y;
     bool left_out = false;  // such a tile with a key that is not there
-    if (count > 0) {
-        // kAhead tiles to a round. Every load is made in every round (past the last tile, of some tile again), so that the
-        // compiler knows how many are on the way and waits for the oldest alone; block numbers come two rounds ahead.
-        Raw raw[kAhead];
-        uint32_t there[kAhead];
-        Blocks blocks = blocks_of(0), next = blocks_of(kAhead);
-        auto bring = [&](int slot, const Blocks& from, int32_t j) {
-            there[slot] = fetch(raw[slot], from, j, slot);
-            __builtin_amdgcn_sched_barrier(0);  // (the tiles' loads in their order)
-        };
-        auto work = [&](int32_t j, Raw& cur, bool all) {
-            const int32_t v = v0 + j * WAVES;
-            if (j >= count || v >= own || (v < near && v >= whole_sinks)) return;
-            if (!all) {
-                left_out = true;
-            } else if constexpr (FP4) {
-                Keys keys;
-                open_keys<false>(keys, cur, turn, lane);
-                open_tile<R, CAP>(w, keys, f.c, f.capped);
-            } else {
-                open_tile<R, CAP>(w, cur, f.c, f.capped);
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < kAhead - 1; ++i) bring(i, blocks, 0);
-#pragma unroll 1
-        for (int32_t q = 0; q * kAhead < count; ++q) {
-            const Blocks after = blocks_of((q + 2) * kAhead);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (i == 0)
-                    bring(kAhead - 1, blocks, q * kAhead);
-                else
-                    bring(i - 1, next, (q + 1) * kAhead);
-                work(q * kAhead + i, raw[i], there[i] == 0xFFFFFFFFu);
-            }
-            blocks = next;
-            next = after;
-        }
-    }
-    // the others
-    auto masked = [&](int32_t v, bool whole) {
-        const int32_t key0 = tiles.key(v * kTile), j = (v - v0) / WAVES;
-        Raw raw;
-        const uint32_t there = below_key(total, key0) & fetch(raw, blocks_of(j), j, 0);
-        if (there == 0u || (whole && there == 0xFFFFFFFFu)) return;  // (nobody's, or done)
+    // A tile that some rows may not see whole, or with keys that are not there.
+    auto masked = [&](int32_t v, const Raw& raw, uint32_t exist) {
+        const int32_t key0 = tiles.key(v * kTile);
+        const uint32_t there = exist & below_key(total, key0);
+        if (there == 0u) return;
         uint32_t sees[R];
 #pragma unroll
         for (int rq = 0; rq < R; ++rq) sees[rq] = there & row_sees(tq, s, row[rq], a.sinks, key0);
@@ -394,14 +341,72 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
             }
         }
     };
-    // (all tiles where some were left out, else those that are not whole)
+    // the wave's first tile from number v on
+    auto own_from = [&](int32_t v) {
+        if (v < first) v = first;
+        return v + ((int32_t)wave - (v - first) % WAVES + WAVES) % WAVES;
+    };
+    int32_t before = own_from(whole_sinks);  // the wave's first tile that is not whole
+    if (before >= near) before = own_from(own);
+    if (count > 0) {
+        // kAhead tiles to a round. Every load is made in every round (past the last tile, of some tile again), so that the
+        // compiler knows how many are on the way and waits for the oldest alone; block numbers come two rounds ahead.
+        // The first tile that is not whole comes behind the first round's, in the slot that is still free.
+        Raw raw[kAhead];
+        uint32_t there[kAhead];
+        Blocks blocks = blocks_of(0), next = blocks_of(kAhead);
+        const int32_t j_before = before < end ? (before - v0) / WAVES : 0;
+        const Blocks blocks_before = blocks_of(j_before);
+        auto bring = [&](int slot, const Blocks& from, int32_t j) {
+            there[slot] = fetch(raw[slot], from, j, slot);
+            __builtin_amdgcn_sched_barrier(0);  // (the tiles' loads in their order)
+        };
+        auto work = [&](int32_t j, Raw& cur, bool all) {
+            const int32_t v = v0 + j * WAVES;
+            if (j >= count || v >= own || (v < near && v >= whole_sinks)) return;
+            if (!all) {
+                left_out = true;
+            } else if constexpr (FP4) {
+                Keys keys;
+                open_keys<false>(keys, cur, turn, lane);
+                open_tile<R, CAP>(w, keys, f.c, f.capped);
+            } else {
+                open_tile<R, CAP>(w, cur, f.c, f.capped);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) bring(i, blocks, 0);
+        if (before < end) {
+            const uint32_t exist = fetch(raw[kAhead - 1], blocks_before, j_before, 0);
+            masked(before, raw[kAhead - 1], exist);
+        }
+#pragma unroll 1
+        for (int32_t q = 0; q * kAhead < count; ++q) {
+            const Blocks after = blocks_of((q + 2) * kAhead);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (i == 0)
+                    bring(kAhead - 1, blocks, q * kAhead);
+                else
+                    bring(i - 1, next, (q + 1) * kAhead);
+                work(q * kAhead + i, raw[i], there[i] == 0xFFFFFFFFu);
+            }
+            blocks = next;
+            next = after;
+        }
+    }
+    // The others (all tiles where some were left out, but those that are done).
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
         const int32_t from = left_out ? (i == 0 ? 0 : tiles.n) : i == 0 ? whole_sinks : own;
         const int32_t upto = left_out ? tiles.n : i == 0 ? near : tiles.n;
-        int32_t v = from < first ? first : from;
-        v += ((int32_t)wave - (v - first) % WAVES + WAVES) % WAVES;
-        for (; v < upto && v < end; v += WAVES) masked(v, v < whole_sinks || (v >= near && v < own));
+        for (int32_t v = own_from(from); v < upto && v < end; v += WAVES) {
+            if (v == before) continue;
+            const int32_t j = (v - v0) / WAVES;
+            Raw raw;
+            const uint32_t exist = fetch(raw, blocks_of(j), j, 0);
+            if (exist != 0xFFFFFFFFu || !(v < whole_sinks || (v >= near && v < own))) masked(v, raw, exist);
+        }
     }
 
     // Join the waves: each leaves m's base, l and O of its rows in LDS.
@@ -518,6 +523,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
     const Factors f = factors<CAP>(tq);
 
+    const uint32_t codes = kFp4Codes * kv.block_size;  // bytes of a page's K codes
     // A thread's quarter (K's halves, V's halves) of its key's cell.
     const uint32_t own_key = tid >> 2, quarter = tid & 3u;
     U32x4 cell[FP4 ? 1 : 4];
@@ -528,26 +534,28 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     };
     auto entry = [&](int32_t v) { return page_of(kv, table, key_of(v < end ? v : end - 1)); };
     auto fetch = [&](int32_t v, uint32_t page) {
-        const uint32_t key = key_of(v);
-        const Place p = place_of<FP4>(kv, key, page);
-        there = p.off >= 0 && key < (uint32_t)total;
-#pragma unroll
-        for (U32x4& c : cell) c = U32x4{0u, 0u, 0u, 0u};
-        scales = 0;
-        if (!there) return;
+        // (a cell that is not there is read from the cache's first page, and dropped)
+        const uint32_t key = key_of(v), blk = block_of(key, kv);
+        there = blk < kv.table_width && page < kv.num_blocks && key < (uint32_t)total;
+        const uint32_t at = there ? key - blk * kv.block_size : 0u;
+        const uint8_t* base = head + (int64_t)(there ? page : 0u) * kv.block_stride * (FP4 ? 1 : 2);
         if constexpr (FP4) {
-            const int64_t codes = (int64_t)kFp4Codes * kv.block_size;
-            cell[0] = load16(head + p.off + (quarter >> 1) * codes + (quarter & 1u) * 16);
-            scales = *reinterpret_cast<const uint32_t*>(head + p.off + 2 * codes - (int64_t)(kFp4Codes - 4) * p.at);
+            cell[0] = load16(base + (int64_t)((quarter >> 1) * codes + at * kFp4Codes + (quarter & 1u) * 16));
+            scales = *reinterpret_cast<const uint32_t*>(base + (int64_t)(2 * codes + 4 * at));
         } else {
-            const uint16_t* at = reinterpret_cast<const uint16_t*>(head) + p.off + 32 * quarter;
+            const uint8_t* own = base + (int64_t)at * kv.page_stride * 2 + 64 * quarter;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cell[i] = load16(at + 8 * i);
+            for (int i = 0; i < 4; ++i) cell[i] = load16(own + 16 * i);
         }
     };
     auto put = [&](int buf) {
         const uint32_t swizzle = quarter < 2 ? own_key & 7u : (own_key >> 1 & 1u) << 2;
         uint8_t* at = lds + buf * (kStage * 256) + (quarter >> 1) * (kStage * 128) + own_key * 128;
+        if (!there) {
+#pragma unroll
+            for (U32x4& c : cell) c = U32x4{0u, 0u, 0u, 0u};
+            scales = 0;
+        }
         if constexpr (FP4) {
             uint32_t byte = scales >> (8 * quarter) & 0xFFu;
             if (quarter >= 2) byte = byte < kScaleHigh ? byte : kScaleHigh;  // (V: see the top)
@@ -871,19 +879,23 @@ uint32_t fill_groups(const WindowArgs& a) {
 }
 
 template <int R, int WAVES, bool FP4>
-void launch_few(const WindowArgs& a, hipStream_t stream) {
+int launch_few(const WindowArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
-    static_assert(kLds <= 65536, "above, the limit would have to be raised");
     static_assert(kTurnBytes <= 16 * R * (kPad + 2) * 4, "a wave's packed tile fits its part of the join's");
     const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
     const dim3 grid(groups + fill_groups(a)), block(64 * WAVES);
     // (32-bit offsets of a page's rows)
     const bool pages = !FP4 && a.kv.block_size % 16 == 0 && a.kv.page_stride < (1 << 24);
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups); };
-    if (a.tq.softcap > 0.0f)
-        pages ? go(window_few_kernel<R, WAVES, true, FP4, !FP4>) : go(window_few_kernel<R, WAVES, true, FP4, false>);
-    else
-        pages ? go(window_few_kernel<R, WAVES, false, FP4, !FP4>) : go(window_few_kernel<R, WAVES, false, FP4, false>);
+    auto kernel = a.tq.softcap > 0.0f
+                      ? (pages ? window_few_kernel<R, WAVES, true, FP4, !FP4> : window_few_kernel<R, WAVES, true, FP4, false>)
+                      : (pages ? window_few_kernel<R, WAVES, false, FP4, !FP4> : window_few_kernel<R, WAVES, false, FP4, false>);
+    if (kLds > 65536) {
+        static std::atomic<int> done[4][64] = {};
+        const int which = 2 * (a.tq.softcap > 0.0f) + pages;
+        if (raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, done[which]) != 0) return -1;
+    }
+    hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups);
+    return 0;
 }
 
 template <int WAVES, bool CAP, bool FP4>
@@ -903,11 +915,8 @@ int launch(const WindowArgs& a, hipStream_t stream) {
     if (a.plan.many)
         return a.plan.waves == 8 ? (capped ? launch_many<8, true, FP4>(a, stream) : launch_many<8, false, FP4>(a, stream))
                                  : (capped ? launch_many<4, true, FP4>(a, stream) : launch_many<4, false, FP4>(a, stream));
-    if (a.plan.waves == 8)
-        launch_few<1, 8, FP4>(a, stream);
-    else
-        a.plan.q_tiles == 1 ? launch_few<1, 4, FP4>(a, stream) : launch_few<2, 4, FP4>(a, stream);
-    return 0;
+    if (a.plan.waves == 8) return a.plan.q_tiles == 1 ? launch_few<1, 8, FP4>(a, stream) : launch_few<2, 8, FP4>(a, stream);
+    return a.plan.q_tiles == 1 ? launch_few<1, 4, FP4>(a, stream) : launch_few<2, 4, FP4>(a, stream);
 }
 
 }  // namespace
@@ -950,7 +959,7 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
         splits = groups >= at_once ? 1 : (2 * at_once + groups - 1) / groups;
         most = tiles / 4;
     } else {
-        if (p.q_tiles == 1 && tiles <= 64 && base <= num_cus) {
+        if (tiles <= 64 && base <= num_cus) {
             p.waves = 8;  // short and few: no second launch
             return p;
         }
