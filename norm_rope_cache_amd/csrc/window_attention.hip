@@ -207,18 +207,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
         return;
     }
     typedef typename RawOf<FP4>::T Raw;
-    constexpr int kAhead = FP4 ? 4 : 2;  // tiles of a wave in registers
+    // tiles of a wave in registers (8 waves: all that they have, of a short window)
+    constexpr int kAhead = FP4 || WAVES == 8 ? 4 : 2;
     const PagedCache& kv = a.kv;
     const TreeQueries& tq = a.tq;
     const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t g = lane >> 4, n16 = lane & 15u;
-    const uint32_t bh = quotient(blockIdx.x, a.by_splits);
-    const int32_t split = (int32_t)(blockIdx.x - bh * a.plan.splits);
+    const uint32_t id = quotient(blockIdx.x, a.by_blocks), bh = quotient(id, a.by_splits);
+    const int32_t row0 = (int32_t)(blockIdx.x - id * a.plan.row_blocks) * 16 * R;
+    const int32_t split = (int32_t)(id - bh * a.plan.splits);
     const int32_t b = (int32_t)quotient(bh, a.by_heads), h = (int32_t)bh - b * tq.H;
     const int32_t* table = kv.tables + (int64_t)b * kv.table_stride;
     const Span s = span_of<kTile>(tq, b);
-    if (s.rows == 0) return;
-    const Keyspan span = keyspan(a, s, 0, s.rows - 1);
+    if (row0 >= s.rows) return;
+    const Keyspan span = keyspan(a, s, row0, row0 + 16 * R - 1);
     const Tiles tiles = tiles_of<kTile>(span, a.sinks);
     const int32_t share = a.plan.share, first = split * share;
     if (first >= tiles.n) return;  // (nor does the join look at such a share)
@@ -282,7 +284,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
             }
             return (there >> (2 * i) & 1u ? 0xFFFFu : 0u) | (there >> (2 * i + 1) & 1u ? 0xFFFF0000u : 0u);
         } else {
-            load_keys(raw, reinterpret_cast<const uint16_t*>(head), is ? (int64_t)page * kv.block_stride + (int64_t)at * kv.page_stride : -1, lane);
+            // a key's cell, from the lane that holds its place
+            const uint64_t cell = (uint64_t)(uintptr_t)(base + (int64_t)at * kv.page_stride * 2);
+            auto of_key = [&](uint32_t k) {
+                const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(k << 2), (int)(uint32_t)cell);
+                const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute((int)(k << 2), (int)(uint32_t)(cell >> 32));
+                return reinterpret_cast<const uint16_t*>((uintptr_t)((uint64_t)hi << 32 | lo));
+            };
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint16_t* k = of_key(16 * t + n16);
+                raw.k[t][0] = load16(k + 8 * g);
+                raw.k[t][1] = load16(k + 32 + 8 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    raw.v[4 * t + r] = *reinterpret_cast<const uint2*>(of_key(16 * t + 4 * g + r) + kHeadDim + 4 * n16);
+            }
             return (uint32_t)there;
         }
     };
@@ -291,7 +308,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     Row row[R];
 #pragma unroll
     for (int rq = 0; rq < R; ++rq) {
-        const int32_t r = 16 * rq + (int32_t)n16;
+        const int32_t r = row0 + 16 * rq + (int32_t)n16;
         row[rq] = row_of(a, s, r);
         w.q[rq][0] = w.q[rq][1] = U32x4{0u, 0u, 0u, 0u};
         if (row[rq].node >= 0) {
@@ -434,7 +451,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
                      a.part + (a.plan.splits * kHeadDim + 2 * split) * rows_all, a.plan.splits == 1};
     for (int32_t e = threadIdx.x; e < 16 * R * 16; e += 64 * WAVES) {
         const int32_t r = e >> 4, d = (e & 15) * 4;
-        if (r >= s.rows) continue;
+        if (row0 + r >= s.rows) continue;
         float top = -__builtin_inff();
 #pragma unroll
         for (int k = 0; k < WAVES; ++k) top = __builtin_fmaxf(top, sm[k * 16 * R + r]);
@@ -449,8 +466,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(p[i], x, o[i]);
         }
-        const int32_t node = (int32_t)quotient((uint32_t)r, a.by_group);
-        put_row4(to, (int64_t)(s.nodes.first + node) * heads + h * tq.G + (r - node * tq.G), d, top, l, o);
+        const int32_t node = (int32_t)quotient((uint32_t)(row0 + r), a.by_group);
+        put_row4(to, (int64_t)(s.nodes.first + node) * heads + h * tq.G + (row0 + r - node * tq.G), d, top, l, o);
     }
 }
 
@@ -879,23 +896,18 @@ uint32_t fill_groups(const WindowArgs& a) {
 }
 
 template <int R, int WAVES, bool FP4>
-int launch_few(const WindowArgs& a, hipStream_t stream) {
+void launch_few(const WindowArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
+    static_assert(kLds <= 65536, "above, the limit would have to be raised");
     static_assert(kTurnBytes <= 16 * R * (kPad + 2) * 4, "a wave's packed tile fits its part of the join's");
-    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits;
+    const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits * a.plan.row_blocks;
     const dim3 grid(groups + fill_groups(a)), block(64 * WAVES);
     // (32-bit offsets of a page's rows)
     const bool pages = !FP4 && a.kv.block_size % 16 == 0 && a.kv.page_stride < (1 << 24);
     auto kernel = a.tq.softcap > 0.0f
                       ? (pages ? window_few_kernel<R, WAVES, true, FP4, !FP4> : window_few_kernel<R, WAVES, true, FP4, false>)
                       : (pages ? window_few_kernel<R, WAVES, false, FP4, !FP4> : window_few_kernel<R, WAVES, false, FP4, false>);
-    if (kLds > 65536) {
-        static std::atomic<int> done[4][64] = {};
-        const int which = 2 * (a.tq.softcap > 0.0f) + pages;
-        if (raise_lds_limit(reinterpret_cast<const void*>(kernel), kLds, done[which]) != 0) return -1;
-    }
     hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups);
-    return 0;
 }
 
 template <int WAVES, bool CAP, bool FP4>
@@ -915,8 +927,11 @@ int launch(const WindowArgs& a, hipStream_t stream) {
     if (a.plan.many)
         return a.plan.waves == 8 ? (capped ? launch_many<8, true, FP4>(a, stream) : launch_many<8, false, FP4>(a, stream))
                                  : (capped ? launch_many<4, true, FP4>(a, stream) : launch_many<4, false, FP4>(a, stream));
-    if (a.plan.waves == 8) return a.plan.q_tiles == 1 ? launch_few<1, 8, FP4>(a, stream) : launch_few<2, 8, FP4>(a, stream);
-    return a.plan.q_tiles == 1 ? launch_few<1, 4, FP4>(a, stream) : launch_few<2, 4, FP4>(a, stream);
+    if (a.plan.waves == 8)
+        launch_few<1, 8, FP4>(a, stream);
+    else
+        a.plan.q_tiles == 1 ? launch_few<1, 4, FP4>(a, stream) : launch_few<2, 4, FP4>(a, stream);
+    return 0;
 }
 
 }  // namespace
@@ -959,8 +974,11 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
         splits = groups >= at_once ? 1 : (2 * at_once + groups - 1) / groups;
         most = tiles / 4;
     } else {
-        if (tiles <= 64 && base <= num_cus) {
-            p.waves = 8;  // short and few: no second launch
+        if (tiles <= 64 && p.q_tiles * base <= num_cus) {
+            // short and few: no second launch, and 16 rows a workgroup, whose waves then have room for all their tiles
+            p.waves = 8;
+            p.row_blocks = p.q_tiles;
+            p.q_tiles = 1;
             return p;
         }
         // until there are several workgroups per CU, each of at least 4 tiles a wave: over a window, of about equal lengths, 2;
