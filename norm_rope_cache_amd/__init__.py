@@ -1057,7 +1057,8 @@ def _get_norm_rotation():
 def _heads(t, name, code, dev, shape=None):
     """Checks of a [T, H, d] tensor with unit last stride: its pointer, row and head strides."""
     torch = _torch or _get_torch()
-    _at(t, dev, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _at(t, dev, name)
     st = t.stride()
     if t.dim() != 3 or st[2] != 1 and t.shape[2] != 1 or shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {'[T, H, d]' if shape is None else list(shape)} with unit last stride")
@@ -1122,7 +1123,9 @@ def qk_norm_rotate(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1
     gains that require grad get their gradients (qk_norm_rotate_grad, on the current
     stream of the backward pass); such a call takes no outputs, and cos_sin gets none."""
     torch = _torch or _get_torch()
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight, cos_sin)):
+    if ((q.requires_grad or cos_sin.requires_grad or k is not None and k.requires_grad
+         or q_weight is not None and q_weight.requires_grad or k_weight is not None and k_weight.requires_grad)
+            and torch.is_grad_enabled()):
         if cos_sin.requires_grad:
             raise ValueError("cos_sin gets no gradient: detach it")
         if out_q is not None or out_k is not None:
@@ -1137,10 +1140,15 @@ def qk_norm_rotate(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1
     flags = 0
     if out_q is None:
         flags = ROPE_PASS_OUTSIDE
+        d = q.shape[2]
         out_q = _empty(q.shape, q.dtype, q.device, stream)
-        out_k = None if k is None else _empty(k.shape, k.dtype, k.device, stream)
-    oq = _heads(out_q, "out_q", code, dev, q.shape)
-    ok = (None, 0, 0) if k is None else _heads(out_k, "out_k", code, dev, k.shape)
+        oq, ok = (out_q.data_ptr(), q.shape[1] * d, d), (None, 0, 0)
+        if k is not None:
+            out_k = _empty(k.shape, k.dtype, q.device, stream)
+            ok = out_k.data_ptr(), k.shape[1] * d, d
+    else:
+        oq = _heads(out_q, "out_q", code, dev, q.shape)
+        ok = (None, 0, 0) if k is None else _heads(out_k, "out_k", code, dev, k.shape)
     _call(q, _load().nrc_qk_norm_rotate, *args, *oq, *ok, flags, _stream(stream, q))
     return out_q, out_k
 
@@ -1540,7 +1548,7 @@ def fp4_page_bytes(block_size):
 def _fp4_block_size(page_bytes):
     """The block_size whose pages have so many bytes."""
     bs = page_bytes // 68
-    if bs < 1 or page_bytes != (68 * bs + 15) // 16 * 16:
+    if bs < 1 or page_bytes != (68 * bs + 15 & ~15):
         raise ValueError(f"pages of {page_bytes} bytes: a cache of 4 bits has fp4_page_bytes(block_size)")
     return bs
 
@@ -1565,25 +1573,30 @@ def _fp4_caches(caches):
 def _fp4_rows(t, name, dev, shape):
     """Checks of [L, T, H, 64] (or [T, H, 64]) rows; pointer and strides."""
     torch = _torch or _get_torch()
-    _at(t, dev, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _at(t, dev, name)
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, not {t.dtype}")
     own, st = t.shape, t.stride()
     if len(own) == 3:
         own, st = (1, *own), (0, *st)
-    if tuple(own) != shape or st[3] != 1:
+    if own != shape or st[3] != 1:
         raise ValueError(f"{name} must be {list(shape)} with unit last stride")
-    return t.data_ptr(), *(s if n > 1 else 0 for s, n in zip(st[:3], shape))
+    L, T, H, _ = shape
+    # (one of a kind has no stride)
+    return t.data_ptr(), st[0] if L > 1 else 0, st[1] if T > 1 else 0, st[2] if H > 1 else 0
 
 
 def _fp4_slots(slots, dev, L):
     torch = _torch or _get_torch()
-    _at(slots, dev, "slots")
-    if slots.dtype != torch.int64 or slots.dim() not in (1, 2) or slots.dim() == 2 and slots.shape[0] != L:
+    if not isinstance(slots, torch.Tensor) or slots.get_device() != dev:
+        _at(slots, dev, "slots")
+    shape, st = slots.shape, slots.stride()
+    if slots.dtype != torch.int64 or len(shape) not in (1, 2) or len(shape) == 2 and shape[0] != L:
         raise ValueError("slots must be an int64 [T] or [L, T] tensor")
-    if slots.shape[-1] > 1 and slots.stride(-1) != 1:
+    if shape[-1] > 1 and st[-1] != 1:
         raise ValueError("slots must have unit last stride")
-    return slots.shape[-1], (slots.data_ptr(), slots.stride(0) if slots.dim() == 2 and L > 1 else 0)
+    return shape[-1], (slots.data_ptr(), st[0] if len(shape) == 2 and L > 1 else 0)
 
 
 def context_fp4_store(k, v, slots, caches, stream=None):
@@ -1621,9 +1634,12 @@ def context_fp4_load(caches, slots, out_k=None, out_v=None, stream=None):
         shape = (L, T, H, HEAD_DIM) if caches.dim() == 4 else (T, H, HEAD_DIM)
         out_k, out_v = (_empty(shape, torch.bfloat16, caches.device, stream) for _ in range(2))
         flags = FP4_FILL
-    shape = (L, T, H, HEAD_DIM)
-    _call(caches, _load().nrc_context_fp4_load, *pages, *at, T, H, L, *_fp4_rows(out_k, "out_k", dev, shape),
-          *_fp4_rows(out_v, "out_v", dev, shape), flags, _stream(stream, caches))
+        ks = out_k.data_ptr(), T * H * HEAD_DIM, H * HEAD_DIM, HEAD_DIM
+        vs = out_v.data_ptr(), T * H * HEAD_DIM, H * HEAD_DIM, HEAD_DIM
+    else:
+        shape = (L, T, H, HEAD_DIM)
+        ks, vs = _fp4_rows(out_k, "out_k", dev, shape), _fp4_rows(out_v, "out_v", dev, shape)
+    _call(caches, _load().nrc_context_fp4_load, *pages, *at, T, H, L, *ks, *vs, flags, _stream(stream, caches))
     return out_k, out_v
 
 
