@@ -1042,6 +1042,7 @@ def _get_norm_rotation():
             return qk_norm_rotate(q, k, positions, cos_sin, q_weight, k_weight, eps, layout, stream=stream)
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, grad_q, grad_k):
             q, k, q_weight, k_weight, positions, cos_sin = ctx.saved_tensors
             # (a gradient of a sum is one value for all: no unit stride)
@@ -1121,7 +1122,8 @@ def qk_norm_rotate(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1
     out_q, out_k  q or k itself, or a tensor apart from both (default: new ones)
     x w / sqrt(mean x^2 + eps), turned, in float32 and rounded once. Inputs and
     gains that require grad get their gradients (qk_norm_rotate_grad, on the current
-    stream of the backward pass); such a call takes no outputs, and cos_sin gets none."""
+    stream of the forward call; once: second derivatives raise); such a call takes no
+    outputs, and cos_sin gets none."""
     torch = _torch or _get_torch()
     if ((q.requires_grad or cos_sin.requires_grad or k is not None and k.requires_grad
          or q_weight is not None and q_weight.requires_grad or k_weight is not None and k_weight.requires_grad)

@@ -237,3 +237,38 @@ def test_calls_at_once(nrc):
     for pair in got:
         for g, w in zip(pair, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_a_captured_training_step(nrc):
+    """Forward and backward with gains captured and replayed on new inputs; a second derivative raises instead of being
+    silently incomplete."""
+    gen = torch.Generator().manual_seed(5)
+    new = lambda *shape: torch.randn(*shape, generator=gen).bfloat16().cuda()
+    T, cs, pos = 70, nrc.rope_table(100, 64), torch.arange(70).cuda()
+    q, k, qw, kw, gq, gk = new(T, 8, 64), new(T, 2, 64), new(64), new(64), new(T, 8, 64), new(T, 2, 64)
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (q, k, qw, kw)]
+        outs = nrc.qk_norm_rotate(leaves[0], leaves[1], pos, cs, leaves[2], leaves[3])
+        return [t.detach() for t in outs] + list(torch.autograd.grad(outs, leaves, [gq, gk]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(3):
+        q.copy_(new(T, 8, 64)), gk.copy_(new(T, 2, 64)), qw.copy_(new(64))
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, step()))
+    leaf = q.float().requires_grad_()
+    out, _ = nrc.qk_norm_rotate(leaf, None, pos, cs)
+    grad, = torch.autograd.grad(out.square().sum(), leaf, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        grad.sum().backward()
