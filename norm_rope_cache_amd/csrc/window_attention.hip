@@ -587,26 +587,48 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         if (quarter == 0) present[buf * kStage + own_key] = there;
     };
 
-    // this lane's places in a stage
-    const uint32_t k_at = n32 * 128, k_c = n32 & 7u, t16 = lane & 15u;
-    const uint32_t v_at = kStage * 128 + (4 * hl + (t16 >> 2)) * 128 +
-                          ((2 * (lane >> 4 & 1u) + (t16 >> 1 & 1u)) ^ (t16 >> 3) << 2) * 16 + (t16 & 1u) * 8;
-    auto read_k = [&](Keys32& k, int buf, int sub) {
-        const uint8_t* at = lds + buf * (kStage * 256) + sub * 4096 + k_at;
+    // This lane's places in a stage, as addresses in LDS: all that the whole tiles' loop adds to them are constants, which
+    // the reads carry (worked out at every read they were a seventh of its vector instructions).
+    struct Places {
+        uint32_t k[4], v[2];
+        __device__ __forceinline__ void move(uint32_t by) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) k.k[i] = load16(at + (((2 * i + hl) ^ k_c) << 4));
+            for (uint32_t& x : k) x += by;
+#pragma unroll
+            for (uint32_t& x : v) x += by;
+        }
+    } places;
+    {
+        const uint32_t t16 = lane & 15u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) places.k[i] = lds0 + n32 * 128 + (((2 * i + hl) ^ (n32 & 7u)) << 4);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            places.v[c] = lds0 + ((kStage * 128 + (4 * hl + (t16 >> 2)) * 128 +
+                                   ((2 * (lane >> 4 & 1u) + (t16 >> 1 & 1u)) ^ (t16 >> 3) << 2) * 16 + (t16 & 1u) * 8) ^ c * 64);
+    }
+    auto place_of = [&](int buf, int sub) {
+        Places p = places;
+        p.move(buf * (kStage * 256) + sub * 4096);
+        return p;
     };
-    auto read_v = [&](Keys32& k, int buf, int sub) {
-        const uint32_t at = buf * (kStage * 256) + sub * 4096;
-        auto four = [&](uint32_t o) {
-            typedef __attribute__((address_space(3))) i16x4 LdsFour;
-            return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsFour*)(uintptr_t)(lds0 + o)));
-        };
+    auto read_k = [&](Keys32& k, const Places& p, int sub) {
+        typedef __attribute__((address_space(3))) const U32x4 Lds;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Lds* from = (Lds*)(uintptr_t)p.k[i] + 256 * sub;
+            k.k[i] = U32x4{from->x, from->y, from->z, from->w};
+        }
+    };
+    auto read_v = [&](Keys32& k, const Places& p, int sub) {
+        typedef __attribute__((address_space(3))) i16x4 LdsFour;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const uint2 a = four(at + (v_at ^ c * 64) + ks * 2048), z = four(at + (v_at ^ c * 64) + ks * 2048 + 1024);
+                LdsFour* from = (LdsFour*)(uintptr_t)p.v[c] + 512 * sub + 256 * ks;
+                const uint2 a = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(from)),
+                            z = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(from + 128));
                 k.v[c][ks] = U32x4{a.x, a.y, z.x, z.y};
             }
     };
@@ -630,8 +652,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     auto masked = [&](int buf, int sub, int32_t key0, uint32_t keys_there) {
         Keys32 k;
         const uint32_t sees = bits_of_scores(keys_there & row_sees(tq, s, row, a.sinks, key0), hl);
-        read_k(k, buf, sub);
-        read_v(k, buf, sub);
+        const Places p = place_of(buf, sub);
+        read_k(k, p, 0);
+        read_v(k, p, 0);
         bool odd = false;  // infinities and NaN in V: see add_odd
         if constexpr (!FP4) {
             u16x2 most{0, 0};
@@ -651,7 +674,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         scores32<1>(sc, w, 0, k);
         add32<1, CAP, true>(w, 0, sc, k, f, sees);
         if (!odd) return;
-        read_v(k, buf, sub);
+        read_v(k, p, 0);
 #pragma unroll 1
         for (int kind = 0; kind < 3; ++kind) {
             const float adds = kind == 0 ? __builtin_inff() : kind == 1 ? -__builtin_inff() : __builtin_nanf("");
@@ -695,14 +718,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         if (from < upto) {
             Keys32 k;
             f32x16 sc[2];
-            read_k(k, buf, from);
+            Places p = place_of(buf, from);
+            read_k(k, p, 0);
             scores32<1>(sc[0], w, 0, k);
             auto step = [&](int32_t sub, f32x16& own, f32x16& next) {
-                read_v(k, buf, sub);
+                read_v(k, p, 0);
                 if (sub + 1 < upto) {
-                    read_k(k, buf, sub + 1);
+                    read_k(k, p, 1);
                     scores32<1>(next, w, 0, k);
                 }
+                p.move(4096);
                 add32<1, CAP, false>(w, 0, own, k, f, 0u);
             };
 #pragma unroll 1
@@ -762,9 +787,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         Keys32 k;
         f32x16 sc[2];
         if (active) {
-            read_k(k, 0, 0);
+            read_k(k, places, 0);
             scores32<1>(sc[0], w, 0, k);
         }
+        Places p = places;
 #pragma unroll 1
         for (int32_t i = 0; i < whole; ++i) {
             const int buf = i & 1;
@@ -772,9 +798,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             if (active) {
 #pragma unroll
                 for (int sub = 0; sub < kSubs; ++sub) {
-                    read_v(k, buf, sub);
+                    read_v(k, p, sub);
                     if (sub + 1 < kSubs) {
-                        read_k(k, buf, sub + 1);
+                        read_k(k, p, sub + 1);
                         scores32<1>(sc[(sub + 1) % 2], w, 0, k);
                         add32<1, CAP, false>(w, 0, sc[sub % 2], k, f, 0u);
                     }
@@ -782,9 +808,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             }
             if (i + 1 < count) put(buf ^ 1);  // (nobody reads it since the last barrier)
             __syncthreads();
+            p.move(buf ? -(kStage * 256) : kStage * 256);
             if (active) {
                 if (i + 1 < whole) {
-                    read_k(k, buf ^ 1, 0);
+                    read_k(k, p, 0);
                     scores32<1>(sc[0], w, 0, k);
                 }
                 add32<1, CAP, false>(w, 0, sc[1], k, f, 0u);
@@ -959,8 +986,8 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     if (p.many) {
         const int64_t at_once = num_cus * (p.waves == 8 ? 1 : 2), groups = base * p.row_blocks;
         p.groups = (int32_t)base;
-        if (ragged && B <= 512) {
-            // shares by the lengths, in one or two rounds of what the chip holds at once
+        if (ragged && B <= 512 && base * tiles < (int64_t)1 << 31) {
+            // shares by the lengths (counted in 32 bits), in one or two rounds of what the chip holds at once
             const int64_t round = at_once / p.row_blocks, rounds = round >= 2 * base ? 1 : 2;
             if (rounds * round >= 2 * base && tiles > 4) {
                 p.by_lengths = true;
