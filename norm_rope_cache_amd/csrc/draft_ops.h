@@ -89,7 +89,7 @@ struct WindowArgs {
     float* part;      // splits > 1: the partial sums' rows, [., 64] then [., 2]
     int32_t* shares;  // by_lengths: [B, 3], each sequence's first group, its shares and their tiles
     WindowPlan plan;
-    Div by_group, by_heads, by_splits, by_blocks;  // tq.G, tq.H, plan.splits, plan.row_blocks
+    Div by_group, by_heads, by_splits, by_blocks, by_block;  // tq.G, tq.H, plan.splits, plan.row_blocks, kv.block_size
     uint32_t fill;                                 // NRC_ATTENTION_FILL_*
 };
 

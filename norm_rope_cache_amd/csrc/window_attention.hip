@@ -481,7 +481,9 @@ template <int WAVES>
 constexpr int stage_of() { return 16 * WAVES; }
 constexpr int many_lds(int waves) { return 2 * 16 * waves * (256 + 4); }
 
-template <int WAVES, bool CAP, bool FP4>
+// PAGES (block_size a multiple of 16, so that a wave's 16 keys of a stage lie in one page): where the tiles that every row sees
+// whole lie is scalar work, and a lane adds its own place in 16 cells, which is always the same.
+template <int WAVES, bool CAP, bool FP4, bool PAGES>
 __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a, uint32_t groups, uint32_t grid) {
     if (blockIdx.x >= grid) {
         fill_rows(a.tq, a.fill, a.out, a.lse, blockIdx.x - grid, gridDim.x - grid);
@@ -565,8 +567,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             for (int i = 0; i < 4; ++i) cell[i] = load16(own + 16 * i);
         }
     };
+    const uint32_t swizzle = quarter < 2 ? own_key & 7u : (own_key >> 1 & 1u) << 2;
     auto put = [&](int buf) {
-        const uint32_t swizzle = quarter < 2 ? own_key & 7u : (own_key >> 1 & 1u) << 2;
         uint8_t* at = lds + buf * (kStage * 256) + (quarter >> 1) * (kStage * 128) + own_key * 128;
         if (!there) {
 #pragma unroll
@@ -782,6 +784,39 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     put(0);
     __syncthreads();
     if (whole > 0) {
+        // Where the whole tiles' keys come from and go to (PAGES): the wave's first key of tile i, a lane's place in 16 cells and in
+        // a stage. Such keys are there, and V's scales need not be held.
+        const int32_t key0 = __builtin_amdgcn_readfirstlane(tiles.key(whole0 * kStage) + 16 * (int32_t)wave);
+        const uint32_t in16 = lane >> 2, own = FP4 ? in16 * kFp4Codes + (quarter >> 1) * codes + (quarter & 1u) * 16
+                                                   : in16 * 2 * (uint32_t)kv.page_stride + 64 * quarter;
+        uint32_t put_at[4];
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            put_at[i] = lds0 + (quarter >> 1) * (kStage * 128) + own_key * 128 + ((4 * (quarter & 1u) + i) ^ swizzle) * 16;
+        auto whole_entry = [&](int32_t i) {
+            return (uint32_t)table[quotient((uint32_t)(key0 + i * kStage), a.by_block)];
+        };
+        auto whole_fetch = [&](int32_t i, uint32_t page) {
+            const uint32_t key = (uint32_t)(key0 + i * kStage), cell_at = key - quotient(key, a.by_block) * kv.block_size;
+            const uint8_t* base = head + (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * kv.block_stride * (FP4 ? 1 : 2);
+            if constexpr (FP4) {
+                cell[0] = load16(base + cell_at * kFp4Codes + own);
+                scales = *reinterpret_cast<const uint32_t*>(base + 2 * codes + 4 * cell_at + 4 * in16);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) cell[c] = load16(base + (int64_t)cell_at * kv.page_stride * 2 + own + 16 * c);
+            }
+        };
+        auto whole_put = [&](int buf) {
+            typedef __attribute__((address_space(3))) U32x4 Lds;
+            const float scale = __uint_as_float(__builtin_amdgcn_alignbit(scales, scales, 8 * quarter + 9));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const U32x4 v = FP4 ? fp4_open((&cell[0].x)[i], scale) : cell[FP4 ? 0 : i];
+                Lds* to = (Lds*)(uintptr_t)(put_at[i] + buf * (kStage * 256));
+                to->x = v.x, to->y = v.y, to->z = v.z, to->w = v.w;
+            }
+        };
         // One 32 keys' scores are on the way in the matrix cores while the vector unit takes the last ones' exponentials,
         // over the barrier too: a tile's last weights are taken behind it, with the next one's first scores on the way.
         Keys32 k;
@@ -794,7 +829,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
 #pragma unroll 1
         for (int32_t i = 0; i < whole; ++i) {
             const int buf = i & 1;
-            bring(i + 1);
+            if (PAGES && i + 1 < whole) {
+                page = after;
+                after = i + 2 < whole ? whole_entry(i + 2) : entry(number(i + 2));
+                whole_fetch(i + 1, page);
+            } else {
+                bring(i + 1);
+            }
             if (active) {
 #pragma unroll
                 for (int sub = 0; sub < kSubs; ++sub) {
@@ -806,7 +847,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
                     }
                 }
             }
-            if (i + 1 < count) put(buf ^ 1);  // (nobody reads it since the last barrier)
+            if (PAGES && i + 1 < whole)
+                whole_put(buf ^ 1);  // (nobody reads it since the last barrier)
+            else if (i + 1 < count)
+                put(buf ^ 1);
             __syncthreads();
             p.move(buf ? -(kStage * 256) : kStage * 256);
             if (active) {
@@ -922,6 +966,9 @@ uint32_t fill_groups(const WindowArgs& a) {
     return (uint32_t)(n < 1024 ? n : 1024);
 }
 
+// Do 16 neighbouring keys lie in one page, with 32-bit offsets between its rows?
+bool in_pages(const WindowArgs& a, bool fp4) { return a.kv.block_size % 16 == 0 && (fp4 || a.kv.page_stride < (1 << 24)); }
+
 template <int R, int WAVES, bool FP4>
 void launch_few(const WindowArgs& a, hipStream_t stream) {
     constexpr int kLds = WAVES * 16 * R * (kPad + 2) * 4;
@@ -929,31 +976,33 @@ void launch_few(const WindowArgs& a, hipStream_t stream) {
     static_assert(kTurnBytes <= 16 * R * (kPad + 2) * 4, "a wave's packed tile fits its part of the join's");
     const uint32_t groups = (uint32_t)a.tq.B * a.tq.H * a.plan.splits * a.plan.row_blocks;
     const dim3 grid(groups + fill_groups(a)), block(64 * WAVES);
-    // (32-bit offsets of a page's rows)
-    const bool pages = !FP4 && a.kv.block_size % 16 == 0 && a.kv.page_stride < (1 << 24);
+    const bool pages = !FP4 && in_pages(a, FP4);
     auto kernel = a.tq.softcap > 0.0f
                       ? (pages ? window_few_kernel<R, WAVES, true, FP4, !FP4> : window_few_kernel<R, WAVES, true, FP4, false>)
                       : (pages ? window_few_kernel<R, WAVES, false, FP4, !FP4> : window_few_kernel<R, WAVES, false, FP4, false>);
     hipLaunchKernelGGL(kernel, grid, block, kLds, stream, a, groups);
 }
 
-template <int WAVES, bool CAP, bool FP4>
+template <int WAVES, bool CAP, bool FP4, bool PAGES>
 int launch_many(const WindowArgs& a, hipStream_t stream) {
     const uint32_t groups = (uint32_t)a.plan.groups;
     const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
-    auto kernel = window_many_kernel<WAVES, CAP, FP4>;
+    auto kernel = window_many_kernel<WAVES, CAP, FP4, PAGES>;
     static std::atomic<int> done[64] = {};
     if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
     hipLaunchKernelGGL(kernel, dim3(grid + fill_groups(a)), dim3(64 * WAVES), many_lds(WAVES), stream, a, groups, grid);
     return 0;
 }
+template <int WAVES, bool FP4>
+int launch_many(const WindowArgs& a, hipStream_t stream) {
+    if (in_pages(a, FP4))
+        return a.tq.softcap > 0.0f ? launch_many<WAVES, true, FP4, true>(a, stream) : launch_many<WAVES, false, FP4, true>(a, stream);
+    return a.tq.softcap > 0.0f ? launch_many<WAVES, true, FP4, false>(a, stream) : launch_many<WAVES, false, FP4, false>(a, stream);
+}
 
 template <bool FP4>
 int launch(const WindowArgs& a, hipStream_t stream) {
-    const bool capped = a.tq.softcap > 0.0f;
-    if (a.plan.many)
-        return a.plan.waves == 8 ? (capped ? launch_many<8, true, FP4>(a, stream) : launch_many<8, false, FP4>(a, stream))
-                                 : (capped ? launch_many<4, true, FP4>(a, stream) : launch_many<4, false, FP4>(a, stream));
+    if (a.plan.many) return a.plan.waves == 8 ? launch_many<8, FP4>(a, stream) : launch_many<4, FP4>(a, stream);
     if (a.plan.waves == 8)
         launch_few<1, 8, FP4>(a, stream);
     else
@@ -1032,6 +1081,7 @@ int64_t window_attention_workspace(const WindowPlan& p, int64_t T, int64_t heads
 int launch_window_attention(const WindowArgs& args, hipStream_t stream) {
     WindowArgs a = args;
     a.by_group = div_by((uint32_t)a.tq.G), a.by_heads = div_by((uint32_t)a.tq.H);
+    a.by_block = div_by(a.kv.block_size);
     a.by_splits = div_by((uint32_t)a.plan.splits), a.by_blocks = div_by((uint32_t)a.plan.row_blocks);
     if (a.tq.B == 0) {
         hipLaunchKernelGGL(window_fill_kernel, dim3(fill_groups(a)), dim3(256), 0, stream, a.tq, a.fill, a.out, a.lse);
