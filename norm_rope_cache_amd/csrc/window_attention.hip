@@ -21,6 +21,7 @@
 // Few rows a KV head (up to 32) are bound by the cache's bytes and, in 4 bits, by
 // the instructions that open them; many rows by the vector unit and the matrix cores.
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/nrc.h"
 #include "attention_core.h"
@@ -817,8 +818,25 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
                 to->x = v.x, to->y = v.y, to->z = v.z, to->w = v.w;
             }
         };
+        // add32 for them, its products in the order in which neighbours do not wait for each other.
+        auto add_whole = [&](f32x16& s, const Keys32& k) {
+            U32x4 pb[2];
+            float sum = weights32<CAP, false>(s, w.base[0], CAP ? f.c : w.c[0], f.capped, 0u, pb);
+            if (__any(!(sum <= kMost))) {
+                raise32<1, CAP>(w, 0, s, f.c, f.capped);
+                sum = weights32<CAP, false>(s, w.base[0], CAP ? f.c : w.c[0], f.capped, 0u, pb);
+            }
+            w.l[0] += sum;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) w.o[0][c] = mfma32(k.v[c][ks], pb[ks], w.o[0][c]);
+        };
         // One 32 keys' scores are on the way in the matrix cores while the vector unit takes the last ones' exponentials,
         // over the barrier too: a tile's last weights are taken behind it, with the next one's first scores on the way.
+        // The stage's last part goes ahead of the other workgroup's waves, so that this one's reach their barrier together; the
+        // phases are kept apart (trees of 48 nodes over 65536 packed keys 214 us; with the phases mixed by the compiler, which
+        // then puts matrix instructions behind each other, 274).
         Keys32 k;
         f32x16 sc[2];
         if (active) {
@@ -826,16 +844,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             scores32<1>(sc[0], w, 0, k);
         }
         Places p = places;
-#pragma unroll 1
-        for (int32_t i = 0; i < whole; ++i) {
+        auto tile = [&](int32_t i, auto inner) {  // inner: the next one is such a tile too, and its cells are PAGES'
+            constexpr bool kInner = decltype(inner)::value;
             const int buf = i & 1;
-            if (PAGES && i + 1 < whole) {
+            if constexpr (kInner) {
                 page = after;
                 after = i + 2 < whole ? whole_entry(i + 2) : entry(number(i + 2));
                 whole_fetch(i + 1, page);
             } else {
                 bring(i + 1);
             }
+            __builtin_amdgcn_sched_barrier(0);
             if (active) {
 #pragma unroll
                 for (int sub = 0; sub < kSubs; ++sub) {
@@ -843,24 +862,36 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
                     if (sub + 1 < kSubs) {
                         read_k(k, p, sub + 1);
                         scores32<1>(sc[(sub + 1) % 2], w, 0, k);
-                        add32<1, CAP, false>(w, 0, sc[sub % 2], k, f, 0u);
+                        add_whole(sc[sub % 2], k);
                     }
                 }
             }
-            if (PAGES && i + 1 < whole)
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
+            if constexpr (kInner)
                 whole_put(buf ^ 1);  // (nobody reads it since the last barrier)
             else if (i + 1 < count)
                 put(buf ^ 1);
             __syncthreads();
+            __builtin_amdgcn_s_setprio(0);
+            __builtin_amdgcn_sched_barrier(0);
             p.move(buf ? -(kStage * 256) : kStage * 256);
             if (active) {
-                if (i + 1 < whole) {
+                if (kInner || i + 1 < whole) {
                     read_k(k, p, 0);
                     scores32<1>(sc[0], w, 0, k);
                 }
-                add32<1, CAP, false>(w, 0, sc[1], k, f, 0u);
+                add_whole(sc[1], k);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int32_t i = 0;
+        if constexpr (PAGES) {
+#pragma unroll 1
+            for (; i + 1 < whole; ++i) tile(i, std::true_type{});
         }
+#pragma unroll 1
+        for (; i < whole; ++i) tile(i, std::false_type{});
     }
 #pragma unroll 1
     for (int32_t i = whole; i < count; ++i) {
