@@ -474,23 +474,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
 
 // ---- many rows ----------------------------------------------------------------------------------------------------
 
-// The WAVES waves of a workgroup hold 32 rows each and share the keys, staged as bf16 in LDS 16 WAVES at a time, in two
+// The WAVES waves of a workgroup hold 32 rows each and share the keys, staged as bf16 in LDS 128 at a time, in two
 // buffers: four threads a key bring a quarter of its cell each into registers while the waves work on the tile before, open it
 // where it is packed, and leave it in the other buffer; one barrier a tile. So a key is opened once for all rows of the
 // workgroup. LDS layout and matrix operands as many_rows_kernel of tree_attention.hip.
-template <int WAVES>
-constexpr int stage_of() { return 16 * WAVES; }
-constexpr int many_lds(int waves) { return 2 * 16 * waves * (256 + 4); }
+// Measured: 4 sequences of up to 65536 packed keys, 8 KV heads, 384 rows a head: 202 us, 666 TFLOP/s (with 64 keys a stage of 4 waves, so
+// twice the barriers, 214); two prompts of 4096 tokens, 64 heads, window 1024: 199 us, 548 TFLOP/s. The vector unit is what is
+// busiest (a score's exponential, its product, sum and rounding: of 32 x 32 scores about 60 instructions of a wave to 8 of the matrix
+// cores, which take half as long); a window's short run of tiles also has its first loads and its masked ends to wait for.
+constexpr int kStage = 128;
+constexpr int kManyLds = 2 * kStage * (256 + 4);
 
-// PAGES (block_size a multiple of 16, so that a wave's 16 keys of a stage lie in one page): where the tiles that every row sees
-// whole lie is scalar work, and a lane adds its own place in 16 cells, which is always the same.
+// PAGES (block_size a multiple of 16, so that a wave's 16 keys lie in one page): where the cells of tiles that every row sees
+// whole lie is scalar work, and a lane adds its own place in 16 cells, which is always the same (worked out by each lane 261 us for what takes 241 so; pages of 24 cells 287 us for 512 rows where those of 64 take 257).
 template <int WAVES, bool CAP, bool FP4, bool PAGES>
 __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a, uint32_t groups, uint32_t grid) {
     if (blockIdx.x >= grid) {
         fill_rows(a.tq, a.fill, a.out, a.lse, blockIdx.x - grid, gridDim.x - grid);
         return;
     }
-    constexpr int kStage = stage_of<WAVES>(), kSubs = kStage / 32;
+    constexpr int kSubs = kStage / 32, kCells = kStage / (16 * WAVES);  // cells of a thread's in a stage, every 16 WAVES keys one
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint32_t* present = reinterpret_cast<uint32_t*>(lds + 2 * kStage * 256);  // [2][kStage]
     const PagedCache& kv = a.kv;
@@ -546,48 +549,68 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     const uint32_t codes = kFp4Codes * kv.block_size;  // bytes of a page's K codes
     // A thread's quarter (K's halves, V's halves) of its key's cell.
     const uint32_t own_key = tid >> 2, quarter = tid & 3u;
-    U32x4 cell[FP4 ? 1 : 4];
-    uint32_t scales = 0;
-    bool there = false;
-    auto key_of = [&](int32_t v) {  // in tile number v
-        return (uint32_t)tiles.key(v * kStage + (int32_t)(own_key & ~31u)) + (own_key & 31u);
+    struct Cell {
+        U32x4 part[FP4 ? 1 : 4];
+        uint32_t scales;
+        bool there;
+    } cell[kCells];
+    struct Pages {
+        uint32_t of[kCells];
     };
-    auto entry = [&](int32_t v) { return page_of(kv, table, key_of(v < end ? v : end - 1)); };
-    auto fetch = [&](int32_t v, uint32_t page) {
-        // (a cell that is not there is read from the cache's first page, and dropped)
-        const uint32_t key = key_of(v), blk = block_of(key, kv);
-        there = blk < kv.table_width && page < kv.num_blocks && key < (uint32_t)total;
-        const uint32_t at = there ? key - blk * kv.block_size : 0u;
-        const uint8_t* base = head + (int64_t)(there ? page : 0u) * kv.block_stride * (FP4 ? 1 : 2);
-        if constexpr (FP4) {
-            cell[0] = load16(base + (int64_t)((quarter >> 1) * codes + at * kFp4Codes + (quarter & 1u) * 16));
-            scales = *reinterpret_cast<const uint32_t*>(base + (int64_t)(2 * codes + 4 * at));
-        } else {
-            const uint8_t* own = base + (int64_t)at * kv.page_stride * 2 + 64 * quarter;
+    auto key_of = [&](int32_t v, int c) {  // in tile number v
+        const uint32_t key = own_key + 16 * WAVES * c;
+        return (uint32_t)tiles.key(v * kStage + (int32_t)(key & ~31u)) + (key & 31u);
+    };
+    auto entry = [&](int32_t v) {
+        Pages p;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) cell[i] = load16(own + 16 * i);
+        for (int c = 0; c < kCells; ++c) p.of[c] = page_of(kv, table, key_of(v < end ? v : end - 1, c));
+        return p;
+    };
+    auto fetch = [&](int32_t v, const Pages& pages) {
+#pragma unroll
+        for (int c = 0; c < kCells; ++c) {
+            // (a cell that is not there is read from the cache's first page, and dropped)
+            const uint32_t key = key_of(v, c), blk = block_of(key, kv), page = pages.of[c];
+            const bool is = blk < kv.table_width && page < kv.num_blocks && key < (uint32_t)total;
+            const uint32_t at = is ? key - blk * kv.block_size : 0u;
+            const uint8_t* base = head + (int64_t)(is ? page : 0u) * kv.block_stride * (FP4 ? 1 : 2);
+            cell[c].there = is;
+            if constexpr (FP4) {
+                cell[c].part[0] = load16(base + (int64_t)((quarter >> 1) * codes + at * kFp4Codes + (quarter & 1u) * 16));
+                cell[c].scales = *reinterpret_cast<const uint32_t*>(base + (int64_t)(2 * codes + 4 * at));
+            } else {
+                const uint8_t* own = base + (int64_t)at * kv.page_stride * 2 + 64 * quarter;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cell[c].part[i] = load16(own + 16 * i);
+            }
         }
     };
     const uint32_t swizzle = quarter < 2 ? own_key & 7u : (own_key >> 1 & 1u) << 2;
     auto put = [&](int buf) {
-        uint8_t* at = lds + buf * (kStage * 256) + (quarter >> 1) * (kStage * 128) + own_key * 128;
-        if (!there) {
 #pragma unroll
-            for (U32x4& c : cell) c = U32x4{0u, 0u, 0u, 0u};
-            scales = 0;
+        for (int n = 0; n < kCells; ++n) {
+            Cell& c = cell[n];
+            const uint32_t key = own_key + 16 * WAVES * n;  // (the swizzles are the same)
+            uint8_t* at = lds + buf * (kStage * 256) + (quarter >> 1) * (kStage * 128) + key * 128;
+            if (!c.there) {
+#pragma unroll
+                for (U32x4& x : c.part) x = U32x4{0u, 0u, 0u, 0u};
+                c.scales = 0;
+            }
+            if constexpr (FP4) {
+                uint32_t byte = c.scales >> (8 * quarter) & 0xFFu;
+                if (quarter >= 2) byte = byte < kScaleHigh ? byte : kScaleHigh;  // (V: see the top)
+                const float scale = __uint_as_float(byte << 23);
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i)
+                    store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, fp4_open((&c.part[0].x)[i], scale));
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 4; ++i) store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, c.part[i]);
+            }
+            if (quarter == 0) present[buf * kStage + key] = c.there;
         }
-        if constexpr (FP4) {
-            uint32_t byte = scales >> (8 * quarter) & 0xFFu;
-            if (quarter >= 2) byte = byte < kScaleHigh ? byte : kScaleHigh;  // (V: see the top)
-            const float scale = __uint_as_float(byte << 23);
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i)
-                store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, fp4_open((&cell[0].x)[i], scale));
-        } else {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) store16(at + ((4 * (quarter & 1u) + i) ^ swizzle) * 16, cell[i]);
-        }
-        if (quarter == 0) present[buf * kStage + own_key] = there;
     };
 
     // This lane's places in a stage, as addresses in LDS: all that the whole tiles' loop adds to them are constants, which
@@ -763,7 +786,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     };
     // The tile after the next one's block numbers are on the way before the next one's cells, so that nobody waits for
     // these with those.
-    uint32_t page = entry(number(0)), after = entry(number(1));
+    Pages page = entry(number(0)), after = entry(number(1));
     auto bring = [&](int32_t i) {
         page = after;
         after = entry(number(i + 1));
@@ -795,27 +818,38 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         for (uint32_t i = 0; i < 4; ++i)
             put_at[i] = lds0 + (quarter >> 1) * (kStage * 128) + own_key * 128 + ((4 * (quarter & 1u) + i) ^ swizzle) * 16;
         auto whole_entry = [&](int32_t i) {
-            return (uint32_t)table[quotient((uint32_t)(key0 + i * kStage), a.by_block)];
-        };
-        auto whole_fetch = [&](int32_t i, uint32_t page) {
-            const uint32_t key = (uint32_t)(key0 + i * kStage), cell_at = key - quotient(key, a.by_block) * kv.block_size;
-            const uint8_t* base = head + (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane(page) * kv.block_stride * (FP4 ? 1 : 2);
-            if constexpr (FP4) {
-                cell[0] = load16(base + cell_at * kFp4Codes + own);
-                scales = *reinterpret_cast<const uint32_t*>(base + 2 * codes + 4 * cell_at + 4 * in16);
-            } else {
+            Pages p;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) cell[c] = load16(base + (int64_t)cell_at * kv.page_stride * 2 + own + 16 * c);
+            for (int c = 0; c < kCells; ++c) p.of[c] = (uint32_t)table[quotient((uint32_t)(key0 + i * kStage + 16 * WAVES * c), a.by_block)];
+            return p;
+        };
+        auto whole_fetch = [&](int32_t i, const Pages& pages) {
+#pragma unroll
+            for (int c = 0; c < kCells; ++c) {
+                const uint32_t key = (uint32_t)(key0 + i * kStage + 16 * WAVES * c);
+                const uint32_t cell_at = key - quotient(key, a.by_block) * kv.block_size;
+                const uint32_t page = __builtin_amdgcn_readfirstlane(pages.of[c]);
+                const uint8_t* base = head + (int64_t)page * kv.block_stride * (FP4 ? 1 : 2);
+                if constexpr (FP4) {
+                    cell[c].part[0] = load16(base + cell_at * kFp4Codes + own);
+                    cell[c].scales = *reinterpret_cast<const uint32_t*>(base + 2 * codes + 4 * cell_at + 4 * in16);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) cell[c].part[n] = load16(base + (int64_t)cell_at * kv.page_stride * 2 + own + 16 * n);
+                }
             }
         };
         auto whole_put = [&](int buf) {
             typedef __attribute__((address_space(3))) U32x4 Lds;
-            const float scale = __uint_as_float(__builtin_amdgcn_alignbit(scales, scales, 8 * quarter + 9));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const U32x4 v = FP4 ? fp4_open((&cell[0].x)[i], scale) : cell[FP4 ? 0 : i];
-                Lds* to = (Lds*)(uintptr_t)(put_at[i] + buf * (kStage * 256));
-                to->x = v.x, to->y = v.y, to->z = v.z, to->w = v.w;
+            for (int c = 0; c < kCells; ++c) {
+                const float scale = __uint_as_float(__builtin_amdgcn_alignbit(cell[c].scales, cell[c].scales, 8 * quarter + 9));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const U32x4 v = FP4 ? fp4_open((&cell[c].part[0].x)[i], scale) : cell[c].part[FP4 ? 0 : i];
+                    Lds* to = (Lds*)(uintptr_t)(put_at[i] + buf * (kStage * 256)) + 128 * WAVES * c;
+                    to->x = v.x, to->y = v.y, to->z = v.z, to->w = v.w;
+                }
             }
         };
         // add32 for them, its products in the order in which neighbours do not wait for each other.
@@ -935,7 +969,7 @@ __global__ __launch_bounds__(256) void window_join_kernel(WindowArgs a) {
     if (a.plan.many) {
         const int32_t rows = 32 * a.plan.waves, block0 = r / rows * rows;
         const Keyspan span = keyspan(a, s, block0, block0 + rows - 1);
-        const int32_t n = a.plan.waves == 8 ? tiles_of<stage_of<8>()>(span, a.sinks).n : tiles_of<stage_of<4>()>(span, a.sinks).n;
+        const int32_t n = tiles_of<kStage>(span, a.sinks).n;
         int32_t group = b * tq.H * a.plan.splits, of_head = a.plan.splits, share = a.plan.share;
         if (a.plan.by_lengths) group = a.shares[3 * b], of_head = a.shares[3 * b + 1], share = a.shares[3 * b + 2];
         splits = (n + share - 1) / share;  // (a chain's first rows may end before the sequence's last share)
@@ -1020,8 +1054,8 @@ int launch_many(const WindowArgs& a, hipStream_t stream) {
     const uint32_t grid = a.plan.row_blocks > 1 ? (groups + 7) / 8 * 8 * a.plan.row_blocks : groups;
     auto kernel = window_many_kernel<WAVES, CAP, FP4, PAGES>;
     static std::atomic<int> done[64] = {};
-    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), many_lds(WAVES), done) != 0) return -1;
-    hipLaunchKernelGGL(kernel, dim3(grid + fill_groups(a)), dim3(64 * WAVES), many_lds(WAVES), stream, a, groups, grid);
+    if (raise_lds_limit(reinterpret_cast<const void*>(kernel), kManyLds, done) != 0) return -1;
+    hipLaunchKernelGGL(kernel, dim3(grid + fill_groups(a)), dim3(64 * WAVES), kManyLds, stream, a, groups, grid);
     return 0;
 }
 template <int WAVES, bool FP4>
@@ -1049,11 +1083,13 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     const int64_t rows = (int64_t)max_nodes * G, base = (int64_t)B * H;
     const bool ragged = window == kNoWindow;  // lengths that differ as the contexts do; over a window they are about equal
     p.many = rows > 32;
+    // (512 rows over contexts of up to 65536 packed keys 257 us; in blocks of 128 rows, which open each key twice as often, 283; a
+    // prompt of 8192 tokens behind a window of 2048 377 and 386)
     p.waves = p.many && rows > 128 ? 8 : 4;
     // waves without rows are idle: blocks of 128 rows where those of 256 would be filled to less than four fifths as much
     if (p.waves == 8 && 4 * ((rows + 255) / 256 * 256) > 5 * ((rows + 127) / 128 * 128)) p.waves = 4;
     p.q_tiles = rows <= 16 ? 1 : 2;
-    const int64_t block_rows = p.many ? 32 * p.waves : rows, keys = p.many ? 16 * p.waves : kTile;
+    const int64_t block_rows = p.many ? 32 * p.waves : rows, keys = p.many ? kStage : kTile;
     p.row_blocks = p.many ? (int32_t)((rows + block_rows - 1) / block_rows) : 1;
     // the tiles that a block of rows looks at (a tree's last share takes what there are more)
     int64_t tiles = (max_ctx + max_nodes + keys - 1) / keys;
