@@ -3,7 +3,8 @@
  * DSpark draft: hidden RMSNorm -> per-layer input RMSNorm, stacked -> batched
  * K/V projection -> weightless 64-wide K-norm -> GPT-J RoPE -> paged-cache
  * insert; and of the operators that use the cache: rotary positions,
- * attention of drafted tokens over it, the weight its cells receive, eviction.
+ * attention of drafted tokens over it, the weight its cells receive, eviction;
+ * norms with the rotation, cells of 4 bits, attention over those and behind a window.
  *
  * Sources: the vLLM API pages of the Muse Spark specialized decode,
  *   "...cutedsl.draft.context"       (ContextNorms, ContextKvStore and their kernels),

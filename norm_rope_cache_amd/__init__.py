@@ -24,7 +24,16 @@ and the operators that use the cache the chain fills:
     context_attention_mass(q, cache, tables, ..., lse, ...)   the weight each cached cell receives
     context_kv_evict(cache, tables, lens, weights, ...)       the cells of most weight kept (in place)
 
-Of these rope_rotate records a gradient; the others' outputs carry no graph.
+and those of a drafted token's own queries and keys, of smaller cells and shorter sights:
+
+    qk_norm_rotate(q, k, positions, cos_sin, ...)  heads normed and rotated in one pass
+    qk_norm_rotate_grad(grad_q, grad_k, q, k, ...) its gradients, the gains' among them
+    context_fp4_store(k, v, slots, caches)         rows into a paged cache of 4 bits (in place)
+    context_fp4_load(caches, slots)                its cells' values -> (k, v)
+    context_fp4_attention(q, cache, tables, ...)   context_tree_attention over such a cache
+    context_window_attention(..., window, sinks)   the same behind a sliding window with sinks
+
+Of these rope_rotate and qk_norm_rotate record a gradient; the others' outputs carry no graph.
 """
 
 import ctypes
