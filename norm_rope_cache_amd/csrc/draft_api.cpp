@@ -109,11 +109,8 @@ int32_t fp4_cache(const char* what, const uint8_t* caches, int64_t layer_stride,
     if (num_blocks * block_stride > (int64_t)1 << 60) return fail(NRC_EINVAL, "%s: cache strides too large", what);
     if (need && !caches) return fail(NRC_EINVAL, "%s: NULL cache", what);
     if (!aligned(caches, 16)) return fail(NRC_EINVAL, "%s: the cache must be 16-byte aligned", what);
-    int32_t shift = -1;
-    if ((block_size & (block_size - 1)) == 0)
-        for (shift = 0; ((int64_t)1 << shift) != block_size;) ++shift;
     *out = Fp4Cache{const_cast<uint8_t*>(caches), layer_stride, block_stride, head_stride, (uint32_t)num_blocks,
-                    (uint32_t)block_size, shift};
+                    (uint32_t)block_size};
     return NRC_OK;
 }
 // From the first page's first byte to the last one's last.

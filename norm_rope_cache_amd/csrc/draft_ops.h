@@ -47,7 +47,6 @@ struct Fp4Cache {
     uint8_t* cache;
     int64_t layer_stride, block_stride, head_stride;
     uint32_t num_blocks, block_size;
-    int32_t bs_shift;  // log2(block_size), or -1 when not a power of two
 };
 
 // K and V rows of L layers, [L, T, H, 64] by strides in elements, and their slots.

@@ -13,6 +13,7 @@
 // group's maximum comes by packed 16-bit maxima of the magnitudes' bits, the codes
 // by the hardware's conversion, two elements a time.
 #include "../../include/nrc.h"
+#include "div.h"
 #include "draft_ops.h"
 #include "fp4.h"
 
@@ -22,14 +23,20 @@ namespace {
 constexpr int kThreads = 256, kGroups = kThreads / 16;
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
+// Both kernels' divisors, as products.
+struct Divs {
+    Div by_heads, by_block;
+};
+Divs divs_of(const Fp4Rows& r, const Fp4Cache& c) { return Divs{div_by((uint32_t)r.H), div_by(c.block_size)}; }
+
 // The cell of a slot: its page's first byte in layer l's head h and its place there; false without one.
 struct Cell {
     int64_t page;
     uint32_t at;
 };
-__device__ __forceinline__ bool cell_of(const Fp4Cache& c, int64_t slot, uint32_t l, uint32_t h, Cell* out) {
+__device__ __forceinline__ bool cell_of(const Fp4Cache& c, Div by_block, int64_t slot, uint32_t l, uint32_t h, Cell* out) {
     if (slot < 0 || slot >= (int64_t)c.num_blocks * c.block_size) return false;
-    const uint32_t block = c.bs_shift >= 0 ? (uint32_t)slot >> c.bs_shift : (uint32_t)slot / c.block_size;
+    const uint32_t block = quotient((uint32_t)slot, by_block);
     out->at = (uint32_t)slot - block * c.block_size;
     out->page = l * c.layer_stride + block * c.block_stride + h * c.head_stride;
     return true;
@@ -48,19 +55,19 @@ struct Unit {
     uint32_t h;
     bool there;
 };
-__device__ __forceinline__ Unit unit_of(const Fp4Rows& r, uint32_t id) {
+__device__ __forceinline__ Unit unit_of(const Fp4Rows& r, Div by_heads, uint32_t id) {
     Unit u;
     u.there = id < (uint32_t)(r.T * r.H);
-    u.t = u.there ? id / (uint32_t)r.H : 0u;
+    u.t = u.there ? quotient(id, by_heads) : 0u;
     u.h = u.there ? id - (uint32_t)u.t * (uint32_t)r.H : 0u;
     return u;
 }
 
 // Four lanes a unit, one group of 32 elements a lane: its 64 bytes in four loads on the way together. (With 16 lanes a
 // unit, 8197 rows of 8 heads in 4 layers take 25.7 us instead of 21.7: four times the lanes work out a cell's place.)
-__global__ __launch_bounds__(kThreads) void fp4_store_kernel(Fp4Rows r, Fp4Cache c) {
+__global__ __launch_bounds__(kThreads) void fp4_store_kernel(Fp4Rows r, Fp4Cache c, Divs by) {
     const uint32_t l = blockIdx.y, group = threadIdx.x & 3u;
-    const Unit u = unit_of(r, blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2));
+    const Unit u = unit_of(r, by.by_heads, blockIdx.x * (kThreads / 4) + (threadIdx.x >> 2));
     if (!u.there) return;  // (a unit's lanes go together)
     const uint16_t* src = (group >> 1 ? r.v + l * r.v_ls + u.t * r.v_rs + u.h * r.v_hs
                                       : r.k + l * r.k_ls + u.t * r.k_rs + u.h * r.k_hs) + 32 * (group & 1u);
@@ -68,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void fp4_store_kernel(Fp4Rows r, Fp4Cache
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = load16(src + 8 * i);
     Cell cell;
-    if (!cell_of(c, r.slots[l * r.slots_ls + u.t], l, u.h, &cell)) return;
+    if (!cell_of(c, by.by_block, r.slots[l * r.slots_ls + u.t], l, u.h, &cell)) return;
     u16x2 most{0, 0};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -94,8 +101,8 @@ __global__ __launch_bounds__(kThreads) void fp4_store_kernel(Fp4Rows r, Fp4Cache
 // us for what takes 22.6 so); U units to a lane, their loads on the way together.
 // fill: rows without a cell become 0, not left as they are.
 template <int U>
-__global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache c, uint16_t* __restrict__ k,
-                                                            uint16_t* __restrict__ v, bool fill) {
+__global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache c, Divs by,
+                                                            uint16_t* __restrict__ k, uint16_t* __restrict__ v, bool fill) {
     const uint32_t l = blockIdx.y, lane = threadIdx.x & 15u, part = lane >> 3;
     uint16_t* dst = (part ? v + l * r.v_ls : k + l * r.k_ls) + 8 * (lane & 7u);
     const int64_t rs = part ? r.v_rs : r.k_rs, hs = part ? r.v_hs : r.k_hs;
@@ -103,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache 
     int64_t slot[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        const Unit u = unit_of(r, id(j));
+        const Unit u = unit_of(r, by.by_heads, id(j));
         slot[j] = u.there ? r.slots[l * r.slots_ls + u.t] : -1;
     }
     uint32_t codes[U], bytes[U];
@@ -111,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache 
 #pragma unroll
     for (int j = 0; j < U; ++j) {
         Cell cell;
-        there[j] = cell_of(c, slot[j], l, unit_of(r, id(j)).h, &cell);
+        there[j] = cell_of(c, by.by_block, slot[j], l, unit_of(r, by.by_heads, id(j)).h, &cell);
         codes[j] = bytes[j] = 0u;
         if (there[j]) {
             codes[j] = *reinterpret_cast<const uint32_t*>(c.cache + codes_at(c, cell, lane));
@@ -120,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache 
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        const Unit u = unit_of(r, id(j));
+        const Unit u = unit_of(r, by.by_heads, id(j));
         if (!u.there || (!there[j] && !fill)) continue;
         const uint32_t byte = bytes[j] >> (8 * (lane >> 2)) & 0xFFu;
         U32x4 x = there[j] ? fp4_open(codes[j], __uint_as_float(byte << 23)) : U32x4{0u, 0u, 0u, 0u};
@@ -136,16 +143,16 @@ dim3 grid_of(const Fp4Rows& r, int64_t units) { return dim3((uint32_t)((r.T * r.
 int64_t fp4_page(int64_t block_size) { return fp4_page_bytes(block_size); }
 
 int launch_fp4_store(const Fp4Rows& r, const Fp4Cache& c, hipStream_t stream) {
-    hipLaunchKernelGGL(fp4_store_kernel, grid_of(r, kThreads / 4), dim3(kThreads), 0, stream, r, c);
+    hipLaunchKernelGGL(fp4_store_kernel, grid_of(r, kThreads / 4), dim3(kThreads), 0, stream, r, c, divs_of(r, c));
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_fp4_load(const Fp4Rows& r, const Fp4Cache& c, uint16_t* k, uint16_t* v, bool fill, hipStream_t stream) {
     // (a drafting step's few rows: a unit a lane, all at once)
     if (r.T * r.H * r.L < 65536)
-        hipLaunchKernelGGL(fp4_load_kernel<1>, grid_of(r, kGroups), dim3(kThreads), 0, stream, r, c, k, v, fill);
+        hipLaunchKernelGGL(fp4_load_kernel<1>, grid_of(r, kGroups), dim3(kThreads), 0, stream, r, c, divs_of(r, c), k, v, fill);
     else
-        hipLaunchKernelGGL(fp4_load_kernel<4>, grid_of(r, 4 * kGroups), dim3(kThreads), 0, stream, r, c, k, v, fill);
+        hipLaunchKernelGGL(fp4_load_kernel<4>, grid_of(r, 4 * kGroups), dim3(kThreads), 0, stream, r, c, divs_of(r, c), k, v, fill);
     return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
