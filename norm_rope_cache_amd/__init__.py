@@ -889,6 +889,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeros(shape, dtype, device, stream):
+    """_empty, filled with zeros by the call's stream: what it launches next reads them, and nothing else orders the two."""
+    torch = _torch or _get_torch()
+    t = _empty(shape, dtype, device, stream)
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return t.zero_()
+
+
 def _fits32(v, name):
     """Raise unless v is an integer of 32 bits (ctypes would cut it)."""
     if not isinstance(v, int) or not -0x80000000 <= v <= 0x7FFFFFFF:
@@ -1175,9 +1183,9 @@ def qk_norm_rotate_grad(grad_q, grad_k, q, k, positions, cos_sin, q_weight=None,
     torch = _torch or _get_torch()
     dev, code, args = _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout)
     if grad_q is None:
-        grad_q = torch.zeros_like(q, memory_format=torch.contiguous_format)
+        grad_q = _zeros(q.shape, q.dtype, q.device, stream)
     if grad_k is None and k is not None:
-        grad_k = torch.zeros_like(k, memory_format=torch.contiguous_format)
+        grad_k = _zeros(k.shape, k.dtype, k.device, stream)
     gq = _heads(grad_q, "grad_q", code, dev, q.shape)
     gk = (None, 0, 0) if k is None else _heads(grad_k, "grad_k", code, dev, k.shape)
     new = lambda t: None if t is None else _empty(t.shape, t.dtype, t.device, stream)

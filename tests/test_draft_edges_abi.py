@@ -1,0 +1,54 @@
+"""Edges of the operators on a drafted token's way to the cache, without a GPU: what
+the binding and the argument checks do before any launch."""
+
+import ctypes
+import os
+
+import pytest
+import torch
+
+EINVAL = -22
+at = ctypes.c_void_p
+
+
+@pytest.fixture(scope="module")
+def nrc():
+    import norm_rope_cache_amd as m
+
+    if not os.path.exists(m.library_path()):
+        from norm_rope_cache_amd import build
+
+        build.build()
+    m._load()
+    return m
+
+
+class Recorder:
+    """qk_norm_rotate_grad on the CPU: its operands' checks and its launch taken out, tensors made on the CPU."""
+
+    def __init__(self, nrc, monkeypatch):
+        self.zeros, self.calls = [], []
+        monkeypatch.setattr(nrc, "_qk_operands", lambda q, k, *rest: (0, 0, ()))
+        monkeypatch.setattr(nrc, "_heads", lambda t, *rest: (t.data_ptr(), *t.stride()[:2]))
+        monkeypatch.setattr(nrc, "_empty", lambda shape, dtype, device, stream: torch.empty(shape, dtype=dtype))
+        monkeypatch.setattr(nrc, "_stream", lambda stream, ref: stream)
+        monkeypatch.setattr(nrc, "_call", lambda ref, fn, *args: self.calls.append(args))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+        def zeros(shape, dtype, device, stream):
+            self.zeros.append((tuple(shape), stream))
+            return torch.zeros(shape, dtype=dtype)
+
+        monkeypatch.setattr(nrc, "_zeros", zeros, raising=False)
+
+
+def test_gradients_that_count_as_zero_are_made_on_the_calls_stream(nrc, monkeypatch):
+    """Zeros of another stream would be read before they are there, and given to others while they are read."""
+    rec = Recorder(nrc, monkeypatch)
+    monkeypatch.setattr(torch, "zeros_like", lambda *a, **kw: pytest.fail("made on the current stream"))
+    q, k = torch.randn(3, 4, 64), torch.randn(3, 2, 64)
+    side = object()
+    nrc.qk_norm_rotate_grad(None, k, q, k, None, None, stream=side)
+    nrc.qk_norm_rotate_grad(q, None, q, k, None, None, stream=side)
+    nrc.qk_norm_rotate_grad(None, None, q, None, None, None, stream=side)
+    assert rec.zeros == [((3, 4, 64), side), ((3, 2, 64), side), ((3, 4, 64), side)]

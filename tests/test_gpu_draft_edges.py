@@ -1,0 +1,47 @@
+"""Edges of the operators on a drafted token's way to the cache, on the GPU."""
+
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_qk_norm import dev, inputs, within  # noqa: E402
+
+
+@pytest.fixture(scope="module")
+def nrc():
+    import norm_rope_cache_amd as m
+
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    m._load()
+    return m
+
+
+@pytest.mark.parametrize("missing", ["q", "k", "both"])
+def test_gradients_that_count_as_zero_on_another_stream(nrc, missing):
+    """The current stream busy, its free memory full of NaN: the call on a side stream waits for neither."""
+    i = inputs(700, 8, 4, 64, 64, torch.bfloat16, torch.float32, 12)
+    args = [dev(t) for t in (i["q"], i["k"], i["pos"], i["cs"], *i["w"])]
+    gq, gk = dev(i["gq"]), dev(i["gk"])
+    given = [None if missing in ("q", "both") else gq, None if missing in ("k", "both") else gk]
+    want = nrc.qk_norm_rotate_grad(*(torch.zeros_like(z) if g is None else g for g, z in zip(given, (gq, gk))), *args)
+    a = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        trash = [torch.full_like(t, math.nan) for t in (gq, gk, gq, gk)]
+        torch.cuda.synchronize()
+        del trash
+        for _ in range(10):
+            b = a @ a
+        got = nrc.qk_norm_rotate_grad(*given, *args, stream=side)
+        later = [torch.full_like(t, math.nan) for t in (gq, gk)]
+        side.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        torch.cuda.synchronize()
+        del later, b
