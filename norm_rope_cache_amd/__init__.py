@@ -962,6 +962,18 @@ def rope_table(count, rotary_dim, base=10000.0, scaling="none", factor=1.0, orig
     return out
 
 
+def _no_tangents(*tensors):
+    """Raise for a dual tensor of forward-mode differentiation: it does not require grad, and the output of a call on its
+    data would count as a constant."""
+    torch = _torch or _get_torch()
+    forward = torch.autograd.forward_ad
+    if getattr(forward, "_current_level", 0) < 0:  # (no such differentiation going on)
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward.unpack_dual(t).tangent is not None:
+            raise ValueError("forward-mode derivatives are not worked out: unpack the dual tensor first")
+
+
 _rotation = None  # the rotation as a torch.autograd.Function, once an x that requires grad has needed it
 
 
@@ -1003,9 +1015,11 @@ def rope_rotate(x, positions, cos_sin, layout="interleaved", inverse=False, out=
     inverse    turn back: the gradient of the rotation
     out        x itself, or a tensor apart from it (default: a new one)
     An x that requires grad gets its gradient (by the inverse, on the current
-    stream of the forward call); it takes no out, and cos_sin gets none.
+    stream of the forward call); it takes no out, and cos_sin gets none. Dual
+    tensors (forward mode) are refused.
     """
     torch = _torch or _get_torch()
+    _no_tangents(x, cos_sin)
     code = _dtype_code(x.dtype, "x")
     dev = x.get_device()
     if dev < 0:
@@ -1140,8 +1154,9 @@ def qk_norm_rotate(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1
     x w / sqrt(mean x^2 + eps), turned, in float32 and rounded once. Inputs and
     gains that require grad get their gradients (qk_norm_rotate_grad, on the current
     stream of the forward call; once: second derivatives raise); such a call takes no
-    outputs, and cos_sin gets none."""
+    outputs, and cos_sin gets none. Dual tensors (forward mode) are refused."""
     torch = _torch or _get_torch()
+    _no_tangents(q, k, cos_sin, q_weight, k_weight)
     if ((q.requires_grad or cos_sin.requires_grad or k is not None and k.requires_grad
          or q_weight is not None and q_weight.requires_grad or k_weight is not None and k_weight.requires_grad)
             and torch.is_grad_enabled()):
@@ -1181,6 +1196,7 @@ def qk_norm_rotate_grad(grad_q, grad_k, q, k, positions, cos_sin, q_weight=None,
     Rows outside the table pass their gradient, and add nothing to the gains'. The
     gains' gradients are float32 sums in one fixed order, rounded to the gains' types."""
     torch = _torch or _get_torch()
+    _no_tangents(grad_q, grad_k, q, k, cos_sin, q_weight, k_weight)
     dev, code, args = _qk_operands(q, k, positions, cos_sin, q_weight, k_weight, eps, layout)
     if grad_q is None:
         grad_q = _zeros(q.shape, q.dtype, q.device, stream)

@@ -52,3 +52,27 @@ def test_gradients_that_count_as_zero_are_made_on_the_calls_stream(nrc, monkeypa
     nrc.qk_norm_rotate_grad(q, None, q, k, None, None, stream=side)
     nrc.qk_norm_rotate_grad(None, None, q, None, None, None, stream=side)
     assert rec.zeros == [((3, 4, 64), side), ((3, 2, 64), side), ((3, 4, 64), side)]
+
+
+def test_dual_tensors_are_refused(nrc):
+    """They do not require grad: their tangents would be lost without a word."""
+    import torch.autograd.forward_ad as forward
+
+    q, k, g = torch.randn(3, 4, 64), torch.randn(3, 2, 64), torch.randn(64)
+    pos, cs = torch.arange(3), torch.ones(8, 64)
+    with forward.dual_level():
+        dual = lambda t: forward.make_dual(t, torch.ones_like(t))
+        for call in (lambda: nrc.rope_rotate(dual(q), pos, cs), lambda: nrc.rope_rotate(q, pos, dual(cs)),
+                     lambda: nrc.rope_rotate(dual(q), pos, cs, out=q),
+                     lambda: nrc.qk_norm_rotate(dual(q), k, pos, cs), lambda: nrc.qk_norm_rotate(q, dual(k), pos, cs),
+                     lambda: nrc.qk_norm_rotate(q, k, pos, dual(cs)), lambda: nrc.qk_norm_rotate(q, k, pos, cs, dual(g), g),
+                     lambda: nrc.qk_norm_rotate(q, k, pos, cs, g, dual(g)),
+                     lambda: nrc.qk_norm_rotate_grad(dual(q), k, q, k, pos, cs),
+                     lambda: nrc.qk_norm_rotate_grad(None, None, q, dual(k), pos, cs)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):  # (which forward mode does not heed)
+                call()
+        for call in (lambda: nrc.rope_rotate(q, pos, cs), lambda: nrc.qk_norm_rotate(dual(q).detach(), k, pos, cs)):
+            with pytest.raises(TypeError, match="GPU"):  # no tangents: on to the other checks
+                call()

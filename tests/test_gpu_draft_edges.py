@@ -45,3 +45,18 @@ def test_gradients_that_count_as_zero_on_another_stream(nrc, missing):
             assert torch.equal(x, y)
         torch.cuda.synchronize()
         del later, b
+
+
+def test_dual_tensors_are_refused(nrc):
+    import torch.autograd.forward_ad as forward
+
+    i = inputs(4, 2, 2, 64, 64, torch.float32, None, 3)
+    q, k, pos, cs = [dev(t) for t in (i["q"], i["k"], i["pos"], i["cs"])]
+    want = nrc.qk_norm_rotate(q, k, pos, cs)
+    with forward.dual_level():
+        dual = forward.make_dual(q, torch.ones_like(q))
+        for call in (lambda: nrc.rope_rotate(dual, pos, cs), lambda: nrc.qk_norm_rotate(dual, k, pos, cs)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+        got = nrc.qk_norm_rotate(forward.unpack_dual(dual).primal, k, pos, cs)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
