@@ -1205,10 +1205,13 @@ def qk_norm_rotate_grad(grad_q, grad_k, q, k, positions, cos_sin, q_weight=None,
     gq = _heads(grad_q, "grad_q", code, dev, q.shape)
     gk = (None, 0, 0) if k is None else _heads(grad_k, "grad_k", code, dev, k.shape)
     new = lambda t: None if t is None else _empty(t.shape, t.dtype, t.device, stream)
-    dq, dk, dqw, dkw = new(q), new(k), new(q_weight), new(k_weight)
+    keys = k is not None and k.shape[1] > 0
+    dq, dk, dqw = new(q), new(k), new(q_weight)
+    # (gains of no heads: the entry has no gradient of theirs)
+    dkw = new(k_weight) if keys or k_weight is None else _zeros(k_weight.shape, k_weight.dtype, k_weight.device, stream)
     lib = _load()
     need, ws = 0, None
-    if q_weight is not None or k_weight is not None:
+    if q_weight is not None or keys and k_weight is not None:
         if dev != torch.cuda.current_device():
             with torch.cuda.device(dev):
                 need = lib.nrc_qk_norm_rotate_grad_workspace_bytes(q.shape[2], 1)
@@ -1218,7 +1221,7 @@ def qk_norm_rotate_grad(grad_q, grad_k, q, k, positions, cos_sin, q_weight=None,
             _check(need)
         ws = _empty((need,), torch.uint8, q.device, stream)
     _call(q, lib.nrc_qk_norm_rotate_grad, *gq, *gk, *args, dq.data_ptr(), *(None if t is None else t.data_ptr() for t in (
-        dk, dqw, dkw, ws)), need, ROPE_PASS_OUTSIDE, _stream(stream, q))
+        dk, dqw, dkw if keys else None, ws)), need, ROPE_PASS_OUTSIDE, _stream(stream, q))
     return dq, dk, dqw, dkw
 
 

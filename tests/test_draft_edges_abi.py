@@ -76,3 +76,13 @@ def test_dual_tensors_are_refused(nrc):
         for call in (lambda: nrc.rope_rotate(q, pos, cs), lambda: nrc.qk_norm_rotate(dual(q).detach(), k, pos, cs)):
             with pytest.raises(TypeError, match="GPU"):  # no tangents: on to the other checks
                 call()
+
+
+def test_gains_of_no_keys(nrc, monkeypatch):
+    """Keys without heads: the C entry takes no gradient of their gains, which is 0."""
+    rec = Recorder(nrc, monkeypatch)
+    q, k, g = torch.randn(3, 4, 64), torch.randn(3, 0, 64), torch.randn(64)
+    dq, dk, dqw, dkw = nrc.qk_norm_rotate_grad(q, k, q, k, None, None, k_weight=g)
+    assert dk.shape == k.shape and dqw is None and torch.equal(dkw, torch.zeros(64))
+    dk_weight, ws, need = rec.calls[0][-5], rec.calls[0][-4], rec.calls[0][-3]
+    assert dk_weight is None and ws is None and need == 0

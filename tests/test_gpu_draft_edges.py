@@ -60,3 +60,21 @@ def test_dual_tensors_are_refused(nrc):
                 call()
         got = nrc.qk_norm_rotate(forward.unpack_dual(dual).primal, k, pos, cs)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("q_gains", [False, True])
+def test_keys_without_heads(nrc, q_gains):
+    """The gradients are those without keys, and 0 of the gains of none; through autograd too."""
+    i = inputs(5, 3, 2, 64, 64, torch.bfloat16, torch.float32, 4)
+    q, k, pos, cs, qw, kw = [dev(t) for t in (i["q"], i["k"][:, :0], i["pos"], i["cs"], *i["w"])]
+    qw = qw if q_gains else None
+    gq = dev(i["gq"])
+    want = nrc.qk_norm_rotate_grad(gq, None, q, None, pos, cs, qw)
+    got = nrc.qk_norm_rotate_grad(gq, k, q, k, pos, cs, qw, kw)
+    assert torch.equal(got[0], want[0]) and got[1].shape == k.shape and torch.equal(got[3], torch.zeros_like(kw))
+    assert got[2] is None if qw is None else torch.equal(got[2], want[2])
+    q.requires_grad_(), kw.requires_grad_()
+    out, none = nrc.qk_norm_rotate(q, k, pos, cs, qw, kw)
+    assert none.shape == k.shape
+    grads = torch.autograd.grad(out, (q, kw), gq)
+    assert torch.equal(grads[0], want[0]) and torch.equal(grads[1], torch.zeros_like(kw))
