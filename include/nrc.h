@@ -540,8 +540,8 @@ int32_t nrc_rope_rotate_ex(const void* x, int32_t dtype, int64_t T, int32_t H, i
  *              position is outside [0, max_position) is left as it is in the outputs
  *              (NRC_ROPE_PASS_OUTSIDE in flags: is copied, without the norm).
  *   out_q, out_k  like q and k, their own strides: the input itself (same pointer
- *              and strides), or apart from q, k and each other. Parts of the rows
- *              of one wider tensor lie apart.
+ *              and strides), or apart from q, k and each other. Parts of the rows of
+ *              one wider tensor lie apart, side by side or head by head ([T, H, 3, d]).
  * y = rot(x w / sqrt(mean x^2 + eps)) in FP32, rounded to the type once (nrc_context_kv_store
  * rounds its keys between the norm and the turn too). T == 0 returns
  * NRC_OK. Errors: NRC_EINVAL (NULL or misaligned operands, shapes, strides,

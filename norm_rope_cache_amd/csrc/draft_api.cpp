@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "api_checks.h"
 #include "draft_ops.h"
@@ -84,13 +85,36 @@ Range rows_range(const QkNormArgs& a, int32_t heads, const void* p, int64_t rs, 
     return Range{a.T > 0 && heads > 0 ? p : nullptr, a.T > 0 && heads > 0 ? span(a.T, heads, a.head_dim, rs, hs) * type_bytes(a.dtype) : 0};
 }
 
-// Are the rows of two views whose spans interleave (parts of one wider row) apart from each other?
-bool rows_interleave(const Range& a, int64_t a_heads, int64_t a_hs, int64_t a_rs, const Range& b, int64_t b_heads,
-                     int64_t b_hs, int64_t b_rs, int64_t d, int64_t eb) {
-    if (a_rs != b_rs || a_rs == 0) return false;
-    const int64_t row = a_rs * eb, in_a = ((a_heads - 1) * a_hs + d) * eb, in_b = ((b_heads - 1) * b_hs + d) * eb;
-    const int64_t apart = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % row, behind = apart < 0 ? apart + row : apart;
-    return behind >= in_a && in_b <= row - behind;
+// A view's steps: their strides in elements and how many there are.
+struct Step {
+    int64_t stride, count;
+};
+
+// Are the elements of two views whose spans interleave apart from each other (parts of one wider row, heads of several
+// tensors by turns)? `a` and `b` begin at multiples of eb bytes, their innermost runs are d elements. They are when, for
+// some of the steps taken as a run of their own (what it spans), both runs lie apart in a period that all other steps of
+// both are multiples of.
+template <int N>
+bool apart_by_steps(const void* a, const Step (&as)[N], const void* b, const Step (&bs)[N], int64_t d, int64_t eb) {
+    const __int128 between = (__int128)(uintptr_t)b - (__int128)(uintptr_t)a;
+    for (int inner = 0; inner < 1 << N; ++inner) {
+        __int128 in_a = d, in_b = d;
+        int64_t period = 0;
+        for (int i = 0; i < N; ++i) {
+            if (inner >> i & 1) {
+                in_a += (__int128)(as[i].count - 1) * as[i].stride;
+                in_b += (__int128)(bs[i].count - 1) * bs[i].stride;
+            } else {
+                if (as[i].count > 1) period = std::gcd(period, as[i].stride);
+                if (bs[i].count > 1) period = std::gcd(period, bs[i].stride);
+            }
+        }
+        if (period == 0) continue;  // (the spans themselves, which meet)
+        __int128 behind = between % (period * (__int128)eb);
+        if (behind < 0) behind += period * (__int128)eb;
+        if (behind >= in_a * eb && in_b * eb <= period * (__int128)eb - behind) return true;
+    }
+    return false;
 }
 
 // A view of layers of 4-bit pages, checked (the pointer with need).
@@ -121,9 +145,7 @@ Range pages_range(const Fp4Cache& c, int32_t H, int32_t L) {
 }
 // Is every page in memory of its own?
 bool pages_apart(const Fp4Cache& c, int32_t H, int32_t L) {
-    struct Step {
-        int64_t stride, count;
-    } steps[] = {{c.layer_stride, L}, {c.block_stride, (int64_t)c.num_blocks}, {c.head_stride, H}};
+    Step steps[] = {{c.layer_stride, L}, {c.block_stride, (int64_t)c.num_blocks}, {c.head_stride, H}};
     std::sort(steps, steps + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
     __int128 reach = fp4_page(c.block_size);
     for (const Step& s : steps) {
@@ -164,9 +186,7 @@ Range rows4_range(const Rows4& r, int64_t T, int32_t H, int32_t L) {
 }
 // Do rows that are written lie in places of their own (layers, rows and heads in any order)?
 bool rows4_apart(const Rows4& r, int64_t T, int32_t H, int32_t L) {
-    struct Step {
-        int64_t stride, count;
-    } steps[] = {{r.ls, L}, {r.rs, T}, {r.hs, H}};
+    Step steps[] = {{r.ls, L}, {r.rs, T}, {r.hs, H}};
     std::sort(steps, steps + 3, [](const Step& a, const Step& b) { return a.stride < b.stride; });
     __int128 reach = NRC_HEAD_DIM;
     for (const Step& s : steps) {
@@ -258,8 +278,8 @@ int32_t nrc_qk_norm_rotate(const void* q, int64_t q_row_stride, int64_t q_head_s
         return fail(NRC_EINVAL, "%s: outputs must lie apart from positions, cos_sin and the gains", what);
     // (queries and keys of one projection's rows: their spans interleave, their heads do not meet)
     auto meets = [&](const Range& w, int64_t wrs, int64_t whs, int32_t wh, const Range& r, int64_t rrs, int64_t rhs, int32_t rh) {
-        if (!any_meet({w}, {r})) return false;
-        return !rows_interleave(w, wh, whs, wrs, r, rh, rhs, rrs, head_dim, type_bytes(dtype));
+        return any_meet({w}, {r}) && !apart_by_steps<2>(w.p, {{wrs, T}, {whs, wh}}, r.p, {{rrs, T}, {rhs, rh}}, head_dim,
+                                                        type_bytes(dtype));
     };
     if ((!q_in_place && meets(ro, oq_row_stride, oq_head_stride, Hq, rq, q_row_stride, q_head_stride, Hq)) ||
         (!k_in_place && meets(rok, ok_row_stride, ok_head_stride, Hk, rk, k_row_stride, k_head_stride, Hk)) ||

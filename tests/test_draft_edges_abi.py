@@ -86,3 +86,40 @@ def test_gains_of_no_keys(nrc, monkeypatch):
     assert dk.shape == k.shape and dqw is None and torch.equal(dkw, torch.zeros(64))
     dk_weight, ws, need = rec.calls[0][-5], rec.calls[0][-4], rec.calls[0][-3]
     assert dk_weight is None and ws is None and need == 0
+
+
+Q, K, OQ, OK, POS, CS = (at(0x40000000 * i) for i in range(1, 7))  # never dereferenced
+
+
+def norm_call(lib, **kw):
+    ok = dict(q=Q, qr=512, qh=64, Hq=8, k=K, kr=128, kh=64, Hk=2, dtype=0, T=4, d=64, qw=None, qwt=0, kw=None, kwt=0, eps=1e-6,
+              pos=POS, cs=CS, tdtype=0, maxp=10, R=64, layout=0, oq=OQ, oqr=512, oqh=64, ok=OK, okr=128, okh=64, flags=0, stream=None)
+    assert not set(kw) - set(ok), kw
+    return lib.nrc_qk_norm_rotate(*{**ok, **kw}.values())
+
+
+def shifted(p, elements):
+    return at(p.value + 2 * elements)
+
+
+def view(name, p, row, head):
+    return {name: p, name + "r": row, name + "h": head}
+
+
+def in_place(q, k, qs, ks, **kw):
+    return dict(view("q", q, *qs), **view("oq", q, *qs), **view("k", k, *ks), **view("ok", k, *ks), **kw)
+
+
+def test_heads_of_one_tensor_that_meet(nrc):
+    """In place over [T, H, 3, 64] and the like: what meets by an element is refused (what lies apart is launched, on a GPU)."""
+    lib = nrc._load()
+    by_heads = (8 * 192, 192)
+    for kw in (in_place(Q, shifted(Q, 63), by_heads, by_heads, Hk=8),  # k begins in q's head
+               in_place(Q, shifted(Q, 129), by_heads, by_heads, Hk=8),  # k ends in q's next head
+               in_place(Q, shifted(Q, 5 * 192 + 32), by_heads, by_heads, Hk=2),
+               in_place(Q, shifted(Q, 64), by_heads, (8 * 192, 160), Hk=8),  # heads that drift into each other
+               in_place(Q, shifted(Q, 64), by_heads, (8 * 192 + 64, 192), Hk=8),  # rows that do
+               in_place(Q, shifted(Q, 64), (192, 4 * 192), (192 - 8, 4 * 192), Hk=8),  # heads before rows
+               dict(view("q", Q, *by_heads), **view("oq", shifted(Q, 32), *by_heads)),
+               in_place(Q, shifted(Q, 32), (0, 192), (0, 192), T=1, Hk=8), in_place(Q, shifted(Q, 32), (64, 0), (64, 0), Hq=1, Hk=1)):
+        assert norm_call(lib, **kw) == EINVAL and b"apart" in lib.nrc_last_error(), kw

@@ -78,3 +78,27 @@ def test_keys_without_heads(nrc, q_gains):
     assert none.shape == k.shape
     grads = torch.autograd.grad(out, (q, kw), gq)
     assert torch.equal(grads[0], want[0]) and torch.equal(grads[1], torch.zeros_like(kw))
+
+
+@pytest.mark.parametrize("T", [1, 9])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kind", ["by heads", "heads first", "one head", "into the third part"])
+def test_parts_of_one_tensor_by_turns(nrc, kind, dtype, T):
+    """Queries, keys and values head by head in one tensor, in place or from part to part: the results are those of new outputs."""
+    H, d = (1 if kind == "one head" else 5), 64
+    gen = torch.Generator().manual_seed(T)
+    if kind == "heads first":
+        wide = torch.randn(H, T, 3, d, generator=gen).to(dtype).cuda().transpose(0, 1)
+    else:
+        wide = torch.randn(T, H, 3, d, generator=gen).to(dtype).cuda()
+    q, k, v = wide.unbind(2)
+    pos = torch.randint(0, 50, (T,), generator=gen).cuda()
+    cs = nrc.rope_table(50, d, dtype=torch.float32)
+    want = nrc.qk_norm_rotate(q.clone(), k.clone(), pos, cs)
+    kept = [q.clone(), k.clone(), v.clone()]
+    if kind == "into the third part":
+        nrc.qk_norm_rotate(q, k, pos, cs, out_q=v, out_k=k)
+        assert torch.equal(v, want[0]) and torch.equal(k, want[1]) and torch.equal(q, kept[0])
+    else:
+        nrc.qk_norm_rotate(q, k, pos, cs, out_q=q, out_k=k)
+        assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept[2])
