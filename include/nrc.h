@@ -635,7 +635,8 @@ int32_t nrc_context_fp4_store(const uint16_t* k, int64_t k_layer_stride, int64_t
  * nrc_context_fp4_load - the values of cells of 4 bits, as bf16 rows (every
  * value is a bf16 number; 0x7FC0 for NaN).
  * Operands as nrc_context_fp4_store, k and v being written: rows in memory of their
- * own, apart from each other, the caches and slots. A row whose slot is negative or
+ * own, apart from each other (side by side in one tensor's rows, or head by head, they
+ * are), the caches and slots. A row whose slot is negative or
  * past the cache is left as it is (NRC_FP4_FILL in flags: becomes 0). A slot may come more
  * than once.
  */

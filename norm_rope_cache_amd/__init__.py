@@ -1661,7 +1661,8 @@ def context_fp4_load(caches, slots, out_k=None, out_v=None, stream=None):
     of one layer's cache).
 
     A row whose slot is negative or past the cache is left as it is in given
-    outputs, and 0 otherwise; slots may repeat."""
+    outputs (which may be parts of one tensor: kv_views), and 0 otherwise; slots may
+    repeat."""
     torch = _torch or _get_torch()
     dev, L, H, pages = _fp4_caches(caches)
     T, at = _fp4_slots(slots, dev, L)

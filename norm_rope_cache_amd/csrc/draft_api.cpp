@@ -403,8 +403,10 @@ int32_t nrc_context_fp4_load(const uint8_t* caches, int64_t layer_stride, int64_
     if (!work) return NRC_OK;
     if (!rows4_apart(kr, T, H, L) || !rows4_apart(vr, T, H, L)) return fail(NRC_EINVAL, "%s: rows of k or v overlap", what);
     const Range k_range = rows4_range(kr, T, H, L), v_range = rows4_range(vr, T, H, L);
+    // (K and V side by side in a row, or head by head: their spans interleave, their rows do not meet)
     if (any_meet({k_range, v_range}, {pages_range(c, H, L), {slots, 8 * ((L - 1) * slots_layer_stride + T)}}) ||
-        any_meet({k_range}, {v_range}))
+        (any_meet({k_range}, {v_range}) && !apart_by_steps<3>(k, {{kr.ls, L}, {kr.rs, T}, {kr.hs, H}}, v,
+                                                              {{vr.ls, L}, {vr.rs, T}, {vr.hs, H}}, NRC_HEAD_DIM, 2)))
         return fail(NRC_EINVAL, "%s: k and v must lie apart from each other, the caches and slots", what);
     return launch_status(launch_fp4_load(r, c, k, v, flags != 0, (hipStream_t)stream), what);
 }

@@ -123,3 +123,18 @@ def test_heads_of_one_tensor_that_meet(nrc):
                dict(view("q", Q, *by_heads), **view("oq", shifted(Q, 32), *by_heads)),
                in_place(Q, shifted(Q, 32), (0, 192), (0, 192), T=1, Hk=8), in_place(Q, shifted(Q, 32), (64, 0), (64, 0), Hq=1, Hk=1)):
         assert norm_call(lib, **kw) == EINVAL and b"apart" in lib.nrc_last_error(), kw
+
+
+def test_loaded_rows_of_one_tensor_that_meet(nrc):
+    """K and V by turns in one tensor: what meets by a few elements is refused."""
+    lib = nrc._load()
+
+    def call(v, ks, vs, T=4, H=2, L=3):
+        return lib.nrc_context_fp4_load(at(0x10000), 1 << 20, 2176, 1088, 8, 16, POS, 0, T, H, L, K, *ks, v, *vs, 0, None)
+
+    rows = (4 * 256, 256, 64)  # [3, 4, 2 (K, V), 2, 64]
+    for v, ks, vs, kw in ((shifted(K, 120), rows, rows, {}), (shifted(K, 136), rows, rows, {}),
+                          (shifted(K, 128), rows, (4 * 256, 264, 64), {}), (shifted(K, 128), rows, (4 * 256 + 8, 256, 64), {}),
+                          (shifted(K, 72), (2048, 256, 128), (2048, 256, 128), {}),
+                          (shifted(K, 56), (2048, 256, 128), (2048, 256, 128), dict(T=1, L=1))):
+        assert call(v, ks, vs, **kw) == EINVAL and b"apart" in lib.nrc_last_error(), (v, ks, vs)

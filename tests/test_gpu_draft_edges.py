@@ -102,3 +102,28 @@ def test_parts_of_one_tensor_by_turns(nrc, kind, dtype, T):
     else:
         nrc.qk_norm_rotate(q, k, pos, cs, out_q=q, out_k=k)
         assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept[2])
+
+
+@pytest.mark.parametrize("kind", ["side by side", "head by head", "layers inside"])
+@pytest.mark.parametrize("L,T,H", [(3, 5, 4), (1, 7, 2), (2, 1, 1)])
+def test_cells_loaded_into_one_tensor(nrc, L, T, H, kind):
+    """K's and V's rows by turns, as a projection leaves them: what new outputs hold, and nothing else is written."""
+    gen = torch.Generator().manual_seed(T)
+    blocks, bs = T // 4 + 2, 4
+    caches = torch.zeros(L, blocks, H, nrc.fp4_page_bytes(bs), dtype=torch.uint8, device="cuda")
+    slots = torch.randperm(blocks * bs, generator=gen)[:T].cuda()
+    rows = torch.randn(2, L, T, H, 64, generator=gen).bfloat16().cuda()
+    nrc.context_fp4_store(rows[0], rows[1], slots, caches)
+    want = nrc.context_fp4_load(caches, slots)
+    if kind == "side by side":
+        wide = torch.full((L, T, 3, H, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        k, v, rest = wide.unbind(2)
+    elif kind == "head by head":
+        wide = torch.full((L, T, H, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        k, v, rest = wide.unbind(3)
+    else:
+        wide = torch.full((T, H, L, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda").permute(2, 0, 1, 3, 4)
+        k, v, rest = wide.unbind(3)
+    got = nrc.context_fp4_load(caches, slots, k, v)
+    assert got[0] is k and got[1] is v
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and bool((rest == 7).all())
