@@ -779,8 +779,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         }
     };
 
-    // First the tiles that every row of the workgroup sees whole, if every block of theirs is there (looked at 64 blocks a
-    // load, up to 1024 of them): nobody asks for single rows or keys in them. Then those before, and those behind.
+    // First the tiles that every row of the workgroup sees whole, up to the first whose blocks are not all there: nobody
+    // asks for single rows or keys in them. Then those before, and those behind.
     const int2 block_whole = whole_tiles<kStage>(block_span, tiles, a.sinks);
     int32_t whole0 = block_whole.x < first ? first : block_whole.x > end ? end : block_whole.x;
     const int32_t whole1 = block_whole.y > end ? end : block_whole.y < whole0 ? whole0 : block_whole.y;
@@ -800,13 +800,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
     };
     fetch(number(0), page);
     if (whole > 0) {
+        // Are their blocks there? Every wave looks at all of them, 64 a load, four loads on the way. (A share of 257 tiles in 2050
+        // blocks of 16 takes as long as in 513 of 64: 32 sequences of 48 nodes over up to 32768 packed keys 797 and 786 us, against
+        // 1568 with places worked out per lane and key.)
         const uint32_t block = block_of((uint32_t)tiles.key(whole0 * kStage), kv);
         const uint32_t blocks = block_of((uint32_t)tiles.key((whole0 + whole) * kStage - 32) + 31, kv) - block + 1;
-        bool is = blocks <= 1024;
-        for (uint32_t i = lane; is && i < blocks; i += 64)
-            is = block + i < kv.table_width && (uint32_t)table[block + i] < kv.num_blocks;
-        if (!__all(is)) {
-            whole = 0;
+        uint32_t gone = 0;  // from the lane's first block that is not there on
+#pragma unroll 4
+        for (uint32_t i = lane; i < blocks; i += 64) {
+            const uint32_t n = block + i, page = (uint32_t)table[n < kv.table_width ? n : kv.table_width - 1];
+            if (!(n < kv.table_width && page < kv.num_blocks) && gone == 0) gone = blocks - i;
+        }
+        if (__any(gone != 0)) {
+            const int64_t left = (int64_t)(block + blocks - wave_most(gone)) * kv.block_size - tiles.key(whole0 * kStage);
+            whole = left < kStage ? 0 : (int32_t)(left / kStage);
             fetch(number(0), entry(number(0)));
             after = entry(number(1));
         }

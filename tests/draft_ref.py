@@ -138,3 +138,43 @@ def make_batch():
                           else torch.full_like(run, byte))
 
     return WindowBatch
+
+
+def dense_attention(bt, scale=0.125):
+    """cache_ref.attention of chains behind bt's window (None: none), all rows of a head at once, on the GPU in 64 bits
+    (for rows and keys too many to go through one by one): (out, lse, bound of out's error, bound of lse's)."""
+    dev = "cuda"
+    T, heads = bt.q.shape[:2]
+    out = torch.zeros(T, heads, 64, dtype=torch.float64, device=dev)
+    lse = torch.full((T, heads), -torch.inf, dtype=torch.float64, device=dev)
+    tol_o, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
+    q, cache, tables = bt.q.to(dev), bt.cache.to(dev), bt.tables.to(dev).long()
+    for b in range(bt.B):
+        lo, n, ctx = int(bt.q_starts[b]), bt.nodes[b], bt.ctx[b]
+        key = torch.arange(ctx + n, device=dev)
+        block = key // bt.bs
+        page = tables[b][block.clamp(max=tables.shape[1] - 1)]
+        there = (block < tables.shape[1]) & (page >= 0) & (page < bt.nb)
+        own = ctx + torch.arange(n, device=dev)[:, None]
+        sees = there & (key <= own)
+        if bt.window is not None:
+            sees &= (key < bt.sinks) | (key > own - bt.window)
+        sees = sees.repeat_interleave(bt.G, 0)
+        for h in range(bt.H):
+            kv = cache[page.clamp(0, bt.nb - 1), h, key % bt.bs].double() * there[:, None]
+            k, v = kv[:, :64], kv[:, 64:]
+            of = slice(h * bt.G, (h + 1) * bt.G)
+            x = q[lo:lo + n, of].double().flatten(0, 1)
+            s = x @ k.T * scale
+            e = 64 * 2.0 ** -23 * (x.abs() @ k.abs().T) * scale + s.abs() * 2.0 ** -21
+            s = s.masked_fill(~sees, -torch.inf)
+            l = torch.logsumexp(s, 1)
+            some = l > -torch.inf
+            p = torch.exp(s - torch.where(some, l, 0.0)[:, None])
+            o, A = p @ v, p @ v.abs()
+            eps = e.masked_fill(~sees, 0.0).amax(1) + 2.0 ** -22 + (ctx + n) * 2.0 ** -24
+            fold = lambda t: t.unflatten(0, (n, bt.G))
+            out[lo:lo + n, of], lse[lo:lo + n, of] = fold(o), fold(l)
+            tol_o[lo:lo + n, of] = fold(o.abs() * 2.0 ** -8 + (2 * eps[:, None] + 2.0 ** -8) * A * 1.01)
+            tol_l[lo:lo + n, of] = fold(torch.where(some, eps * 1.01 + (l.abs() + 24) * 3 * 2.0 ** -24, 0.0))
+    return out, lse, tol_o, tol_l

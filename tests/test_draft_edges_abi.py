@@ -138,3 +138,21 @@ def test_loaded_rows_of_one_tensor_that_meet(nrc):
                           (shifted(K, 72), (2048, 256, 128), (2048, 256, 128), {}),
                           (shifted(K, 56), (2048, 256, 128), (2048, 256, 128), dict(T=1, L=1))):
         assert call(v, ks, vs, **kw) == EINVAL and b"apart" in lib.nrc_last_error(), (v, ks, vs)
+
+
+def test_reference_of_all_rows_at_once(monkeypatch):
+    """dense_attention against the row by row reference, with a window, sinks and a block that is not there."""
+    import cache_ref
+    from draft_ref import dense_attention, make_batch
+
+    to = torch.Tensor.to
+    monkeypatch.setattr(torch.Tensor, "to", lambda t, *a, **kw: t if a[:1] == ("cuda",) else to(t, *a, **kw))
+    for f in ("zeros", "full", "arange"):
+        made = getattr(torch, f)
+        monkeypatch.setattr(torch, f, lambda *a, made=made, **kw: made(*a, **{k: v for k, v in kw.items() if k != "device"}))
+    for window in (None, 11):
+        bt = make_batch()([40, 0, 17], [5, 3, 2], H=2, G=3, block_size=4, tree=False, seed=2).behind(window, 3)
+        bt.tables[0, 7] = -1
+        bt.tables[2, :] = bt.nb  # nothing at all
+        for a, b in zip(dense_attention(bt), cache_ref.attention(bt)):
+            assert torch.allclose(a, b, rtol=1e-9, atol=1e-12)

@@ -8,7 +8,10 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
+from draft_ref import dense_attention, make_batch  # noqa: E402
 from test_gpu_qk_norm import dev, inputs, within  # noqa: E402
+
+Batch = make_batch()
 
 
 @pytest.fixture(scope="module")
@@ -127,3 +130,74 @@ def test_cells_loaded_into_one_tensor(nrc, L, T, H, kind):
     got = nrc.context_fp4_load(caches, slots, k, v)
     assert got[0] is k and got[1] is v
     assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and bool((rest == 7).all())
+
+
+def attend(nrc, bt, packed, **kw):
+    d = bt.dev()
+    args = (d["q"], d["cache"] if packed is None else packed, d["tables"], d["ctx_lens"], d["q_starts"], d["max_nodes"])
+    if packed is None:
+        return nrc.context_window_attention(*args, bt.window, bt.sinks, **kw)
+    return nrc.context_fp4_attention(*args, window=bt.window or 0, sinks=bt.sinks, **kw)
+
+
+def attention_within(got, want):
+    out, lse, tol_o, tol_l = want
+    empty = lse == -math.inf
+    assert torch.equal(got[1] == -math.inf, empty) and bool((got[0][empty] == 0).all())
+    bad = ~((got[0].double() - out).abs() <= tol_o + 1e-30)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4], got[0][bad][:4], out[bad][:4], tol_o[bad][:4])
+    bad = ~(((got[1].double() - lse).abs() <= tol_l) | empty)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4], got[1][bad][:4], lse[bad][:4])
+
+
+@pytest.mark.parametrize("fp4,window", [(True, None), (True, 1100), (False, 1100)])
+@pytest.mark.parametrize("nodes", [12, 30])  # workgroups of 4 waves and of 8
+@pytest.mark.parametrize("bs", [16, 24, 64, 1])
+@pytest.mark.parametrize("gone", ["first", "middle", "last", "several", "most"])
+def test_missing_blocks_among_whole_tiles(nrc, gone, bs, nodes, fp4, window):
+    """Blocks that are not there in tiles of 128 keys that every row would see whole: the tiles before them, theirs, those behind."""
+    bt = Batch([1700, 1300], [nodes, nodes - 3], H=1, G=8, block_size=bs, tree=False, seed=bs + nodes).behind(window, 5)
+    packed = bt.pack(nrc) if fp4 else None
+    first, last = (640 // bs, 1600 // bs)  # (of the keys that all rows see)
+    for at, byte in dict(first=[(first, -1)], middle=[(1000 // bs, bt.nb)], last=[(last, -2 ** 31)],
+                         several=[(first + 1, -1), (1000 // bs, -1), (last, -1)],
+                         most=[(i, -1) for i in range(first, last) if i % 7]).items():
+        if at == gone:
+            for i, page in byte:
+                bt.tables[0, i] = page
+    attention_within(attend(nrc, bt, packed), dense_attention(bt))
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+@pytest.mark.parametrize("bs,gone", [(1, []), (1, [2900]), (1, [700, 1900]), (2, [1200])])
+def test_shares_of_many_blocks(nrc, bs, gone, fp4):
+    """A workgroup's keys in more than a thousand blocks, with some that are not there."""
+    nodes = [256, 250, 200, 256]
+    bt = Batch([3100, 3000, 2500, 3199], nodes, H=8, G=8, block_size=bs, tree=False, seed=bs).behind(3000, 5)
+    need = nrc._load().nrc_context_window_attention_workspace_bytes(4, sum(nodes), 64, 8, 256, 3199, 3000, 5)
+    assert need == 0  # not split: a workgroup's share is all that its rows see
+    packed = bt.pack(nrc) if fp4 else None
+    for i in gone:
+        bt.tables[1:, i // bs] = -1
+    attention_within(attend(nrc, bt, packed, max_ctx=3199), dense_attention(bt))
+
+
+def test_pages_of_other_sizes_give_the_same_bits(nrc):
+    """A long share's tiles go the same way whatever the pages: the same keys in 263, 1050 and 4200 blocks."""
+    ctx, n, H = 16500, 300, 32
+    bt = Batch([ctx], [n], H=H, G=8, block_size=64, tree=False, seed=4, spare=0).behind(17000)
+    assert nrc._load().nrc_context_window_attention_workspace_bytes(1, n, 8 * H, H, n, ctx, 17000, 0) == 0  # not split
+    keys = bt.cache[bt.tables[0].long()].transpose(1, 2).flatten(0, 1)  # in their order
+    want = None
+    for bs in (64, 16, 4):
+        bt.bs, bt.nb = bs, keys.shape[0] // bs
+        order = torch.randperm(bt.nb, generator=torch.Generator().manual_seed(bs))
+        bt.cache = torch.empty(bt.nb, H, bs, 128, dtype=torch.bfloat16)
+        bt.cache[order] = keys.unflatten(0, (bt.nb, bs)).transpose(1, 2)
+        bt.tables = order.to(torch.int32)[None]
+        packed = bt.pack(nrc)
+        got = attend(nrc, bt, packed, max_ctx=ctx)
+        if want is None:
+            want = got
+            attention_within(got, dense_attention(bt))
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), bs
