@@ -73,12 +73,9 @@ __device__ __forceinline__ int2 whole_tiles(const Keyspan& k, const Tiles& t, in
     return int2{(int32_t)first, (int32_t)(upto < first ? first : upto)};
 }
 
-enum Seen { kNobody, kSome, kEverybody };
-template <int KEYS>
-__device__ __forceinline__ Seen seen_by(const Keyspan& k, int32_t sinks, int32_t key0) {
-    if (key0 > k.hi_max || (key0 + (KEYS - 1) < k.lo_min && key0 >= sinks)) return kNobody;
-    if (key0 + (KEYS - 1) <= k.hi_min && (key0 >= k.lo_max || key0 + (KEYS - 1) < sinks)) return kEverybody;
-    return kSome;
+// May any of the rows see one of the 32 keys from key0 on?
+__device__ __forceinline__ bool may_be_seen(const Keyspan& k, int32_t sinks, int32_t key0) {
+    return key0 <= k.hi_max && (key0 + 31 >= k.lo_min || key0 < sinks);
 }
 
 // The bits i of a word of 32 with i < n (any n).
@@ -775,7 +772,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
             if (sub >= from && sub < upto) continue;
             const uint32_t keys_there = (uint32_t)((kStage > 64 && sub & 2 ? exists[kStage / 64 - 1] : exists[0]) >> (32 * (sub & 1)));
             const int32_t at = tiles.key(v * kStage + 32 * sub);
-            if (seen_by<32>(span, a.sinks, at) != kNobody && keys_there != 0u) masked(buf, sub, at, keys_there);
+            if (may_be_seen(span, a.sinks, at) && keys_there != 0u) masked(buf, sub, at, keys_there);
         }
     };
 
