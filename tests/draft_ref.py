@@ -178,3 +178,27 @@ def dense_attention(bt, scale=0.125):
             tol_o[lo:lo + n, of] = fold(o.abs() * 2.0 ** -8 + (2 * eps[:, None] + 2.0 ** -8) * A * 1.01)
             tol_l[lo:lo + n, of] = fold(torch.where(some, eps * 1.01 + (l.abs() + 24) * 3 * 2.0 ** -24, 0.0))
     return out, lse, tol_o, tol_l
+
+
+def sum_depth(T, heads, others, lanes, num_cus):
+    """How many additions a term of the gains' gradients passes at most: the heads of T rows go two (or one) a group of `lanes` lanes, to
+    workgroups of 256 / lanes groups, 8 a CU that the queries and keys (heads and others) share; a lane adds its group's
+    rounds, a workgroup its groups, the joining launch's threads a 64th of the workgroups each in four sums (and up to three
+    more in the first), then these, then 64 threads' by halves."""
+    groups, pairs, other_pairs = 256 // lanes, T * (-(-heads // 2)), T * (-(-others // 2))
+    most = 8 * num_cus
+    blocks = min(-(-pairs // groups), max(1, most * pairs // (pairs + other_pairs) - 1))
+    return 2 * -(-pairs // (blocks * groups)) + groups + blocks // 256 + 4 + 2 + 6
+
+
+def gains_grad(gy, x, w, pos, table, layout, eps, depth):
+    """(dw, its bound) of norm_rotate_grad by the depth of the sums, which is far less than the number of their terms: with e = (d
+    / 2 + 8) 2^-24 for x r a term g x r is off by e + 4 2^-24 of G |x r|, each addition that it passes adds 2^-24 of it, and
+    the sum is rounded to the gains' type."""
+    d = x.shape[-1]
+    x, gy = x.double(), gy.double()
+    u = x / torch.sqrt(x.square().mean(-1, keepdim=True) + eps)
+    g, G = turn(gy, pos, table, layout, -1.0)
+    dw = (g * u).sum((0, 1))
+    tol = (G * u.abs()).sum((0, 1)) * (d / 2 + 12 + depth) * 2.0 ** -24 * 1.01 + dw.abs() * half_step(w.dtype) * 1.01
+    return dw, tol + torch.finfo(w.dtype).smallest_normal * torch.finfo(w.dtype).eps

@@ -156,3 +156,45 @@ def test_reference_of_all_rows_at_once(monkeypatch):
         bt.tables[2, :] = bt.nb  # nothing at all
         for a, b in zip(dense_attention(bt), cache_ref.attention(bt)):
             assert torch.allclose(a, b, rtol=1e-9, atol=1e-12)
+
+
+def gains_inputs(T, heads, d, along, seed):
+    """x, its outputs' gradients, gains, positions and a table; along: gradients that are near the outputs, so that the gains' sums
+    grow with every row."""
+    from draft_ref import turn
+
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, heads, d, generator=gen).bfloat16()
+    w = 1 + 0.2 * torch.randn(d, generator=gen)
+    pos = torch.randint(0, 300, (T,), generator=gen)
+    angle = torch.arange(300)[:, None] * 10000.0 ** (-torch.arange(d // 2) / (d / 2))
+    cs = torch.cat([angle.cos(), angle.sin()], 1)
+    g = torch.randn(T, heads, d, generator=gen)
+    if along:
+        g = turn(x.double(), pos, cs, "half")[0].float() + 0.1 * g
+    return x, g.bfloat16(), w, pos, cs
+
+
+@pytest.mark.parametrize("along", [False, True])
+def test_bound_of_the_gains_gradients_rejects_lost_rows(along):
+    """Of 4099 rows of 23 heads: one row, a workgroup's rows, the last of a walk's rounds left out, heads counted twice, all of it
+    lost; and the sums in FP32 in another order are within it."""
+    from draft_ref import gains_grad, sum_depth
+
+    x, g, w, pos, cs = gains_inputs(4099, 23, 64, along, 5)
+    depth = sum_depth(4099, 23, 3, 4, 256)
+    assert depth < 128
+    dw, tol = gains_grad(g, x, w, pos, cs, "half", 1e-6, depth)
+    rejects = lambda other: int(((other - dw).abs() > tol).sum())
+    part = lambda rows: gains_grad(g[rows], x[rows], w, pos[rows], cs, "half", 1e-6, depth)[0]
+    one = part(slice(4098, 4099))
+    assert rejects(dw - one) >= 50 and rejects(dw + one) >= 50
+    for rows in (slice(100, 106), slice(4000, 4099), slice(0, 2)):
+        assert rejects(dw - part(rows)) >= 50, rows
+    assert rejects(torch.zeros_like(dw)) == 64
+    xf, gf = x.float(), g.float()
+    u = xf * torch.rsqrt(xf.square().mean(-1, keepdim=True) + 1e-6)
+    back = cs[pos][:, None, :]
+    a, b = gf[..., :32], gf[..., 32:]
+    gf = torch.cat([a * back[..., :32] + b * back[..., 32:], b * back[..., :32] - a * back[..., 32:]], -1)
+    assert rejects((gf * u).flip(0).sum((0, 1)).double()) == 0

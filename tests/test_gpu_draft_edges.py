@@ -8,7 +8,8 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from draft_ref import dense_attention, make_batch  # noqa: E402
+from draft_ref import dense_attention, gains_grad, make_batch, sum_depth  # noqa: E402
+from test_draft_edges_abi import gains_inputs  # noqa: E402
 from test_gpu_qk_norm import dev, inputs, within  # noqa: E402
 
 Batch = make_batch()
@@ -201,3 +202,21 @@ def test_pages_of_other_sizes_give_the_same_bits(nrc):
             want = got
             attention_within(got, dense_attention(bt))
         assert all(torch.equal(a, b) for a, b in zip(got, want)), bs
+
+
+@pytest.mark.parametrize("along", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,d", [(4099, 23, 3, 64), (20000, 5, 1, 64), (3001, 2, 31, 128), (70000, 8, 2, 64)])
+def test_gains_gradients_of_many_rows(nrc, T, Hq, Hk, d, along):
+    """By the depth of the sums: one row that is lost or counted twice is outside the bound."""
+    parts = [gains_inputs(T, h, d, along, T + h) for h in (Hq, Hk)]
+    pos, cs = parts[0][3], parts[0][4]
+    if along:  # (the keys' gradients are along the outputs of their own positions)
+        parts[1] = (*parts[1][:3], pos, cs)
+        from draft_ref import turn
+
+        parts[1] = (parts[1][0], turn(parts[1][0].double(), pos, cs, "half")[0].bfloat16(), *parts[1][2:])
+    (q, gq, qw, *_), (k, gk, kw, *_) = parts
+    back = nrc.qk_norm_rotate_grad(*(dev(t) for t in (gq, gk, q, k, pos, cs, qw, kw)), layout="half")
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    for i, (x, g, w, h, o) in enumerate(((q, gq, qw, Hq, Hk), (k, gk, kw, Hk, Hq))):
+        within(back[2 + i], *gains_grad(g, x, w, pos, cs, "half", 1e-6, sum_depth(T, h, o, d // 16, cus)))
