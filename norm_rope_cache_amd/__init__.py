@@ -1078,9 +1078,15 @@ def _get_norm_rotation():
             q, k, q_weight, k_weight, positions, cos_sin = ctx.saved_tensors
             # (a gradient of a sum is one value for all: no unit stride)
             whole = lambda g: g.clone(memory_format=torch.contiguous_format) if g is not None and g.stride(2) != 1 else g
-            back = qk_norm_rotate_grad(whole(grad_q), whole(grad_k), q, k, positions, cos_sin, q_weight, k_weight, ctx.eps,
-                                       ctx.layout)
-            return back + (None,) * 5
+            rest = positions, cos_sin
+            need = ctx.needs_input_grad  # (frozen queries, or keys: nothing of theirs is read or worked out)
+            if not (need[0] or need[2]) and k is not None and k.shape[1] > 0:
+                dk, _, dkw, _ = qk_norm_rotate_grad(whole(grad_k), None, k, None, *rest, k_weight, None, ctx.eps, ctx.layout)
+                return (None, dk, None, dkw) + (None,) * 5
+            if not (need[1] or need[3]):
+                k = grad_k = k_weight = None
+            return qk_norm_rotate_grad(whole(grad_q), whole(grad_k), q, k, *rest, q_weight, k_weight, ctx.eps,
+                                       ctx.layout) + (None,) * 5
 
     _norm_rotation = NormRotation
     return NormRotation

@@ -220,3 +220,29 @@ def test_gains_gradients_of_many_rows(nrc, T, Hq, Hk, d, along):
     cus = torch.cuda.get_device_properties(0).multi_processor_count
     for i, (x, g, w, h, o) in enumerate(((q, gq, qw, Hq, Hk), (k, gk, kw, Hk, Hq))):
         within(back[2 + i], *gains_grad(g, x, w, pos, cs, "half", 1e-6, sum_depth(T, h, o, d // 16, cus)))
+
+
+@pytest.mark.parametrize("wanted", ["q", "k", "qw", "kw", "q kw", "q qw", "k kw", "q k qw kw"])
+def test_frozen_parts_are_not_worked_out(nrc, monkeypatch, wanted):
+    """Gradients of some inputs: those of all, without the queries' or the keys' work where nobody asks for it."""
+    i = inputs(30, 4, 2, 64, 32, torch.bfloat16, torch.float32, 6)
+    all_of = dict(zip(("q", "k", "pos", "cs", "qw", "kw"), (dev(t) for t in (i["q"], i["k"], i["pos"], i["cs"], *i["w"]))))
+    gq, gk = dev(i["gq"]), dev(i["gk"])
+    full = dict(zip(("q", "k", "qw", "kw"), nrc.qk_norm_rotate_grad(gq, gk, *all_of.values())))
+    names = wanted.split()
+    leaves = [all_of[n].requires_grad_() for n in names]
+    heads, plain = [], nrc.qk_norm_rotate_grad
+
+    def counted(grad_q, grad_k, q, k, *rest, **kw):
+        heads.append(q.shape[1] + (0 if k is None else k.shape[1]))
+        return plain(grad_q, grad_k, q, k, *rest, **kw)
+
+    monkeypatch.setattr(nrc, "qk_norm_rotate_grad", counted)
+    out = nrc.qk_norm_rotate(*all_of.values())
+    got = torch.autograd.grad(out, leaves, (gq, gk))
+    assert heads == [4 * any(n[0] == "q" for n in names) + 2 * any(n[0] == "k" for n in names)]
+    tols = {n + "w": gains_grad(i["g" + n], i[n], w, i["pos"], i["cs"], "interleaved", 1e-6, sum_depth(30, h, 6 - h, 4, 256))[1]
+            for n, w, h in zip("qk", i["w"], (4, 2))}
+    for n, g in zip(names, got):
+        # (another number of workgroups: the gains' sums in another order, each within the bound)
+        assert torch.equal(g, full[n]) if n in "qk" else bool(((g - full[n]).abs().cpu() <= 2 * tols[n]).all())
