@@ -593,7 +593,8 @@ int64_t nrc_qk_norm_rotate_grad_workspace_bytes(int32_t head_dim, int32_t with_g
  * A code is 4 bits, the sign on top: 0 .5 1 1.5 2 3 4 6; element 2 i of a row is the
  * low half of its byte i. A cell's scale bytes belong to elements 0 .. 31 and
  * 32 .. 63 of K, then of V; an element stands for its code's value times 2^(byte -
- * 127). nrc_context_fp4_store writes bytes 7 .. 252, and 255 in all four of a cell
+ * 127). nrc_context_attention_mass and nrc_context_kv_evict take bf16 caches alone.
+ * nrc_context_fp4_store writes bytes 7 .. 252, and 255 in all four of a cell
  * that had an infinity or NaN in K or V: such a cell stands for NaN. Others
  * (3 of 4 bytes 255, 253, 254, 0 .. 6) mean nothing that is promised.
  */
@@ -742,8 +743,12 @@ int64_t nrc_context_tree_attention_workspace_bytes(int32_t B, int64_t T, int32_t
  * Without tree_mask node i stands at ctx_lens[b] + i, and nodes are keys like the
  * context's: node j is seen if j <= i and it lies in the window or among the sinks. With
  * tree_mask a row stands at ctx_lens[b] + the nodes it sees - 1 (its depth in the
- * tree), and over its nodes the mask alone decides. Keys that no row of a call can see are
- * not read: a row costs its window, not its context.
+ * tree), and over its nodes the mask alone decides. As long as no path of nodes is longer than the window,
+ * a row sees what the same path's row sees as a chain; behind a shorter window it also sees those
+ * nodes of its path that a chain's row would not: over a tree's nodes nothing slides.
+ * A key's place in the cache counts as its position: behind nrc_context_kv_evict, which moves cells to
+ * other places, a window means nothing. Keys that no row of a call can see are not read: a row
+ * costs its window, not its context.
  * Prompts are chains too: max_nodes up to 65535, and rows far apart share no work.
  * The other arguments, results and errors as nrc_context_tree_attention_ex, the workspace
  * as nrc_context_window_attention_workspace_bytes says. Errors also: NRC_EINVAL for a

@@ -1552,9 +1552,11 @@ def context_window_attention(q, cache, tables, ctx_lens, q_starts, max_nodes, wi
     sinks   and the keys j < sinks
     Without tree_mask node i stands at ctx_lens + i, and the window goes over the nodes too;
     with it a row stands at ctx_lens + the nodes it sees - 1, and over its
-    nodes the mask alone decides. Keys that no row can see are not read. A prompt's
-    chunk is a chain of up to 65535 nodes. Other arguments and results as
-    context_tree_attention."""
+    nodes the mask alone decides: where a path of a tree is longer than the window, its
+    rows see more than a chain's would. A key's place counts as its position: not for a cache that
+    context_kv_evict has moved cells in. Keys that no row can see are not read. A
+    prompt's chunk is a chain of up to 65535 nodes. Other arguments and results
+    as context_tree_attention."""
     _bf16_cache(cache)
     if isinstance(window, int) and window < 1:
         raise ValueError("window must be at least 1")

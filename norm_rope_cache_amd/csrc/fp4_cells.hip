@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kThreads) void fp4_store_kernel(Fp4Rows r, Fp4Cache
 }
 
 // 16 lanes a unit, a dword of codes a lane, so that rows are written in whole runs of 128 bytes (a group a lane: 29.6
-// us for what takes 22.6 so); U units to a lane, their loads on the way together.
+// us for what took 22.1 so; 21.1 with places by products); U units to a lane, their loads on the way together.
 // fill: rows without a cell become 0, not left as they are.
 template <int U>
 __global__ __launch_bounds__(kThreads) void fp4_load_kernel(Fp4Rows r, Fp4Cache c, Divs by,

@@ -366,7 +366,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
     if (count > 0) {
         // kAhead tiles to a round. Every load is made in every round (past the last tile, of some tile again), so that the
         // compiler knows how many are on the way and waits for the oldest alone; block numbers come two rounds ahead. The last round
-        // brings nothing for a next one (a token behind a window of 1024 keys: 17 us with such loads, 13 without).
+        // brings nothing for a next one (in a captured graph, with such loads and without: a token behind a window of 1024 keys
+        // 16.2 and 12.6 us, 64 sequences of up to 1024 packed keys 20.6 and 16.3, of 4096 33.8 and 31.5, of 16384 93.6 and
+        // 98.1, 16 of 65536 98.6 and 96.8).
         // The first tile that is not whole comes behind the first round's, in the slot that is still free.
         Raw raw[kAhead];
         uint32_t there[kAhead];
@@ -481,15 +483,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_few_kernel(WindowArgs a,
 // buffers: four threads a key bring a quarter of its cell each into registers while the waves work on the tile before, open it
 // where it is packed, and leave it in the other buffer; one barrier a tile. So a key is opened once for all rows of the
 // workgroup. LDS layout and matrix operands as many_rows_kernel of tree_attention.hip.
-// Measured: 4 sequences of up to 65536 packed keys, 8 KV heads, 384 rows a head: 202 us, 666 TFLOP/s (with 64 keys a stage of 4 waves, so
-// twice the barriers, 214); two prompts of 4096 tokens, 64 heads, window 1024: 199 us, 548 TFLOP/s. The vector unit is what is
+// Measured: 4 sequences of up to 65536 packed keys, 8 KV heads, 384 rows a head: 203 us, 660 TFLOP/s (with 64 keys a stage of 4 waves, so
+// twice the barriers, 214); two prompts of 4096 tokens, 64 heads, window 1024: 200 us, 545 TFLOP/s. The vector unit is what is
 // busiest (a score's exponential, its product, sum and rounding: of 32 x 32 scores about 60 instructions of a wave to 8 of the matrix
 // cores, which take half as long); a window's short run of tiles also has its first loads and its masked ends to wait for.
 constexpr int kStage = 128;
 constexpr int kManyLds = 2 * kStage * (256 + 4);
 
 // PAGES (block_size a multiple of 16, so that a wave's 16 keys lie in one page): where the cells of tiles that every row sees
-// whole lie is scalar work, and a lane adds its own place in 16 cells, which is always the same (worked out by each lane 261 us for what takes 241 so; pages of 24 cells 287 us for 512 rows where those of 64 take 257).
+// whole lie is scalar work, and a lane adds its own place in 16 cells, which is always the same (pages of 24
+// cells, for which each lane works it out: 250 us for 384 rows where pages of 64 take 204, 262 for 512 rows where those take 226).
 template <int WAVES, bool CAP, bool FP4, bool PAGES>
 __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a, uint32_t groups, uint32_t grid) {
     if (blockIdx.x >= grid) {
@@ -879,7 +882,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void window_many_kernel(WindowArgs a
         // One 32 keys' scores are on the way in the matrix cores while the vector unit takes the last ones' exponentials,
         // over the barrier too: a tile's last weights are taken behind it, with the next one's first scores on the way.
         // The stage's last part goes ahead of the other workgroup's waves, so that this one's reach their barrier together; the
-        // phases are kept apart (trees of 48 nodes over 65536 packed keys 214 us; with the phases mixed by the compiler, which
+        // phases are kept apart (trees of 48 nodes over 65536 packed keys, 64 a stage: 214 us; with the phases mixed by the compiler, which
         // then puts matrix instructions behind each other, 274).
         Keys32 k;
         f32x16 sc[2];
@@ -1093,8 +1096,8 @@ WindowPlan plan_window_attention(int32_t B, int32_t H, int32_t G, int32_t max_no
     const int64_t rows = (int64_t)max_nodes * G, base = (int64_t)B * H;
     const bool ragged = window == kNoWindow;  // lengths that differ as the contexts do; over a window they are about equal
     p.many = rows > 32;
-    // (512 rows over contexts of up to 65536 packed keys 257 us; in blocks of 128 rows, which open each key twice as often, 283; a
-    // prompt of 8192 tokens behind a window of 2048 377 and 386)
+    // (512 rows over contexts of up to 65536 packed keys 226 us; in blocks of 128 rows, which open each key twice as often, 258; a
+    // prompt of 8192 tokens behind a window of 2048 370 and 380; but two prompts of 4096 behind 1024 196 and 183)
     p.waves = p.many && rows > 128 ? 8 : 4;
     // waves without rows are idle: blocks of 128 rows where those of 256 would be filled to less than four fifths as much
     if (p.waves == 8 && 4 * ((rows + 255) / 256 * 256) > 5 * ((rows + 127) / 128 * 128)) p.waves = 4;
